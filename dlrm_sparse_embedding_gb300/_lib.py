@@ -33,6 +33,9 @@ EXPORTS = (
     "emb_set_timing", "emb_phase_times", "emb_unique_noalloc", "emb_set_early_dedup",
     "emb_get_master_rows", "emb_set_master_rows", "emb_gather_master_rows", "emb_find_keys",
     "emb_cache_build", "emb_forward_infer", "emb_status_string",
+    "emb_expert_sort_workspace", "emb_expert_sort", "emb_expert_dispatch", "emb_expert_dispatch_grad",
+    "emb_expert_combine", "emb_expert_combine_grad", "emb_expert_linear", "emb_expert_linear_grad_rows",
+    "emb_expert_linear_grad_weight", "emb_orthogonalize_workspace", "emb_orthogonalize", "emb_dense_status",
 )
 UNIQUE_NOALLOC_MAX_KEYS = 262144
 PHASES = ("forward", "dedup", "reduce_update")
@@ -43,6 +46,11 @@ class EmbTableSpec(ctypes.Structure):
                 ("pooling", ctypes.c_int32), ("opt", ctypes.c_int32), ("lr", ctypes.c_float),
                 ("eps", ctypes.c_float), ("init_acc", ctypes.c_float), ("master_fp32", ctypes.c_int32),
                 ("dynamic", ctypes.c_int32)]
+
+
+class EmbExpertPlan(ctypes.Structure):
+    _fields_ = [("offsets", ctypes.c_void_p), ("src", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("tokens", ctypes.c_int64), ("k", ctypes.c_int32), ("experts", ctypes.c_int32)]
 
 
 class EmbError(RuntimeError):
@@ -88,6 +96,19 @@ def _load() -> ctypes.CDLL:
     L.emb_launch_count.argtypes = [vp, ctypes.POINTER(i64), i32]
     L.emb_set_timing.argtypes = [vp, i32]
     L.emb_phase_times.argtypes = [vp, ctypes.POINTER(f32), i32, ctypes.POINTER(i64), i32]
+    plan, size = ctypes.POINTER(EmbExpertPlan), ctypes.POINTER(ctypes.c_size_t)
+    L.emb_expert_sort_workspace.argtypes = [i64, i32, i32, size]
+    L.emb_expert_sort.argtypes = [vp, i32, plan, vp, ctypes.c_size_t, vp]
+    L.emb_expert_dispatch.argtypes = [plan, vp, i32, i64, i64, vp, i32, vp]
+    L.emb_expert_dispatch_grad.argtypes = [plan, vp, i32, i64, i64, vp, i32, vp]
+    L.emb_expert_combine.argtypes = [plan, vp, i32, i64, vp, i64, vp, i32, vp]
+    L.emb_expert_combine_grad.argtypes = [plan, vp, i32, i64, vp, i32, i64, vp, i64, vp, vp, vp]
+    L.emb_expert_linear.argtypes = [plan, vp, i64, vp, i64, i64, i32, vp, vp]
+    L.emb_expert_linear_grad_rows.argtypes = [plan, vp, i64, vp, i64, i64, i32, vp, vp]
+    L.emb_expert_linear_grad_weight.argtypes = [plan, vp, i64, vp, i64, i64, i64, i32, vp, vp]
+    L.emb_orthogonalize_workspace.argtypes = [i64, i64, i64, size]
+    L.emb_orthogonalize.argtypes = [vp, i32, i64, i64, i64, i64, i64, i32, f32, f32, f32, f32, vp, vp, ctypes.c_size_t, vp]
+    L.emb_dense_status.argtypes = [vp]
     L.emb_status_string.argtypes = [c_int]
     L.emb_status_string.restype = ctypes.c_char_p
     for name in EXPORTS:

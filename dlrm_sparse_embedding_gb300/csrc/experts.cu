@@ -1,0 +1,562 @@
+// The expert layer's data movement: the stable sort of a batch's assignments
+// by expert, the gather of the tokens' rows into expert order, the weighted sum
+// back, and the gradients of both.
+//
+// All of it is bound by memory: each row is read once and written once per
+// place it goes to.  The kernels that touch rows therefore walk the tokens, not
+// the sorted rows: a token's row (its gradient) is loaded into registers once
+// and stored to (combined from) its k places, so the k copies never come from
+// memory again.
+#include <mutex>
+
+#include "dense_internal.cuh"
+#include "emb_internal.cuh"
+
+namespace emb {
+namespace {
+
+constexpr int kMaxDevices = 64;
+__device__ int g_status[2];   // [0] sticky bits, [1] the bits taken by emb_dense_status
+
+std::mutex g_status_mutex;
+int* g_status_addr[kMaxDevices] = {};
+
+__global__ void take_status(int* status) { status[1] = atomicExch(&status[0], 0); }
+
+// ---------------------------------------------------------------------------
+// sort
+// ---------------------------------------------------------------------------
+// A counting sort in chunks of consecutive assignments.  Every block counts its
+// chunk's experts; with more than one chunk, expert_count has left all counts
+// in memory and a block adds up the chunks before its own instead of waiting
+// for them (E counts a chunk, read from L2).  Bucket E holds the assignments
+// without an expert, so they too have a row, the tail's.
+constexpr int kPlaceThreads = 1024;
+constexpr int kPlaceWarps = kPlaceThreads / 32;
+constexpr int kMaxChunks = 2 * 152;           // at most two blocks an SM
+constexpr int kPlaceChunk = 8 * kPlaceThreads;   // assignments a block; below it one launch does everything
+
+template <class ID>
+__device__ __forceinline__ int bucket_of(const ID* ids, int64_t a, int E, int* status)
+{
+    const long long v = (long long)ids[a];
+    if (v >= 0 && v < E) return (int)v;
+    if (v != -1 && status) atomicOr(status, ERRBIT_KEY_RANGE);
+    return E;
+}
+
+template <class ID>
+__global__ void __launch_bounds__(kPlaceThreads) expert_count(const ID* __restrict__ ids, int P, int E, int chunk,
+                                                             int* __restrict__ counts)
+{
+    extern __shared__ int cnt[];
+    for (int e = threadIdx.x; e <= E; e += kPlaceThreads) cnt[e] = 0;
+    __syncthreads();
+    const int lo = blockIdx.x * chunk, hi = min(P, lo + chunk);
+    for (int a = lo + threadIdx.x; a < hi; a += kPlaceThreads) atomicAdd(&cnt[bucket_of(ids, a, E, nullptr)], 1);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= E; e += kPlaceThreads) counts[(int64_t)blockIdx.x * (E + 1) + e] = cnt[e];
+}
+
+// Exclusive prefix sum of v[0..n) in place, n <= 2 * kPlaceThreads.
+__device__ void block_exclusive_scan(int* v, int n, int* warp_sums)
+{
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+    const int a = 2 * t < n ? v[2 * t] : 0, b = 2 * t + 1 < n ? v[2 * t + 1] : 0;
+    int s = a + b;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, s, d);
+        if (lane >= d) s += u;
+    }
+    if (lane == 31) warp_sums[w] = s;
+    __syncthreads();
+    if (w == 0) {
+        int x = warp_sums[lane];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += u;
+        }
+        warp_sums[lane] = x;
+    }
+    __syncthreads();
+    const int before = s - (a + b) + (w ? warp_sums[w - 1] : 0);
+    if (2 * t < n) v[2 * t] = before;
+    if (2 * t + 1 < n) v[2 * t + 1] = before + a;
+    __syncthreads();
+}
+
+// Shared memory: next[E + 1] (row the next assignment of each bucket gets),
+// warp_sums[32], and per warp a count for each bucket.
+template <class ID>
+__global__ void __launch_bounds__(kPlaceThreads) expert_place(const ID* __restrict__ ids, int P, int E, int chunk,
+                                                             const int* __restrict__ counts, int32_t* __restrict__ offsets,
+                                                             int32_t* __restrict__ src, int32_t* __restrict__ pos,
+                                                             int* status)
+{
+    extern __shared__ int smem[];
+    int* const next = smem;
+    int* const warp_sums = next + (E + 1);
+    unsigned short* const of_warp = reinterpret_cast<unsigned short*>(warp_sums + 32);   // [bucket][warp]
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+    const int lo = blockIdx.x * chunk, hi = min(P, lo + chunk);
+
+    // the first row of every bucket, and of this chunk's part of it
+    int mine_before[2] = {0, 0};   // this chunk's predecessors in buckets t and t + kPlaceThreads
+    if (counts) {
+        for (int q = 0; q < 2; ++q) {
+            const int e = t + q * kPlaceThreads;
+            if (e > E) break;
+            int total = 0, before = 0;
+            for (int c = 0; c < (int)gridDim.x; ++c) {
+                const int v = __ldg(&counts[(int64_t)c * (E + 1) + e]);
+                if (c < (int)blockIdx.x) before += v;
+                total += v;
+            }
+            next[e] = total;
+            mine_before[q] = before;
+        }
+    } else {
+        for (int e = t; e <= E; e += kPlaceThreads) next[e] = 0;
+        __syncthreads();
+        for (int a = lo + t; a < hi; a += kPlaceThreads) atomicAdd(&next[bucket_of(ids, a, E, nullptr)], 1);
+    }
+    __syncthreads();
+    block_exclusive_scan(next, E + 1, warp_sums);
+    for (int q = 0; q < 2; ++q) {
+        const int e = t + q * kPlaceThreads;
+        if (e > E) break;
+        if (blockIdx.x == 0) offsets[e] = next[e];
+        next[e] += mine_before[q];
+    }
+    for (int i = t; i < (E + 1) * kPlaceWarps; i += kPlaceThreads) of_warp[i] = 0;
+    __syncthreads();
+
+    // kPlaceThreads assignments at a time, in order: an assignment's row is its
+    // bucket's next one, plus those of earlier warps, plus those of lower lanes
+    for (int base = lo; base < hi; base += kPlaceThreads) {
+        const int a = base + t;
+        const int e = a < hi ? bucket_of(ids, a, E, status) : E + 1;
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        const int rank = __popc(same & ((1u << lane) - 1));
+        if (e <= E && rank == 0) of_warp[e * kPlaceWarps + w] = (unsigned short)__popc(same);
+        __syncthreads();
+        if (e <= E) {
+            int row = next[e] + rank;
+            for (int v = 0; v < w; ++v) row += of_warp[e * kPlaceWarps + v];
+            pos[a] = e < E ? row : -1;
+            src[row] = e < E ? a : -1;
+        }
+        __syncthreads();
+        // one thread of each bucket that occurred moves its next row on and clears its counts
+        for (int b = t; b <= E; b += kPlaceThreads) {
+            int n = 0;
+            for (int v = 0; v < kPlaceWarps; ++v) {
+                n += of_warp[b * kPlaceWarps + v];
+                of_warp[b * kPlaceWarps + v] = 0;
+            }
+            next[b] += n;
+        }
+        __syncthreads();
+    }
+}
+
+size_t place_smem(int E) { return sizeof(int) * (E + 1 + 32) + sizeof(unsigned short) * (size_t)(E + 1) * kPlaceWarps; }
+
+// ---------------------------------------------------------------------------
+// rows
+// ---------------------------------------------------------------------------
+// V consecutive elements: 8 (moved 16 bytes at a time) where everything is
+// aligned for it, else 1.
+template <int V, class T>
+__device__ __forceinline__ void load_vec(const T* p, float (&v)[V])
+{
+    if constexpr (V == 1) {
+        v[0] = to_float<T>(*p);
+    } else if constexpr (sizeof(T) == 4) {
+        const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+        const uint4 r = *reinterpret_cast<const uint4*>(p);
+        const T* e = reinterpret_cast<const T*>(&r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = to_float<T>(e[i]);
+    }
+}
+
+template <int V, class T>
+__device__ __forceinline__ void store_vec(T* p, const float (&v)[V])
+{
+    if constexpr (V == 1) {
+        *p = from_float<T>(v[0]);
+    } else if constexpr (sizeof(T) == 4) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        uint4 r;
+        T* e = reinterpret_cast<T*>(&r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = from_float<T>(v[i]);
+        *reinterpret_cast<uint4*>(p) = r;
+    }
+}
+
+constexpr int kRowThreads = 256;
+constexpr int kUnroll = 4;   // vectors a lane holds at once
+
+// Zero the rows past the last group; warps first, first + step, ... of the
+// caller share them.
+template <int V, class T>
+__device__ __forceinline__ void zero_tail(T* rows, int64_t width, int kept, int P, int64_t first, int64_t step, int lane)
+{
+    const float zero[V] = {};
+    for (int64_t p = kept + first; p < P; p += step)
+        for (int64_t c = (int64_t)lane * V; c < width; c += 32 * V) store_vec<V, T>(rows + p * width + c, zero);
+}
+
+// A warp takes kUnroll * 32 vectors of one token's row: loaded once, stored to
+// each of its k rows.
+template <int V, class X, class R>
+__global__ void __launch_bounds__(kRowThreads) dispatch_rows(emb_expert_plan plan, const X* __restrict__ x,
+                                                             int64_t x_stride, int64_t width, int64_t pieces,
+                                                             R* __restrict__ rows)
+{
+    const int lane = threadIdx.x & 31, P = (int)(plan.tokens * plan.k);
+    const int64_t warps = (int64_t)gridDim.x * (kRowThreads / 32);
+    const int64_t first = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+    for (int64_t u = first; u < plan.tokens * pieces; u += warps) {
+        const int64_t token = u / pieces, c0 = (u - token * pieces) * (32 * V * kUnroll) + lane * V;
+        float v[kUnroll][V];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i)
+            if (c0 + i * 32 * V < width) load_vec<V, X>(x + token * x_stride + c0 + i * 32 * V, v[i]);
+        for (int j = 0; j < plan.k; ++j) {
+            const int p = __ldg(&plan.pos[token * plan.k + j]);
+            if ((unsigned)p >= (unsigned)P) continue;
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i)
+                if (c0 + i * 32 * V < width) store_vec<V, R>(rows + (int64_t)p * width + c0 + i * 32 * V, v[i]);
+        }
+    }
+    zero_tail<V, R>(rows, width, plan_offset(plan.offsets, plan.experts, P), P, first, warps, lane);
+}
+
+// out[t] = sum_j w[t, j] rows[pos[t, j]]; without weights, the plain sum (the
+// dispatch's gradient).
+template <int V, class R, class O, bool WEIGHTED>
+__global__ void __launch_bounds__(kRowThreads) gather_sum(emb_expert_plan plan, const R* __restrict__ rows,
+                                                          int64_t rows_stride, const float* __restrict__ weights,
+                                                          int64_t width, int64_t pieces, O* __restrict__ out)
+{
+    const int lane = threadIdx.x & 31, P = (int)(plan.tokens * plan.k);
+    const int64_t warps = (int64_t)gridDim.x * (kRowThreads / 32);
+    const int64_t first = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+    for (int64_t u = first; u < plan.tokens * pieces; u += warps) {
+        const int64_t token = u / pieces, c0 = (u - token * pieces) * (32 * V * kUnroll) + lane * V;
+        float s[kUnroll][V] = {};
+        for (int j = 0; j < plan.k; ++j) {
+            const int p = __ldg(&plan.pos[token * plan.k + j]);
+            if ((unsigned)p >= (unsigned)P) continue;
+            const float w = WEIGHTED ? __ldg(&weights[token * plan.k + j]) : 1.f;
+            float v[kUnroll][V];
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i)
+                if (c0 + i * 32 * V < width) load_vec<V, R>(rows + p * rows_stride + c0 + i * 32 * V, v[i]);
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i)
+                if (c0 + i * 32 * V < width) {
+#pragma unroll
+                    for (int q = 0; q < V; ++q) s[i][q] = WEIGHTED ? __fmaf_rn(w, v[i][q], s[i][q]) : s[i][q] + v[i][q];
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i)
+            if (c0 + i * 32 * V < width) store_vec<V, O>(out + token * width + c0 + i * 32 * V, s[i]);
+    }
+}
+
+// Both gradients of the weighted sum.  blockDim.x threads take a token: its
+// gradient is loaded once for kPart of its experts at a time.
+constexpr int kPart = 4;
+
+template <int V, class O, class R>
+__global__ void __launch_bounds__(kRowThreads) combine_grad(emb_expert_plan plan, const O* __restrict__ grad_out,
+                                                            int64_t grad_stride, const R* __restrict__ rows,
+                                                            int64_t rows_stride, const float* __restrict__ weights,
+                                                            int64_t width, R* __restrict__ grad_rows,
+                                                            float* __restrict__ grad_weights)
+{
+    __shared__ float part[kRowThreads / 32][kPart];
+    const int P = (int)(plan.tokens * plan.k), lane = threadIdx.x & 31;
+    const int warps_of = blockDim.x / 32, wx = threadIdx.x >> 5, wy = threadIdx.y * warps_of;
+    const int64_t step = (int64_t)gridDim.x * blockDim.y;
+    // a block's tokens move on together: every thread meets every barrier
+    for (int64_t t0 = (int64_t)blockIdx.x * blockDim.y; t0 < plan.tokens; t0 += step) {
+        const int64_t token = t0 + threadIdx.y;
+        const bool has = token < plan.tokens;
+        for (int j0 = 0; j0 < plan.k; j0 += kPart) {
+            float dot[kPart] = {}, w[kPart] = {};
+            int p[kPart];
+#pragma unroll
+            for (int q = 0; q < kPart; ++q) {
+                p[q] = has && j0 + q < plan.k ? __ldg(&plan.pos[token * plan.k + j0 + q]) : -1;
+                if ((unsigned)p[q] >= (unsigned)P) p[q] = -1;
+                if (p[q] >= 0) w[q] = __ldg(&weights[token * plan.k + j0 + q]);
+            }
+            if (has) {
+                for (int64_t c = (int64_t)threadIdx.x * V; c < width; c += (int64_t)blockDim.x * V) {
+                    float g[V], y[kPart][V];
+                    load_vec<V, O>(grad_out + token * grad_stride + c, g);
+#pragma unroll
+                    for (int q = 0; q < kPart; ++q)
+                        if (p[q] >= 0) load_vec<V, R>(rows + p[q] * rows_stride + c, y[q]);
+#pragma unroll
+                    for (int q = 0; q < kPart; ++q)
+                        if (p[q] >= 0) {
+                            float d[V];
+#pragma unroll
+                            for (int i = 0; i < V; ++i) {
+                                dot[q] = __fmaf_rn(g[i], y[q][i], dot[q]);
+                                d[i] = w[q] * g[i];
+                            }
+                            store_vec<V, R>(grad_rows + (int64_t)p[q] * width + c, d);
+                        }
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < kPart; ++q) {
+#pragma unroll
+                for (int d = 16; d; d >>= 1) dot[q] += __shfl_xor_sync(0xffffffffu, dot[q], d);
+                if (lane == 0) part[wy + wx][q] = dot[q];
+            }
+            __syncthreads();
+            if (has && threadIdx.x < kPart && j0 + threadIdx.x < plan.k) {
+                float s = 0.f;
+                for (int v = 0; v < warps_of; ++v) s += part[wy + v][threadIdx.x];
+                grad_weights[token * plan.k + j0 + threadIdx.x] = s;
+            }
+            __syncthreads();
+        }
+    }
+    const int64_t warps = (int64_t)gridDim.x * (kRowThreads / 32);
+    zero_tail<V, R>(grad_rows, width, plan_offset(plan.offsets, plan.experts, P), P,
+                    (int64_t)blockIdx.x * (kRowThreads / 32) + wy + wx, warps, lane);
+}
+
+int launched() { return cudaGetLastError() == cudaSuccess ? EMB_OK : EMB_ERR_CUDA; }
+
+// Whether rows of `width` elements can be moved 16 bytes at a time.
+bool wide(const void* p, int dtype, int64_t stride, int64_t width)
+{
+    return aligned_to(p, 16) && (stride * dtype_bytes(dtype)) % 16 == 0 && width % 8 == 0;
+}
+
+bool rows_valid(const void* p, int dtype, int64_t stride, int64_t width, int64_t n)
+{
+    return dtype_valid(dtype) && stride >= width && aligned_to(p, dtype_bytes(dtype)) && (p || n == 0);
+}
+
+int64_t pieces_of(int64_t width, int V) { return (width + 32 * V * kUnroll - 1) / (32 * V * kUnroll); }
+
+unsigned row_blocks(int64_t warps)
+{
+    const int64_t per = kRowThreads / 32, b = (warps + per - 1) / per;
+    return (unsigned)(b < 1 ? 1 : b > (1 << 20) ? (1 << 20) : b);
+}
+
+template <class F>
+int with_type(int dtype, F f)
+{
+    if (dtype == EMB_F32) return f(float());
+    if (dtype == EMB_F16) return f(__half());
+    return f(__nv_bfloat16());
+}
+
+template <bool WEIGHTED>
+int launch_gather_sum(const emb_expert_plan& plan, const void* rows, int rows_dtype, int64_t stride, const float* weights,
+                      int64_t width, void* out, int out_dtype, cudaStream_t st)
+{
+    const bool w8 = wide(rows, rows_dtype, stride, width) && wide(out, out_dtype, width, width);
+    return with_type(rows_dtype, [&](auto r) {
+        return with_type(out_dtype, [&](auto o) {
+            using R = decltype(r);
+            using O = decltype(o);
+            const int64_t pieces = pieces_of(width, w8 ? 8 : 1);
+            const unsigned blocks = row_blocks(plan.tokens * pieces);
+            if (w8)
+                gather_sum<8, R, O, WEIGHTED><<<blocks, kRowThreads, 0, st>>>(plan, (const R*)rows, stride, weights, width, pieces, (O*)out);
+            else
+                gather_sum<1, R, O, WEIGHTED><<<blocks, kRowThreads, 0, st>>>(plan, (const R*)rows, stride, weights, width, pieces, (O*)out);
+            return launched();
+        });
+    });
+}
+
+}  // namespace
+
+int* dense_status_word()
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+    std::lock_guard<std::mutex> lock(g_status_mutex);
+    if (!g_status_addr[dev]) {
+        void* p = nullptr;
+        if (cudaGetSymbolAddress(&p, g_status) != cudaSuccess) {
+            cudaGetLastError();
+            return nullptr;
+        }
+        g_status_addr[dev] = static_cast<int*>(p);
+    }
+    return g_status_addr[dev];
+}
+
+bool expert_plan_valid(const emb_expert_plan* plan)
+{
+    if (!plan || plan->tokens < 0 || plan->k < 1 || plan->k > kMaxExpertsPerToken || plan->experts < 1 ||
+        plan->experts > kMaxExperts || plan->tokens > INT32_MAX / plan->k)
+        return false;
+    if (!plan->offsets || !aligned_to(plan->offsets, 4) || !aligned_to(plan->src, 4) || !aligned_to(plan->pos, 4)) return false;
+    return plan->tokens == 0 || (plan->src && plan->pos);
+}
+
+}  // namespace emb
+
+using namespace emb;
+
+extern "C" int emb_dense_status(void* stream)
+{
+    int* const word = dense_status_word();
+    if (!word) return EMB_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int bits = 0;
+    take_status<<<1, 1, 0, st>>>(word);
+    if (cudaGetLastError() != cudaSuccess || cudaMemcpyAsync(&bits, word + 1, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
+        return EMB_ERR_CUDA;
+    return bits & ERRBIT_TIMEOUT ? EMB_ERR_TIMEOUT : bits & ERRBIT_KEY_RANGE ? EMB_ERR_KEY_RANGE : EMB_OK;
+}
+
+// Assignments a block of the sort takes: kPlaceChunk, more where that would make
+// so many blocks that adding up the earlier ones' counts costs more than the rest.
+static int sort_chunk(int64_t P)
+{
+    const int64_t even = (P + kMaxChunks - 1) / kMaxChunks;
+    return even <= kPlaceChunk ? kPlaceChunk : (int)((even + kPlaceThreads - 1) / kPlaceThreads * kPlaceThreads);
+}
+static int sort_chunks(int64_t P) { return (int)((P + sort_chunk(P) - 1) / sort_chunk(P)); }
+
+extern "C" int emb_expert_sort_workspace(int64_t tokens, int32_t k, int32_t experts, size_t* bytes)
+{
+    if (!bytes || tokens < 0 || k < 1 || k > kMaxExpertsPerToken || experts < 1 || experts > kMaxExperts || tokens > INT32_MAX / k)
+        return EMB_ERR_INVALID_ARG;
+    const int chunks = sort_chunks(tokens * k);
+    *bytes = chunks > 1 ? ((sizeof(int) * (size_t)chunks * (experts + 1) + 255) & ~size_t(255)) : 256;
+    return EMB_OK;
+}
+
+extern "C" int emb_expert_sort(const void* ids, int32_t id_bytes, const emb_expert_plan* plan, void* workspace,
+                               size_t workspace_bytes, void* stream)
+{
+    size_t need = 0;
+    if (!expert_plan_valid(plan) || emb_expert_sort_workspace(plan->tokens, plan->k, plan->experts, &need) != EMB_OK ||
+        (id_bytes != 4 && id_bytes != 8) || (!ids && plan->tokens) || !aligned_to(ids, id_bytes) || !workspace ||
+        !aligned_to(workspace, 256) || workspace_bytes < need)
+        return EMB_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int* const word = dense_status_word();
+    if (!word) return EMB_ERR_CUDA;
+    const int P = (int)(plan->tokens * plan->k), E = plan->experts, chunks = sort_chunks(P), chunk = sort_chunk(P);
+    if (P == 0) return cudaMemsetAsync(plan->offsets, 0, sizeof(int32_t) * (E + 1), st) == cudaSuccess ? EMB_OK : EMB_ERR_CUDA;
+    int* const counts = chunks > 1 ? static_cast<int*>(workspace) : nullptr;
+    const size_t smem = place_smem(E);
+    const auto go = [&](auto id) {
+        using ID = decltype(id);
+        if (cudaFuncSetAttribute(expert_place<ID>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+            cudaGetLastError();
+            return (int)EMB_ERR_CUDA;
+        }
+        if (counts) {
+            expert_count<ID><<<chunks, kPlaceThreads, sizeof(int) * (E + 1), st>>>((const ID*)ids, P, E, chunk, counts);
+            if (int rc = launched()) return rc;
+        }
+        expert_place<ID><<<chunks, kPlaceThreads, smem, st>>>((const ID*)ids, P, E, chunk, counts, plan->offsets, plan->src, plan->pos, word);
+        return launched();
+    };
+    return id_bytes == 4 ? go(int32_t()) : go((long long)0);
+}
+
+extern "C" int emb_expert_dispatch(const emb_expert_plan* plan, const void* x, int32_t x_dtype, int64_t x_stride, int64_t width,
+                                   void* rows, int32_t rows_dtype, void* stream)
+{
+    if (!expert_plan_valid(plan) || width < 1 || !rows_valid(x, x_dtype, x_stride, width, plan->tokens) ||
+        !rows_valid(rows, rows_dtype, width, width, plan->tokens))
+        return EMB_ERR_INVALID_ARG;
+    if (plan->tokens == 0) return EMB_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool w8 = wide(x, x_dtype, x_stride, width) && wide(rows, rows_dtype, width, width);
+    return with_type(x_dtype, [&](auto xt) {
+        return with_type(rows_dtype, [&](auto rt) {
+            using X = decltype(xt);
+            using R = decltype(rt);
+            const int64_t pieces = pieces_of(width, w8 ? 8 : 1);
+            const unsigned blocks = row_blocks(plan->tokens * pieces);
+            if (w8)
+                dispatch_rows<8, X, R><<<blocks, kRowThreads, 0, st>>>(*plan, (const X*)x, x_stride, width, pieces, (R*)rows);
+            else
+                dispatch_rows<1, X, R><<<blocks, kRowThreads, 0, st>>>(*plan, (const X*)x, x_stride, width, pieces, (R*)rows);
+            return launched();
+        });
+    });
+}
+
+extern "C" int emb_expert_dispatch_grad(const emb_expert_plan* plan, const void* grad_rows, int32_t rows_dtype,
+                                        int64_t grad_stride, int64_t width, void* grad_x, int32_t x_dtype, void* stream)
+{
+    if (!expert_plan_valid(plan) || width < 1 || !rows_valid(grad_rows, rows_dtype, grad_stride, width, plan->tokens) ||
+        !rows_valid(grad_x, x_dtype, width, width, plan->tokens))
+        return EMB_ERR_INVALID_ARG;
+    if (plan->tokens == 0) return EMB_OK;
+    return launch_gather_sum<false>(*plan, grad_rows, rows_dtype, grad_stride, nullptr, width, grad_x, x_dtype, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int emb_expert_combine(const emb_expert_plan* plan, const void* rows, int32_t rows_dtype, int64_t rows_stride,
+                                  const float* weights, int64_t width, void* out, int32_t out_dtype, void* stream)
+{
+    if (!expert_plan_valid(plan) || width < 1 || !rows_valid(rows, rows_dtype, rows_stride, width, plan->tokens) ||
+        !rows_valid(out, out_dtype, width, width, plan->tokens) || !aligned_to(weights, 4) || (!weights && plan->tokens))
+        return EMB_ERR_INVALID_ARG;
+    if (plan->tokens == 0) return EMB_OK;
+    return launch_gather_sum<true>(*plan, rows, rows_dtype, rows_stride, weights, width, out, out_dtype, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int emb_expert_combine_grad(const emb_expert_plan* plan, const void* grad_out, int32_t out_dtype, int64_t grad_stride,
+                                       const void* rows, int32_t rows_dtype, int64_t rows_stride, const float* weights,
+                                       int64_t width, void* grad_rows, float* grad_weights, void* stream)
+{
+    if (!expert_plan_valid(plan) || width < 1 || !rows_valid(grad_out, out_dtype, grad_stride, width, plan->tokens) ||
+        !rows_valid(rows, rows_dtype, rows_stride, width, plan->tokens) || !rows_valid(grad_rows, rows_dtype, width, width, plan->tokens) ||
+        !aligned_to(weights, 4) || !aligned_to(grad_weights, 4) || ((!weights || !grad_weights) && plan->tokens))
+        return EMB_ERR_INVALID_ARG;
+    if (plan->tokens == 0) return EMB_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool w8 = wide(grad_out, out_dtype, grad_stride, width) && wide(rows, rows_dtype, rows_stride, width) &&
+                    wide(grad_rows, rows_dtype, width, width);
+    const int V = w8 ? 8 : 1;
+    int tx = 32;   // threads a token: enough that each has two vectors of its row
+    while (tx < kRowThreads && (int64_t)tx * 2 * V < width) tx *= 2;
+    const dim3 block(tx, kRowThreads / tx);
+    const int64_t b = (plan->tokens + block.y - 1) / block.y;
+    const unsigned blocks = (unsigned)(b > (1 << 20) ? (1 << 20) : b);
+    return with_type(out_dtype, [&](auto ot) {
+        return with_type(rows_dtype, [&](auto rt) {
+            using O = decltype(ot);
+            using R = decltype(rt);
+            if (w8)
+                combine_grad<8, O, R><<<blocks, block, 0, st>>>(*plan, (const O*)grad_out, grad_stride, (const R*)rows, rows_stride, weights, width, (R*)grad_rows, grad_weights);
+            else
+                combine_grad<1, O, R><<<blocks, block, 0, st>>>(*plan, (const O*)grad_out, grad_stride, (const R*)rows, rows_stride, weights, width, (R*)grad_rows, grad_weights);
+            return launched();
+        });
+    });
+}

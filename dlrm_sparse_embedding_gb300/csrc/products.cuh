@@ -1,0 +1,51 @@
+// Matrix products of the expert layer and of the orthogonalisation (sm_103a):
+// what a product computes, shared by its callers and its kernel.
+#pragma once
+
+#include "dense_internal.cuh"
+
+namespace emb {
+
+// A number held as fp16 h plus fp16 l / kLowScale: l is h's rounding error, at
+// most 2^-11 |h|, scaled up so that it is not lost where h is subnormal.
+constexpr float kLowScale = 2048.f;
+
+// D = epilogue(sum_k A[m][k] B[n][k]) over a list of independent problems.  An
+// operand is "k-major" when its k runs along memory, "mn-major" when its m (n)
+// does.
+struct ProductArgs {
+    int dtype = EMB_F16;           // of A and B: EMB_F16 or EMB_BF16
+    const void* a = nullptr;
+    const void* b = nullptr;
+    int64_t lda = 0, ldb = 0;      // elements between consecutive rows in memory
+    bool a_mn = false, b_mn = false;
+    int64_t m = 0, n = 0, k = 0;
+
+    // grouped rows: problem e's rows are [offsets[e], offsets[e + 1]) of P
+    //   m_grouped: they are A's and D's m (B is the e-th of a stack)
+    //   k_grouped: they are k of A and B (D is the e-th of a stack)
+    const int32_t* offsets = nullptr;
+    bool m_grouped = false, k_grouped = false;
+
+    // a batch: problem i has its own A, B, C and D, batch strides apart
+    int64_t batch = 1, batch_a = 0, batch_b = 0;
+
+    // epilogue: D = alpha * s^power * (acc + ...) with the terms a caller asks for
+    const float* scale = nullptr;  // per problem, or null for 1
+    int scale_power = 1;
+    float alpha = 1.f;             // factor of the accumulated product
+    float beta = 0.f;              // factor of C (+ C's low part)
+    float diagonal = 0.f;          // added to D[i][i]
+    const void* c = nullptr;       // as D; fp16
+    const void* c_low = nullptr;   // C's scaled rounding error (see kLowScale), or null
+    int64_t ldc = 0, batch_c = 0;
+    void* d = nullptr;
+    void* d_low = nullptr;         // takes D's scaled rounding error, or null
+    int d_dtype = EMB_F16;
+    int64_t ldd = 0, batch_d = 0;
+};
+
+// Enqueue the product.  EMB_OK or an error with nothing enqueued.
+int launch_product(const ProductArgs& p, cudaStream_t st);
+
+}  // namespace emb

@@ -51,7 +51,7 @@ typedef enum {
     EMB_ERR_CUDA = -3,          /* a CUDA runtime call or launch failed */
     EMB_ERR_KEY_RANGE = -4,     /* GPU saw a key outside [0, rows) */
     EMB_ERR_CAPACITY = -5,      /* GPU hash table full */
-    EMB_ERR_TIMEOUT = -6,       /* a bounded GPU wait gave up (reserved: no current kernel waits) */
+    EMB_ERR_TIMEOUT = -6,       /* a bounded GPU wait gave up (see emb_dense_status) */
     EMB_ERR_STATE = -7          /* call out of order (e.g. backward before any forward) */
 } emb_status;
 
@@ -362,6 +362,116 @@ int emb_launch_count(emb_layer* layer, int64_t* count_host, int32_t reset);
 enum { EMB_PHASE_FORWARD = 0, EMB_PHASE_DEDUP = 1, EMB_PHASE_REDUCE_UPDATE = 2, EMB_NUM_PHASES = 3 };
 int emb_set_timing(emb_layer* layer, int32_t enable);
 int emb_phase_times(emb_layer* layer, float* ms_host, int32_t n, int64_t* steps_host, int32_t reset);
+
+/* -------------------------------------------------------------------------
+ * Experts.  The dense side of a recommender sends each sample (token) of the
+ * pooled embeddings to k of E experts and adds their answers up, weighted.
+ * The calls below are the data movement and the products of that layer; the
+ * router's scores, the activation between two products and the loss are the
+ * caller's.  They keep no state and need no layer: every array is the
+ * caller's.  Types named "dtype" are an emb_dtype.  A "stride" is the distance
+ * in elements between the starts of two consecutive rows, at least the row's
+ * width; the elements of a row are contiguous.  Arrays without a stride are
+ * contiguous.  A 16-byte aligned array with rows of a multiple of 16 bytes is
+ * moved 16 bytes at a time, any other one element at a time.
+ * What the GPU alone can see (an id outside [-1, E), a bounded wait that ran
+ * out) is recorded in a sticky word of the device, see emb_dense_status.
+ * ------------------------------------------------------------------------- */
+
+/* Where each assignment of a batch goes.  Assignment a = t * k + j is token t's
+ * j-th expert, P = tokens * k (0 <= P < 2^31).  Device arrays:
+ *   offsets[E + 1]  first row of each expert's group; offsets[E] rows are kept
+ *   src[P]          the assignment in row p, in increasing order within a
+ *                   group; -1 for p >= offsets[E]
+ *   pos[P]          the row of assignment a, -1 for one without an expert
+ * The calls that read a plan skip a pos outside [0, P) and read offsets
+ * clamped into [0, P] and made non-decreasing, so no plan sends them outside
+ * the arrays.  tokens >= 0, k in [1, 64], experts (E) in [1, 1024]. */
+typedef struct {
+    int32_t* offsets;
+    int32_t* src;
+    int32_t* pos;
+    int64_t tokens;
+    int32_t k;
+    int32_t experts;
+} emb_expert_plan;
+
+/* Build a plan: a stable sort of the assignments by expert.  ids[P] are int32
+ * (id_bytes 4) or int64 (id_bytes 8); id -1 is an assignment without an expert
+ * (a dropped one).  Any other id outside [0, E) is treated as -1 and recorded
+ * as EMB_ERR_KEY_RANGE.  The arrays of `plan` are written.  The workspace
+ * (256-byte aligned, emb_expert_sort_workspace bytes) is free again once the
+ * call's work on the stream is done.  No passage: library convenience (the
+ * pages stop at the embeddings). */
+int emb_expert_sort_workspace(int64_t tokens, int32_t k, int32_t experts, size_t* bytes);
+int emb_expert_sort(const void* ids, int32_t id_bytes, const emb_expert_plan* plan, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* Gather the tokens' rows in expert order, rows[p] = x[src[p] / k] for
+ * p < offsets[E] and 0 for the rows after them, x [tokens, width] and rows
+ * [P, width]; and the gradient of x, grad_x[t] = sum_j grad_rows[pos[t, j]],
+ * added in fp32 in the order of j and rounded once.  A token without experts
+ * gets a zero gradient.  Both types are any emb_dtype.  No passage: library
+ * convenience. */
+int emb_expert_dispatch(const emb_expert_plan* plan, const void* x, int32_t x_dtype, int64_t x_stride, int64_t width,
+                        void* rows, int32_t rows_dtype, void* stream);
+int emb_expert_dispatch_grad(const emb_expert_plan* plan, const void* grad_rows, int32_t rows_dtype,
+                             int64_t grad_stride, int64_t width, void* grad_x, int32_t x_dtype, void* stream);
+
+/* Back to tokens, weighted: out[t] = sum_j weights[t, j] * rows[pos[t, j]],
+ * fp32 weights and sums, in the order of j, rounded once to out_dtype; a token
+ * without experts gets zeros.  The gradients:
+ *   grad_rows[p]       = weights[src[p]] * grad_out[src[p] / k]   (0 for p >= offsets[E]),  in rows' dtype
+ *   grad_weights[t, j] = <grad_out[t], rows[pos[t, j]]>           (0 without an expert),    fp32
+ * The weight of an assignment without an expert is not used: it may be
+ * anything, NaN included.  No passage: library convenience. */
+int emb_expert_combine(const emb_expert_plan* plan, const void* rows, int32_t rows_dtype, int64_t rows_stride,
+                       const float* weights, int64_t width, void* out, int32_t out_dtype, void* stream);
+int emb_expert_combine_grad(const emb_expert_plan* plan, const void* grad_out, int32_t out_dtype, int64_t grad_stride,
+                            const void* rows, int32_t rows_dtype, int64_t rows_stride, const float* weights,
+                            int64_t width, void* grad_rows, float* grad_weights, void* stream);
+
+/* Each expert's product over its own rows.  dtype is EMB_F16 or EMB_BF16 for
+ * every array; in_width and out_width are multiples of 8; all arrays are
+ * 16-byte aligned and strides multiples of 8; weight is
+ * [E, out_width, in_width].  For p in group e (offsets[e] <= p < offsets[e+1]):
+ *   y[p]           = weight[e] rows[p]                         [P, out_width]
+ *   grad_rows[p]   = weight[e]^T grad_y[p]                     [P, in_width]
+ *   grad_weight[e] = sum over the group of grad_y[p] rows[p]^T [E, out_width, in_width]
+ * with products exact, sums in fp32 and one rounding.  Rows p >= offsets[E] are
+ * written as zeros and not read; an expert without rows has a zero grad_weight.
+ * A group's results do not depend on the rows of the others, whatever they
+ * hold.  No passage: library convenience. */
+int emb_expert_linear(const emb_expert_plan* plan, const void* rows, int64_t rows_stride, const void* weight,
+                      int64_t in_width, int64_t out_width, int32_t dtype, void* y, void* stream);
+int emb_expert_linear_grad_rows(const emb_expert_plan* plan, const void* grad_y, int64_t grad_stride,
+                                const void* weight, int64_t in_width, int64_t out_width, int32_t dtype,
+                                void* grad_rows, void* stream);
+int emb_expert_linear_grad_weight(const emb_expert_plan* plan, const void* grad_y, int64_t grad_stride,
+                                  const void* rows, int64_t rows_stride, int64_t in_width, int64_t out_width,
+                                  int32_t dtype, void* grad_weight, void* stream);
+
+/* Orthogonalise `batch` matrices G [rows, cols] by `steps` (1..32) quintic
+ * Newton-Schulz steps, as the Muon optimiser does with a momentum
+ * (K. Jordan et al., 2024):
+ *   X = G / (|G|_F + eps);  steps times:  A = X X^T,  X <- a X + (b A + c A A) X
+ * (on the transpose where rows > cols).  G is any emb_dtype, with
+ * batch_stride and row_stride in elements; out is bf16 [batch, rows, cols],
+ * contiguous.  Between the steps X is held as the sum of two fp16 numbers and
+ * A as one, sums are fp32: about a tenth of the error of bf16 arithmetic.  A
+ * zero matrix stays zero; one that holds an infinity or a NaN gives NaNs and
+ * leaves the others alone.  rows and cols in [1, 65536].  The workspace is
+ * 256-byte aligned, emb_orthogonalize_workspace bytes.  No passage: library
+ * convenience. */
+int emb_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols, size_t* bytes);
+int emb_orthogonalize(const void* update, int32_t dtype, int64_t batch_stride, int64_t row_stride, int64_t batch,
+                      int64_t rows, int64_t cols, int32_t steps, float a, float b, float c, float eps, void* out,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* Wait for the stream; return and clear the device's sticky status of the
+ * calls of this section (EMB_OK, EMB_ERR_KEY_RANGE or EMB_ERR_TIMEOUT).  No
+ * passage: library convenience. */
+int emb_dense_status(void* stream);
 
 /* Static description of an emb_status value.  No passage: library convenience. */
 const char* emb_status_string(int status);
