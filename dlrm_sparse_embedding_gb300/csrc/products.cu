@@ -1,107 +1,529 @@
-// Matrix products of the expert layer and of the orthogonalisation.
+// Matrix products of the expert layer and of the orthogonalisation, on the
+// tensor cores.
+//
+// A persistent grid: each CTA, or pair of CTAs on one 256 x 256 tile, walks the
+// tiles of all problems.  One warp's thread copies 64-wide steps of A and B to a
+// ring of stages, one issues the products into one of two accumulators in
+// tensor memory, and four warps take the other accumulator through the epilogue
+// meanwhile.
+//
+// Groups of rows start anywhere and have any length.  Where they are m, a tile
+// reads whatever follows its group and does not store it: a row's garbage stays
+// in its row.  Where they are k (a weight's gradient), the last step's rows past
+// the group are zeroed in shared memory, in both operands, before it is
+// multiplied: 0 times an infinity or a NaN of the next group would not be 0.
+#include <atomic>
+
+#include "emb_internal.cuh"
 #include "products.cuh"
+#include "tensor_core.cuh"
 
 namespace emb {
 namespace {
 
-constexpr int kTile = 64, kStep = 16, kThreads = 256;
+constexpr int kRows = 128;                      // of A a CTA holds a step: its accumulator's lanes
+constexpr int kStep = 64;                       // k of a stage: 128 bytes
+constexpr int kThreads = 256;                   // warps: copy, products, tails, (none), 4 of the epilogue
+constexpr int kBlockBytes = 64 * 128;           // an mn-major block: 64 k of 64 m
+constexpr int kStageOperand = kRows * 128;      // bytes of one operand a stage
+constexpr int kStages = 6;
+constexpr int kChunk = 32;                      // columns an epilogue warp takes at once
+constexpr int kStagingWarp = 32 * kChunk * 4;
+constexpr int kMaxDevices = 64;
 
-template <class T>
-__device__ __forceinline__ float element(const void* p, int64_t ld, bool mn, int64_t r, int64_t k)
+template <int CTAS_, int BN_>
+struct Shape {
+    static constexpr int CTAS = CTAS_;
+    static constexpr int BM = kRows * CTAS, BN = BN_;
+    static constexpr int kBRows = BN / CTAS;    // of B a CTA holds a step
+    static constexpr uint32_t kColumns = 2 * BN;   // two accumulators
+};
+
+struct Control {
+    uint64_t full[kStages], empty[kStages], part[kStages];   // part: a step whose rows past the group are still to be zeroed
+    uint64_t acc_full[2], acc_empty[2];
+    uint32_t tmem;
+    int gave_up;
+};
+
+constexpr int smem_bytes() { return 1024 + kStages * 2 * kStageOperand + 4 * kStagingWarp + 512 + 2 * (kMaxExperts + 2) * 4; }
+
+struct Tile {
+    int problem;         // B's (and D's) index in its stack
+    int64_t m0, m_end;   // rows of D
+    int64_t n0;
+    int64_t k0, k_end;
+    int steps;
+};
+
+struct Problems {
+    ProductArgs p;
+    CUtensorMap a, b;
+    int tiles_n, tiles_m;   // of one problem; tiles_m of k-grouped and batched ones
+    int* status;
+};
+
+// The list of tiles.  m-grouped problems have as many tiles as their rows need,
+// one problem after another, and last the rows without an expert.
+template <class S>
+struct List {
+    const Problems& q;
+    const int* start;    // m-grouped: first row tile of each group, the tail's and the end; shared memory
+    const int* rows;     // grouped: first row of each group, the tail's and the end
+    int64_t total;
+
+    __device__ Tile at(int64_t t) const
+    {
+        Tile r;
+        const int64_t row_tile = t / q.tiles_n;
+        r.n0 = (t - row_tile * q.tiles_n) * S::BN;
+        r.k0 = 0, r.k_end = q.p.k;
+        if (q.p.m_grouped) {
+            int lo = 0, hi = (int)q.p.batch;   // the last group that starts at or before row_tile
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (start[mid] <= row_tile) lo = mid; else hi = mid - 1;
+            }
+            r.problem = lo;
+            r.m0 = rows[lo] + (row_tile - start[lo]) * S::BM;
+            r.m_end = rows[lo + 1];
+            if (lo == q.p.batch) r.k_end = 0;
+        } else {
+            r.problem = (int)(row_tile / q.tiles_m);
+            r.m0 = (row_tile - (int64_t)r.problem * q.tiles_m) * S::BM;
+            r.m_end = q.p.m;
+            if (q.p.k_grouped) r.k0 = rows[r.problem], r.k_end = rows[r.problem + 1];
+        }
+        r.steps = (int)((r.k_end - r.k0 + kStep - 1) / kStep);
+        return r;
+    }
+};
+
+// Both tables, by the whole block: rows is the plan's offsets made sound, start
+// the running count of row tiles.
+template <class S>
+__device__ void make_tables(const Problems& q, int* start, int* rows)
 {
-    return to_float<T>(static_cast<const T*>(p)[mn ? k * ld + r : r * ld + k]);
+    const int E = (int)q.p.batch, P = (int)(q.p.m_grouped ? q.p.m : q.p.k);
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int carried = 0, tiles = 0;
+        for (int base = 0; base <= E; base += 32) {   // offsets never decrease: a running maximum
+            const int e = base + lane;
+            int v = e <= E ? plan_offset(q.p.offsets, e, P) : P;
+            v = max(v, carried);
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, d);
+                if (lane >= d) v = max(v, u);
+            }
+            if (e <= E) rows[e] = v;
+            carried = __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) rows[E + 1] = P;
+        __syncwarp();
+        for (int base = 0; base <= E; base += 32) {
+            const int e = base + lane;
+            const int mine = e <= E ? (rows[e + 1] - rows[e] + S::BM - 1) / S::BM : 0;
+            int s = mine;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, s, d);
+                if (lane >= d) s += u;
+            }
+            if (e <= E) start[e] = tiles + s - mine;
+            tiles += __shfl_sync(0xffffffffu, s, 31);
+        }
+        if (lane == 0) start[E + 1] = tiles;
+    }
 }
 
-// One 64 x 64 tile of one problem a block; a thread has 4 x 4 of it.
-template <class T>
-__global__ void __launch_bounds__(kThreads) product_tiles(ProductArgs p, int experts)
+// Eight consecutive elements of a row of D from the accumulated products.
+__device__ __forceinline__ void finish(const ProductArgs& p, int64_t problem, float s, int64_t m, int64_t n, float (&v)[8])
 {
-    __shared__ float as[kStep][kTile + 1], bs[kStep][kTile + 1];
-    const int t = threadIdx.x, tm = t / 16, tn = t % 16;
-    int64_t m0 = (int64_t)blockIdx.y * kTile, m_end = p.m, k0 = 0, k_end = p.k;
-    const int64_t n0 = (int64_t)blockIdx.x * kTile;
-    int problem = blockIdx.z;
-    const int P = (int)(p.k_grouped ? p.k : p.m);
-    bool tail = false;
-    if (p.m_grouped) {   // blockIdx.y counts the groups' tiles one after another; the rows after them are zeroed
-        int64_t left = blockIdx.y;
-        int first = 0;
-        for (problem = 0; problem <= experts; ++problem) {
-            const int lo = max(first, plan_offset(p.offsets, problem, P));
-            const int hi = problem < experts ? max(lo, plan_offset(p.offsets, problem + 1, P)) : P;
-            const int64_t tiles = (hi - lo + kTile - 1) / kTile;
-            if (left < tiles) {
-                m0 = lo + left * kTile;
-                m_end = hi;
-                break;
-            }
-            left -= tiles;
-            first = lo;
+    const int64_t at_c = (p.m_grouped ? 0 : problem * p.batch_c) + m * p.ldc + n;
+    const int64_t at = (p.m_grouped ? 0 : problem * p.batch_d) + m * p.ldd + n;
+    if (p.c) {
+        // C's rows are padded to a multiple of 8 elements
+        const uint4 h = *reinterpret_cast<const uint4*>(static_cast<const __half*>(p.c) + at_c);
+        const __half* hv = reinterpret_cast<const __half*>(&h);
+        float c[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = __half2float(hv[i]);
+        if (p.c_low) {
+            const uint4 l = *reinterpret_cast<const uint4*>(static_cast<const __half*>(p.c_low) + at_c);
+            const __half* lv = reinterpret_cast<const __half*>(&l);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c[i] = __fmaf_rn(1.f / kLowScale, __half2float(lv[i]), c[i]);
         }
-        if (problem > experts) return;
-        tail = problem == experts;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __fmaf_rn(p.beta, c[i], p.alpha * v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= p.alpha;
     }
-    if (p.k_grouped) {
-        k0 = plan_offset(p.offsets, problem, P);
-        k_end = max((int64_t)k0, (int64_t)plan_offset(p.offsets, problem + 1, P));
-    }
-    const T* const a = static_cast<const T*>(p.a) + (p.m_grouped || p.k_grouped ? 0 : problem * p.batch_a);
-    const T* const b = static_cast<const T*>(p.b) + (p.k_grouped || tail ? 0 : problem * p.batch_b);
-    float acc[4][4] = {};
-    if (!tail)
-        for (int64_t k = k0; k < k_end; k += kStep) {
-            for (int i = t; i < kTile * kStep; i += kThreads) {
-                const int r = p.a_mn ? i % kTile : i / kStep, c = p.a_mn ? i / kTile : i % kStep;
-                as[c][r] = m0 + r < m_end && k + c < k_end ? element<T>(a, p.lda, p.a_mn, m0 + r, k + c) : 0.f;
-                const int rb = p.b_mn ? i % kTile : i / kStep, cb = p.b_mn ? i / kTile : i % kStep;
-                bs[cb][rb] = n0 + rb < p.n && k + cb < k_end ? element<T>(b, p.ldb, p.b_mn, n0 + rb, k + cb) : 0.f;
-            }
-            __syncthreads();
-            for (int c = 0; c < kStep; ++c)
-                for (int i = 0; i < 4; ++i)
-                    for (int j = 0; j < 4; ++j) acc[i][j] = __fmaf_rn(as[c][tm * 4 + i], bs[c][tn * 4 + j], acc[i][j]);
-            __syncthreads();
-        }
-    float s = 1.f;
     if (p.scale) {
-        s = p.scale[problem];
-        if (p.scale_power == 2) s *= s;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= s;
     }
-    const int64_t at_c = p.m_grouped ? 0 : problem * p.batch_c, at_d = p.m_grouped ? 0 : problem * p.batch_d;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + tm * 4 + i, n = n0 + tn * 4 + j;
-            if (m >= m_end || n >= p.n) continue;
-            float v = p.alpha * acc[i][j];
-            if (p.c) {
-                float c = __half2float(static_cast<const __half*>(p.c)[at_c + m * p.ldc + n]);
-                if (p.c_low) c = __fmaf_rn(1.f / kLowScale, __half2float(static_cast<const __half*>(p.c_low)[at_c + m * p.ldc + n]), c);
-                v = __fmaf_rn(p.beta, c, v);
-            }
-            v *= s;
-            if (m == n) v += p.diagonal;
-            const int64_t at = at_d + m * p.ldd + n;
-            if (p.d_dtype == EMB_BF16) {
-                static_cast<__nv_bfloat16*>(p.d)[at] = __float2bfloat16_rn(v);
-            } else {
-                const __half h = __float2half_rn(v);
-                static_cast<__half*>(p.d)[at] = h;
-                if (p.d_low) static_cast<__half*>(p.d_low)[at] = __float2half_rn(kLowScale * (v - __half2float(h)));
+    if (p.diagonal != 0.f && m >= n && m < n + 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (m == n + i) v[i] += p.diagonal;
+    }
+    uint4 o;
+    if (p.d_dtype == EMB_BF16) {
+        __nv_bfloat16* ov = reinterpret_cast<__nv_bfloat16*>(&o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ov[i] = __float2bfloat16_rn(v[i]);
+    } else {
+        __half* ov = reinterpret_cast<__half*>(&o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ov[i] = __float2half_rn(v[i]);
+    }
+    if ((p.ldd & 7) == 0 && (p.batch_d & 7) == 0 && (reinterpret_cast<uintptr_t>(p.d) & 15) == 0) {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.d) + at) = o;
+    } else {
+        const uint16_t* ov = reinterpret_cast<const uint16_t*>(&o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (n + i < p.n) static_cast<uint16_t*>(p.d)[at + i] = ov[i];
+    }
+    if (p.d_low) {
+        uint4 l;
+        __half* lv = reinterpret_cast<__half*>(&l);
+        const __half* ov = reinterpret_cast<const __half*>(&o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) lv[i] = __float2half_rn(kLowScale * (v[i] - __half2float(ov[i])));
+        *reinterpret_cast<uint4*>(static_cast<__half*>(p.d_low) + at) = l;
+    }
+}
+
+template <class S, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(kThreads, 1) product_tiles(const __grid_constant__ Problems q)
+{
+    constexpr int CTAS = S::CTAS;
+    constexpr int kBBytes = S::kBRows * 128;
+    constexpr uint32_t kTx = CTAS * (kStageOperand + kBBytes);
+    extern __shared__ __align__(1024) unsigned char dynamic[];
+    unsigned char* const base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dynamic) + 1023) & ~uintptr_t(1023));
+    unsigned char* const stage_a = base;
+    unsigned char* const stage_b = base + kStages * kStageOperand;
+    float* const staging = reinterpret_cast<float*>(base + 2 * kStages * kStageOperand);
+    Control* const ctl = reinterpret_cast<Control*>(reinterpret_cast<unsigned char*>(staging) + 4 * kStagingWarp);
+    int* const start = reinterpret_cast<int*>(reinterpret_cast<unsigned char*>(ctl) + 512);
+    int* const rows = start + kMaxExperts + 2;
+    static_assert(sizeof(Control) <= 512, "the control block's room");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CTAS == 2 ? tc::cluster_rank() : 0;
+    volatile int* const gave_up = &ctl->gave_up;
+
+    if (warp == 0 && lane == 0) {
+        tc::prefetch_map(&q.a);
+        tc::prefetch_map(&q.b);
+        for (int i = 0; i < kStages; ++i) {
+            tc::bar_init(tc::smem_addr(&ctl->full[i]), CTAS);     // each CTA's copies, or its tail's zeroing
+            tc::bar_init(tc::smem_addr(&ctl->empty[i]), 1);
+            tc::bar_init(tc::smem_addr(&ctl->part[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::bar_init(tc::smem_addr(&ctl->acc_full[i]), 1);
+            tc::bar_init(tc::smem_addr(&ctl->acc_empty[i]), 4 * CTAS);
+        }
+        ctl->gave_up = 0;
+        tc::bar_init_fence();
+    }
+    if (warp == 2) tc::tmem_alloc<CTAS>(tc::smem_addr(&ctl->tmem), S::kColumns);
+    if (q.p.offsets) make_tables<S>(q, start, rows);
+    tc::fence_before();
+    __syncthreads();
+    if constexpr (CTAS == 2) tc::cluster_sync();
+    tc::fence_after();
+    const uint32_t tmem = ctl->tmem;
+
+    List<S> list{q, start, rows, 0};
+    list.total = (q.p.m_grouped ? (int64_t)start[q.p.batch + 1] : q.p.batch * q.tiles_m) * q.tiles_n;
+    const int64_t first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
+    const bool tails = q.p.k_grouped;
+
+    if (warp == 0 && tc::elect_one()) {
+        // copies
+        uint32_t n = 0;
+        bool ok = true;
+        for (int64_t t = first; ok && t < list.total; t += step) {
+            const Tile tile = list.at(t);
+            const int za = q.p.m_grouped || q.p.k_grouped ? 0 : tile.problem, zb = q.p.k_grouped ? 0 : tile.problem;
+            const int m = (int)tile.m0 + (int)rank * kRows, nn = (int)tile.n0 + (int)rank * S::kBRows;
+            for (int i = 0; i < tile.steps; ++i, ++n) {
+                const uint32_t s = n % kStages, phase = (n / kStages) & 1;
+                if (!tc::bar_wait(tc::smem_addr(&ctl->empty[s]), phase ^ 1, gave_up)) { ok = false; break; }
+                const int k = (int)tile.k0 + i * kStep;
+                const uint32_t a = tc::smem_addr(stage_a + s * kStageOperand), b = tc::smem_addr(stage_b + s * kStageOperand);
+                const bool part = tails && k + kStep > tile.k_end;
+                uint32_t bar;
+                if (part) {
+                    bar = tc::smem_addr(&ctl->part[s]);
+                    tc::bar_expect(bar, kTx / CTAS);
+                } else {
+                    bar = tc::smem_addr(&ctl->full[s]);
+                    if constexpr (CTAS == 2) {
+                        if (rank == 0) {
+                            tc::bar_expect(bar, kTx);
+                        } else {
+                            bar = tc::in_cta(bar, 0);
+                            tc::bar_arrive(bar);
+                        }
+                    } else {
+                        tc::bar_expect(bar, kTx);
+                    }
+                }
+                if constexpr (A_MN) {
+                    for (int j = 0; j < kRows / 64; ++j) tc::load_box<CTAS>(a + j * kBlockBytes, &q.a, bar, m + 64 * j, k, za);
+                } else {
+                    tc::load_box<CTAS>(a, &q.a, bar, k, m, za);
+                }
+                if constexpr (B_MN) {
+                    for (int j = 0; j < S::kBRows / 64; ++j) tc::load_box<CTAS>(b + j * kBlockBytes, &q.b, bar, nn + 64 * j, k, zb);
+                } else {
+                    tc::load_box<CTAS>(b, &q.b, bar, k, nn, zb);
+                }
             }
         }
+        // the last products of every stage are done, here and in the pair's other CTA, before either ends
+        for (uint32_t i = n < kStages ? 0 : n - kStages; ok && i < n; ++i)
+            ok = tc::bar_wait(tc::smem_addr(&ctl->empty[i % kStages]), (i / kStages) & 1, gave_up);
+        if (!ok) {   // what was copied last lands before the block ends
+            const uint64_t t0 = tc::now_ns();
+            while (tc::now_ns() - t0 < 2000000) {}
+        }
+    } else if (warp == 1 && rank == 0 && tc::elect_one()) {
+        // products
+        constexpr uint32_t kInstr = tc::instruction(false, A_MN, B_MN, S::BM, S::BN), kInstrBf16 = tc::instruction(true, A_MN, B_MN, S::BM, S::BN);
+        const uint32_t instr = q.p.dtype == EMB_BF16 ? kInstrBf16 : kInstr;
+        uint32_t n = 0, made = 0;
+        bool ok = true;
+        for (int64_t t = first; ok && t < list.total; t += step) {
+            const Tile tile = list.at(t);
+            if (!tile.steps) continue;
+            const uint32_t acc = made & 1, acc_phase = (made >> 1) & 1;
+            ++made;
+            if (!tc::bar_wait(tc::smem_addr(&ctl->acc_empty[acc]), acc_phase ^ 1, gave_up)) break;
+            tc::fence_after();
+            for (int i = 0; i < tile.steps; ++i, ++n) {
+                const uint32_t s = n % kStages, phase = (n / kStages) & 1;
+                if (!tc::bar_wait(tc::smem_addr(&ctl->full[s]), phase, gave_up)) { ok = false; break; }
+                tc::fence_after();
+                const uint64_t a = tc::operand(tc::smem_addr(stage_a + s * kStageOperand), A_MN, kBlockBytes);
+                const uint64_t b = tc::operand(tc::smem_addr(stage_b + s * kStageOperand), B_MN, kBlockBytes);
+#pragma unroll
+                for (int j = 0; j < kStep / 16; ++j)
+                    tc::mma<CTAS>(tmem + acc * S::BN, a + j * tc::operand_step(A_MN), b + j * tc::operand_step(B_MN), instr, i > 0 || j > 0);
+                tc::commit<CTAS>(tc::smem_addr(&ctl->empty[s]));
+            }
+            if (ok) tc::commit<CTAS>(tc::smem_addr(&ctl->acc_full[acc]));
+        }
+    } else if (warp == 2 && tails) {
+        // zero the rows past a group in its last step, then hand the step on
+        uint32_t n = 0, parts[kStages] = {};
+        bool ok = true;
+        for (int64_t t = first; ok && t < list.total; t += step) {
+            const Tile tile = list.at(t);
+            const int left = (int)((tile.k_end - tile.k0) % kStep);
+            if (tile.steps && left) {
+                const uint32_t s = (n + tile.steps - 1) % kStages;
+                uint32_t turn = 0;
+#pragma unroll
+                for (int i = 0; i < kStages; ++i)
+                    if (i == (int)s) turn = parts[i]++;
+                ok = tc::bar_wait(tc::smem_addr(&ctl->part[s]), turn & 1, gave_up);
+                if (ok) {
+                    const uint4 zero = make_uint4(0, 0, 0, 0);
+                    for (int j = 0; j < kRows / 64; ++j)
+                        for (int i = left * 128 + lane * 16; i < kBlockBytes; i += 512)
+                            *reinterpret_cast<uint4*>(stage_a + s * kStageOperand + j * kBlockBytes + i) = zero;
+                    for (int j = 0; j < S::kBRows / 64; ++j)
+                        for (int i = left * 128 + lane * 16; i < kBlockBytes; i += 512)
+                            *reinterpret_cast<uint4*>(stage_b + s * kStageOperand + j * kBlockBytes + i) = zero;
+                    tc::fence_async();
+                    __syncwarp();
+                    if (lane == 0) tc::bar_arrive(tc::in_cta(tc::smem_addr(&ctl->full[s]), 0));
+                }
+            }
+            n += tile.steps;
+        }
+    } else if (warp >= 4) {
+        // epilogue: 32 rows a warp, kChunk columns at a time through shared memory, so that a row's
+        // columns leave (and C's arrive) in whole sectors
+        const int w = warp - 4;
+        float* const mine = staging + w * (kStagingWarp / 4);
+        uint32_t made = 0;
+        for (int64_t t = first; t < list.total; t += step) {
+            const Tile tile = list.at(t);
+            const int64_t m_first = tile.m0 + (int64_t)rank * kRows + w * 32;
+            const int64_t problem = tile.problem;
+            const uint32_t acc = made & 1, acc_phase = (made >> 1) & 1;
+            if (tile.steps) {
+                ++made;
+                if (!tc::bar_wait(tc::smem_addr(&ctl->acc_full[acc]), acc_phase, gave_up)) break;
+                tc::fence_after();
+            }
+            float s = 1.f;
+            if (q.p.scale) {
+                s = q.p.scale[problem];
+                if (q.p.scale_power == 2) s *= s;
+            }
+            for (int c = 0; c < S::BN; c += kChunk) {
+                if (tile.steps) {
+                    uint32_t v[32];
+                    tc::tmem_load32(tmem + acc * S::BN + c + ((uint32_t)(w * 32) << 16), v);
+                    if (c + kChunk == S::BN) {
+                        tc::fence_before();
+                        if (lane == 0) tc::bar_arrive(tc::in_cta(tc::smem_addr(&ctl->acc_empty[acc]), 0));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4*>(mine + lane * kChunk + ((i ^ (lane & 7)) * 4)) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    __syncwarp();
+                }
+                const int64_t n = tile.n0 + c + (lane & 3) * 8;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = i * 8 + (lane >> 2);
+                    float v[8] = {};
+                    if (tile.steps) {
+                        const int j = (lane & 3) * 2;
+                        const float4 x = *reinterpret_cast<const float4*>(mine + r * kChunk + ((j ^ (r & 7)) * 4));
+                        const float4 y = *reinterpret_cast<const float4*>(mine + r * kChunk + (((j + 1) ^ (r & 7)) * 4));
+                        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+                    }
+                    if (m_first + r < tile.m_end && n < q.p.n) finish(q.p, problem, s, m_first + r, n, v);
+                }
+                __syncwarp();
+            }
+        }
+    }
+
+    __syncwarp();
+    __syncthreads();
+    if (threadIdx.x == 0 && *gave_up && q.status) atomicOr(q.status, ERRBIT_TIMEOUT);
+    tc::fence_before();
+    if constexpr (CTAS == 2) tc::cluster_sync();
+    tc::fence_after();
+    if (warp == 2) tc::tmem_free<CTAS>(tmem, S::kColumns);
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                            const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+Encode encoder()
+{
+    static std::atomic<void*> found{nullptr};
+    void* f = found.load(std::memory_order_acquire);
+    if (!f) {
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return nullptr;
+        }
+        found.store(f, std::memory_order_release);
+    }
+    return reinterpret_cast<Encode>(f);
+}
+
+// A stack of matrices in memory, copied in boxes of 64 columns; what lies
+// outside a matrix is read as zeros.
+bool make_map(CUtensorMap* map, int dtype, const void* p, int64_t cols, int64_t nrows, int64_t stack, int64_t ld, int64_t stack_stride, int box_rows)
+{
+    const Encode encode = encoder();
+    if (!encode) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)nrows, (cuuint64_t)stack};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(stack > 1 ? stack_stride : ld) * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, ones[3] = {1, 1, 1};
+    return encode(map, dtype == EMB_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(p), dims, strides,
+                  box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int multiprocessors()
+{
+    static std::atomic<int> known[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (!n) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+template <class S, bool A_MN, bool B_MN>
+int launch(Problems& q, cudaStream_t st)
+{
+    const ProductArgs& p = q.p;
+    const int sms = multiprocessors();
+    q.status = dense_status_word();
+    if (!sms || !q.status) return EMB_ERR_CUDA;
+    const int64_t stack_a = p.m_grouped || p.k_grouped ? 1 : p.batch, stack_b = p.k_grouped ? 1 : p.batch;
+    if (!(A_MN ? make_map(&q.a, p.dtype, p.a, p.m, p.k, stack_a, p.lda, p.batch_a, kStep) : make_map(&q.a, p.dtype, p.a, p.k, p.m, stack_a, p.lda, p.batch_a, kRows)) ||
+        !(B_MN ? make_map(&q.b, p.dtype, p.b, p.n, p.k, stack_b, p.ldb, p.batch_b, kStep) : make_map(&q.b, p.dtype, p.b, p.k, p.n, stack_b, p.ldb, p.batch_b, S::kBRows)))
+        return EMB_ERR_CUDA;
+    q.tiles_n = (int)((p.n + S::BN - 1) / S::BN);
+    q.tiles_m = (int)((p.m + S::BM - 1) / S::BM);
+    // m-grouped: every group may add a partly filled tile, and the tail one
+    const int64_t tiles = (p.m_grouped ? q.tiles_m + p.batch + 1 : q.tiles_m * p.batch) * q.tiles_n;
+    const int blocks = (int)(tiles < sms / S::CTAS ? tiles : sms / S::CTAS) * S::CTAS;
+    auto* const kernel = product_tiles<S, A_MN, B_MN>;
+    static std::atomic<bool> sized[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return EMB_ERR_CUDA;
+    if (!sized[dev].load(std::memory_order_relaxed)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes()) != cudaSuccess) {
+            cudaGetLastError();
+            return EMB_ERR_CUDA;
+        }
+        sized[dev].store(true, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes();
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)S::CTAS, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, q) != cudaSuccess) {
+        cudaGetLastError();
+        return EMB_ERR_CUDA;
+    }
+    return EMB_OK;
+}
+
+template <class S>
+int launch_shape(Problems& q, cudaStream_t st)
+{
+    if (q.p.a_mn) return q.p.b_mn ? launch<S, true, true>(q, st) : (int)EMB_ERR_INVALID_ARG;
+    return q.p.b_mn ? launch<S, false, true>(q, st) : launch<S, false, false>(q, st);
 }
 
 }  // namespace
 
 int launch_product(const ProductArgs& p, cudaStream_t st)
 {
-    const int64_t tm = (p.m + kTile - 1) / kTile, tn = (p.n + kTile - 1) / kTile;
-    const dim3 grid((unsigned)tn, (unsigned)(p.m_grouped ? tm + p.batch + 1 : tm), (unsigned)(p.m_grouped ? 1 : p.batch));
-    if (p.dtype == EMB_F16)
-        product_tiles<__half><<<grid, kThreads, 0, st>>>(p, (int)p.batch);
-    else
-        product_tiles<__nv_bfloat16><<<grid, kThreads, 0, st>>>(p, (int)p.batch);
-    return cudaGetLastError() == cudaSuccess ? EMB_OK : EMB_ERR_CUDA;
+    Problems q;
+    q.p = p;
+    // pairs of CTAs on 256 x 256 tiles move half the bytes of single ones on
+    // 128 x 128; these fill the GPU with less work
+    const int64_t big = ((p.m + 255) / 256) * ((p.n + 255) / 256) * (p.m_grouped ? 1 : p.batch);
+    if (big >= 76 && !(p.m_grouped && p.m < 128 * p.batch)) return launch_shape<Shape<2, 256>>(q, st);
+    return launch_shape<Shape<1, 128>>(q, st);
 }
 
 }  // namespace emb
