@@ -82,55 +82,111 @@ __device__ __forceinline__ double block_sum(double v, double* warp_sums)
     return s;
 }
 
-// Sum of squares of each matrix, in blocks of a fixed order.
-template <class T>
+// Calls f(row, first column, the V values there) for the elements of a matrix
+// that are this warp's: rows are dealt out warp by warp, in pieces of 32 V
+// columns.
+template <int V, class T, class F>
+__device__ __forceinline__ void each_piece(const T* g, int64_t row_stride, int64_t rows, int64_t cols, F f)
+{
+    constexpr int kWarps = kNormThreads / 32;
+    const int lane = threadIdx.x & 31;
+    const int64_t pieces = (cols + 32 * V - 1) / (32 * V), step = (int64_t)gridDim.x * kWarps;
+    int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    int64_t row = u / pieces, piece = u - row * pieces;
+    const int64_t row_step = step / pieces, piece_step = step - row_step * pieces;
+    while (row < rows) {
+        const int64_t c = (piece * 32 + lane) * V;
+        if (c < cols) {
+            float v[V];
+            const T* const p = g + row * row_stride + c;
+            if constexpr (V == 1) {
+                v[0] = to_float<T>(*p);
+            } else if constexpr (sizeof(T) == 4) {
+                const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
+                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+            } else {
+                const uint4 r = *reinterpret_cast<const uint4*>(p);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = to_float<T>(reinterpret_cast<const T*>(&r)[i]);
+            }
+            f(row, c, v);
+        }
+        row += row_step, piece += piece_step;
+        if (piece >= pieces) piece -= pieces, ++row;
+    }
+}
+
+// Sum of squares of each matrix, in a fixed order: fp32 within a thread, which
+// has some dozens of elements, double from there.  A thread whose squares could
+// leave fp32's range adds them again in double.
+template <int V, class T>
 __global__ void __launch_bounds__(kNormThreads) norm_partials(const T* __restrict__ g, int64_t batch_stride, int64_t row_stride,
                                                               int64_t rows, int64_t cols, double* __restrict__ partial)
 {
     __shared__ double warp_sums[kNormThreads / 32];
     const T* const mine = g + blockIdx.y * batch_stride;
-    double s = 0;
-    for (int64_t i = (int64_t)blockIdx.x * kNormThreads + threadIdx.x; i < rows * cols; i += (int64_t)gridDim.x * kNormThreads) {
-        const double v = to_float<T>(mine[i / cols * row_stride + i % cols]);
-        s += v * v;
+    float s = 0.f, top = 0.f;
+    each_piece<V, T>(mine, row_stride, rows, cols, [&](int64_t, int64_t, const float (&v)[V]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            s = __fmaf_rn(v[i], v[i], s);
+            top = fmaxf(top, fabsf(v[i]));
+        }
+    });
+    double d = s;
+    if (top > 1e15f || (top < 1e-15f && top > 0.f)) {
+        d = 0;
+        each_piece<V, T>(mine, row_stride, rows, cols, [&](int64_t, int64_t, const float (&v)[V]) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) d = fma((double)v[i], (double)v[i], d);
+        });
     }
-    s = block_sum(s, warp_sums);
-    if (threadIdx.x == 0) partial[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = s;
+    d = block_sum(d, warp_sums);
+    if (threadIdx.x == 0) partial[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = d;
 }
 
 // X = G 2^e as a sum of two fp16, and the factor that makes it G / (|G| + eps).
-template <class T>
+template <int V, class T>
 __global__ void __launch_bounds__(kNormThreads) scale_in(const T* __restrict__ g, int64_t batch_stride, int64_t row_stride,
                                                          int64_t rows, int64_t cols, int norm_blocks, const double* __restrict__ partial,
                                                          float eps, int64_t ld, __half* __restrict__ x, __half* __restrict__ x_low,
                                                          float* __restrict__ scale)
 {
     __shared__ double warp_sums[kNormThreads / 32];
+    static_assert(kMaxNormBlocks <= kNormThreads, "one partial sum a thread");
     const double sum = block_sum(threadIdx.x < norm_blocks ? partial[(int64_t)blockIdx.y * norm_blocks + threadIdx.x] : 0.0, warp_sums);
     const double norm = sqrt(sum);
     int e = 0;
     if (norm > 0 && norm < INFINITY) e = max(-120, min(120, ilogbf(kRange) - ilogb(norm)));
     const float up = ldexpf(1.f, e);
     if (blockIdx.x == 0 && threadIdx.x == 0) scale[blockIdx.y] = (float)(1.0 / ((norm + eps) * up));
-    const T* const mine = g + blockIdx.y * batch_stride;
     const int64_t at = (int64_t)blockIdx.y * rows * ld;
-    for (int64_t i = (int64_t)blockIdx.x * kNormThreads + threadIdx.x; i < rows * cols; i += (int64_t)gridDim.x * kNormThreads) {
-        const float v = up * to_float<T>(mine[i / cols * row_stride + i % cols]);
-        const __half h = __float2half_rn(v);
-        x[at + i / cols * ld + i % cols] = h;
-        x_low[at + i / cols * ld + i % cols] = __float2half_rn(kLowScale * (v - __half2float(h)));
-    }
+    each_piece<V, T>(g + blockIdx.y * batch_stride, row_stride, rows, cols, [&](int64_t row, int64_t c, const float (&v)[V]) {
+        alignas(16) __half h[V], l[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            h[i] = __float2half_rn(up * v[i]);
+            l[i] = __float2half_rn(kLowScale * (up * v[i] - __half2float(h[i])));
+        }
+        if constexpr (V == 8) {
+            *reinterpret_cast<uint4*>(x + at + row * ld + c) = *reinterpret_cast<const uint4*>(h);
+            *reinterpret_cast<uint4*>(x_low + at + row * ld + c) = *reinterpret_cast<const uint4*>(l);
+        } else {
+            x[at + row * ld + c] = h[0];
+            x_low[at + row * ld + c] = l[0];
+        }
+    });
 }
 
-template <class T>
-int start(const void* g, int64_t bs, int64_t rs, int64_t batch, int64_t rows, int64_t cols, float eps, const Layout& l, char* ws, cudaStream_t st)
+template <int V, class T>
+int start(const T* g, int64_t bs, int64_t rs, int64_t batch, int64_t rows, int64_t cols, float eps, const Layout& l, char* ws, cudaStream_t st)
 {
     const dim3 grid(l.norm_blocks, (unsigned)batch);
     double* const partial = reinterpret_cast<double*>(ws + l.partial);
-    norm_partials<T><<<grid, kNormThreads, 0, st>>>((const T*)g, bs, rs, rows, cols, partial);
-    scale_in<T><<<grid, kNormThreads, 0, st>>>((const T*)g, bs, rs, rows, cols, l.norm_blocks, partial, eps, l.ld,
-                                               reinterpret_cast<__half*>(ws + l.x[0]), reinterpret_cast<__half*>(ws + l.x_low[0]),
-                                               reinterpret_cast<float*>(ws + l.scale));
+    norm_partials<V, T><<<grid, kNormThreads, 0, st>>>(g, bs, rs, rows, cols, partial);
+    scale_in<V, T><<<grid, kNormThreads, 0, st>>>(g, bs, rs, rows, cols, l.norm_blocks, partial, eps, l.ld,
+                                                  reinterpret_cast<__half*>(ws + l.x[0]), reinterpret_cast<__half*>(ws + l.x_low[0]),
+                                                  reinterpret_cast<float*>(ws + l.scale));
     return cudaGetLastError() == cudaSuccess ? EMB_OK : EMB_ERR_CUDA;
 }
 
@@ -367,9 +423,14 @@ extern "C" int emb_orthogonalize(const void* update, int32_t dtype, int64_t batc
         return dtype == EMB_F32 ? go(float()) : dtype == EMB_F16 ? go(__half()) : go(__nv_bfloat16());
     }
     const Layout l = layout_of(batch, rows, cols);
-    int rc = dtype == EMB_F32   ? start<float>(update, batch_stride, row_stride, batch, rows, cols, eps, l, ws, st)
-             : dtype == EMB_F16 ? start<__half>(update, batch_stride, row_stride, batch, rows, cols, eps, l, ws, st)
-                                : start<__nv_bfloat16>(update, batch_stride, row_stride, batch, rows, cols, eps, l, ws, st);
+    const bool wide = cols % 8 == 0 && row_stride % 8 == 0 && batch_stride % 8 == 0 && aligned_to(update, 16);
+    const auto begin = [&](auto t) {
+        using T = decltype(t);
+        const T* const g = static_cast<const T*>(update);
+        return wide ? start<8, T>(g, batch_stride, row_stride, batch, rows, cols, eps, l, ws, st)
+                    : start<1, T>(g, batch_stride, row_stride, batch, rows, cols, eps, l, ws, st);
+    };
+    int rc = dtype == EMB_F32 ? begin(float()) : dtype == EMB_F16 ? begin(__half()) : begin(__nv_bfloat16());
     const bool tall = rows > cols;
     const float* const scale = reinterpret_cast<const float*>(ws + l.scale);
     for (int i = 0; i < steps && rc == EMB_OK; ++i) {
@@ -380,7 +441,7 @@ extern "C" int emb_orthogonalize(const void* update, int32_t dtype, int64_t batc
         s.a = s.b = x, s.lda = s.ldb = l.ld, s.batch_a = s.batch_b = l.x_elems;
         s.a_mn = s.b_mn = tall;
         s.m = s.n = l.m, s.k = std::max(rows, cols);
-        if (i == 0) s.scale = scale, s.scale_power = 2;
+        if (i == 0) s.scale = scale;
         s.d = ws + l.a, s.ldd = l.ldm, s.batch_d = l.a_elems;
         rc = launch_product(s, st);
         if (rc != EMB_OK) break;

@@ -23,12 +23,14 @@ namespace {
 
 constexpr int kRows = 128;                      // of A a CTA holds a step: its accumulator's lanes
 constexpr int kStep = 64;                       // k of a stage: 128 bytes
-constexpr int kThreads = 256;                   // warps: copy, products, tails, (none), 4 of the epilogue
+constexpr int kEpilogueWarps = 8;               // two to each quarter of the accumulator's lanes, half its columns each
+constexpr int kThreads = 128 + 32 * kEpilogueWarps;   // warps: copy, products, tails, (none), epilogue
 constexpr int kBlockBytes = 64 * 128;           // an mn-major block: 64 k of 64 m
 constexpr int kStageOperand = kRows * 128;      // bytes of one operand a stage
 constexpr int kStages = 6;
 constexpr int kChunk = 32;                      // columns an epilogue warp takes at once
-constexpr int kStagingWarp = 32 * kChunk * 4;
+constexpr int kStagingGroup = 32 * kChunk * 2;  // bytes of shared memory a warp takes them through, 16-bit
+constexpr int kStagingStep = 32 * kChunk * 4;   // or fp32
 constexpr int kMaxDevices = 64;
 
 template <int CTAS_, int BN_>
@@ -40,13 +42,28 @@ struct Shape {
 };
 
 struct Control {
-    uint64_t full[kStages], empty[kStages], part[kStages];   // part: a step whose rows past the group are still to be zeroed
+    uint64_t full[kStages], empty[kStages];
+    uint64_t part[kStages], peer_part[kStages];   // a step whose rows past the group are still to be zeroed; the other CTA's is done
     uint64_t acc_full[2], acc_empty[2];
     uint32_t tmem;
     int gave_up;
 };
 
-constexpr int smem_bytes() { return 1024 + kStages * 2 * kStageOperand + 4 * kStagingWarp + 512 + 2 * (kMaxExperts + 2) * 4; }
+// What follows the sum.
+enum Finish {
+    kGroup,     // rounded to 16 bits: the experts' products
+    kGram,      // A = s X X^T
+    kQuadratic, // B = alpha A A + beta A + diagonal I
+    kUpdate,    // X' = s (B X + beta X)
+};
+
+// Grouped problems need their tables, the others' sums pass as fp32.
+constexpr int tail_bytes(bool group)
+{
+    return group ? kEpilogueWarps * kStagingGroup + 2 * (kMaxExperts + 2) * 4 : kEpilogueWarps * kStagingStep;
+}
+constexpr int smem_bytes(bool group) { return 1024 + kStages * 2 * kStageOperand + 512 + tail_bytes(group); }
+static_assert(smem_bytes(true) <= 227 * 1024 && smem_bytes(false) <= 227 * 1024, "the SM's shared memory");
 
 struct Tile {
     int problem;         // B's (and D's) index in its stack
@@ -138,68 +155,175 @@ __device__ void make_tables(const Problems& q, int* start, int* rows)
     }
 }
 
-// Eight consecutive elements of a row of D from the accumulated products.
-__device__ __forceinline__ void finish(const ProductArgs& p, int64_t problem, float s, int64_t m, int64_t n, float (&v)[8])
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float x, float y);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float x, float y)
 {
-    const int64_t at_c = (p.m_grouped ? 0 : problem * p.batch_c) + m * p.ldc + n;
-    const int64_t at = (p.m_grouped ? 0 : problem * p.batch_d) + m * p.ldd + n;
-    if (p.c) {
-        // C's rows are padded to a multiple of 8 elements
-        const uint4 h = *reinterpret_cast<const uint4*>(static_cast<const __half*>(p.c) + at_c);
-        const __half* hv = reinterpret_cast<const __half*>(&h);
-        float c[8];
+    const __half2 v = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ void unpack8(const uint4& p, float (&v)[8])
+{
+    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = __half2float(hv[i]);
-        if (p.c_low) {
-            const uint4 l = *reinterpret_cast<const uint4*>(static_cast<const __half*>(p.c_low) + at_c);
-            const __half* lv = reinterpret_cast<const __half*>(&l);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) c[i] = __fmaf_rn(1.f / kLowScale, __half2float(lv[i]), c[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __fmaf_rn(p.beta, c[i], p.alpha * v[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= p.alpha;
-    }
-    if (p.scale) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= s;
-    }
-    if (p.diagonal != 0.f && m >= n && m < n + 8) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (m == n + i) v[i] += p.diagonal;
-    }
-    uint4 o;
-    if (p.d_dtype == EMB_BF16) {
-        __nv_bfloat16* ov = reinterpret_cast<__nv_bfloat16*>(&o);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ov[i] = __float2bfloat16_rn(v[i]);
-    } else {
-        __half* ov = reinterpret_cast<__half*>(&o);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ov[i] = __float2half_rn(v[i]);
-    }
-    if ((p.ldd & 7) == 0 && (p.batch_d & 7) == 0 && (reinterpret_cast<uintptr_t>(p.d) & 15) == 0) {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.d) + at) = o;
-    } else {
-        const uint16_t* ov = reinterpret_cast<const uint16_t*>(&o);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (n + i < p.n) static_cast<uint16_t*>(p.d)[at + i] = ov[i];
-    }
-    if (p.d_low) {
-        uint4 l;
-        __half* lv = reinterpret_cast<__half*>(&l);
-        const __half* ov = reinterpret_cast<const __half*>(&o);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) lv[i] = __float2half_rn(kLowScale * (v[i] - __half2float(ov[i])));
-        *reinterpret_cast<uint4*>(static_cast<__half*>(p.d_low) + at) = l;
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        v[2 * i] = f.x, v[2 * i + 1] = f.y;
     }
 }
 
-template <class S, bool A_MN, bool B_MN>
+template <class T>
+__device__ __forceinline__ uint4 pack8(const float (&v)[8])
+{
+    return make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+}
+
+// The columns [c0, c1) of a tile of the experts' products.  A lane has one row's
+// 32 columns; through shared memory four lanes get to store 64 bytes of a row
+// each time.
+template <class T>
+__device__ __forceinline__ void finish_group(const ProductArgs& p, uint32_t tmem, bool empty, unsigned char* mine, int64_t m_first, int rows,
+                                             int64_t n0, int c0, int c1, uint32_t acc_empty)
+{
+    const int lane = threadIdx.x & 31, r0 = lane >> 2, q = lane & 3;
+    T* const d = static_cast<T*>(p.d) + (m_first + r0) * p.ldd + n0 + q * 8;
+    for (int c = c0; c < c1; c += kChunk) {
+        if (!empty) {
+            uint32_t v[32];
+            tc::tmem_load32(tmem + c, v);
+            if (c + kChunk == c1) {
+                tc::fence_before();
+                if (lane == 0) tc::bar_arrive(acc_empty);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(v[8 * i + j]);
+                *reinterpret_cast<uint4*>(mine + lane * 64 + ((i ^ ((lane >> 1) & 3)) * 16)) = pack8<T>(x);
+            }
+            __syncwarp();
+        }
+        const bool in = n0 + c + q * 8 < p.n;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + r0;
+            uint4 o = make_uint4(0, 0, 0, 0);
+            if (!empty) o = *reinterpret_cast<const uint4*>(mine + r * 64 + ((q ^ ((r >> 1) & 3)) * 16));
+            if (in && r < rows) *reinterpret_cast<uint4*>(d + i * 8 * p.ldd + c) = o;
+        }
+        __syncwarp();
+    }
+}
+
+// The same for a step of the orthogonalisation: a lane's four pieces of eight
+// columns, in rows r0 + 8 i, meet C there and leave again.  C for the next
+// columns is on its way meanwhile.
+template <Finish F>
+__device__ __forceinline__ void finish_step(const ProductArgs& p, uint32_t tmem, float* mine, int64_t problem, int64_t m_first, int rows,
+                                            int64_t n0, int c0, int c1, uint32_t acc_full, uint32_t phase, uint32_t acc_empty,
+                                            volatile int* gave_up)
+{
+    const int lane = threadIdx.x & 31, r0 = lane >> 2, q = lane & 3;
+    const int64_t at_c = problem * p.batch_c + (m_first + r0) * p.ldc + n0 + q * 8;
+    const int64_t at_d = problem * p.batch_d + (m_first + r0) * p.ldd + n0 + q * 8;
+    const __half* const c_high = static_cast<const __half*>(p.c) + at_c;
+    const __half* const c_low = static_cast<const __half*>(p.c_low) + at_c;
+    float s = 1.f;
+    if (F != kQuadratic && p.scale) {
+        s = p.scale[problem];
+        if (F == kGram) s *= s;
+    }
+    uint4 h[4], l[4];
+    const auto fetch = [&](int c) {
+        const bool in = n0 + c + q * 8 < p.n;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool has = in && r0 + 8 * i < rows;
+            if (F != kGram) h[i] = has ? *reinterpret_cast<const uint4*>(c_high + i * 8 * p.ldc + c) : make_uint4(0, 0, 0, 0);
+            if (F == kUpdate) l[i] = has ? *reinterpret_cast<const uint4*>(c_low + i * 8 * p.ldc + c) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    fetch(c0);
+    if (!tc::bar_wait(acc_full, phase, gave_up)) return;
+    tc::fence_after();
+    const bool wide = (p.ldd & 7) == 0 && (p.batch_d & 7) == 0 && (reinterpret_cast<uintptr_t>(p.d) & 15) == 0;
+    for (int c = c0; c < c1; c += kChunk) {
+        uint32_t v[32];
+        tc::tmem_load32(tmem + c, v);
+        if (c + kChunk == c1) {
+            tc::fence_before();
+            if (lane == 0) tc::bar_arrive(acc_empty);
+        }
+        // 16-byte piece i of row r is at i ^ (r & 7) ^ 2 (r >> 3): rows, and columns of eight rows, without conflicts
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(mine + lane * kChunk + ((i ^ (lane & 7) ^ ((lane >> 3) << 1)) * 4)) =
+                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        __syncwarp();
+        const bool in = n0 + c + q * 8 < p.n;
+        uint4 high[4], low[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) high[i] = h[i], low[i] = l[i];
+        if (c + kChunk < c1) fetch(c + kChunk);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + r0, turn = (r & 7) ^ ((r >> 3) << 1);
+            const float4 x = *reinterpret_cast<const float4*>(mine + r * kChunk + (((2 * q) ^ turn) * 4));
+            const float4 y = *reinterpret_cast<const float4*>(mine + r * kChunk + (((2 * q + 1) ^ turn) * 4));
+            float o[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+            if (F == kGram) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] *= s;
+            } else {
+                float cv[8];
+                unpack8(high[i], cv);
+                if (F == kUpdate) {
+                    float lv[8];
+                    unpack8(low[i], lv);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o[j] = s * __fmaf_rn(p.beta, __fmaf_rn(1.f / kLowScale, lv[j], cv[j]), o[j]);
+                } else {
+                    const int64_t on = m_first + r - (n0 + c + q * 8);   // which of them is on the diagonal
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o[j] = __fmaf_rn(p.beta, cv[j], p.alpha * o[j]) + (on == j ? p.diagonal : 0.f);
+                }
+            }
+            if (!in || r >= rows) continue;
+            if (F == kUpdate && p.d_dtype == EMB_BF16) {
+                __nv_bfloat16* const d = static_cast<__nv_bfloat16*>(p.d) + at_d + i * 8 * p.ldd + c;
+                if (wide) {
+                    *reinterpret_cast<uint4*>(d) = pack8<__nv_bfloat16>(o);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (n0 + c + q * 8 + j < p.n) d[j] = __float2bfloat16_rn(o[j]);
+                }
+                continue;
+            }
+            const uint4 packed = pack8<__half>(o);
+            *reinterpret_cast<uint4*>(static_cast<__half*>(p.d) + at_d + i * 8 * p.ldd + c) = packed;
+            if (F == kUpdate) {
+                float back[8];
+                unpack8(packed, back);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) back[j] = kLowScale * (o[j] - back[j]);
+                *reinterpret_cast<uint4*>(static_cast<__half*>(p.d_low) + at_d + i * 8 * p.ldd + c) = pack8<__half>(back);
+            }
+        }
+        __syncwarp();
+    }
+}
+
+template <class S, bool A_MN, bool B_MN, Finish F>
 __global__ void __launch_bounds__(kThreads, 1) product_tiles(const __grid_constant__ Problems q)
 {
     constexpr int CTAS = S::CTAS;
@@ -209,9 +333,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_tiles(const __grid_consta
     unsigned char* const base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dynamic) + 1023) & ~uintptr_t(1023));
     unsigned char* const stage_a = base;
     unsigned char* const stage_b = base + kStages * kStageOperand;
-    float* const staging = reinterpret_cast<float*>(base + 2 * kStages * kStageOperand);
-    Control* const ctl = reinterpret_cast<Control*>(reinterpret_cast<unsigned char*>(staging) + 4 * kStagingWarp);
-    int* const start = reinterpret_cast<int*>(reinterpret_cast<unsigned char*>(ctl) + 512);
+    Control* const ctl = reinterpret_cast<Control*>(base + 2 * kStages * kStageOperand);
+    unsigned char* const staging = reinterpret_cast<unsigned char*>(ctl) + 512;
+    int* const start = reinterpret_cast<int*>(staging + kEpilogueWarps * kStagingGroup);   // grouped problems only
     int* const rows = start + kMaxExperts + 2;
     static_assert(sizeof(Control) <= 512, "the control block's room");
 
@@ -223,19 +347,20 @@ __global__ void __launch_bounds__(kThreads, 1) product_tiles(const __grid_consta
         tc::prefetch_map(&q.a);
         tc::prefetch_map(&q.b);
         for (int i = 0; i < kStages; ++i) {
-            tc::bar_init(tc::smem_addr(&ctl->full[i]), CTAS);     // each CTA's copies, or its tail's zeroing
+            tc::bar_init(tc::smem_addr(&ctl->full[i]), 1);
+            tc::bar_init(tc::smem_addr(&ctl->peer_part[i]), 1);
             tc::bar_init(tc::smem_addr(&ctl->empty[i]), 1);
             tc::bar_init(tc::smem_addr(&ctl->part[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             tc::bar_init(tc::smem_addr(&ctl->acc_full[i]), 1);
-            tc::bar_init(tc::smem_addr(&ctl->acc_empty[i]), 4 * CTAS);
+            tc::bar_init(tc::smem_addr(&ctl->acc_empty[i]), kEpilogueWarps * CTAS);
         }
         ctl->gave_up = 0;
         tc::bar_init_fence();
     }
     if (warp == 2) tc::tmem_alloc<CTAS>(tc::smem_addr(&ctl->tmem), S::kColumns);
-    if (q.p.offsets) make_tables<S>(q, start, rows);
+    if (F == kGroup) make_tables<S>(q, start, rows);
     tc::fence_before();
     __syncthreads();
     if constexpr (CTAS == 2) tc::cluster_sync();
@@ -266,17 +391,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_tiles(const __grid_consta
                     bar = tc::smem_addr(&ctl->part[s]);
                     tc::bar_expect(bar, kTx / CTAS);
                 } else {
-                    bar = tc::smem_addr(&ctl->full[s]);
-                    if constexpr (CTAS == 2) {
-                        if (rank == 0) {
-                            tc::bar_expect(bar, kTx);
-                        } else {
-                            bar = tc::in_cta(bar, 0);
-                            tc::bar_arrive(bar);
-                        }
-                    } else {
-                        tc::bar_expect(bar, kTx);
-                    }
+                    // the pair's first CTA expects both CTAs' bytes; the second one's may come first
+                    bar = tc::in_cta(tc::smem_addr(&ctl->full[s]), 0);
+                    if (rank == 0) tc::bar_expect(tc::smem_addr(&ctl->full[s]), kTx);
                 }
                 if constexpr (A_MN) {
                     for (int j = 0; j < kRows / 64; ++j) tc::load_box<CTAS>(a + j * kBlockBytes, &q.a, bar, m + 64 * j, k, za);
@@ -336,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_tiles(const __grid_consta
 #pragma unroll
                 for (int i = 0; i < kStages; ++i)
                     if (i == (int)s) turn = parts[i]++;
-                ok = tc::bar_wait(tc::smem_addr(&ctl->part[s]), turn & 1, gave_up);
+                ok = tc::bar_wait(tc::smem_addr(&ctl->part[s]), turn & 1, gave_up);   // the same in every lane
                 if (ok) {
                     const uint4 zero = make_uint4(0, 0, 0, 0);
                     for (int j = 0; j < kRows / 64; ++j)
@@ -347,59 +464,43 @@ __global__ void __launch_bounds__(kThreads, 1) product_tiles(const __grid_consta
                             *reinterpret_cast<uint4*>(stage_b + s * kStageOperand + j * kBlockBytes + i) = zero;
                     tc::fence_async();
                     __syncwarp();
-                    if (lane == 0) tc::bar_arrive(tc::in_cta(tc::smem_addr(&ctl->full[s]), 0));
+                    if (rank) {
+                        if (lane == 0) tc::bar_arrive(tc::in_cta(tc::smem_addr(&ctl->peer_part[s]), 0));
+                    } else {
+                        if (CTAS == 2) ok = tc::bar_wait(tc::smem_addr(&ctl->peer_part[s]), turn & 1, gave_up);
+                        if (ok && lane == 0) tc::bar_arrive(tc::smem_addr(&ctl->full[s]));
+                    }
                 }
             }
             n += tile.steps;
         }
     } else if (warp >= 4) {
-        // epilogue: 32 rows a warp, kChunk columns at a time through shared memory, so that a row's
-        // columns leave (and C's arrive) in whole sectors
-        const int w = warp - 4;
-        float* const mine = staging + w * (kStagingWarp / 4);
+        // epilogue: a warp has 32 rows (those of the tensor memory it can read) and half the columns
+        const int w = warp & 3, c0 = (warp - 4) / 4 * (S::BN / 2), c1 = c0 + S::BN / 2;
         uint32_t made = 0;
-        for (int64_t t = first; t < list.total; t += step) {
+        for (int64_t t = first; t < list.total && !*gave_up; t += step) {
             const Tile tile = list.at(t);
-            const int64_t m_first = tile.m0 + (int64_t)rank * kRows + w * 32;
-            const int64_t problem = tile.problem;
+            const int64_t m_first = tile.m0 + (int64_t)rank * kRows + w * 32, left = tile.m_end - m_first;
+            const int have = left < 0 ? 0 : left > 32 ? 32 : (int)left;
             const uint32_t acc = made & 1, acc_phase = (made >> 1) & 1;
-            if (tile.steps) {
-                ++made;
-                if (!tc::bar_wait(tc::smem_addr(&ctl->acc_full[acc]), acc_phase, gave_up)) break;
-                tc::fence_after();
-            }
-            float s = 1.f;
-            if (q.p.scale) {
-                s = q.p.scale[problem];
-                if (q.p.scale_power == 2) s *= s;
-            }
-            for (int c = 0; c < S::BN; c += kChunk) {
+            const uint32_t full = tc::smem_addr(&ctl->acc_full[acc]), empty = tc::in_cta(tc::smem_addr(&ctl->acc_empty[acc]), 0);
+            const uint32_t mine = tmem + acc * S::BN + ((uint32_t)(w * 32) << 16);
+            if (tile.steps) ++made;
+            if constexpr (F == kGroup) {
                 if (tile.steps) {
-                    uint32_t v[32];
-                    tc::tmem_load32(tmem + acc * S::BN + c + ((uint32_t)(w * 32) << 16), v);
-                    if (c + kChunk == S::BN) {
-                        tc::fence_before();
-                        if (lane == 0) tc::bar_arrive(tc::in_cta(tc::smem_addr(&ctl->acc_empty[acc]), 0));
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<uint4*>(mine + lane * kChunk + ((i ^ (lane & 7)) * 4)) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                    __syncwarp();
+                    if (!tc::bar_wait(full, acc_phase, gave_up)) break;
+                    tc::fence_after();
                 }
-                const int64_t n = tile.n0 + c + (lane & 3) * 8;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = i * 8 + (lane >> 2);
-                    float v[8] = {};
-                    if (tile.steps) {
-                        const int j = (lane & 3) * 2;
-                        const float4 x = *reinterpret_cast<const float4*>(mine + r * kChunk + ((j ^ (r & 7)) * 4));
-                        const float4 y = *reinterpret_cast<const float4*>(mine + r * kChunk + (((j + 1) ^ (r & 7)) * 4));
-                        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-                    }
-                    if (m_first + r < tile.m_end && n < q.p.n) finish(q.p, problem, s, m_first + r, n, v);
-                }
-                __syncwarp();
+                ProductArgs p = q.p;
+                if (tails) p.d = static_cast<uint16_t*>(p.d) + tile.problem * p.batch_d;
+                unsigned char* const room = staging + (warp - 4) * kStagingGroup;
+                if (p.dtype == EMB_BF16)
+                    finish_group<__nv_bfloat16>(p, mine, !tile.steps, room, m_first, have, tile.n0, c0, c1, empty);
+                else
+                    finish_group<__half>(p, mine, !tile.steps, room, m_first, have, tile.n0, c0, c1, empty);
+            } else {
+                finish_step<F>(q.p, mine, reinterpret_cast<float*>(staging + (warp - 4) * kStagingStep), tile.problem, m_first, have, tile.n0, c0, c1,
+                               full, acc_phase, empty, gave_up);
             }
         }
     }
@@ -462,7 +563,7 @@ int multiprocessors()
     return n;
 }
 
-template <class S, bool A_MN, bool B_MN>
+template <class S, bool A_MN, bool B_MN, Finish F>
 int launch(Problems& q, cudaStream_t st)
 {
     const ProductArgs& p = q.p;
@@ -478,12 +579,12 @@ int launch(Problems& q, cudaStream_t st)
     // m-grouped: every group may add a partly filled tile, and the tail one
     const int64_t tiles = (p.m_grouped ? q.tiles_m + p.batch + 1 : q.tiles_m * p.batch) * q.tiles_n;
     const int blocks = (int)(tiles < sms / S::CTAS ? tiles : sms / S::CTAS) * S::CTAS;
-    auto* const kernel = product_tiles<S, A_MN, B_MN>;
+    auto* const kernel = product_tiles<S, A_MN, B_MN, F>;
     static std::atomic<bool> sized[kMaxDevices];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return EMB_ERR_CUDA;
     if (!sized[dev].load(std::memory_order_relaxed)) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes()) != cudaSuccess) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(F == kGroup)) != cudaSuccess) {
             cudaGetLastError();
             return EMB_ERR_CUDA;
         }
@@ -492,7 +593,7 @@ int launch(Problems& q, cudaStream_t st)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_bytes();
+    cfg.dynamicSmemBytes = smem_bytes(F == kGroup);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -506,11 +607,16 @@ int launch(Problems& q, cudaStream_t st)
     return EMB_OK;
 }
 
+// The combinations that the callers have.
 template <class S>
 int launch_shape(Problems& q, cudaStream_t st)
 {
-    if (q.p.a_mn) return q.p.b_mn ? launch<S, true, true>(q, st) : (int)EMB_ERR_INVALID_ARG;
-    return q.p.b_mn ? launch<S, false, true>(q, st) : launch<S, false, false>(q, st);
+    const ProductArgs& p = q.p;
+    if (p.m_grouped) return p.b_mn ? launch<S, false, true, kGroup>(q, st) : launch<S, false, false, kGroup>(q, st);
+    if (p.k_grouped) return launch<S, true, true, kGroup>(q, st);
+    if (!p.c) return p.a_mn ? launch<S, true, true, kGram>(q, st) : launch<S, false, false, kGram>(q, st);
+    if (!p.c_low) return launch<S, false, false, kQuadratic>(q, st);
+    return p.b_mn ? launch<S, false, true, kUpdate>(q, st) : launch<S, false, false, kUpdate>(q, st);
 }
 
 }  // namespace

@@ -30,17 +30,19 @@ struct ProductArgs {
     // a batch: problem i has its own A, B, C and D, batch strides apart
     int64_t batch = 1, batch_a = 0, batch_b = 0;
 
-    // epilogue: D = alpha * s^power * (acc + ...) with the terms a caller asks for
-    const float* scale = nullptr;  // per problem, or null for 1
-    int scale_power = 1;
-    float alpha = 1.f;             // factor of the accumulated product
-    float beta = 0.f;              // factor of C (+ C's low part)
-    float diagonal = 0.f;          // added to D[i][i]
-    const void* c = nullptr;       // as D; fp16
-    const void* c_low = nullptr;   // C's scaled rounding error (see kLowScale), or null
+    // what follows the sum; every D's and C's row starts at a multiple of 16
+    // bytes but a bf16 D's
+    //   grouped:             D = sum, in dtype
+    //   else, without c:     D = s^2 sum, fp16
+    //   with c alone:        D = alpha sum + beta C + diagonal I, fp16
+    //   with c and c_low:    D = s (sum + beta (C + C's low part)), fp16 with its low part in d_low, or bf16
+    const float* scale = nullptr;  // s of each problem, or null for 1
+    float alpha = 1.f, beta = 0.f, diagonal = 0.f;
+    const void* c = nullptr;       // laid out as D; fp16
+    const void* c_low = nullptr;   // C's scaled rounding error (see kLowScale)
     int64_t ldc = 0, batch_c = 0;
     void* d = nullptr;
-    void* d_low = nullptr;         // takes D's scaled rounding error, or null
+    void* d_low = nullptr;
     int d_dtype = EMB_F16;
     int64_t ldd = 0, batch_d = 0;
 };
