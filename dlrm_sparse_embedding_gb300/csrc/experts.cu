@@ -8,6 +8,7 @@
 // and stored to (combined from) its k places, so the k copies never come from
 // memory again.
 #include <mutex>
+#include <type_traits>
 
 #include "dense_internal.cuh"
 #include "emb_internal.cuh"
@@ -26,15 +27,15 @@ __global__ void take_status(int* status) { status[1] = atomicExch(&status[0], 0)
 // ---------------------------------------------------------------------------
 // sort
 // ---------------------------------------------------------------------------
-// A counting sort in chunks of consecutive assignments.  Every block counts its
-// chunk's experts; with more than one chunk, expert_count has left all counts
-// in memory and a block adds up the chunks before its own instead of waiting
-// for them (E counts a chunk, read from L2).  Bucket E holds the assignments
-// without an expert, so they too have a row, the tail's.
+// A counting sort in chunks of consecutive assignments, one a block.  With more
+// than one chunk, expert_count leaves the chunks' counts in memory, and every
+// block of expert_place adds up those before its own instead of waiting for
+// them.  Bucket E holds the assignments without an expert, so they too have a
+// row, the tail's.
 constexpr int kPlaceThreads = 1024;
 constexpr int kPlaceWarps = kPlaceThreads / 32;
-constexpr int kMaxChunks = 2 * 152;           // at most two blocks an SM
-constexpr int kPlaceChunk = 8 * kPlaceThreads;   // assignments a block; below it one launch does everything
+constexpr int kOneChunk = 4 * kPlaceThreads;   // up to so many assignments one block does everything, without expert_count
+constexpr int kMaxChunks = 2 * 152;            // at most two blocks an SM
 
 template <class ID>
 __device__ __forceinline__ int bucket_of(const ID* ids, int64_t a, int E, int* status)
@@ -45,17 +46,28 @@ __device__ __forceinline__ int bucket_of(const ID* ids, int64_t a, int E, int* s
     return E;
 }
 
+// counts[bucket][chunk]
 template <class ID>
 __global__ void __launch_bounds__(kPlaceThreads) expert_count(const ID* __restrict__ ids, int P, int E, int chunk,
-                                                             int* __restrict__ counts)
+                                                              int* __restrict__ counts)
 {
     extern __shared__ int cnt[];
     for (int e = threadIdx.x; e <= E; e += kPlaceThreads) cnt[e] = 0;
     __syncthreads();
-    const int lo = blockIdx.x * chunk, hi = min(P, lo + chunk);
+    const int lo = blockIdx.x * chunk, hi = min((int64_t)P, (int64_t)lo + chunk);
     for (int a = lo + threadIdx.x; a < hi; a += kPlaceThreads) atomicAdd(&cnt[bucket_of(ids, a, E, nullptr)], 1);
     __syncthreads();
-    for (int e = threadIdx.x; e <= E; e += kPlaceThreads) counts[(int64_t)blockIdx.x * (E + 1) + e] = cnt[e];
+    for (int e = threadIdx.x; e <= E; e += kPlaceThreads) counts[(int64_t)e * gridDim.x + blockIdx.x] = cnt[e];
+}
+
+__device__ __forceinline__ int warp_inclusive_scan(int v)
+{
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, d);
+        if ((threadIdx.x & 31) >= d) v += u;
+    }
+    return v;
 }
 
 // Exclusive prefix sum of v[0..n) in place, n <= 2 * kPlaceThreads.
@@ -63,23 +75,10 @@ __device__ void block_exclusive_scan(int* v, int n, int* warp_sums)
 {
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
     const int a = 2 * t < n ? v[2 * t] : 0, b = 2 * t + 1 < n ? v[2 * t + 1] : 0;
-    int s = a + b;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, s, d);
-        if (lane >= d) s += u;
-    }
+    const int s = warp_inclusive_scan(a + b);
     if (lane == 31) warp_sums[w] = s;
     __syncthreads();
-    if (w == 0) {
-        int x = warp_sums[lane];
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, x, d);
-            if (lane >= d) x += u;
-        }
-        warp_sums[lane] = x;
-    }
+    if (w == 0) warp_sums[lane] = warp_inclusive_scan(warp_sums[lane]);
     __syncthreads();
     const int before = s - (a + b) + (w ? warp_sums[w - 1] : 0);
     if (2 * t < n) v[2 * t] = before;
@@ -87,119 +86,117 @@ __device__ void block_exclusive_scan(int* v, int n, int* warp_sums)
     __syncthreads();
 }
 
-// Shared memory: next[E + 1] (row the next assignment of each bucket gets),
-// warp_sums[32], and per warp a count for each bucket.
+// Shared memory: next[E + 1] (the row the next assignment of each bucket gets),
+// base[E + 1] (the same at the start of a round), warp_sums[32] and, for each
+// bucket, a number a warp: its count, then the earlier warps' sum.
 template <class ID>
 __global__ void __launch_bounds__(kPlaceThreads) expert_place(const ID* __restrict__ ids, int P, int E, int chunk,
-                                                             const int* __restrict__ counts, int32_t* __restrict__ offsets,
-                                                             int32_t* __restrict__ src, int32_t* __restrict__ pos,
-                                                             int* status)
+                                                              const int* __restrict__ counts, int32_t* __restrict__ offsets,
+                                                              int32_t* __restrict__ src, int32_t* __restrict__ pos,
+                                                              int* status)
 {
     extern __shared__ int smem[];
     int* const next = smem;
-    int* const warp_sums = next + (E + 1);
-    unsigned short* const of_warp = reinterpret_cast<unsigned short*>(warp_sums + 32);   // [bucket][warp]
+    int* const base = next + (E + 1);
+    int* const warp_sums = base + (E + 1);
+    unsigned short* const of_warp = reinterpret_cast<unsigned short*>(warp_sums + 32);
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
-    const int lo = blockIdx.x * chunk, hi = min(P, lo + chunk);
+    const int lo = blockIdx.x * chunk, hi = min((int64_t)P, (int64_t)lo + chunk);
 
+    for (int i = t; i < (E + 1) * kPlaceWarps; i += kPlaceThreads) of_warp[i] = 0;
     // the first row of every bucket, and of this chunk's part of it
-    int mine_before[2] = {0, 0};   // this chunk's predecessors in buckets t and t + kPlaceThreads
     if (counts) {
-        for (int q = 0; q < 2; ++q) {
-            const int e = t + q * kPlaceThreads;
-            if (e > E) break;
+        for (int e = w; e <= E; e += kPlaceWarps) {   // a warp adds up a bucket's chunks
             int total = 0, before = 0;
-            for (int c = 0; c < (int)gridDim.x; ++c) {
-                const int v = __ldg(&counts[(int64_t)c * (E + 1) + e]);
+            for (int c = lane; c < (int)gridDim.x; c += 32) {
+                const int v = __ldg(&counts[(int64_t)e * gridDim.x + c]);
                 if (c < (int)blockIdx.x) before += v;
                 total += v;
             }
-            next[e] = total;
-            mine_before[q] = before;
+            total = __reduce_add_sync(0xffffffffu, total);
+            before = __reduce_add_sync(0xffffffffu, before);
+            if (lane == 0) next[e] = total, base[e] = before;
         }
     } else {
-        for (int e = t; e <= E; e += kPlaceThreads) next[e] = 0;
+        for (int e = t; e <= E; e += kPlaceThreads) next[e] = 0, base[e] = 0;
         __syncthreads();
         for (int a = lo + t; a < hi; a += kPlaceThreads) atomicAdd(&next[bucket_of(ids, a, E, nullptr)], 1);
     }
     __syncthreads();
     block_exclusive_scan(next, E + 1, warp_sums);
-    for (int q = 0; q < 2; ++q) {
-        const int e = t + q * kPlaceThreads;
-        if (e > E) break;
+    for (int e = t; e <= E; e += kPlaceThreads) {
         if (blockIdx.x == 0) offsets[e] = next[e];
-        next[e] += mine_before[q];
+        next[e] += base[e];
     }
-    for (int i = t; i < (E + 1) * kPlaceWarps; i += kPlaceThreads) of_warp[i] = 0;
-    __syncthreads();
 
-    // kPlaceThreads assignments at a time, in order: an assignment's row is its
+    // kPlaceThreads assignments a round, in order: an assignment's row is its
     // bucket's next one, plus those of earlier warps, plus those of lower lanes
-    for (int base = lo; base < hi; base += kPlaceThreads) {
-        const int a = base + t;
-        const int e = a < hi ? bucket_of(ids, a, E, status) : E + 1;
+    for (int start = lo; start < hi; start += kPlaceThreads) {
+        const int a = start + t;
+        const bool has = a < hi;
+        const int e = has ? bucket_of(ids, a, E, status) : E + 1;
         const unsigned same = __match_any_sync(0xffffffffu, e);
         const int rank = __popc(same & ((1u << lane) - 1));
-        if (e <= E && rank == 0) of_warp[e * kPlaceWarps + w] = (unsigned short)__popc(same);
+        if (has && rank == 0) of_warp[e * kPlaceWarps + w] = (unsigned short)__popc(same);
         __syncthreads();
-        if (e <= E) {
-            int row = next[e] + rank;
-            for (int v = 0; v < w; ++v) row += of_warp[e * kPlaceWarps + v];
+        for (int b = w; b <= E; b += kPlaceWarps) {
+            const int mine = of_warp[b * kPlaceWarps + lane];
+            const int upto = warp_inclusive_scan(mine);
+            if (lane == 31) {
+                const int first = next[b];
+                base[b] = first;
+                next[b] = first + upto;
+            }
+            of_warp[b * kPlaceWarps + lane] = (unsigned short)(upto - mine);
+        }
+        __syncthreads();
+        if (has) {
+            const int row = base[e] + of_warp[e * kPlaceWarps + w] + rank;
             pos[a] = e < E ? row : -1;
             src[row] = e < E ? a : -1;
         }
-        __syncthreads();
-        // one thread of each bucket that occurred moves its next row on and clears its counts
-        for (int b = t; b <= E; b += kPlaceThreads) {
-            int n = 0;
-            for (int v = 0; v < kPlaceWarps; ++v) {
-                n += of_warp[b * kPlaceWarps + v];
-                of_warp[b * kPlaceWarps + v] = 0;
-            }
-            next[b] += n;
+        if (start + kPlaceThreads < hi) {
+            __syncthreads();
+            for (int i = t; i < (E + 1) * kPlaceWarps; i += kPlaceThreads) of_warp[i] = 0;
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 
-size_t place_smem(int E) { return sizeof(int) * (E + 1 + 32) + sizeof(unsigned short) * (size_t)(E + 1) * kPlaceWarps; }
+size_t place_smem(int E)
+{
+    return sizeof(int) * (2 * (E + 1) + 32) + sizeof(unsigned short) * (size_t)(E + 1) * kPlaceWarps;
+}
 
 // ---------------------------------------------------------------------------
 // rows
 // ---------------------------------------------------------------------------
 // V consecutive elements: 8 (moved 16 bytes at a time) where everything is
-// aligned for it, else 1.
+// aligned for it, else 1.  They are kept as they are in memory until they are
+// used: a load in flight costs no more registers than its bytes.
 template <int V, class T>
-__device__ __forceinline__ void load_vec(const T* p, float (&v)[V])
-{
-    if constexpr (V == 1) {
-        v[0] = to_float<T>(*p);
-    } else if constexpr (sizeof(T) == 4) {
-        const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-        const uint4 r = *reinterpret_cast<const uint4*>(p);
-        const T* e = reinterpret_cast<const T*>(&r);
+struct Raw {
+    using Word = typename std::conditional<V == 1, T, uint4>::type;
+    static constexpr int kWords = V * sizeof(T) / sizeof(Word);
+    Word w[kWords];
+
+    __device__ __forceinline__ void load(const T* p)
+    {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = to_float<T>(e[i]);
+        for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const Word*>(p)[i];
     }
-}
+    __device__ __forceinline__ float operator[](int i) const { return to_float<T>(reinterpret_cast<const T*>(w)[i]); }
+};
 
 template <int V, class T>
 __device__ __forceinline__ void store_vec(T* p, const float (&v)[V])
 {
-    if constexpr (V == 1) {
-        *p = from_float<T>(v[0]);
-    } else if constexpr (sizeof(T) == 4) {
-        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-        uint4 r;
-        T* e = reinterpret_cast<T*>(&r);
+    using Word = typename Raw<V, T>::Word;
+    Raw<V, T> r;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = from_float<T>(v[i]);
-        *reinterpret_cast<uint4*>(p) = r;
-    }
+    for (int i = 0; i < V; ++i) reinterpret_cast<T*>(r.w)[i] = from_float<T>(v[i]);
+#pragma unroll
+    for (int i = 0; i < Raw<V, T>::kWords; ++i) reinterpret_cast<Word*>(p)[i] = r.w[i];
 }
 
 constexpr int kRowThreads = 256;
@@ -227,10 +224,15 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_rows(emb_expert_plan pla
     const int64_t first = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
     for (int64_t u = first; u < plan.tokens * pieces; u += warps) {
         const int64_t token = u / pieces, c0 = (u - token * pieces) * (32 * V * kUnroll) + lane * V;
+        Raw<V, X> raw[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i)
+            if (c0 + i * 32 * V < width) raw[i].load(x + token * x_stride + c0 + i * 32 * V);
         float v[kUnroll][V];
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i)
-            if (c0 + i * 32 * V < width) load_vec<V, X>(x + token * x_stride + c0 + i * 32 * V, v[i]);
+#pragma unroll
+            for (int q = 0; q < V; ++q) v[i][q] = raw[i][q];
         for (int j = 0; j < plan.k; ++j) {
             const int p = __ldg(&plan.pos[token * plan.k + j]);
             if ((unsigned)p >= (unsigned)P) continue;
@@ -243,35 +245,48 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_rows(emb_expert_plan pla
 }
 
 // out[t] = sum_j w[t, j] rows[pos[t, j]]; without weights, the plain sum (the
-// dispatch's gradient).
-template <int V, class R, class O, bool WEIGHTED>
+// dispatch's gradient).  Bound by memory: a lane has kInFlight loads on their
+// way, ROWS rows' pieces of kInFlight / ROWS vectors.
+constexpr int kInFlight = 8;
+
+template <int V, class R, class O, bool WEIGHTED, int ROWS>
 __global__ void __launch_bounds__(kRowThreads) gather_sum(emb_expert_plan plan, const R* __restrict__ rows,
                                                           int64_t rows_stride, const float* __restrict__ weights,
                                                           int64_t width, int64_t pieces, O* __restrict__ out)
 {
+    constexpr int U = kInFlight / ROWS;
     const int lane = threadIdx.x & 31, P = (int)(plan.tokens * plan.k);
     const int64_t warps = (int64_t)gridDim.x * (kRowThreads / 32);
     const int64_t first = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
     for (int64_t u = first; u < plan.tokens * pieces; u += warps) {
-        const int64_t token = u / pieces, c0 = (u - token * pieces) * (32 * V * kUnroll) + lane * V;
-        float s[kUnroll][V] = {};
-        for (int j = 0; j < plan.k; ++j) {
-            const int p = __ldg(&plan.pos[token * plan.k + j]);
-            if ((unsigned)p >= (unsigned)P) continue;
-            const float w = WEIGHTED ? __ldg(&weights[token * plan.k + j]) : 1.f;
-            float v[kUnroll][V];
+        const int64_t token = u / pieces, c0 = (u - token * pieces) * (32 * V * U) + lane * V;
+        float s[U][V] = {};
+        for (int j0 = 0; j0 < plan.k; j0 += ROWS) {
+            int p[ROWS];
+            float w[ROWS];
 #pragma unroll
-            for (int i = 0; i < kUnroll; ++i)
-                if (c0 + i * 32 * V < width) load_vec<V, R>(rows + p * rows_stride + c0 + i * 32 * V, v[i]);
+            for (int j = 0; j < ROWS; ++j) {
+                p[j] = j0 + j < plan.k ? __ldg(&plan.pos[token * plan.k + j0 + j]) : -1;
+                w[j] = WEIGHTED && j0 + j < plan.k ? __ldg(&weights[token * plan.k + j0 + j]) : 1.f;
+            }
+            Raw<V, R> v[ROWS][U];
 #pragma unroll
-            for (int i = 0; i < kUnroll; ++i)
-                if (c0 + i * 32 * V < width) {
+            for (int j = 0; j < ROWS; ++j)
 #pragma unroll
-                    for (int q = 0; q < V; ++q) s[i][q] = WEIGHTED ? __fmaf_rn(w, v[i][q], s[i][q]) : s[i][q] + v[i][q];
-                }
+                for (int i = 0; i < U; ++i)
+                    if ((unsigned)p[j] < (unsigned)P && c0 + i * 32 * V < width)
+                        v[j][i].load(rows + p[j] * rows_stride + c0 + i * 32 * V);
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j) {
+                if ((unsigned)p[j] >= (unsigned)P) continue;
+#pragma unroll
+                for (int i = 0; i < U; ++i)
+#pragma unroll
+                    for (int q = 0; q < V; ++q) s[i][q] = WEIGHTED ? __fmaf_rn(w[j], v[j][i][q], s[i][q]) : s[i][q] + v[j][i][q];
+            }
         }
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i)
+        for (int i = 0; i < U; ++i)
             if (c0 + i * 32 * V < width) store_vec<V, O>(out + token * width + c0 + i * 32 * V, s[i]);
     }
 }
@@ -306,11 +321,12 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad(emb_expert_plan plan
             }
             if (has) {
                 for (int64_t c = (int64_t)threadIdx.x * V; c < width; c += (int64_t)blockDim.x * V) {
-                    float g[V], y[kPart][V];
-                    load_vec<V, O>(grad_out + token * grad_stride + c, g);
+                    Raw<V, O> g;
+                    Raw<V, R> y[kPart];
+                    g.load(grad_out + token * grad_stride + c);
 #pragma unroll
                     for (int q = 0; q < kPart; ++q)
-                        if (p[q] >= 0) load_vec<V, R>(rows + p[q] * rows_stride + c, y[q]);
+                        if (p[q] >= 0) y[q].load(rows + p[q] * rows_stride + c);
 #pragma unroll
                     for (int q = 0; q < kPart; ++q)
                         if (p[q] >= 0) {
@@ -357,7 +373,7 @@ bool rows_valid(const void* p, int dtype, int64_t stride, int64_t width, int64_t
     return dtype_valid(dtype) && stride >= width && aligned_to(p, dtype_bytes(dtype)) && (p || n == 0);
 }
 
-int64_t pieces_of(int64_t width, int V) { return (width + 32 * V * kUnroll - 1) / (32 * V * kUnroll); }
+int64_t pieces_of(int64_t width, int V, int unroll) { return (width + 32 * V * unroll - 1) / (32 * V * unroll); }
 
 unsigned row_blocks(int64_t warps)
 {
@@ -382,13 +398,20 @@ int launch_gather_sum(const emb_expert_plan& plan, const void* rows, int rows_dt
         return with_type(out_dtype, [&](auto o) {
             using R = decltype(r);
             using O = decltype(o);
-            const int64_t pieces = pieces_of(width, w8 ? 8 : 1);
+            const int at_once = plan.k <= 1 ? 1 : plan.k <= 2 ? 2 : 4;
+            const int64_t pieces = pieces_of(width, w8 ? 8 : 1, kInFlight / at_once);
             const unsigned blocks = row_blocks(plan.tokens * pieces);
+            const auto go = [&](auto kernel) {
+                kernel<<<blocks, kRowThreads, 0, st>>>(plan, (const R*)rows, stride, weights, width, pieces, (O*)out);
+                return launched();
+            };
             if (w8)
-                gather_sum<8, R, O, WEIGHTED><<<blocks, kRowThreads, 0, st>>>(plan, (const R*)rows, stride, weights, width, pieces, (O*)out);
-            else
-                gather_sum<1, R, O, WEIGHTED><<<blocks, kRowThreads, 0, st>>>(plan, (const R*)rows, stride, weights, width, pieces, (O*)out);
-            return launched();
+                return at_once == 1   ? go(gather_sum<8, R, O, WEIGHTED, 1>)
+                       : at_once == 2 ? go(gather_sum<8, R, O, WEIGHTED, 2>)
+                                      : go(gather_sum<8, R, O, WEIGHTED, 4>);
+            return at_once == 1   ? go(gather_sum<1, R, O, WEIGHTED, 1>)
+                   : at_once == 2 ? go(gather_sum<1, R, O, WEIGHTED, 2>)
+                                  : go(gather_sum<1, R, O, WEIGHTED, 4>);
         });
     });
 }
@@ -437,12 +460,13 @@ extern "C" int emb_dense_status(void* stream)
     return bits & ERRBIT_TIMEOUT ? EMB_ERR_TIMEOUT : bits & ERRBIT_KEY_RANGE ? EMB_ERR_KEY_RANGE : EMB_OK;
 }
 
-// Assignments a block of the sort takes: kPlaceChunk, more where that would make
-// so many blocks that adding up the earlier ones' counts costs more than the rest.
+// Assignments a block of the sort takes: one round, more where that would make
+// more than kMaxChunks blocks.
 static int sort_chunk(int64_t P)
 {
+    if (P <= kOneChunk) return kOneChunk;
     const int64_t even = (P + kMaxChunks - 1) / kMaxChunks;
-    return even <= kPlaceChunk ? kPlaceChunk : (int)((even + kPlaceThreads - 1) / kPlaceThreads * kPlaceThreads);
+    return (int)((even + kPlaceThreads - 1) / kPlaceThreads * kPlaceThreads);
 }
 static int sort_chunks(int64_t P) { return (int)((P + sort_chunk(P) - 1) / sort_chunk(P)); }
 
@@ -499,7 +523,7 @@ extern "C" int emb_expert_dispatch(const emb_expert_plan* plan, const void* x, i
         return with_type(rows_dtype, [&](auto rt) {
             using X = decltype(xt);
             using R = decltype(rt);
-            const int64_t pieces = pieces_of(width, w8 ? 8 : 1);
+            const int64_t pieces = pieces_of(width, w8 ? 8 : 1, kUnroll);
             const unsigned blocks = row_blocks(plan->tokens * pieces);
             if (w8)
                 dispatch_rows<8, X, R><<<blocks, kRowThreads, 0, st>>>(*plan, (const X*)x, x_stride, width, pieces, (R*)rows);

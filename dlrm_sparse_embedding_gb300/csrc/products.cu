@@ -623,6 +623,7 @@ int launch_shape(Problems& q, cudaStream_t st)
 
 int launch_product(const ProductArgs& p, cudaStream_t st)
 {
+    if (p.m_grouped && !p.b_mn && p.m <= kFewRows) return launch_few_rows(p, st);
     Problems q;
     q.p = p;
     // pairs of CTAs on 256 x 256 tiles move half the bytes of single ones on

@@ -47,6 +47,10 @@ struct ProductArgs {
     int64_t ldd = 0, batch_d = 0;
 };
 
+// The same for m-grouped forward products of up to kFewRows rows (few_rows.cu).
+constexpr int64_t kFewRows = 4;
+int launch_few_rows(const ProductArgs& p, cudaStream_t st);
+
 // Enqueue the product.  EMB_OK or an error with nothing enqueued.
 int launch_product(const ProductArgs& p, cudaStream_t st);
 

@@ -2,13 +2,13 @@
 each expert's weights and added back, with the gradients.
 
 Argument checks and marshalling only; the work is in libemb.so.  Tensors are on
-the current CUDA device, calls run on the current torch stream or on `stream`,
-and what they return is allocated for that stream.
+the current CUDA device.  Every call takes `stream`: it runs on that stream
+(default: the current one), and what it returns is allocated for it.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -20,13 +20,21 @@ MAX_EXPERTS = 1024
 MAX_EXPERTS_PER_TOKEN = 64
 
 
-def _on(stream):
-    """Allocations belong to the stream that the call runs on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def on_stream(call):
+    """Gives `call` a `stream` argument: with one, it runs, and what it returns is
+    allocated, on that stream instead of the current one."""
+    @functools.wraps(call)
+    def run(*args, stream=None, **kwargs):
+        if stream is None:
+            return call(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            return call(*args, **kwargs)
+    return run
 
 
-def _handle(stream) -> int:
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _stream(device: torch.device) -> int:
+    """The device's current stream, as an address."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _matrix(t, name: str, rows: int, width: Optional[int] = None, dtype=None, device=None) -> int:
@@ -65,7 +73,7 @@ class ExpertPlan:
     src[p] = t * k + j, and token t's j-th expert has row pos[t, j] (-1: none).
     """
 
-    __slots__ = ("offsets", "src", "pos", "tokens", "k", "experts", "device", "_c", "_ref")
+    __slots__ = ("offsets", "src", "pos", "tokens", "k", "experts", "assignments", "device", "_c", "_ref")
 
     def __init__(self, offsets: torch.Tensor, src: torch.Tensor, pos: torch.Tensor):
         for t, name, dims in ((offsets, "offsets", 1), (src, "src", 1), (pos, "pos", 2)):
@@ -81,14 +89,14 @@ class ExpertPlan:
                              % (MAX_EXPERTS, MAX_EXPERTS_PER_TOKEN, E, k))
         if src.shape[0] != T * k:
             raise ValueError("src holds %d assignments, pos %d" % (src.shape[0], T * k))
+        self._set(offsets, src, pos, T, k, E, offsets.device)
+
+    def _set(self, offsets, src, pos, T, k, E, device):
         self.offsets, self.src, self.pos = offsets, src, pos
-        self.tokens, self.k, self.experts, self.device = T, k, E, offsets.device
+        self.tokens, self.k, self.experts, self.assignments, self.device = T, k, E, T * k, device
         self._c = EmbExpertPlan(offsets.data_ptr(), src.data_ptr(), pos.data_ptr(), T, k, E)
         self._ref = ctypes.byref(self._c)
-
-    @property
-    def assignments(self) -> int:
-        return self.tokens * self.k
+        return self
 
 
 def _plan(plan) -> ExpertPlan:
@@ -97,7 +105,15 @@ def _plan(plan) -> ExpertPlan:
     return plan
 
 
-def expert_sort(ids: torch.Tensor, num_experts: int, stream=None) -> ExpertPlan:
+@functools.lru_cache(maxsize=256)
+def _sort_workspace(tokens: int, k: int, experts: int) -> int:
+    n = ctypes.c_size_t()
+    check(lib.emb_expert_sort_workspace(tokens, k, experts, ctypes.byref(n)), "emb_expert_sort_workspace")
+    return n.value
+
+
+@on_stream
+def expert_sort(ids: torch.Tensor, num_experts: int) -> ExpertPlan:
     """The plan of int32 or int64 ids [tokens, k] of experts in [0, num_experts).
 
     A stable sort: within an expert, assignments stay in order.  -1 marks an
@@ -114,44 +130,42 @@ def expert_sort(ids: torch.Tensor, num_experts: int, stream=None) -> ExpertPlan:
     if not 1 <= k <= MAX_EXPERTS_PER_TOKEN or not 1 <= E <= MAX_EXPERTS:
         raise ValueError("1 to %d experts and 1 to %d experts a token are supported, got %d and %d"
                          % (MAX_EXPERTS, MAX_EXPERTS_PER_TOKEN, E, k))
-    n = ctypes.c_size_t()
-    check(lib.emb_expert_sort_workspace(T, k, E, ctypes.byref(n)), "emb_expert_sort_workspace")
-    with _on(stream):
-        i32 = dict(dtype=torch.int32, device=ids.device)
-        plan = ExpertPlan(torch.empty(E + 1, **i32), torch.empty(T * k, **i32), torch.empty((T, k), **i32))
-        ws = torch.empty(n.value, dtype=torch.uint8, device=ids.device)   # torch's blocks start at 512 bytes
-        check(lib.emb_expert_sort(ids.data_ptr(), ids.element_size(), plan._ref, ws.data_ptr(), n.value,
-                                  _handle(stream)), "emb_expert_sort")
+    device, i32 = ids.device, torch.int32
+    plan = ExpertPlan.__new__(ExpertPlan)._set(
+        torch.empty(E + 1, dtype=i32, device=device), torch.empty(T * k, dtype=i32, device=device),
+        torch.empty((T, k), dtype=i32, device=device), T, k, E, device)
+    size = _sort_workspace(T, k, E)
+    ws = torch.empty(size, dtype=torch.uint8, device=device)   # torch's blocks start at 512 bytes
+    check(lib.emb_expert_sort(ids.data_ptr(), ids.element_size(), plan._ref, ws.data_ptr(), size, _stream(device)),
+          "emb_expert_sort")
     return plan
 
 
-def expert_dispatch(plan: ExpertPlan, x: torch.Tensor, dtype: Optional[torch.dtype] = None,
-                    stream=None) -> torch.Tensor:
+@on_stream
+def expert_dispatch(plan: ExpertPlan, x: torch.Tensor, dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """Rows [tokens * k, width] in expert order of x [tokens, width], in `dtype`
     (default x's); the rows after the last group are zero."""
     plan = _plan(plan)
     stride = _matrix(x, "x", plan.tokens, device=plan.device)
     dtype = _dtype(dtype, x.dtype)
     width = x.shape[1]
-    with _on(stream):
-        rows = torch.empty((plan.assignments, width), dtype=dtype, device=plan.device)
-        check(lib.emb_expert_dispatch(plan._ref, x.data_ptr(), _DTYPE_CODE[x.dtype], stride, width, rows.data_ptr(),
-                                      _DTYPE_CODE[dtype], _handle(stream)), "emb_expert_dispatch")
+    rows = torch.empty((plan.assignments, width), dtype=dtype, device=plan.device)
+    check(lib.emb_expert_dispatch(plan._ref, x.data_ptr(), _DTYPE_CODE[x.dtype], stride, width, rows.data_ptr(),
+                                  _DTYPE_CODE[dtype], _stream(plan.device)), "emb_expert_dispatch")
     return rows
 
 
-def expert_dispatch_grad(plan: ExpertPlan, grad_rows: torch.Tensor, dtype: Optional[torch.dtype] = None,
-                         stream=None) -> torch.Tensor:
+@on_stream
+def expert_dispatch_grad(plan: ExpertPlan, grad_rows: torch.Tensor, dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """Gradient [tokens, width] of expert_dispatch's x, in `dtype` (default grad_rows's)."""
     plan = _plan(plan)
     stride = _matrix(grad_rows, "grad_rows", plan.assignments, device=plan.device)
     dtype = _dtype(dtype, grad_rows.dtype)
     width = grad_rows.shape[1]
-    with _on(stream):
-        grad_x = torch.empty((plan.tokens, width), dtype=dtype, device=plan.device)
-        check(lib.emb_expert_dispatch_grad(plan._ref, grad_rows.data_ptr(), _DTYPE_CODE[grad_rows.dtype], stride, width,
-                                           grad_x.data_ptr(), _DTYPE_CODE[dtype], _handle(stream)),
-              "emb_expert_dispatch_grad")
+    grad_x = torch.empty((plan.tokens, width), dtype=dtype, device=plan.device)
+    check(lib.emb_expert_dispatch_grad(plan._ref, grad_rows.data_ptr(), _DTYPE_CODE[grad_rows.dtype], stride, width,
+                                       grad_x.data_ptr(), _DTYPE_CODE[dtype], _stream(plan.device)),
+          "emb_expert_dispatch_grad")
     return grad_x
 
 
@@ -163,8 +177,8 @@ def _weights(plan, weights) -> None:
         raise ValueError("weights is on %s, the plan on %s" % (weights.device, plan.device))
 
 
-def expert_combine(plan: ExpertPlan, rows: torch.Tensor, weights: torch.Tensor, dtype: Optional[torch.dtype] = None,
-                   stream=None) -> torch.Tensor:
+@on_stream
+def expert_combine(plan: ExpertPlan, rows: torch.Tensor, weights: torch.Tensor, dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """[tokens, width]: each token's rows, weighted by float32 weights [tokens, k]
     and added in fp32, in `dtype` (default rows's)."""
     plan = _plan(plan)
@@ -172,28 +186,26 @@ def expert_combine(plan: ExpertPlan, rows: torch.Tensor, weights: torch.Tensor, 
     _weights(plan, weights)
     dtype = _dtype(dtype, rows.dtype)
     width = rows.shape[1]
-    with _on(stream):
-        out = torch.empty((plan.tokens, width), dtype=dtype, device=plan.device)
-        check(lib.emb_expert_combine(plan._ref, rows.data_ptr(), _DTYPE_CODE[rows.dtype], stride, weights.data_ptr(),
-                                     width, out.data_ptr(), _DTYPE_CODE[dtype], _handle(stream)), "emb_expert_combine")
+    out = torch.empty((plan.tokens, width), dtype=dtype, device=plan.device)
+    check(lib.emb_expert_combine(plan._ref, rows.data_ptr(), _DTYPE_CODE[rows.dtype], stride, weights.data_ptr(),
+                                 width, out.data_ptr(), _DTYPE_CODE[dtype], _stream(plan.device)), "emb_expert_combine")
     return out
 
 
-def expert_combine_grad(plan: ExpertPlan, grad_out: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor,
-                        stream=None):
+@on_stream
+def expert_combine_grad(plan: ExpertPlan, grad_out: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor):
     """(grad_rows in rows's dtype, grad_weights float32 [tokens, k]) of expert_combine."""
     plan = _plan(plan)
     stride = _matrix(rows, "rows", plan.assignments, device=plan.device)
     width = rows.shape[1]
     grad_stride = _matrix(grad_out, "grad_out", plan.tokens, width, device=plan.device)
     _weights(plan, weights)
-    with _on(stream):
-        grad_rows = torch.empty((plan.assignments, width), dtype=rows.dtype, device=plan.device)
-        grad_weights = torch.empty((plan.tokens, plan.k), dtype=torch.float32, device=plan.device)
-        check(lib.emb_expert_combine_grad(plan._ref, grad_out.data_ptr(), _DTYPE_CODE[grad_out.dtype], grad_stride,
-                                          rows.data_ptr(), _DTYPE_CODE[rows.dtype], stride, weights.data_ptr(), width,
-                                          grad_rows.data_ptr(), grad_weights.data_ptr(), _handle(stream)),
-              "emb_expert_combine_grad")
+    grad_rows = torch.empty((plan.assignments, width), dtype=rows.dtype, device=plan.device)
+    grad_weights = torch.empty((plan.tokens, plan.k), dtype=torch.float32, device=plan.device)
+    check(lib.emb_expert_combine_grad(plan._ref, grad_out.data_ptr(), _DTYPE_CODE[grad_out.dtype], grad_stride,
+                                      rows.data_ptr(), _DTYPE_CODE[rows.dtype], stride, weights.data_ptr(), width,
+                                      grad_rows.data_ptr(), grad_weights.data_ptr(), _stream(plan.device)),
+          "emb_expert_combine_grad")
     return grad_rows, grad_weights
 
 
@@ -218,22 +230,23 @@ def _weight(plan, weight):
     return N, K
 
 
-def expert_linear(plan: ExpertPlan, rows: torch.Tensor, weight: torch.Tensor, stream=None) -> torch.Tensor:
+@on_stream
+def expert_linear(plan: ExpertPlan, rows: torch.Tensor, weight: torch.Tensor) -> torch.Tensor:
     """[tokens * k, out]: each expert's rows times the transpose of its own
     weight [out, in] of ``weight`` [E, out, in]; float16 or bfloat16, fp32 sums.
     Rows after the last group are not read; their products are zero."""
     plan = _plan(plan)
     N, K = _weight(plan, weight)
     stride = _linear(plan, rows, "rows", K, weight.dtype)
-    with _on(stream):
-        y = torch.empty((plan.assignments, N), dtype=weight.dtype, device=plan.device)
-        check(lib.emb_expert_linear(plan._ref, rows.data_ptr(), stride, weight.data_ptr(), K, N,
-                                    _DTYPE_CODE[weight.dtype], y.data_ptr(), _handle(stream)), "emb_expert_linear")
+    y = torch.empty((plan.assignments, N), dtype=weight.dtype, device=plan.device)
+    check(lib.emb_expert_linear(plan._ref, rows.data_ptr(), stride, weight.data_ptr(), K, N,
+                                _DTYPE_CODE[weight.dtype], y.data_ptr(), _stream(plan.device)), "emb_expert_linear")
     return y
 
 
+@on_stream
 def expert_linear_grad(plan: ExpertPlan, grad_y: torch.Tensor, rows: Optional[torch.Tensor], weight: torch.Tensor,
-                       need_rows: bool = True, need_weight: bool = True, stream=None):
+                       need_rows: bool = True, need_weight: bool = True):
     """(grad_rows, grad_weight) of expert_linear; None in the place of one that is not needed."""
     plan = _plan(plan)
     N, K = _weight(plan, weight)
@@ -242,21 +255,20 @@ def expert_linear_grad(plan: ExpertPlan, grad_y: torch.Tensor, rows: Optional[to
     grad_rows = grad_weight = None
     if need_weight:
         stride = _linear(plan, rows, "rows", K, weight.dtype)
-    with _on(stream):
-        if need_rows:
-            grad_rows = torch.empty((plan.assignments, K), dtype=weight.dtype, device=plan.device)
-            check(lib.emb_expert_linear_grad_rows(plan._ref, grad_y.data_ptr(), grad_stride, weight.data_ptr(), K, N,
-                                                  code, grad_rows.data_ptr(), _handle(stream)),
-                  "emb_expert_linear_grad_rows")
-        if need_weight:
-            grad_weight = torch.empty_like(weight)
-            check(lib.emb_expert_linear_grad_weight(plan._ref, grad_y.data_ptr(), grad_stride, rows.data_ptr(), stride,
-                                                    K, N, code, grad_weight.data_ptr(), _handle(stream)),
-                  "emb_expert_linear_grad_weight")
+    if need_rows:
+        grad_rows = torch.empty((plan.assignments, K), dtype=weight.dtype, device=plan.device)
+        check(lib.emb_expert_linear_grad_rows(plan._ref, grad_y.data_ptr(), grad_stride, weight.data_ptr(), K, N,
+                                              code, grad_rows.data_ptr(), _stream(plan.device)),
+              "emb_expert_linear_grad_rows")
+    if need_weight:
+        grad_weight = torch.empty_like(weight)
+        check(lib.emb_expert_linear_grad_weight(plan._ref, grad_y.data_ptr(), grad_stride, rows.data_ptr(), stride,
+                                                K, N, code, grad_weight.data_ptr(), _stream(plan.device)),
+              "emb_expert_linear_grad_weight")
     return grad_rows, grad_weight
 
 
 def dense_status(stream=None) -> int:
     """Waits for the stream; returns and clears the device's sticky status of the
     expert calls and of orthogonalize (EMB_OK, EMB_ERR_KEY_RANGE, EMB_ERR_TIMEOUT)."""
-    return int(lib.emb_dense_status(_handle(stream)))
+    return int(lib.emb_dense_status((torch.cuda.current_stream() if stream is None else stream).cuda_stream))

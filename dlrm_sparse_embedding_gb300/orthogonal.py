@@ -2,19 +2,28 @@
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Tuple
 
 import torch
 
 from ._lib import check, lib
-from .experts import _DTYPE_CODE, _handle, _on
+from .experts import _DTYPE_CODE, _stream, on_stream
 
 #: K. Jordan et al., "Muon" (2024)
 COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 
 
+@functools.lru_cache(maxsize=256)
+def _workspace(batch: int, rows: int, cols: int) -> int:
+    n = ctypes.c_size_t()
+    check(lib.emb_orthogonalize_workspace(batch, rows, cols, ctypes.byref(n)), "emb_orthogonalize_workspace")
+    return n.value
+
+
+@on_stream
 def orthogonalize(update: torch.Tensor, steps: int = 5, coefficients: Tuple[float, float, float] = COEFFICIENTS,
-                  eps: float = 1e-7, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                  eps: float = 1e-7, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """bfloat16 [..., rows, cols]: each matrix of `update` (float32, float16 or
     bfloat16) with its singular values driven towards 1, by `steps` steps
     X <- a X + (b A + c A A) X, A = X X^T, from X = update / (|update|_F + eps).
@@ -43,16 +52,14 @@ def orthogonalize(update: torch.Tensor, steps: int = 5, coefficients: Tuple[floa
     if not float(eps) >= 0:
         raise ValueError("eps must not be negative, got %r" % (eps,))
     a, b, c = (float(v) for v in coefficients)
-    n = ctypes.c_size_t()
-    check(lib.emb_orthogonalize_workspace(batch, rows, cols, ctypes.byref(n)), "emb_orthogonalize_workspace")
+    size = _workspace(batch, rows, cols)
     if out is not None and (not isinstance(out, torch.Tensor) or out.dtype != torch.bfloat16 or out.shape != update.shape
                             or not out.is_contiguous() or out.device != update.device):
         raise ValueError("out must be contiguous bfloat16 %s on %s" % (tuple(update.shape), update.device))
-    with _on(stream):
-        if out is None:
-            out = torch.empty(update.shape, dtype=torch.bfloat16, device=update.device)
-        ws = torch.empty(n.value, dtype=torch.uint8, device=update.device)   # torch's blocks start at 512 bytes
-        check(lib.emb_orthogonalize(update.data_ptr(), _DTYPE_CODE[update.dtype], batch_stride, row_stride, batch, rows,
-                                    cols, int(steps), a, b, c, float(eps), out.data_ptr(), ws.data_ptr(), n.value,
-                                    _handle(stream)), "emb_orthogonalize")
+    if out is None:
+        out = torch.empty(update.shape, dtype=torch.bfloat16, device=update.device)
+    ws = torch.empty(size, dtype=torch.uint8, device=update.device)   # torch's blocks start at 512 bytes
+    check(lib.emb_orthogonalize(update.data_ptr(), _DTYPE_CODE[update.dtype], batch_stride, row_stride, batch, rows, cols,
+                                int(steps), a, b, c, float(eps), out.data_ptr(), ws.data_ptr(), size,
+                                _stream(update.device)), "emb_orthogonalize")
     return out
