@@ -79,7 +79,7 @@ int launch_few_rows(const ProductArgs& p, cudaStream_t st)
     const auto go = [&](auto t) {
         using T = decltype(t);
         const dim3 grid((unsigned)((p.n + kWarps - 1) / kWarps), (unsigned)p.m);
-        few_forward<T><<<grid, kThreads, 0, st>>>((const T*)p.a, p.lda, (const T*)p.b, p.k, p.n, p.offsets, (int)p.batch, (T*)p.d);
+        few_forward<T><<<grid, kThreads, 0, st>>>((const T*)p.a, p.lda, (const T*)p.b, p.k, p.n, p.offsets, p.experts, (T*)p.d);
         return cudaGetLastError() == cudaSuccess ? EMB_OK : EMB_ERR_CUDA;
     };
     return p.dtype == EMB_F16 ? go(__half()) : go(__nv_bfloat16());

@@ -30,11 +30,16 @@
 // G is scaled by a power of two before it is rounded, exact for bf16, and the
 // rest of the norm goes into the first step's factors.
 #include <algorithm>
+#include <climits>
 
-#include "products.cuh"
+#include "product_core.cuh"
 
 namespace emb {
 namespace {
+
+// A number is held as fp16 h plus fp16 l / kLowScale: l is h's rounding error,
+// at most 2^-11 |h|, scaled up so that it is not lost where h is subnormal.
+constexpr float kLowScale = 2048.f;
 
 constexpr int kNormThreads = 256;
 constexpr int kMaxNormBlocks = 256;   // per matrix
@@ -43,7 +48,7 @@ constexpr float kRange = 256.f;       // the scaled norm is in [kRange, 2 kRange
 struct Layout {
     int64_t ld, ldm, m, x_elems, a_elems;   // pitches (multiples of 8), the short side, elements a matrix
     int norm_blocks;
-    size_t x[2], x_low[2], a, b, scale, partial, total;   // byte offsets
+    size_t x[2], x_low[2], a, b, scale, done, partial, total;   // byte offsets
 };
 
 Layout layout_of(int64_t batch, int64_t rows, int64_t cols)
@@ -66,6 +71,7 @@ Layout layout_of(int64_t batch, int64_t rows, int64_t cols)
     l.a = take(2 * (size_t)batch * l.a_elems);
     l.b = take(2 * (size_t)batch * l.a_elems);
     l.scale = take(sizeof(float) * (size_t)batch);
+    l.done = take(sizeof(unsigned) * (size_t)batch);
     l.partial = take(sizeof(double) * (size_t)batch * l.norm_blocks);
     l.total = at;
     return l;
@@ -150,7 +156,7 @@ template <int V, class T>
 __global__ void __launch_bounds__(kNormThreads) scale_in(const T* __restrict__ g, int64_t batch_stride, int64_t row_stride,
                                                          int64_t rows, int64_t cols, int norm_blocks, const double* __restrict__ partial,
                                                          float eps, int64_t ld, __half* __restrict__ x, __half* __restrict__ x_low,
-                                                         float* __restrict__ scale)
+                                                         float* __restrict__ scale, unsigned* __restrict__ done)
 {
     __shared__ double warp_sums[kNormThreads / 32];
     static_assert(kMaxNormBlocks <= kNormThreads, "one partial sum a thread");
@@ -159,7 +165,10 @@ __global__ void __launch_bounds__(kNormThreads) scale_in(const T* __restrict__ g
     int e = 0;
     if (norm > 0 && norm < INFINITY) e = max(-120, min(120, ilogbf(kRange) - ilogb(norm)));
     const float up = ldexpf(1.f, e);
-    if (blockIdx.x == 0 && threadIdx.x == 0) scale[blockIdx.y] = (float)(1.0 / ((norm + eps) * up));
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        scale[blockIdx.y] = (float)(1.0 / ((norm + eps) * up));
+        done[blockIdx.y] = 0;
+    }
     const int64_t at = (int64_t)blockIdx.y * rows * ld;
     each_piece<V, T>(g + blockIdx.y * batch_stride, row_stride, rows, cols, [&](int64_t row, int64_t c, const float (&v)[V]) {
         alignas(16) __half h[V], l[V];
@@ -186,8 +195,374 @@ int start(const T* g, int64_t bs, int64_t rs, int64_t batch, int64_t rows, int64
     norm_partials<V, T><<<grid, kNormThreads, 0, st>>>(g, bs, rs, rows, cols, partial);
     scale_in<V, T><<<grid, kNormThreads, 0, st>>>(g, bs, rs, rows, cols, l.norm_blocks, partial, eps, l.ld,
                                                   reinterpret_cast<__half*>(ws + l.x[0]), reinterpret_cast<__half*>(ws + l.x_low[0]),
-                                                  reinterpret_cast<float*>(ws + l.scale));
+                                                  reinterpret_cast<float*>(ws + l.scale), reinterpret_cast<unsigned*>(ws + l.done));
     return cudaGetLastError() == cudaSuccess ? EMB_OK : EMB_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------------------
+// the steps
+// ---------------------------------------------------------------------------
+// All products of all steps are one list of tiles for one persistent grid: step
+// by step, in a step A's, B's and then X's tiles, in each the matrices one after
+// another.  A tile needs its own matrix's earlier tiles and no other's, so
+// matrices run into each other's products instead of waiting at 3 x steps
+// launches; a counter a matrix says how far it is.  CTAs take tiles in the
+// list's order, and the launch is cooperative, so what a tile waits for is done
+// or running.
+//
+// A and B are symmetric: only the tiles on and below the diagonal are computed,
+// the others are written as their transposes.
+using namespace core;
+
+enum Product { kGram, kQuadratic, kUpdate };
+
+constexpr int kStaging = 32 * kChunk * 4;       // bytes of shared memory an epilogue warp takes its columns through, in fp32
+constexpr int kSmem = smem_bytes(kEpilogueWarps * kStaging);
+static_assert(kSmem <= 227 * 1024, "the SM's shared memory");
+
+struct Steps {
+    CUtensorMap x_gram[2], x_update[2], a_map, b_map;   // x_gram: of A = X X^T; x_update: of X' = B X
+    __half *x[2], *x_low[2], *a, *b;
+    __nv_bfloat16* out;
+    const float* scale;
+    unsigned* done;          // of each matrix: finished epilogue warps
+    int64_t rows, cols, ld, ldm, m;
+    int batch, steps;
+    bool tall;
+    float ca, cb, cc;
+    int side, tiles_m, tiles_n;   // tiles along A; of X
+    int* status;
+};
+
+struct Tile {
+    Product product;
+    int step, matrix;
+    int64_t m0, n0;
+    int k_steps;
+    unsigned needs;          // of done[matrix]
+};
+
+template <class S>
+__device__ __forceinline__ Tile tile_at(const Steps& q, int64_t t)
+{
+    Tile r;
+    const int64_t gram = (int64_t)q.side * (q.side + 1) / 2, update = (int64_t)q.tiles_m * q.tiles_n;
+    const int64_t per = 2 * gram + update;
+    r.step = (int)(t / (per * q.batch));
+    t -= r.step * per * q.batch;
+    int64_t before = r.step * per;
+    int64_t k = q.m;
+    if (t < 2 * gram * q.batch) {
+        r.product = t < gram * q.batch ? kGram : kQuadratic;
+        if (r.product == kGram) k = q.rows + q.cols - q.m;
+        else t -= gram * q.batch, before += gram;
+        r.matrix = (int)(t / gram);
+        const int idx = (int)(t - r.matrix * gram);
+        int i = (int)((sqrtf(8.f * (float)idx + 1.f) - 1.f) * 0.5f);   // row i of the triangle starts at i (i + 1) / 2
+        while ((int64_t)i * (i + 1) / 2 > idx) --i;
+        while ((int64_t)(i + 1) * (i + 2) / 2 <= idx) ++i;
+        r.m0 = (int64_t)i * S::kTile;
+        r.n0 = (int64_t)(idx - i * (i + 1) / 2) * S::kTile;
+    } else {
+        r.product = kUpdate;
+        t -= 2 * gram * q.batch, before += 2 * gram;
+        r.matrix = (int)(t / update);
+        const int idx = (int)(t - r.matrix * update);
+        r.m0 = (int64_t)(idx / q.tiles_n) * S::kTile;
+        r.n0 = (int64_t)(idx % q.tiles_n) * S::kTile;
+    }
+    r.k_steps = (int)((k + kStep - 1) / kStep);
+    r.needs = (unsigned)(before * (kEpilogueWarps * S::CTAS));
+    return r;
+}
+
+// Waits until a matrix has got so far; false when the limit ran out.
+__device__ __forceinline__ bool wait_done(const unsigned* done, unsigned needs, volatile int* gave_up)
+{
+    const auto reached = [&] {
+        unsigned v;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(done) : "memory");
+        return (int)(v - needs) >= 0;
+    };
+    if (!needs || reached()) return true;
+    const uint64_t start = tc::now_ns();
+    while (!reached()) {
+        if (*gave_up) return false;
+        if (tc::now_ns() - start > tc::kWaitLimitNs) {
+            *gave_up = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& p, float (&v)[8])
+{
+    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    }
+}
+
+// An epilogue warp's columns of a tile.  Through shared memory (a lane has one
+// row's 32 columns of the accumulator) a lane gets four pieces of eight columns,
+// in rows r0 + 8 i, which meet C there and leave again.  C for the next columns
+// is on its way meanwhile; it was written in this launch by other SMs, so it
+// comes from L2.
+//   kGram       D = s^2 sum, s in the first step
+//   kQuadratic  D = cc sum + cb C + diagonal I
+//   kUpdate     D = s (sum + beta (C + C's low part))
+template <Product F>
+__device__ __forceinline__ void finish(const Steps& q, const Tile& tile, const Part& part, float* mine, uint32_t rank, volatile int* gave_up)
+{
+    const int lane = threadIdx.x & 31, r0 = lane >> 2, p = lane & 3;
+    const int64_t height = F == kUpdate ? q.rows : q.m, width = F == kUpdate ? q.cols : q.m, ld = F == kUpdate ? q.ld : q.ldm;
+    const int64_t m_first = tile.m0 + rank * kRows + part.row, left = height - m_first;
+    const int rows = left < 0 ? 0 : left > 32 ? 32 : (int)left;
+    const int64_t of_matrix = tile.matrix * (F == kUpdate ? q.rows * q.ld : q.m * q.ldm);
+    const int64_t at = of_matrix + (m_first + r0) * ld + tile.n0 + p * 8;
+    const __half *high = nullptr, *low = nullptr;
+    __half *d = nullptr, *d_low = nullptr;
+    float diagonal = 0.f;   // the shift of B that the last two steps use, taken off again in their update
+    if (tile.step > 0 && tile.step >= q.steps - 2) diagonal = (tile.step == q.steps - 1 ? -0.9f : -0.73f) * (q.cb + q.cc);
+    const bool last = F == kUpdate && tile.step == q.steps - 1;
+    if (F == kGram) {
+        d = q.a + at;
+    } else if (F == kQuadratic) {
+        high = q.a + at;
+        d = q.b + at;
+    } else {
+        high = q.x[tile.step & 1] + at, low = q.x_low[tile.step & 1] + at;
+        d = q.x[(tile.step + 1) & 1] + at, d_low = q.x_low[(tile.step + 1) & 1] + at;
+    }
+    const float beta = F == kUpdate ? q.ca - diagonal : q.cb;
+    const float s = F != kQuadratic && tile.step == 0 ? (F == kGram ? q.scale[tile.matrix] * q.scale[tile.matrix] : q.scale[tile.matrix]) : 1.f;
+    const bool out_wide = (q.cols & 7) == 0 && (reinterpret_cast<uintptr_t>(q.out) & 15) == 0;
+    __nv_bfloat16* const out = q.out + tile.matrix * q.rows * q.cols + (m_first + r0) * q.cols + tile.n0 + p * 8;
+
+    uint4 h[4], l[4];
+    const auto fetch = [&](int c) {
+        const bool in = tile.n0 + c + p * 8 < width;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool has = in && r0 + 8 * i < rows;
+            if (F != kGram) h[i] = has ? __ldcg(reinterpret_cast<const uint4*>(high + i * 8 * ld + c)) : make_uint4(0, 0, 0, 0);
+            if (F == kUpdate) l[i] = has ? __ldcg(reinterpret_cast<const uint4*>(low + i * 8 * ld + c)) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    if (F != kGram) {
+        // the products' operands were waited for by the copies; what this warp reads itself, it waits for itself
+        if (!wait_done(q.done + tile.matrix, tile.needs, gave_up)) return;
+        fetch(part.c0);
+    }
+    if (!tc::bar_wait(part.full, part.phase, gave_up)) return;
+    tc::fence_after();
+    for (int c = part.c0; c < part.c1; c += kChunk) {
+        uint32_t v[32];
+        tc::tmem_load32(part.tmem + c, v);
+        if (c + kChunk == part.c1) {
+            tc::fence_before();
+            if (lane == 0) tc::bar_arrive(part.empty);
+        }
+        // 16-byte piece i of row r is at i ^ (r & 7) ^ 2 (r >> 3): rows, and columns of eight rows, without conflicts
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(mine + lane * kChunk + ((i ^ (lane & 7) ^ ((lane >> 3) << 1)) * 4)) =
+                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        __syncwarp();
+        const int64_t n = tile.n0 + c + p * 8;
+        uint4 ch[4], cl[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ch[i] = h[i], cl[i] = l[i];
+        if (F != kGram && c + kChunk < part.c1) fetch(c + kChunk);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + r0, turn = (r & 7) ^ ((r >> 3) << 1);
+            float4* const px = reinterpret_cast<float4*>(mine + r * kChunk + (((2 * p) ^ turn) * 4));
+            float4* const py = reinterpret_cast<float4*>(mine + r * kChunk + (((2 * p + 1) ^ turn) * 4));
+            const float4 x = *px, y = *py;
+            float o[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+            if (F == kGram) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] *= s;
+            } else {
+                float cv[8];
+                unpack8(ch[i], cv);
+                if (F == kUpdate) {
+                    float lv[8];
+                    unpack8(cl[i], lv);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o[j] = s * __fmaf_rn(beta, __fmaf_rn(1.f / kLowScale, lv[j], cv[j]), o[j]);
+                } else {
+                    const int64_t on = m_first + r - n;   // which of them is on the diagonal
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o[j] = __fmaf_rn(beta, cv[j], q.cc * o[j]) + (on == j ? diagonal : 0.f);
+                }
+            }
+            if (F != kUpdate && tile.m0 != tile.n0) {   // for the transpose below
+                *px = make_float4(o[0], o[1], o[2], o[3]);
+                *py = make_float4(o[4], o[5], o[6], o[7]);
+            }
+            if (n >= width || r >= rows) continue;
+            if (last) {
+                __nv_bfloat16* const to = out + i * 8 * q.cols + c;
+                if (out_wide) {
+                    *reinterpret_cast<uint4*>(to) = pack8<__nv_bfloat16>(o);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (n + j < width) to[j] = __float2bfloat16_rn(o[j]);
+                }
+                continue;
+            }
+            const uint4 packed = pack8<__half>(o);
+            *reinterpret_cast<uint4*>(d + i * 8 * ld + c) = packed;
+            if (F == kUpdate) {
+                float back[8];
+                unpack8(packed, back);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) back[j] = kLowScale * (o[j] - back[j]);
+                *reinterpret_cast<uint4*>(d_low + i * 8 * ld + c) = pack8<__half>(back);
+            }
+        }
+        __syncwarp();
+        if (F != kUpdate && tile.m0 != tile.n0) {
+            // column n of these 32 rows is 32 elements of row n of the other triangle: four lanes store 64 bytes of it
+            __half* const t = (F == kGram ? q.a : q.b) + of_matrix + (tile.n0 + c + r0) * ld + m_first + p * 8;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int col = i * 8 + r0;
+                float o[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    o[j] = mine[(p * 8 + j) * kChunk + (((col >> 2) ^ j ^ (p << 1)) * 4) + (col & 3)];
+                if (tile.n0 + c + col < width && p * 8 < rows) *reinterpret_cast<uint4*>(t + i * 8 * ld) = pack8<__half>(o);
+            }
+            __syncwarp();
+        }
+    }
+    // every lane's stores, for copies and loads of other SMs, before the count
+    tc::fence_async();
+    __syncwarp();
+    if (lane == 0) {
+        __threadfence();
+        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(q.done + tile.matrix) : "memory");
+    }
+}
+
+template <class S>
+__global__ void __launch_bounds__(kThreads, 1) newton_schulz(const __grid_constant__ Steps q)
+{
+    extern __shared__ __align__(1024) unsigned char dynamic[];
+    Block b = block_of(dynamic);
+    const int warp = threadIdx.x >> 5;
+    open<S>(b);
+    const int64_t total = (int64_t)q.steps * q.batch * ((int64_t)q.side * (q.side + 1) + (int64_t)q.tiles_m * q.tiles_n);
+    const int64_t first = blockIdx.x / S::CTAS, step = gridDim.x / S::CTAS;
+
+    if (warp == 0 && tc::elect_one()) {
+        uint32_t n = 0;
+        bool ok = true;
+        for (int64_t t = first; ok && t < total; t += step) {
+            const Tile tile = tile_at<S>(q, t);
+            const int m = (int)tile.m0 + (int)b.rank * kRows, nn = (int)tile.n0 + (int)b.rank * kRows, z = tile.matrix;
+            ok = wait_done(q.done + tile.matrix, tile.needs, b.gave_up);
+            tc::fence_async();
+            const CUtensorMap *ma = &q.a_map, *mb = &q.a_map;
+            bool a_mn = false, b_mn = false;
+            if (tile.product == kGram) {
+                ma = mb = &q.x_gram[tile.step & 1];
+                a_mn = b_mn = q.tall;
+            } else if (tile.product == kUpdate) {
+                ma = q.tall ? &q.x_update[tile.step & 1] : &q.b_map;
+                mb = q.tall ? &q.b_map : &q.x_update[tile.step & 1];
+                b_mn = !q.tall;
+            }
+            for (int i = 0; ok && i < tile.k_steps; ++i, ++n) ok = copy_step<S>(b, n, false, ma, a_mn, m, z, mb, b_mn, nn, z, i * kStep);
+        }
+        finish_copies(b, n, ok);
+    } else if (warp == 1 && b.rank == 0 && tc::elect_one()) {
+        uint32_t n = 0, made = 0;
+        for (int64_t t = first; t < total; t += step) {
+            const Tile tile = tile_at<S>(q, t);
+            const bool a_mn = tile.product == kGram && q.tall, b_mn = tile.product == kGram ? q.tall : tile.product == kUpdate && !q.tall;
+            if (!multiply<S>(b, made++, n, tile.k_steps, tc::instruction(false, a_mn, b_mn, S::kTile, S::kTile), a_mn, b_mn)) break;
+            n += tile.k_steps;
+        }
+    } else if (warp >= 4) {
+        uint32_t made = 0;
+        float* const mine = reinterpret_cast<float*>(b.own + (warp - 4) * kStaging);
+        for (int64_t t = first; t < total && !*b.gave_up; t += step) {
+            const Tile tile = tile_at<S>(q, t);
+            const Part part = part_of<S>(b, made++);
+            if (tile.product == kGram) finish<kGram>(q, tile, part, mine, b.rank, b.gave_up);
+            else if (tile.product == kQuadratic) finish<kQuadratic>(q, tile, part, mine, b.rank, b.gave_up);
+            else finish<kUpdate>(q, tile, part, mine, b.rank, b.gave_up);
+        }
+    }
+    close<S>(b, q.status);
+}
+
+template <class S>
+int launch_steps(Steps& q, cudaStream_t st)
+{
+    const Device dev = device();
+    q.status = dense_status_word();
+    if (!dev.sms || !q.status) return EMB_ERR_CUDA;
+    q.side = (int)((q.m + S::kTile - 1) / S::kTile);
+    q.tiles_m = (int)((q.rows + S::kTile - 1) / S::kTile);
+    q.tiles_n = (int)((q.cols + S::kTile - 1) / S::kTile);
+    auto* const kernel = newton_schulz<S>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(S::CTAS);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)S::CTAS, 1, 1};
+    attr[1].id = cudaLaunchAttributeCooperative;
+    attr[1].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    static std::atomic<int> resident[kMaxDevices];   // clusters that run at the same time
+    int clusters = resident[dev.number].load(std::memory_order_relaxed);
+    if (!clusters) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess || clusters < 1) {
+            cudaGetLastError();
+            return EMB_ERR_CUDA;
+        }
+        resident[dev.number].store(clusters, std::memory_order_relaxed);
+    }
+    const int64_t most = q.batch * std::max<int64_t>((int64_t)q.side * (q.side + 1) / 2, (int64_t)q.tiles_m * q.tiles_n);
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(clusters, most) * S::CTAS);
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kernel, q) != cudaSuccess) {
+        cudaGetLastError();
+        return EMB_ERR_CUDA;
+    }
+    return EMB_OK;
+}
+
+// Rounds of tiles a step takes, times a tile's products: a pair's tile has four
+// times those of a single CTA's on twice its SMs.
+int64_t rounds(const Steps& q, int64_t tile, int64_t units)
+{
+    const auto along = [&](int64_t v) { return (v + tile - 1) / tile; };
+    const int64_t gram = q.batch * along(q.m) * (along(q.m) + 1) / 2, update = q.batch * along(q.rows) * along(q.cols);
+    const int64_t gram_k = q.rows + q.cols - q.m;
+    return (gram + units - 1) / units * (gram_k + q.m) + (update + units - 1) / units * q.m;
+}
+
+int run_steps(Steps& q, cudaStream_t st)
+{
+    // a pair's tile takes twice a single CTA's time, which the single ones' twice as many bytes a product eat up again
+    const Device dev = device();
+    if (!dev.sms) return EMB_ERR_CUDA;
+    return 2 * rounds(q, 256, dev.sms / 2) <= rounds(q, 128, dev.sms) * 5 / 4 ? launch_steps<Shape<2>>(q, st) : launch_steps<Shape<1>>(q, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -431,42 +806,28 @@ extern "C" int emb_orthogonalize(const void* update, int32_t dtype, int64_t batc
                     : start<1, T>(g, batch_stride, row_stride, batch, rows, cols, eps, l, ws, st);
     };
     int rc = dtype == EMB_F32 ? begin(float()) : dtype == EMB_F16 ? begin(__half()) : begin(__nv_bfloat16());
-    const bool tall = rows > cols;
-    const float* const scale = reinterpret_cast<const float*>(ws + l.scale);
-    for (int i = 0; i < steps && rc == EMB_OK; ++i) {
-        char *const x = ws + l.x[i & 1], *const x_low = ws + l.x_low[i & 1];
-        const float d = i == 0 ? 0.f : i == steps - 1 ? -0.9f * (b + c) : i == steps - 2 ? -0.73f * (b + c) : 0.f;
-        ProductArgs s;   // A = X X^T, or X^T X
-        s.batch = batch;
-        s.a = s.b = x, s.lda = s.ldb = l.ld, s.batch_a = s.batch_b = l.x_elems;
-        s.a_mn = s.b_mn = tall;
-        s.m = s.n = l.m, s.k = std::max(rows, cols);
-        if (i == 0) s.scale = scale;
-        s.d = ws + l.a, s.ldd = l.ldm, s.batch_d = l.a_elems;
-        rc = launch_product(s, st);
-        if (rc != EMB_OK) break;
-        ProductArgs q;   // B = c A A + b A + d I
-        q.batch = batch;
-        q.a = q.b = q.c = ws + l.a, q.lda = q.ldb = q.ldc = l.ldm, q.batch_a = q.batch_b = q.batch_c = l.a_elems;
-        q.m = q.n = q.k = l.m;
-        q.alpha = c, q.beta = b, q.diagonal = d;
-        q.d = ws + l.b, q.ldd = l.ldm, q.batch_d = l.a_elems;
-        rc = launch_product(q, st);
-        if (rc != EMB_OK) break;
-        ProductArgs n;   // X <- (a - d) X + B X, or X B
-        n.batch = batch;
-        n.a = tall ? x : ws + l.b, n.lda = tall ? l.ld : l.ldm, n.batch_a = tall ? l.x_elems : l.a_elems;
-        n.b = tall ? ws + l.b : x, n.ldb = tall ? l.ldm : l.ld, n.batch_b = tall ? l.a_elems : l.x_elems;
-        n.b_mn = !tall;
-        n.m = rows, n.n = cols, n.k = l.m;
-        if (i == 0) n.scale = scale;
-        n.beta = a - d, n.c = x, n.c_low = x_low, n.ldc = l.ld, n.batch_c = l.x_elems;
-        if (i == steps - 1) {
-            n.d = out, n.d_dtype = EMB_BF16, n.ldd = cols, n.batch_d = rows * cols;
-        } else {
-            n.d = ws + l.x[(i + 1) & 1], n.d_low = ws + l.x_low[(i + 1) & 1], n.ldd = l.ld, n.batch_d = l.x_elems;
-        }
-        rc = launch_product(n, st);
+    if (rc != EMB_OK) return rc;
+    Steps q;
+    q.tall = rows > cols;
+    q.rows = rows, q.cols = cols, q.ld = l.ld, q.ldm = l.ldm, q.m = l.m;
+    q.batch = (int)batch, q.steps = steps;
+    q.ca = a, q.cb = b, q.cc = c;
+    for (int i = 0; i < 2; ++i) {
+        q.x[i] = reinterpret_cast<__half*>(ws + l.x[i]);
+        q.x_low[i] = reinterpret_cast<__half*>(ws + l.x_low[i]);
     }
-    return rc;
+    q.a = reinterpret_cast<__half*>(ws + l.a);
+    q.b = reinterpret_cast<__half*>(ws + l.b);
+    q.out = static_cast<__nv_bfloat16*>(out);
+    q.scale = reinterpret_cast<const float*>(ws + l.scale);
+    q.done = reinterpret_cast<unsigned*>(ws + l.done);
+    // A's products run along the long side: X is k-major in them where its rows are long, and in the update where not
+    for (int i = 0; i < 2; ++i)
+        if (!make_map(&q.x_gram[i], EMB_F16, q.x[i], q.tall, cols, rows, batch, l.ld, l.x_elems) ||
+            !make_map(&q.x_update[i], EMB_F16, q.x[i], !q.tall, cols, rows, batch, l.ld, l.x_elems))
+            return EMB_ERR_CUDA;
+    if (!make_map(&q.a_map, EMB_F16, q.a, false, l.m, l.m, batch, l.ldm, l.a_elems) ||
+        !make_map(&q.b_map, EMB_F16, q.b, false, l.m, l.m, batch, l.ldm, l.a_elems))
+        return EMB_ERR_CUDA;
+    return run_steps(q, st);
 }
