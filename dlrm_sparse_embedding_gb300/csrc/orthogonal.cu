@@ -31,11 +31,14 @@
 // rest of the norm goes into the first step's factors.
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "product_core.cuh"
 
 namespace emb {
 namespace {
+
+using namespace core;
 
 // A number is held as fp16 h plus fp16 l / kLowScale: l is h's rounding error,
 // at most 2^-11 |h|, scaled up so that it is not lost where h is subnormal.
@@ -100,25 +103,32 @@ __device__ __forceinline__ void each_piece(const T* g, int64_t row_stride, int64
     int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     int64_t row = u / pieces, piece = u - row * pieces;
     const int64_t row_step = step / pieces, piece_step = step - row_step * pieces;
+    constexpr int kAhead = 4;   // loads on their way at once
     while (row < rows) {
-        const int64_t c = (piece * 32 + lane) * V;
-        if (c < cols) {
-            float v[V];
-            const T* const p = g + row * row_stride + c;
-            if constexpr (V == 1) {
-                v[0] = to_float<T>(*p);
-            } else if constexpr (sizeof(T) == 4) {
-                const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
-                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-            } else {
-                const uint4 r = *reinterpret_cast<const uint4*>(p);
+        using Word = typename std::conditional<V == 1, T, uint4>::type;
+        constexpr int kWords = V * sizeof(T) / sizeof(Word);
+        Word w[kAhead][kWords];
+        int64_t at_row[kAhead], at_col[kAhead];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = to_float<T>(reinterpret_cast<const T*>(&r)[i]);
+        for (int a = 0; a < kAhead; ++a) {
+            at_row[a] = row, at_col[a] = (piece * 32 + lane) * V;
+            if (row < rows && at_col[a] < cols) {
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) w[a][i] = reinterpret_cast<const Word*>(g + row * row_stride + at_col[a])[i];
+            } else {
+                at_row[a] = rows;
             }
-            f(row, c, v);
+            row += row_step, piece += piece_step;
+            if (piece >= pieces) piece -= pieces, ++row;
         }
-        row += row_step, piece += piece_step;
-        if (piece >= pieces) piece -= pieces, ++row;
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a)
+            if (at_row[a] < rows) {
+                float v[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] = to_float<T>(reinterpret_cast<const T*>(w[a])[i]);
+                f(at_row[a], at_col[a], v);
+            }
     }
 }
 
@@ -151,7 +161,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_partials(const T* __restric
     if (threadIdx.x == 0) partial[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = d;
 }
 
-// X = G 2^e as a sum of two fp16, and the factor that makes it G / (|G| + eps).
+// X = G 2^e as a sum of two fp16 (for 16-bit G one: its 8 or 11 bits fit, but for
+// entries below 2^-24 of the norm), and the factor that makes it G / (|G| + eps).
 template <int V, class T>
 __global__ void __launch_bounds__(kNormThreads) scale_in(const T* __restrict__ g, int64_t batch_stride, int64_t row_stride,
                                                          int64_t rows, int64_t cols, int norm_blocks, const double* __restrict__ partial,
@@ -171,18 +182,18 @@ __global__ void __launch_bounds__(kNormThreads) scale_in(const T* __restrict__ g
     }
     const int64_t at = (int64_t)blockIdx.y * rows * ld;
     each_piece<V, T>(g + blockIdx.y * batch_stride, row_stride, rows, cols, [&](int64_t row, int64_t c, const float (&v)[V]) {
-        alignas(16) __half h[V], l[V];
+        float h[V], l[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            h[i] = __float2half_rn(up * v[i]);
-            l[i] = __float2half_rn(kLowScale * (up * v[i] - __half2float(h[i])));
+            h[i] = up * v[i];
+            l[i] = kLowScale * (h[i] - __half2float(__float2half_rn(h[i])));
         }
         if constexpr (V == 8) {
-            *reinterpret_cast<uint4*>(x + at + row * ld + c) = *reinterpret_cast<const uint4*>(h);
-            *reinterpret_cast<uint4*>(x_low + at + row * ld + c) = *reinterpret_cast<const uint4*>(l);
+            *reinterpret_cast<uint4*>(x + at + row * ld + c) = pack8<__half>(h);
+            if (sizeof(T) == 4) *reinterpret_cast<uint4*>(x_low + at + row * ld + c) = pack8<__half>(l);
         } else {
-            x[at + row * ld + c] = h[0];
-            x_low[at + row * ld + c] = l[0];
+            x[at + row * ld + c] = __float2half_rn(h[0]);
+            if (sizeof(T) == 4) x_low[at + row * ld + c] = __float2half_rn(l[0]);
         }
     });
 }
@@ -212,12 +223,10 @@ int start(const T* g, int64_t bs, int64_t rs, int64_t batch, int64_t rows, int64
 //
 // A and B are symmetric: only the tiles on and below the diagonal are computed,
 // the others are written as their transposes.
-using namespace core;
-
 enum Product { kGram, kQuadratic, kUpdate };
 
 constexpr int kStaging = 32 * kChunk * 4;       // bytes of shared memory an epilogue warp takes its columns through, in fp32
-constexpr int kSmem = smem_bytes(kEpilogueWarps * kStaging);
+constexpr int kSmem = smem_bytes(kEpilogueWarps * kStaging + 64);
 static_assert(kSmem <= 227 * 1024, "the SM's shared memory");
 
 struct Steps {
@@ -225,12 +234,14 @@ struct Steps {
     __half *x[2], *x_low[2], *a, *b;
     __nv_bfloat16* out;
     const float* scale;
-    unsigned* done;          // of each matrix: finished epilogue warps
+    unsigned* done;          // of each matrix: CTAs that have finished a tile
     int64_t rows, cols, ld, ldm, m;
-    int batch, steps;
+    unsigned batch;
+    int steps;
     bool tall;
     float ca, cb, cc;
-    int side, tiles_m, tiles_n;   // tiles along A; of X
+    unsigned side, tiles_m, tiles_n;   // tiles along A; of X
+    bool low_in;             // the first X has a low part
     int* status;
 };
 
@@ -243,36 +254,35 @@ struct Tile {
 };
 
 template <class S>
-__device__ __forceinline__ Tile tile_at(const Steps& q, int64_t t)
+__device__ __forceinline__ Tile tile_at(const Steps& q, unsigned t)
 {
     Tile r;
-    const int64_t gram = (int64_t)q.side * (q.side + 1) / 2, update = (int64_t)q.tiles_m * q.tiles_n;
-    const int64_t per = 2 * gram + update;
-    r.step = (int)(t / (per * q.batch));
+    const unsigned gram = q.side * (q.side + 1) / 2, update = q.tiles_m * q.tiles_n, per = 2 * gram + update;
+    r.step = t / (per * q.batch);
     t -= r.step * per * q.batch;
-    int64_t before = r.step * per;
+    unsigned before = r.step * per;
     int64_t k = q.m;
     if (t < 2 * gram * q.batch) {
         r.product = t < gram * q.batch ? kGram : kQuadratic;
         if (r.product == kGram) k = q.rows + q.cols - q.m;
         else t -= gram * q.batch, before += gram;
-        r.matrix = (int)(t / gram);
-        const int idx = (int)(t - r.matrix * gram);
-        int i = (int)((sqrtf(8.f * (float)idx + 1.f) - 1.f) * 0.5f);   // row i of the triangle starts at i (i + 1) / 2
-        while ((int64_t)i * (i + 1) / 2 > idx) --i;
-        while ((int64_t)(i + 1) * (i + 2) / 2 <= idx) ++i;
+        r.matrix = t / gram;
+        const unsigned idx = t - r.matrix * gram;
+        unsigned i = (unsigned)((sqrtf(8.f * (float)idx + 1.f) - 1.f) * 0.5f);   // row i of the triangle starts at i (i + 1) / 2
+        while (i * (i + 1) / 2 > idx) --i;
+        while ((i + 1) * (i + 2) / 2 <= idx) ++i;
         r.m0 = (int64_t)i * S::kTile;
         r.n0 = (int64_t)(idx - i * (i + 1) / 2) * S::kTile;
     } else {
         r.product = kUpdate;
         t -= 2 * gram * q.batch, before += 2 * gram;
-        r.matrix = (int)(t / update);
-        const int idx = (int)(t - r.matrix * update);
+        r.matrix = t / update;
+        const unsigned idx = t - r.matrix * update;
         r.m0 = (int64_t)(idx / q.tiles_n) * S::kTile;
         r.n0 = (int64_t)(idx % q.tiles_n) * S::kTile;
     }
     r.k_steps = (int)((k + kStep - 1) / kStep);
-    r.needs = (unsigned)(before * (kEpilogueWarps * S::CTAS));
+    r.needs = before * S::CTAS;
     return r;
 }
 
@@ -296,6 +306,32 @@ __device__ __forceinline__ bool wait_done(const unsigned* done, unsigned needs, 
     return true;
 }
 
+// Counters in shared memory, one writer each.
+__device__ __forceinline__ bool wait_count(const int* count, int least, volatile int* gave_up)
+{
+    const auto reached = [&] {
+        int v;
+        asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(v) : "r"(tc::smem_addr(count)) : "memory");
+        return v >= least;
+    };
+    if (reached()) return true;
+    const uint64_t start = tc::now_ns();
+    while (!reached()) {
+        if (*gave_up) return false;
+        if (tc::now_ns() - start > tc::kWaitLimitNs) {
+            *gave_up = 1;
+            return false;
+        }
+        __nanosleep(40);   // the issue slots are the epilogue's
+    }
+    return true;
+}
+
+__device__ __forceinline__ void set_count(int* count, int v)
+{
+    asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(tc::smem_addr(count)), "r"(v) : "memory");
+}
+
 __device__ __forceinline__ void unpack8(const uint4& p, float (&v)[8])
 {
     const uint32_t w[4] = {p.x, p.y, p.z, p.w};
@@ -315,7 +351,8 @@ __device__ __forceinline__ void unpack8(const uint4& p, float (&v)[8])
 //   kQuadratic  D = cc sum + cb C + diagonal I
 //   kUpdate     D = s (sum + beta (C + C's low part))
 template <Product F>
-__device__ __forceinline__ void finish(const Steps& q, const Tile& tile, const Part& part, float* mine, uint32_t rank, volatile int* gave_up)
+__device__ __forceinline__ bool finish(const Steps& q, const Tile& tile, const Part& part, float* mine, uint32_t rank, int* stored,
+                                       int tiles, volatile int* gave_up)
 {
     const int lane = threadIdx.x & 31, r0 = lane >> 2, p = lane & 3;
     const int64_t height = F == kUpdate ? q.rows : q.m, width = F == kUpdate ? q.cols : q.m, ld = F == kUpdate ? q.ld : q.ldm;
@@ -334,7 +371,7 @@ __device__ __forceinline__ void finish(const Steps& q, const Tile& tile, const P
         high = q.a + at;
         d = q.b + at;
     } else {
-        high = q.x[tile.step & 1] + at, low = q.x_low[tile.step & 1] + at;
+        high = q.x[tile.step & 1] + at, low = tile.step || q.low_in ? q.x_low[tile.step & 1] + at : nullptr;
         d = q.x[(tile.step + 1) & 1] + at, d_low = q.x_low[(tile.step + 1) & 1] + at;
     }
     const float beta = F == kUpdate ? q.ca - diagonal : q.cb;
@@ -349,15 +386,11 @@ __device__ __forceinline__ void finish(const Steps& q, const Tile& tile, const P
         for (int i = 0; i < 4; ++i) {
             const bool has = in && r0 + 8 * i < rows;
             if (F != kGram) h[i] = has ? __ldcg(reinterpret_cast<const uint4*>(high + i * 8 * ld + c)) : make_uint4(0, 0, 0, 0);
-            if (F == kUpdate) l[i] = has ? __ldcg(reinterpret_cast<const uint4*>(low + i * 8 * ld + c)) : make_uint4(0, 0, 0, 0);
+            if (F == kUpdate) l[i] = has && low ? __ldcg(reinterpret_cast<const uint4*>(low + i * 8 * ld + c)) : make_uint4(0, 0, 0, 0);
         }
     };
-    if (F != kGram) {
-        // the products' operands were waited for by the copies; what this warp reads itself, it waits for itself
-        if (!wait_done(q.done + tile.matrix, tile.needs, gave_up)) return;
-        fetch(part.c0);
-    }
-    if (!tc::bar_wait(part.full, part.phase, gave_up)) return;
+    if (F != kGram) fetch(part.c0);
+    if (!tc::bar_wait_warp(part.full, part.phase, gave_up)) return false;
     tc::fence_after();
     for (int c = part.c0; c < part.c1; c += kChunk) {
         uint32_t v[32];
@@ -443,12 +476,42 @@ __device__ __forceinline__ void finish(const Steps& q, const Tile& tile, const P
             __syncwarp();
         }
     }
-    // every lane's stores, for copies and loads of other SMs, before the count
-    tc::fence_async();
+    // this warp's stores, for the warp that tells the other SMs of them
     __syncwarp();
-    if (lane == 0) {
-        __threadfence();
-        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(q.done + tile.matrix) : "memory");
+    if (lane == 0) set_count(stored, tiles);
+    return true;
+}
+
+// What the epilogue reads of C, asked for while the tile's products still run:
+// one warp goes a tile ahead, waits for the matrix and has the low parts of X
+// brought to L2 (the high parts come with the products' operands).
+struct Counts {
+    int ahead;   // tiles whose C may be read
+    int taken;   // tiles the epilogue has begun
+    int stored[kEpilogueWarps];   // tiles each of its warps has stored
+};
+
+template <class S>
+__device__ __forceinline__ void scout(const Steps& q, const Block& b, Counts* s, unsigned first, unsigned total, unsigned step)
+{
+    const int lane = threadIdx.x & 31;
+    int n = 0;
+    for (unsigned t = first; t < total; t += step, ++n) {
+        const Tile tile = tile_at<S>(q, t);
+        if (!__all_sync(0xffffffffu, wait_count(&s->taken, n - 1, b.gave_up))) return;
+        if (tile.product != kGram) {
+            if (!__all_sync(0xffffffffu, wait_done(q.done + tile.matrix, tile.needs, b.gave_up))) return;
+        }
+        if (lane == 0) set_count(&s->ahead, n + 1);
+        if (tile.product == kUpdate && (tile.step || q.low_in)) {
+            const int64_t width = q.ld - tile.n0 < S::kTile ? q.ld - tile.n0 : S::kTile;
+            for (int r = lane; r < kRows; r += 32) {
+                const int64_t m = tile.m0 + b.rank * kRows + r;
+                if (m < q.rows)
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
+                                 ::"l"(q.x_low[tile.step & 1] + tile.matrix * q.rows * q.ld + m * q.ld + tile.n0), "r"((int)width * 2) : "memory");
+            }
+        }
     }
 }
 
@@ -458,14 +521,19 @@ __global__ void __launch_bounds__(kThreads, 1) newton_schulz(const __grid_consta
     extern __shared__ __align__(1024) unsigned char dynamic[];
     Block b = block_of(dynamic);
     const int warp = threadIdx.x >> 5;
+    Counts* const counts = reinterpret_cast<Counts*>(b.own + kEpilogueWarps * kStaging);
+    if (threadIdx.x == 0) {
+        counts->ahead = counts->taken = 0;
+        for (int i = 0; i < kEpilogueWarps; ++i) counts->stored[i] = 0;
+    }
     open<S>(b);
-    const int64_t total = (int64_t)q.steps * q.batch * ((int64_t)q.side * (q.side + 1) + (int64_t)q.tiles_m * q.tiles_n);
-    const int64_t first = blockIdx.x / S::CTAS, step = gridDim.x / S::CTAS;
+    const unsigned total = q.steps * q.batch * (q.side * (q.side + 1) + q.tiles_m * q.tiles_n);
+    const unsigned first = blockIdx.x / S::CTAS, step = gridDim.x / S::CTAS;
 
     if (warp == 0 && tc::elect_one()) {
         uint32_t n = 0;
         bool ok = true;
-        for (int64_t t = first; ok && t < total; t += step) {
+        for (unsigned t = first; ok && t < total; t += step) {
             const Tile tile = tile_at<S>(q, t);
             const int m = (int)tile.m0 + (int)b.rank * kRows, nn = (int)tile.n0 + (int)b.rank * kRows, z = tile.matrix;
             ok = wait_done(q.done + tile.matrix, tile.needs, b.gave_up);
@@ -485,25 +553,48 @@ __global__ void __launch_bounds__(kThreads, 1) newton_schulz(const __grid_consta
         finish_copies(b, n, ok);
     } else if (warp == 1 && b.rank == 0 && tc::elect_one()) {
         uint32_t n = 0, made = 0;
-        for (int64_t t = first; t < total; t += step) {
+        for (unsigned t = first; t < total; t += step) {
             const Tile tile = tile_at<S>(q, t);
             const bool a_mn = tile.product == kGram && q.tall, b_mn = tile.product == kGram ? q.tall : tile.product == kUpdate && !q.tall;
             if (!multiply<S>(b, made++, n, tile.k_steps, tc::instruction(false, a_mn, b_mn, S::kTile, S::kTile), a_mn, b_mn)) break;
             n += tile.k_steps;
         }
+    } else if (warp == 2) {
+        // a tile's stores, once all its warps have made them, are ordered before the matrix's count by one
+        // thread: each warp waiting for its own to reach L2 would hold the epilogue up
+        const int lane = threadIdx.x & 31;
+        int made = 0;
+        for (unsigned t = first; t < total; t += step) {
+            const Tile tile = tile_at<S>(q, t);
+            ++made;
+            if (!__all_sync(0xffffffffu, wait_count(&counts->stored[lane % kEpilogueWarps], made, b.gave_up))) break;
+            if (lane == 0) {
+                __threadfence();
+                asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(q.done + tile.matrix) : "memory");
+            }
+        }
+    } else if (warp == 3) {
+        scout<S>(q, b, counts, first, total, step);
     } else if (warp >= 4) {
-        uint32_t made = 0;
+        int made = 0;
+        int* const stored = &counts->stored[warp - 4];
         float* const mine = reinterpret_cast<float*>(b.own + (warp - 4) * kStaging);
-        for (int64_t t = first; t < total && !*b.gave_up; t += step) {
+        for (unsigned t = first; t < total; t += step) {
             const Tile tile = tile_at<S>(q, t);
             const Part part = part_of<S>(b, made++);
-            if (tile.product == kGram) finish<kGram>(q, tile, part, mine, b.rank, b.gave_up);
-            else if (tile.product == kQuadratic) finish<kQuadratic>(q, tile, part, mine, b.rank, b.gave_up);
-            else finish<kUpdate>(q, tile, part, mine, b.rank, b.gave_up);
+            if (threadIdx.x == 4 * 32) set_count(&counts->taken, made);
+            if (!__all_sync(0xffffffffu, wait_count(&counts->ahead, made, b.gave_up))) break;
+            const bool ok = tile.product == kGram        ? finish<kGram>(q, tile, part, mine, b.rank, stored, made, b.gave_up)
+                            : tile.product == kQuadratic ? finish<kQuadratic>(q, tile, part, mine, b.rank, stored, made, b.gave_up)
+                                                         : finish<kUpdate>(q, tile, part, mine, b.rank, stored, made, b.gave_up);
+            if (!ok) break;
         }
     }
     close<S>(b, q.status);
 }
+
+// Tiles of a matrix a step.
+__host__ __device__ inline int64_t steps_tiles(const Steps& q) { return (int64_t)q.side * (q.side + 1) + (int64_t)q.tiles_m * q.tiles_n; }
 
 template <class S>
 int launch_steps(Steps& q, cudaStream_t st)
@@ -511,9 +602,11 @@ int launch_steps(Steps& q, cudaStream_t st)
     const Device dev = device();
     q.status = dense_status_word();
     if (!dev.sms || !q.status) return EMB_ERR_CUDA;
-    q.side = (int)((q.m + S::kTile - 1) / S::kTile);
-    q.tiles_m = (int)((q.rows + S::kTile - 1) / S::kTile);
-    q.tiles_n = (int)((q.cols + S::kTile - 1) / S::kTile);
+    q.side = (unsigned)((q.m + S::kTile - 1) / S::kTile);
+    q.tiles_m = (unsigned)((q.rows + S::kTile - 1) / S::kTile);
+    q.tiles_n = (unsigned)((q.cols + S::kTile - 1) / S::kTile);
+    const int64_t tiles = (int64_t)steps_tiles(q) * q.batch * q.steps;
+    if (tiles > INT_MAX) return EMB_ERR_INVALID_ARG;
     auto* const kernel = newton_schulz<S>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(S::CTAS);
@@ -810,7 +903,7 @@ extern "C" int emb_orthogonalize(const void* update, int32_t dtype, int64_t batc
     Steps q;
     q.tall = rows > cols;
     q.rows = rows, q.cols = cols, q.ld = l.ld, q.ldm = l.ldm, q.m = l.m;
-    q.batch = (int)batch, q.steps = steps;
+    q.batch = (unsigned)batch, q.steps = steps, q.low_in = dtype == EMB_F32;
     q.ca = a, q.cb = b, q.cc = c;
     for (int i = 0; i < 2; ++i) {
         q.x[i] = reinterpret_cast<__half*>(ws + l.x[i]);

@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_products(const __grid_cons
 #pragma unroll
                 for (int i = 0; i < kStages; ++i)
                     if (i == (int)s) turn = turns[i]++;
-                ok = tc::bar_wait(tc::smem_addr(&b.ring->part[s]), turn & 1, b.gave_up);
+                ok = tc::bar_wait_warp(tc::smem_addr(&b.ring->part[s]), turn & 1, b.gave_up);
                 if (ok) {
                     const uint4 zero = make_uint4(0, 0, 0, 0);
                     for (int j = 0; j < 2; ++j)
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_products(const __grid_cons
                     if (b.rank) {
                         if (lane == 0) tc::bar_arrive(tc::in_cta(tc::smem_addr(&b.ring->peer_part[s]), 0));
                     } else {
-                        if (S::CTAS == 2) ok = tc::bar_wait(tc::smem_addr(&b.ring->peer_part[s]), turn & 1, b.gave_up);
+                        if (S::CTAS == 2) ok = tc::bar_wait_warp(tc::smem_addr(&b.ring->peer_part[s]), turn & 1, b.gave_up);
                         if (ok && lane == 0) tc::bar_arrive(tc::smem_addr(&b.ring->full[s]));
                     }
                 }
@@ -224,12 +224,12 @@ __global__ void __launch_bounds__(kThreads, 1) expert_products(const __grid_cons
     } else if (warp >= 4) {
         uint32_t made = 0;
         unsigned char* const mine = staging + (warp - 4) * kStaging;
-        for (int64_t t = first; t < total && !*b.gave_up; t += step) {
+        for (int64_t t = first; t < total; t += step) {
             const Tile tile = list.at(t);
             const Part part = part_of<S>(b, made);
             if (tile.steps) {
                 ++made;
-                if (!tc::bar_wait(part.full, part.phase, b.gave_up)) break;
+                if (!tc::bar_wait_warp(part.full, part.phase, b.gave_up)) break;
                 tc::fence_after();
             }
             const int64_t m = tile.m0 + b.rank * kRows + part.row, left = tile.m_end - m;

@@ -92,6 +92,12 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     return true;
 }
 
+// The same by a whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity, volatile int* gave_up)
+{
+    return __all_sync(0xffffffffu, bar_wait(bar, parity, gave_up));
+}
+
 // ---------------------------------------------------------------------------
 // copies: a box of a 3-d tensor to shared memory; coordinates from the
 // innermost dimension.  With 2 CTAs the barrier may be the pair's other one's.
