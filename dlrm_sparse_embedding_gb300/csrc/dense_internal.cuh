@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "emb.h"
+#include "launch.cuh"
 
 namespace emb {
 

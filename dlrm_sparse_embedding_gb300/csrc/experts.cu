@@ -52,6 +52,8 @@ __global__ void __launch_bounds__(kPlaceThreads) expert_count(const ID* __restri
                                                               int* __restrict__ counts)
 {
     extern __shared__ int cnt[];
+    let_next_begin();
+    wait_for_earlier();
     for (int e = threadIdx.x; e <= E; e += kPlaceThreads) cnt[e] = 0;
     __syncthreads();
     const int lo = blockIdx.x * chunk, hi = min((int64_t)P, (int64_t)lo + chunk);
@@ -104,6 +106,8 @@ __global__ void __launch_bounds__(kPlaceThreads) expert_place(const ID* __restri
     const int lo = blockIdx.x * chunk, hi = min((int64_t)P, (int64_t)lo + chunk);
 
     for (int i = t; i < (E + 1) * kPlaceWarps; i += kPlaceThreads) of_warp[i] = 0;
+    let_next_begin();
+    wait_for_earlier();
     // the first row of every bucket, and of this chunk's part of it
     if (counts) {
         for (int e = w; e <= E; e += kPlaceWarps) {   // a warp adds up a bucket's chunks
@@ -220,6 +224,8 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_rows(emb_expert_plan pla
                                                              R* __restrict__ rows)
 {
     const int lane = threadIdx.x & 31, P = (int)(plan.tokens * plan.k);
+    let_next_begin();
+    wait_for_earlier();
     const int64_t warps = (int64_t)gridDim.x * (kRowThreads / 32);
     const int64_t first = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
     for (int64_t u = first; u < plan.tokens * pieces; u += warps) {
@@ -256,6 +262,8 @@ __global__ void __launch_bounds__(kRowThreads) gather_sum(emb_expert_plan plan, 
 {
     constexpr int U = kInFlight / ROWS;
     const int lane = threadIdx.x & 31, P = (int)(plan.tokens * plan.k);
+    let_next_begin();
+    wait_for_earlier();
     const int64_t warps = (int64_t)gridDim.x * (kRowThreads / 32);
     const int64_t first = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
     for (int64_t u = first; u < plan.tokens * pieces; u += warps) {
@@ -306,6 +314,8 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad(emb_expert_plan plan
     const int P = (int)(plan.tokens * plan.k), lane = threadIdx.x & 31;
     const int warps_of = blockDim.x / 32, wx = threadIdx.x >> 5, wy = threadIdx.y * warps_of;
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
+    let_next_begin();
+    wait_for_earlier();
     // a block's tokens move on together: every thread meets every barrier
     for (int64_t t0 = (int64_t)blockIdx.x * blockDim.y; t0 < plan.tokens; t0 += step) {
         const int64_t token = t0 + threadIdx.y;
@@ -360,8 +370,6 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad(emb_expert_plan plan
                     (int64_t)blockIdx.x * (kRowThreads / 32) + wy + wx, warps, lane);
 }
 
-int launched() { return cudaGetLastError() == cudaSuccess ? EMB_OK : EMB_ERR_CUDA; }
-
 // Whether rows of `width` elements can be moved 16 bytes at a time.
 bool wide(const void* p, int dtype, int64_t stride, int64_t width)
 {
@@ -402,8 +410,7 @@ int launch_gather_sum(const emb_expert_plan& plan, const void* rows, int rows_dt
             const int64_t pieces = pieces_of(width, w8 ? 8 : 1, kInFlight / at_once);
             const unsigned blocks = row_blocks(plan.tokens * pieces);
             const auto go = [&](auto kernel) {
-                kernel<<<blocks, kRowThreads, 0, st>>>(plan, (const R*)rows, stride, weights, width, pieces, (O*)out);
-                return launched();
+                return launch_next(kernel, blocks, kRowThreads, 0, st, 1, plan, (const R*)rows, stride, weights, width, pieces, (O*)out);
             };
             if (w8)
                 return at_once == 1   ? go(gather_sum<8, R, O, WEIGHTED, 1>)
@@ -496,16 +503,15 @@ extern "C" int emb_expert_sort(const void* ids, int32_t id_bytes, const emb_expe
     const size_t smem = place_smem(E);
     const auto go = [&](auto id) {
         using ID = decltype(id);
-        if (cudaFuncSetAttribute(expert_place<ID>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+        if (smem > 48 * 1024 && cudaFuncSetAttribute(expert_place<ID>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
             cudaGetLastError();
             return (int)EMB_ERR_CUDA;
         }
         if (counts) {
-            expert_count<ID><<<chunks, kPlaceThreads, sizeof(int) * (E + 1), st>>>((const ID*)ids, P, E, chunk, counts);
-            if (int rc = launched()) return rc;
+            if (int rc = launch_next(expert_count<ID>, chunks, kPlaceThreads, sizeof(int) * (E + 1), st, 1, (const ID*)ids, P, E, chunk, counts)) return rc;
         }
-        expert_place<ID><<<chunks, kPlaceThreads, smem, st>>>((const ID*)ids, P, E, chunk, counts, plan->offsets, plan->src, plan->pos, word);
-        return launched();
+        return launch_next(expert_place<ID>, chunks, kPlaceThreads, smem, st, 1, (const ID*)ids, P, E, chunk, (const int*)counts, plan->offsets, plan->src,
+                           plan->pos, word);
     };
     return id_bytes == 4 ? go(int32_t()) : go((long long)0);
 }
@@ -525,11 +531,8 @@ extern "C" int emb_expert_dispatch(const emb_expert_plan* plan, const void* x, i
             using R = decltype(rt);
             const int64_t pieces = pieces_of(width, w8 ? 8 : 1, kUnroll);
             const unsigned blocks = row_blocks(plan->tokens * pieces);
-            if (w8)
-                dispatch_rows<8, X, R><<<blocks, kRowThreads, 0, st>>>(*plan, (const X*)x, x_stride, width, pieces, (R*)rows);
-            else
-                dispatch_rows<1, X, R><<<blocks, kRowThreads, 0, st>>>(*plan, (const X*)x, x_stride, width, pieces, (R*)rows);
-            return launched();
+            return launch_next(w8 ? dispatch_rows<8, X, R> : dispatch_rows<1, X, R>, blocks, kRowThreads, 0, st, 1, *plan, (const X*)x, x_stride,
+                               width, pieces, (R*)rows);
         });
     });
 }
@@ -576,11 +579,8 @@ extern "C" int emb_expert_combine_grad(const emb_expert_plan* plan, const void* 
         return with_type(rows_dtype, [&](auto rt) {
             using O = decltype(ot);
             using R = decltype(rt);
-            if (w8)
-                combine_grad<8, O, R><<<blocks, block, 0, st>>>(*plan, (const O*)grad_out, grad_stride, (const R*)rows, rows_stride, weights, width, (R*)grad_rows, grad_weights);
-            else
-                combine_grad<1, O, R><<<blocks, block, 0, st>>>(*plan, (const O*)grad_out, grad_stride, (const R*)rows, rows_stride, weights, width, (R*)grad_rows, grad_weights);
-            return launched();
+            return launch_next(w8 ? combine_grad<8, O, R> : combine_grad<1, O, R>, blocks, block, 0, st, 1, *plan, (const O*)grad_out, grad_stride,
+                               (const R*)rows, rows_stride, weights, width, (R*)grad_rows, grad_weights);
         });
     });
 }

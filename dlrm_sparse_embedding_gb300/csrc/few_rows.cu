@@ -41,6 +41,8 @@ __global__ void __launch_bounds__(kThreads) few_forward(const T* __restrict__ ro
                                                         int64_t in_width, int64_t out_width, const int32_t* __restrict__ offsets,
                                                         int experts, T* __restrict__ y)
 {
+    let_next_begin();
+    wait_for_earlier();
     const int p = blockIdx.y, lane = threadIdx.x & 31;
     const int64_t n = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int e = expert_of(offsets, experts, p);
@@ -79,8 +81,7 @@ int launch_few_rows(const ProductArgs& p, cudaStream_t st)
     const auto go = [&](auto t) {
         using T = decltype(t);
         const dim3 grid((unsigned)((p.n + kWarps - 1) / kWarps), (unsigned)p.m);
-        few_forward<T><<<grid, kThreads, 0, st>>>((const T*)p.a, p.lda, (const T*)p.b, p.k, p.n, p.offsets, p.experts, (T*)p.d);
-        return cudaGetLastError() == cudaSuccess ? EMB_OK : EMB_ERR_CUDA;
+        return launch_next(few_forward<T>, grid, kThreads, 0, st, 1, (const T*)p.a, p.lda, (const T*)p.b, p.k, p.n, p.offsets, p.experts, (T*)p.d);
     };
     return p.dtype == EMB_F16 ? go(__half()) : go(__nv_bfloat16());
 }

@@ -140,6 +140,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_partials(const T* __restric
                                                               int64_t rows, int64_t cols, double* __restrict__ partial)
 {
     __shared__ double warp_sums[kNormThreads / 32];
+    let_next_begin();
+    wait_for_earlier();
     const T* const mine = g + blockIdx.y * batch_stride;
     float s = 0.f, top = 0.f;
     each_piece<V, T>(mine, row_stride, rows, cols, [&](int64_t, int64_t, const float (&v)[V]) {
@@ -171,6 +173,8 @@ __global__ void __launch_bounds__(kNormThreads) scale_in(const T* __restrict__ g
 {
     __shared__ double warp_sums[kNormThreads / 32];
     static_assert(kMaxNormBlocks <= kNormThreads, "one partial sum a thread");
+    let_next_begin();
+    wait_for_earlier();
     const double sum = block_sum(threadIdx.x < norm_blocks ? partial[(int64_t)blockIdx.y * norm_blocks + threadIdx.x] : 0.0, warp_sums);
     const double norm = sqrt(sum);
     int e = 0;
@@ -203,11 +207,10 @@ int start(const T* g, int64_t bs, int64_t rs, int64_t batch, int64_t rows, int64
 {
     const dim3 grid(l.norm_blocks, (unsigned)batch);
     double* const partial = reinterpret_cast<double*>(ws + l.partial);
-    norm_partials<V, T><<<grid, kNormThreads, 0, st>>>(g, bs, rs, rows, cols, partial);
-    scale_in<V, T><<<grid, kNormThreads, 0, st>>>(g, bs, rs, rows, cols, l.norm_blocks, partial, eps, l.ld,
-                                                  reinterpret_cast<__half*>(ws + l.x[0]), reinterpret_cast<__half*>(ws + l.x_low[0]),
-                                                  reinterpret_cast<float*>(ws + l.scale), reinterpret_cast<unsigned*>(ws + l.done));
-    return cudaGetLastError() == cudaSuccess ? EMB_OK : EMB_ERR_CUDA;
+    if (int rc = launch_next(norm_partials<V, T>, grid, kNormThreads, 0, st, 1, g, bs, rs, rows, cols, partial)) return rc;
+    return launch_next(scale_in<V, T>, grid, kNormThreads, 0, st, 1, g, bs, rs, rows, cols, l.norm_blocks, (const double*)partial, eps, l.ld,
+                       reinterpret_cast<__half*>(ws + l.x[0]), reinterpret_cast<__half*>(ws + l.x_low[0]),
+                       reinterpret_cast<float*>(ws + l.scale), reinterpret_cast<unsigned*>(ws + l.done));
 }
 
 // ---------------------------------------------------------------------------

@@ -161,8 +161,11 @@ __global__ void __launch_bounds__(kThreads, 1) expert_products(const __grid_cons
         tc::prefetch_map(&q.a);
         tc::prefetch_map(&q.b);
     }
-    make_tables<S>(q, start, rows);
     open<S>(b);
+    let_next_begin();
+    wait_for_earlier();
+    make_tables<S>(q, start, rows);
+    __syncthreads();
 
     const List<S, K_GROUPED> list{q, start, rows};
     const int64_t total = list.total(), first = blockIdx.x / S::CTAS, step = gridDim.x / S::CTAS;
@@ -268,21 +271,7 @@ int launch(Problems& q, cudaStream_t st)
         }
         sized[dev.number].store(true, std::memory_order_relaxed);
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {(unsigned)S::CTAS, 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, q) != cudaSuccess) {
-        cudaGetLastError();
-        return EMB_ERR_CUDA;
-    }
-    return EMB_OK;
+    return launch_next(kernel, blocks, kThreads, kSmem, st, S::CTAS, q);
 }
 
 template <class S>
