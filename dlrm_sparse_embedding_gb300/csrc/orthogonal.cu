@@ -21,11 +21,7 @@
 // smaller size.  (In earlier steps the shift would let the dropped low part of
 // X back into the small directions.)
 //
-// Matrices whose short side m is at most kSmall go another way, in fp32: there a
-// rounding has few others to average with (a 1 x 1 matrix would be 5e-3 off), and
-// the work is small.  All steps are polynomials of A0 = X0 X0^T, so
-//   Q = a I + b A + c A A,  A <- Q A Q,  W <- Q W,  at the end  W X0
-// needs the long side only at both ends.
+// Matrices whose short side is at most 128 go another way (orthogonal_short.cu).
 //
 // G is scaled by a power of two before it is rounded, exact for bf16, and the
 // rest of the norm goes into the first step's factors.
@@ -33,16 +29,12 @@
 #include <climits>
 #include <type_traits>
 
-#include "product_core.cuh"
+#include "orthogonal.cuh"
 
 namespace emb {
 namespace {
 
 using namespace core;
-
-// A number is held as fp16 h plus fp16 l / kLowScale: l is h's rounding error,
-// at most 2^-11 |h|, scaled up so that it is not lost where h is subnormal.
-constexpr float kLowScale = 2048.f;
 
 constexpr int kNormThreads = 256;
 constexpr int kMaxNormBlocks = 256;   // per matrix
@@ -61,7 +53,7 @@ Layout layout_of(int64_t batch, int64_t rows, int64_t cols)
     l.ld = (cols + 7) / 8 * 8;
     l.ldm = (l.m + 7) / 8 * 8;
     l.x_elems = rows * l.ld;
-    l.a_elems = l.m * l.ldm;
+    l.a_elems = l.m <= kShort ? kShort * kShort : l.m * l.ldm;   // W's two parts, for short sides
     l.norm_blocks = (int)std::min<int64_t>(kMaxNormBlocks, (rows * cols + 8 * kNormThreads - 1) / (8 * kNormThreads));
     size_t at = 0;
     const auto take = [&](size_t bytes) {
@@ -335,16 +327,6 @@ __device__ __forceinline__ void set_count(int* count, int v)
     asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(tc::smem_addr(count)), "r"(v) : "memory");
 }
 
-__device__ __forceinline__ void unpack8(const uint4& p, float (&v)[8])
-{
-    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        v[2 * i] = f.x, v[2 * i + 1] = f.y;
-    }
-}
-
 // An epilogue warp's columns of a tile.  Through shared memory (a lane has one
 // row's 32 columns of the accumulator) a lane gets four pieces of eight columns,
 // in rows r0 + 8 i, which meet C there and leave again.  C for the next columns
@@ -453,14 +435,13 @@ __device__ __forceinline__ bool finish(const Steps& q, const Tile& tile, const P
                 }
                 continue;
             }
-            const uint4 packed = pack8<__half>(o);
-            *reinterpret_cast<uint4*>(d + i * 8 * ld + c) = packed;
             if (F == kUpdate) {
-                float back[8];
-                unpack8(packed, back);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) back[j] = kLowScale * (o[j] - back[j]);
-                *reinterpret_cast<uint4*>(d_low + i * 8 * ld + c) = pack8<__half>(back);
+                uint4 top, rest;
+                split8(o, top, rest);
+                *reinterpret_cast<uint4*>(d + i * 8 * ld + c) = top;
+                *reinterpret_cast<uint4*>(d_low + i * 8 * ld + c) = rest;
+            } else {
+                *reinterpret_cast<uint4*>(d + i * 8 * ld + c) = pack8<__half>(o);
             }
         }
         __syncwarp();
@@ -661,202 +642,6 @@ int run_steps(Steps& q, cudaStream_t st)
     return 2 * rounds(q, 256, dev.sms / 2) <= rounds(q, 128, dev.sms) * 5 / 4 ? launch_steps<Shape<2>>(q, st) : launch_steps<Shape<1>>(q, st);
 }
 
-// ---------------------------------------------------------------------------
-// short sides up to kSmall
-// ---------------------------------------------------------------------------
-constexpr int kSmall = 64;
-constexpr int kSmallPitch = kSmall + 1;
-constexpr int kSlice = 64;            // columns of the long side staged at once
-constexpr int kSmallThreads = 256;
-constexpr int kMaxGramBlocks = 64;    // per matrix
-
-// Element (i, j) of the matrix with the short side first.
-template <class T>
-__device__ __forceinline__ float element(const T* g, int64_t row_stride, bool tall, int64_t i, int64_t j)
-{
-    return to_float<T>(tall ? g[j * row_stride + i] : g[i * row_stride + j]);
-}
-
-// Stage columns [j0, j0 + kSlice) of the long side, in a layout both later
-// kernels read without conflicts; zeros outside the matrix.
-template <class T>
-__device__ __forceinline__ void stage(float (*s)[kSlice + 1], const T* g, int64_t row_stride, bool tall, int m, int64_t n, int64_t j0, float up)
-{
-    for (int q = threadIdx.x; q < kSmall * kSlice; q += kSmallThreads) {
-        const int i = tall ? q % kSmall : q / kSlice, j = tall ? q / kSmall : q % kSlice;
-        s[i][j] = i < m && j0 + j < n ? up * element<T>(g, row_stride, tall, i, j0 + j) : 0.f;
-    }
-    __syncthreads();
-}
-
-// One power of two for every matrix brings its largest entry near 1, so that
-// no square under- or overflows.
-template <class T>
-__global__ void __launch_bounds__(kSmallThreads) small_largest(const T* __restrict__ g, int64_t batch_stride, int64_t row_stride,
-                                                               int64_t rows, int64_t cols, unsigned* __restrict__ largest)
-{
-    const T* const mine = g + blockIdx.y * batch_stride;
-    unsigned top = 0;   // magnitudes of floats order like their bits; NaNs come last
-    for (int64_t i = (int64_t)blockIdx.x * kSmallThreads + threadIdx.x; i < rows * cols; i += (int64_t)gridDim.x * kSmallThreads)
-        top = max(top, __float_as_uint(to_float<T>(mine[i / cols * row_stride + i % cols])) & 0x7fffffffu);
-    top = __reduce_max_sync(0xffffffffu, top);
-    if ((threadIdx.x & 31) == 0) atomicMax(&largest[blockIdx.y], top);
-}
-
-__device__ __forceinline__ int small_exponent(unsigned largest)
-{
-    const float v = __uint_as_float(largest);
-    return v > 0.f && v < INFINITY ? max(-120, min(120, -ilogbf(v))) : 0;
-}
-
-// Partial sums of G G^T (short side m) over a block's columns of the long side.
-template <class T>
-__global__ void __launch_bounds__(kSmallThreads) small_gram(const T* __restrict__ g, int64_t batch_stride, int64_t row_stride, bool tall, int m,
-                                                            int64_t n, const unsigned* __restrict__ largest, float* __restrict__ partial)
-{
-    __shared__ float s[kSmall][kSlice + 1];
-    const float up = ldexpf(1.f, small_exponent(largest[blockIdx.y]));
-    const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
-    float acc[4][4] = {};
-    for (int64_t j0 = (int64_t)blockIdx.x * kSlice; j0 < n; j0 += (int64_t)gridDim.x * kSlice) {
-        stage<T>(s, g + blockIdx.y * batch_stride, row_stride, tall, m, n, j0, up);
-        for (int j = 0; j < kSlice; ++j)
-            for (int p = 0; p < 4; ++p)
-                for (int q = 0; q < 4; ++q) acc[p][q] = __fmaf_rn(s[ti + 16 * p][j], s[tj + 16 * q][j], acc[p][q]);
-        __syncthreads();
-    }
-    float* const to = partial + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kSmall * kSmall;
-    for (int p = 0; p < 4; ++p)
-        for (int q = 0; q < 4; ++q) to[(ti + 16 * p) * kSmall + tj + 16 * q] = acc[p][q];
-}
-
-// d = alpha * x y + beta * z + gamma * I for 64 x 64 matrices of which y is symmetric; d may be any of them.
-__device__ void small_product(float* d, const float* x, const float* y, float alpha, const float* z, float beta, float gamma)
-{
-    const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
-    float acc[4][4] = {};
-    for (int k = 0; k < kSmall; ++k)
-        for (int p = 0; p < 4; ++p)
-            for (int q = 0; q < 4; ++q)
-                acc[p][q] = __fmaf_rn(x[(ti + 16 * p) * kSmallPitch + k], y[(tj + 16 * q) * kSmallPitch + k], acc[p][q]);
-    for (int p = 0; p < 4; ++p)
-        for (int q = 0; q < 4; ++q) {
-            const int i = ti + 16 * p, j = tj + 16 * q;
-            acc[p][q] = alpha * acc[p][q] + (z ? beta * z[i * kSmallPitch + j] : 0.f) + (i == j ? gamma : 0.f);
-        }
-    __syncthreads();
-    for (int p = 0; p < 4; ++p)
-        for (int q = 0; q < 4; ++q) d[(ti + 16 * p) * kSmallPitch + tj + 16 * q] = acc[p][q];
-    __syncthreads();
-}
-
-// W, the product of all steps' Q, with the factor that takes 2^e G to X0.
-__global__ void __launch_bounds__(kSmallThreads) small_steps(const float* __restrict__ partial, int parts, const unsigned* __restrict__ largest,
-                                                             int m, int steps, float a, float b, float c, float eps, float* __restrict__ w_out)
-{
-    extern __shared__ float smem[];
-    float *const A = smem, *const Q = A + kSmall * kSmallPitch, *const W = Q + kSmall * kSmallPitch;
-    __shared__ float scale;
-    for (int i = threadIdx.x; i < kSmall * kSmall; i += kSmallThreads) {
-        float v = 0.f;
-        for (int p = 0; p < parts; ++p) v += partial[((int64_t)blockIdx.x * parts + p) * kSmall * kSmall + i];
-        A[i / kSmall * kSmallPitch + i % kSmall] = v;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {   // |2^e G|_F^2 is A's trace
-        double t = 0;
-        for (int i = 0; i < m; ++i) t += A[i * kSmallPitch + i];
-        scale = (float)(1.0 / (sqrt(t) + (double)eps * ldexp(1.0, small_exponent(largest[blockIdx.x]))));
-    }
-    __syncthreads();
-    const float s = scale;
-    for (int i = threadIdx.x; i < kSmall * kSmallPitch; i += kSmallThreads) A[i] *= s * s;
-    __syncthreads();
-    for (int i = 0; i < steps; ++i) {
-        small_product(Q, A, A, c, A, b, a);
-        if (i == 0) {
-            for (int q = threadIdx.x; q < kSmall * kSmallPitch; q += kSmallThreads) W[q] = s * Q[q];
-            __syncthreads();
-        } else {
-            small_product(W, W, Q, 1.f, nullptr, 0.f, 0.f);
-        }
-        if (i + 1 < steps) {
-            small_product(A, Q, A, 1.f, nullptr, 0.f, 0.f);
-            small_product(A, A, Q, 1.f, nullptr, 0.f, 0.f);
-        }
-    }
-    for (int i = threadIdx.x; i < kSmall * kSmall; i += kSmallThreads)
-        w_out[(int64_t)blockIdx.x * kSmall * kSmall + i] = W[i / kSmall * kSmallPitch + i % kSmall];
-}
-
-template <class T>
-__global__ void __launch_bounds__(kSmallThreads) small_apply(const T* __restrict__ g, int64_t batch_stride, int64_t row_stride, bool tall, int m,
-                                                             int64_t n, const unsigned* __restrict__ largest, const float* __restrict__ w,
-                                                             __nv_bfloat16* __restrict__ out)
-{
-    __shared__ float s[kSmall][kSlice + 1], ws[kSmall][kSmallPitch];
-    const float up = ldexpf(1.f, small_exponent(largest[blockIdx.y]));
-    for (int i = threadIdx.x; i < kSmall * kSmall; i += kSmallThreads) ws[i / kSmall][i % kSmall] = w[(int64_t)blockIdx.y * kSmall * kSmall + i];
-    const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
-    for (int64_t j0 = (int64_t)blockIdx.x * kSlice; j0 < n; j0 += (int64_t)gridDim.x * kSlice) {
-        stage<T>(s, g + blockIdx.y * batch_stride, row_stride, tall, m, n, j0, up);
-        float acc[4][4] = {};
-        for (int k = 0; k < kSmall; ++k)
-            for (int p = 0; p < 4; ++p)
-                for (int q = 0; q < 4; ++q) acc[p][q] = __fmaf_rn(ws[ti + 16 * p][k], s[k][tj + 16 * q], acc[p][q]);
-        __syncthreads();
-        for (int p = 0; p < 4; ++p)
-            for (int q = 0; q < 4; ++q) s[ti + 16 * p][tj + 16 * q] = acc[p][q];
-        __syncthreads();
-        for (int q = threadIdx.x; q < kSmall * kSlice; q += kSmallThreads) {
-            const int i = tall ? q % kSmall : q / kSlice, j = tall ? q / kSmall : q % kSlice;
-            if (i < m && j0 + j < n) out[(int64_t)blockIdx.y * m * n + (tall ? (j0 + j) * m + i : i * n + j0 + j)] = __float2bfloat16_rn(s[i][j]);
-        }
-        __syncthreads();
-    }
-}
-
-struct SmallLayout {
-    int blocks;
-    size_t largest, partial, w, total;
-};
-
-SmallLayout small_layout_of(int64_t batch, int64_t rows, int64_t cols)
-{
-    SmallLayout l;
-    l.blocks = (int)std::min<int64_t>(kMaxGramBlocks, (std::max(rows, cols) + kSlice - 1) / kSlice);
-    l.largest = 0;
-    l.partial = (sizeof(unsigned) * batch + 255) & ~size_t(255);
-    l.w = l.partial + sizeof(float) * (size_t)batch * l.blocks * kSmall * kSmall;
-    l.total = l.w + sizeof(float) * (size_t)batch * kSmall * kSmall;
-    return l;
-}
-
-template <class T>
-int small(const void* update, int64_t bs, int64_t rs, int64_t batch, int64_t rows, int64_t cols, int steps, float a, float b, float c,
-          float eps, void* out, char* ws, cudaStream_t st)
-{
-    const SmallLayout l = small_layout_of(batch, rows, cols);
-    const bool tall = rows > cols;
-    const int m = (int)std::min(rows, cols);
-    const int64_t n = std::max(rows, cols);
-    const T* const g = static_cast<const T*>(update);
-    unsigned* const largest = reinterpret_cast<unsigned*>(ws + l.largest);
-    float *const partial = reinterpret_cast<float*>(ws + l.partial), *const w = reinterpret_cast<float*>(ws + l.w);
-    const int smem = 3 * kSmall * kSmallPitch * (int)sizeof(float);
-    const dim3 grid(l.blocks, (unsigned)batch);
-    if (cudaMemsetAsync(largest, 0, sizeof(unsigned) * batch, st) != cudaSuccess ||
-        cudaFuncSetAttribute(small_steps, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
-        cudaGetLastError();
-        return EMB_ERR_CUDA;
-    }
-    small_largest<T><<<grid, kSmallThreads, 0, st>>>(g, bs, rs, rows, cols, largest);
-    small_gram<T><<<grid, kSmallThreads, 0, st>>>(g, bs, rs, tall, m, n, largest, partial);
-    small_steps<<<(unsigned)batch, kSmallThreads, smem, st>>>(partial, l.blocks, largest, m, steps, a, b, c, eps, w);
-    small_apply<T><<<grid, kSmallThreads, 0, st>>>(g, bs, rs, tall, m, n, largest, w, static_cast<__nv_bfloat16*>(out));
-    return cudaGetLastError() == cudaSuccess ? EMB_OK : EMB_ERR_CUDA;
-}
-
 bool sizes_valid(int64_t batch, int64_t rows, int64_t cols)
 {
     return batch >= 0 && batch <= 65535 && rows >= 1 && cols >= 1 && rows <= 65536 && cols <= 65536;
@@ -870,8 +655,7 @@ using namespace emb;
 extern "C" int emb_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols, size_t* bytes)
 {
     if (!bytes || !sizes_valid(batch, rows, cols)) return EMB_ERR_INVALID_ARG;
-    const size_t need = std::min(rows, cols) <= kSmall ? small_layout_of(batch, rows, cols).total : layout_of(batch, rows, cols).total;
-    *bytes = std::max<size_t>(256, (need + 255) & ~size_t(255));
+    *bytes = std::max<size_t>(256, layout_of(batch, rows, cols).total);
     return EMB_OK;
 }
 
@@ -887,12 +671,6 @@ extern "C" int emb_orthogonalize(const void* update, int32_t dtype, int64_t batc
     if (!update || !out || !workspace || !aligned_to(workspace, 256) || workspace_bytes < need) return EMB_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     char* const ws = static_cast<char*>(workspace);
-    if (std::min(rows, cols) <= kSmall) {
-        const auto go = [&](auto t) {
-            return small<decltype(t)>(update, batch_stride, row_stride, batch, rows, cols, steps, a, b, c, eps, out, ws, st);
-        };
-        return dtype == EMB_F32 ? go(float()) : dtype == EMB_F16 ? go(__half()) : go(__nv_bfloat16());
-    }
     const Layout l = layout_of(batch, rows, cols);
     const bool wide = cols % 8 == 0 && row_stride % 8 == 0 && batch_stride % 8 == 0 && aligned_to(update, 16);
     const auto begin = [&](auto t) {
@@ -903,19 +681,29 @@ extern "C" int emb_orthogonalize(const void* update, int32_t dtype, int64_t batc
     };
     int rc = dtype == EMB_F32 ? begin(float()) : dtype == EMB_F16 ? begin(__half()) : begin(__nv_bfloat16());
     if (rc != EMB_OK) return rc;
+    StepsArgs p;
+    for (int i = 0; i < 2; ++i) {
+        p.x[i] = reinterpret_cast<__half*>(ws + l.x[i]);
+        p.x_low[i] = reinterpret_cast<__half*>(ws + l.x_low[i]);
+    }
+    p.low_in = dtype == EMB_F32;
+    p.scale = reinterpret_cast<const float*>(ws + l.scale);
+    p.batch = batch, p.rows = rows, p.cols = cols, p.ld = l.ld;
+    p.steps = steps;
+    p.a = a, p.b = b, p.c = c;
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.w = reinterpret_cast<__half*>(ws + l.a);
+    p.w_low = reinterpret_cast<__half*>(ws + l.b);
+    if (l.m <= kShort) return run_short(p, st);
     Steps q;
     q.tall = rows > cols;
     q.rows = rows, q.cols = cols, q.ld = l.ld, q.ldm = l.ldm, q.m = l.m;
-    q.batch = (unsigned)batch, q.steps = steps, q.low_in = dtype == EMB_F32;
+    q.batch = (unsigned)batch, q.steps = steps, q.low_in = p.low_in;
     q.ca = a, q.cb = b, q.cc = c;
-    for (int i = 0; i < 2; ++i) {
-        q.x[i] = reinterpret_cast<__half*>(ws + l.x[i]);
-        q.x_low[i] = reinterpret_cast<__half*>(ws + l.x_low[i]);
-    }
-    q.a = reinterpret_cast<__half*>(ws + l.a);
-    q.b = reinterpret_cast<__half*>(ws + l.b);
-    q.out = static_cast<__nv_bfloat16*>(out);
-    q.scale = reinterpret_cast<const float*>(ws + l.scale);
+    for (int i = 0; i < 2; ++i) q.x[i] = p.x[i], q.x_low[i] = p.x_low[i];
+    q.a = p.w, q.b = p.w_low;
+    q.out = p.out;
+    q.scale = p.scale;
     q.done = reinterpret_cast<unsigned*>(ws + l.done);
     // A's products run along the long side: X is k-major in them where its rows are long, and in the update where not
     for (int i = 0; i < 2; ++i)
