@@ -38,6 +38,8 @@ using namespace core;
 
 constexpr int kNormThreads = 256;
 constexpr int kMaxNormBlocks = 256;   // per matrix
+constexpr int kOneBlockThreads = 1024;
+constexpr int64_t kOneBlock = 8 * 8 * kOneBlockThreads;   // elements that one block reads twice sooner than two launches pass
 constexpr float kRange = 256.f;       // the scaled norm is in [kRange, 2 kRange)
 
 struct Layout {
@@ -72,15 +74,20 @@ Layout layout_of(int64_t batch, int64_t rows, int64_t cols)
     return l;
 }
 
-__device__ __forceinline__ double block_sum(double v, double* warp_sums)
+// Sums: double is slow here, so only one number a warp is added up in it.
+__device__ __forceinline__ double warp_sum(double v)
 {
 #pragma unroll
     for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    if ((threadIdx.x & 31) == 0) warp_sums[threadIdx.x >> 5] = v;
+    return v;
+}
+
+// The sum of the warps' numbers (in their lane 0), in warp 0's lanes; room for one a warp.
+__device__ __forceinline__ double block_sum(double of_warp, double* room)
+{
+    if ((threadIdx.x & 31) == 0) room[threadIdx.x >> 5] = of_warp;
     __syncthreads();
-    double s = 0;
-    for (int w = 0; w < kNormThreads / 32; ++w) s += warp_sums[w];
-    return s;
+    return threadIdx.x < 32 ? warp_sum(threadIdx.x < blockDim.x / 32 ? room[threadIdx.x] : 0.0) : 0.0;
 }
 
 // Calls f(row, first column, the V values there) for the elements of a matrix
@@ -89,10 +96,9 @@ __device__ __forceinline__ double block_sum(double v, double* warp_sums)
 template <int V, class T, class F>
 __device__ __forceinline__ void each_piece(const T* g, int64_t row_stride, int64_t rows, int64_t cols, F f)
 {
-    constexpr int kWarps = kNormThreads / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t pieces = (cols + 32 * V - 1) / (32 * V), step = (int64_t)gridDim.x * kWarps;
-    int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
+    const int64_t pieces = (cols + 32 * V - 1) / (32 * V), step = (int64_t)gridDim.x * warps;
+    int64_t u = (int64_t)blockIdx.x * warps + (threadIdx.x >> 5);
     int64_t row = u / pieces, piece = u - row * pieces;
     const int64_t row_step = step / pieces, piece_step = step - row_step * pieces;
     constexpr int kAhead = 4;   // loads on their way at once
@@ -124,60 +130,64 @@ __device__ __forceinline__ void each_piece(const T* g, int64_t row_stride, int64
     }
 }
 
-// Sum of squares of each matrix, in a fixed order: fp32 within a thread, which
-// has some dozens of elements, double from there.  A thread whose squares could
-// leave fp32's range adds them again in double.
+// This warp's sum of squares, in every lane: fp32, a thread has some dozens of
+// elements; in double again where the squares could leave fp32's range.
 template <int V, class T>
-__global__ void __launch_bounds__(kNormThreads) norm_partials(const T* __restrict__ g, int64_t batch_stride, int64_t row_stride,
-                                                              int64_t rows, int64_t cols, double* __restrict__ partial)
+__device__ __forceinline__ double squares(const T* g, int64_t row_stride, int64_t rows, int64_t cols)
 {
-    __shared__ double warp_sums[kNormThreads / 32];
-    let_next_begin();
-    wait_for_earlier();
-    const T* const mine = g + blockIdx.y * batch_stride;
     float s = 0.f, top = 0.f;
-    each_piece<V, T>(mine, row_stride, rows, cols, [&](int64_t, int64_t, const float (&v)[V]) {
+    each_piece<V, T>(g, row_stride, rows, cols, [&](int64_t, int64_t, const float (&v)[V]) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             s = __fmaf_rn(v[i], v[i], s);
             top = fmaxf(top, fabsf(v[i]));
         }
     });
-    double d = s;
-    if (top > 1e15f || (top < 1e-15f && top > 0.f)) {
-        d = 0;
-        each_piece<V, T>(mine, row_stride, rows, cols, [&](int64_t, int64_t, const float (&v)[V]) {
+    if (__any_sync(0xffffffffu, top > 1e15f || (top < 1e-15f && top > 0.f))) {
+        double d = 0;
+        each_piece<V, T>(g, row_stride, rows, cols, [&](int64_t, int64_t, const float (&v)[V]) {
 #pragma unroll
             for (int i = 0; i < V; ++i) d = fma((double)v[i], (double)v[i], d);
         });
+        return warp_sum(d);
     }
-    d = block_sum(d, warp_sums);
-    if (threadIdx.x == 0) partial[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = d;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    return s;
 }
+
+struct Input {
+    int64_t batch_stride, row_stride, rows, cols;
+    float eps;
+    int64_t ld;              // of X
+    __half *x, *x_low;
+    float* scale;
+    unsigned* done;
+    double* partial;         // norm_blocks of each matrix
+    int norm_blocks;
+};
 
 // X = G 2^e as a sum of two fp16 (for 16-bit G one: its 8 or 11 bits fit, but for
 // entries below 2^-24 of the norm), and the factor that makes it G / (|G| + eps).
+// Thread 0 has the sum of squares.
 template <int V, class T>
-__global__ void __launch_bounds__(kNormThreads) scale_in(const T* __restrict__ g, int64_t batch_stride, int64_t row_stride,
-                                                         int64_t rows, int64_t cols, int norm_blocks, const double* __restrict__ partial,
-                                                         float eps, int64_t ld, __half* __restrict__ x, __half* __restrict__ x_low,
-                                                         float* __restrict__ scale, unsigned* __restrict__ done)
+__device__ __forceinline__ void put_scaled(const Input& q, const T* g, double sum_of_squares)
 {
-    __shared__ double warp_sums[kNormThreads / 32];
-    static_assert(kMaxNormBlocks <= kNormThreads, "one partial sum a thread");
-    let_next_begin();
-    wait_for_earlier();
-    const double sum = block_sum(threadIdx.x < norm_blocks ? partial[(int64_t)blockIdx.y * norm_blocks + threadIdx.x] : 0.0, warp_sums);
-    const double norm = sqrt(sum);
-    int e = 0;
-    if (norm > 0 && norm < INFINITY) e = max(-120, min(120, ilogbf(kRange) - ilogb(norm)));
-    const float up = ldexpf(1.f, e);
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        scale[blockIdx.y] = (float)(1.0 / ((norm + eps) * up));
-        done[blockIdx.y] = 0;
+    __shared__ float factor;
+    if (threadIdx.x == 0) {
+        const double norm = sqrt(sum_of_squares);
+        int e = 0;
+        if (norm > 0 && norm < INFINITY) e = max(-120, min(120, ilogbf(kRange) - ilogb(norm)));
+        factor = ldexpf(1.f, e);
+        if (blockIdx.x == 0) {
+            q.scale[blockIdx.y] = (float)(1.0 / ((norm + q.eps) * factor));
+            q.done[blockIdx.y] = 0;
+        }
     }
-    const int64_t at = (int64_t)blockIdx.y * rows * ld;
-    each_piece<V, T>(g + blockIdx.y * batch_stride, row_stride, rows, cols, [&](int64_t row, int64_t c, const float (&v)[V]) {
+    __syncthreads();
+    const float up = factor;
+    const int64_t at = (int64_t)blockIdx.y * q.rows * q.ld;
+    each_piece<V, T>(g, q.row_stride, q.rows, q.cols, [&](int64_t row, int64_t c, const float (&v)[V]) {
         float h[V], l[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -185,24 +195,55 @@ __global__ void __launch_bounds__(kNormThreads) scale_in(const T* __restrict__ g
             l[i] = kLowScale * (h[i] - __half2float(__float2half_rn(h[i])));
         }
         if constexpr (V == 8) {
-            *reinterpret_cast<uint4*>(x + at + row * ld + c) = pack8<__half>(h);
-            if (sizeof(T) == 4) *reinterpret_cast<uint4*>(x_low + at + row * ld + c) = pack8<__half>(l);
+            *reinterpret_cast<uint4*>(q.x + at + row * q.ld + c) = pack8<__half>(h);
+            if (sizeof(T) == 4) *reinterpret_cast<uint4*>(q.x_low + at + row * q.ld + c) = pack8<__half>(l);
         } else {
-            x[at + row * ld + c] = __float2half_rn(h[0]);
-            if (sizeof(T) == 4) x_low[at + row * ld + c] = __float2half_rn(l[0]);
+            q.x[at + row * q.ld + c] = __float2half_rn(h[0]);
+            if (sizeof(T) == 4) q.x_low[at + row * q.ld + c] = __float2half_rn(l[0]);
         }
     });
 }
 
+// Sums of squares, in blocks of a fixed order, then X.
 template <int V, class T>
-int start(const T* g, int64_t bs, int64_t rs, int64_t batch, int64_t rows, int64_t cols, float eps, const Layout& l, char* ws, cudaStream_t st)
+__global__ void __launch_bounds__(kNormThreads) norm_partials(Input q, const T* __restrict__ g)
 {
-    const dim3 grid(l.norm_blocks, (unsigned)batch);
-    double* const partial = reinterpret_cast<double*>(ws + l.partial);
-    if (int rc = launch_next(norm_partials<V, T>, grid, kNormThreads, 0, st, 1, g, bs, rs, rows, cols, partial)) return rc;
-    return launch_next(scale_in<V, T>, grid, kNormThreads, 0, st, 1, g, bs, rs, rows, cols, l.norm_blocks, (const double*)partial, eps, l.ld,
-                       reinterpret_cast<__half*>(ws + l.x[0]), reinterpret_cast<__half*>(ws + l.x_low[0]),
-                       reinterpret_cast<float*>(ws + l.scale), reinterpret_cast<unsigned*>(ws + l.done));
+    __shared__ double warp_sums[kNormThreads / 32];
+    let_next_begin();
+    wait_for_earlier();
+    const double d = block_sum(squares<V, T>(g + blockIdx.y * q.batch_stride, q.row_stride, q.rows, q.cols), warp_sums);
+    if (threadIdx.x == 0) q.partial[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = d;
+}
+
+template <int V, class T>
+__global__ void __launch_bounds__(kNormThreads) scale_in(Input q, const T* __restrict__ g)
+{
+    __shared__ double warp_sums[kNormThreads / 32];
+    static_assert(kMaxNormBlocks <= kNormThreads, "one partial sum a thread");
+    let_next_begin();
+    wait_for_earlier();
+    const double d = (int)threadIdx.x < q.norm_blocks ? q.partial[(int64_t)blockIdx.y * q.norm_blocks + threadIdx.x] : 0.0;
+    put_scaled<V, T>(q, g + blockIdx.y * q.batch_stride, block_sum(warp_sum(d), warp_sums));
+}
+
+// Both by one block a matrix.
+template <int V, class T>
+__global__ void __launch_bounds__(kOneBlockThreads) norm_and_scale(Input q, const T* __restrict__ g)
+{
+    __shared__ double warp_sums[kOneBlockThreads / 32];
+    let_next_begin();
+    wait_for_earlier();
+    const T* const mine = g + blockIdx.y * q.batch_stride;
+    put_scaled<V, T>(q, mine, block_sum(squares<V, T>(mine, q.row_stride, q.rows, q.cols), warp_sums));
+}
+
+template <int V, class T>
+int start(const Input& q, const T* g, int64_t batch, cudaStream_t st)
+{
+    if (q.rows * q.cols <= kOneBlock) return launch_next(norm_and_scale<V, T>, dim3(1, (unsigned)batch), kOneBlockThreads, 0, st, 1, q, g);
+    const dim3 grid(q.norm_blocks, (unsigned)batch);
+    if (int rc = launch_next(norm_partials<V, T>, grid, kNormThreads, 0, st, 1, q, g)) return rc;
+    return launch_next(scale_in<V, T>, grid, kNormThreads, 0, st, 1, q, g);
 }
 
 // ---------------------------------------------------------------------------
@@ -673,13 +714,21 @@ extern "C" int emb_orthogonalize(const void* update, int32_t dtype, int64_t batc
     char* const ws = static_cast<char*>(workspace);
     const Layout l = layout_of(batch, rows, cols);
     const bool wide = cols % 8 == 0 && row_stride % 8 == 0 && batch_stride % 8 == 0 && aligned_to(update, 16);
+    Input in;
+    in.batch_stride = batch_stride, in.row_stride = row_stride, in.rows = rows, in.cols = cols;
+    in.eps = eps, in.ld = l.ld;
+    in.x = reinterpret_cast<__half*>(ws + l.x[0]);
+    in.x_low = reinterpret_cast<__half*>(ws + l.x_low[0]);
+    in.scale = reinterpret_cast<float*>(ws + l.scale);
+    in.done = reinterpret_cast<unsigned*>(ws + l.done);
+    in.partial = reinterpret_cast<double*>(ws + l.partial);
+    in.norm_blocks = l.norm_blocks;
     const auto begin = [&](auto t) {
         using T = decltype(t);
         const T* const g = static_cast<const T*>(update);
-        return wide ? start<8, T>(g, batch_stride, row_stride, batch, rows, cols, eps, l, ws, st)
-                    : start<1, T>(g, batch_stride, row_stride, batch, rows, cols, eps, l, ws, st);
+        return wide ? start<8, T>(in, g, batch, st) : start<1, T>(in, g, batch, st);
     };
-    int rc = dtype == EMB_F32 ? begin(float()) : dtype == EMB_F16 ? begin(__half()) : begin(__nv_bfloat16());
+    const int rc = dtype == EMB_F32 ? begin(float()) : dtype == EMB_F16 ? begin(__half()) : begin(__nv_bfloat16());
     if (rc != EMB_OK) return rc;
     StepsArgs p;
     for (int i = 0; i < 2; ++i) {

@@ -36,15 +36,19 @@ __device__ __forceinline__ void unpack8(const uint4& p, float (&v)[8])
     }
 }
 
-// v as two fp16 numbers each.
+// v as two fp16 numbers each, two at a time.
 __device__ __forceinline__ void split8(const float (&v)[8], uint4& high, uint4& low)
 {
     high = core::pack8<__half>(v);
-    float back[8];
-    unpack8(high, back);
+    const uint32_t h[4] = {high.x, high.y, high.z, high.w};
+    uint32_t l[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) back[j] = kLowScale * (v[j] - back[j]);
-    low = core::pack8<__half>(back);
+    for (int i = 0; i < 4; ++i) {
+        const float2 off = sub2(make_float2(v[2 * i], v[2 * i + 1]), __half22float2(*reinterpret_cast<const __half2*>(&h[i])));
+        const float2 up = mul2(off, make_float2(kLowScale, kLowScale));
+        l[i] = core::pack2<__half>(up.x, up.y);
+    }
+    low = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
 }  // namespace emb

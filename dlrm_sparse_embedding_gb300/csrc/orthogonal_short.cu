@@ -49,6 +49,9 @@ struct Short {
 // ---------------------------------------------------------------------------
 // all steps of a matrix
 // ---------------------------------------------------------------------------
+constexpr int kWarps = 16;                       // of the epilogue: four to each quarter of the rows, 32 columns each
+constexpr int kStepsThreads = 128 + 32 * kWarps;
+
 struct Control {
     uint64_t full[kStages], empty[kStages];
     uint64_t done[2];    // the products into the first (second) pair of accumulators
@@ -107,7 +110,7 @@ constexpr int kStepsSmem = 1024 + 6 * kMatrix + 512;
 static_assert(kStages * 2 * kOperand == 6 * kMatrix, "the ring of A0's sum is the matrices' room");
 static_assert(sizeof(Control) <= 512 && kStepsSmem <= 227 * 1024, "the SM's shared memory");
 
-__global__ void __launch_bounds__(kThreads, 1) short_steps(const __grid_constant__ Short q)
+__global__ void __launch_bounds__(kStepsThreads, 1) short_steps(const __grid_constant__ Short q)
 {
     extern __shared__ __align__(1024) unsigned char dynamic[];
     unsigned char* const base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dynamic) + 1023) & ~uintptr_t(1023));
@@ -122,9 +125,9 @@ __global__ void __launch_bounds__(kThreads, 1) short_steps(const __grid_constant
         }
         for (int i = 0; i < 2; ++i) {
             tc::bar_init(tc::smem_addr(&ctl->done[i]), 1);
-            tc::bar_init(tc::smem_addr(&ctl->drained[i]), kEpilogueWarps);
+            tc::bar_init(tc::smem_addr(&ctl->drained[i]), kWarps);
         }
-        tc::bar_init(tc::smem_addr(&ctl->ready), kEpilogueWarps);
+        tc::bar_init(tc::smem_addr(&ctl->ready), kWarps);
         ctl->gave_up = 0;
         tc::bar_init_fence();
         tc::prefetch_map(&q.x);
@@ -202,8 +205,8 @@ __global__ void __launch_bounds__(kThreads, 1) short_steps(const __grid_constant
             }
         }
     } else if (warp >= 4) {
-        // a lane has a row, its warp half the columns
-        const int row = (warp & 3) * 32 + lane, c0 = (warp - 4) / 4 * 64;
+        // a lane has 32 columns of a row
+        const int row = (warp & 3) * 32 + lane, c0 = (warp - 4) / 4 * 32;
         const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         uint32_t dones[2] = {};
         bool ok = true;
@@ -214,20 +217,18 @@ __global__ void __launch_bounds__(kThreads, 1) short_steps(const __grid_constant
         };
         // every eight columns of a pair of accumulators, added up
         const auto each = [&](int pair, bool has_low, auto f) {
-            for (int c = c0; c < c0 + 64; c += 32) {
-                uint32_t v[32], l[32];
-                tc::tmem_load32(mine + pair * 2 * kRows + c, v);
-                if (has_low) tc::tmem_load32(mine + pair * 2 * kRows + kRows + c, l);
+            uint32_t v[32], l[32];
+            tc::tmem_load32(mine + pair * 2 * kRows + c0, v);
+            if (has_low) tc::tmem_load32(mine + pair * 2 * kRows + kRows + c0, l);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float o[8];
+            for (int i = 0; i < 4; ++i) {
+                float o[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        o[j] = __uint_as_float(v[8 * i + j]);
-                        if (has_low) o[j] = __fmaf_rn(1.f / kLowScale, __uint_as_float(l[8 * i + j]), o[j]);
-                    }
-                    f(c + 8 * i, o);
+                for (int j = 0; j < 8; ++j) {
+                    o[j] = __uint_as_float(v[8 * i + j]);
+                    if (has_low) o[j] = __fmaf_rn(1.f / kLowScale, __uint_as_float(l[8 * i + j]), o[j]);
                 }
+                f(c0 + 8 * i, o);
             }
         };
         const auto written = [&] {
@@ -247,21 +248,18 @@ __global__ void __launch_bounds__(kThreads, 1) short_steps(const __grid_constant
         {
             const float s = q.scale ? q.scale[z] * q.scale[z] : 1.f;
             const int chains = (q.k_steps + kChain - 1) / kChain;
-            float sum[64] = {};
+            float sum[32] = {};
             for (int chain = 0; chain < chains; ++chain) {
                 const int pair = chain & 1;
                 if (!wait_done(pair)) break;
+                uint32_t v[32];
+                tc::tmem_load32(mine + pair * 2 * kRows + c0, v);
 #pragma unroll
-                for (int c = 0; c < 64; c += 32) {
-                    uint32_t v[32];
-                    tc::tmem_load32(mine + pair * 2 * kRows + c0 + c, v);
+                for (int i = 0; i < 32; ++i) sum[i] += __uint_as_float(v[i]);
+                if (q.low_in) {
+                    tc::tmem_load32(mine + pair * 2 * kRows + kRows + c0, v);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) sum[c + i] += __uint_as_float(v[i]);
-                    if (q.low_in) {
-                        tc::tmem_load32(mine + pair * 2 * kRows + kRows + c0 + c, v);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) sum[c + i] = __fmaf_rn(1.f / kLowScale, __uint_as_float(v[i]), sum[c + i]);
-                    }
+                    for (int i = 0; i < 32; ++i) sum[i] = __fmaf_rn(1.f / kLowScale, __uint_as_float(v[i]), sum[i]);
                 }
                 tc::fence_before();
                 __syncwarp();
@@ -269,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) short_steps(const __grid_constant
             }
             if (ok) {
 #pragma unroll
-                for (int c = 0; c < 64; c += 8) {
+                for (int c = 0; c < 32; c += 8) {
                     float o[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) o[j] = s * sum[c + j];
@@ -495,7 +493,7 @@ int run_short(const StepsArgs& p, cudaStream_t st)
             !make_map(&q.x_apply, EMB_F16, p.x[from], !q.tall, p.cols, p.rows, p.batch, p.ld, x_elems) ||
             !make_map(&q.x_low_apply, EMB_F16, p.x_low[from], !q.tall, p.cols, p.rows, p.batch, p.ld, x_elems))
             return EMB_ERR_CUDA;
-        if (int rc = launch_next(short_steps, (unsigned)p.batch, kThreads, kStepsSmem, st, 1, q)) return rc;
+        if (int rc = launch_next(short_steps, (unsigned)p.batch, kStepsThreads, kStepsSmem, st, 1, q)) return rc;
         if (int rc = launch_next(short_apply, (unsigned)(p.batch * q.tiles), kThreads, kApplySmem, st, 1, q)) return rc;
     }
     return EMB_OK;
