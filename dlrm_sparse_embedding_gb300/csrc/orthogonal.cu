@@ -261,9 +261,32 @@ int start(const Input& q, const T* g, int64_t batch, cudaStream_t st)
 // the others are written as their transposes.
 enum Product { kGram, kQuadratic, kUpdate };
 
-constexpr int kStaging = 32 * kChunk * 4;       // bytes of shared memory an epilogue warp takes its columns through, in fp32
-constexpr int kSmem = smem_bytes(kEpilogueWarps * kStaging + 64);
-static_assert(kSmem <= 227 * 1024, "the SM's shared memory");
+//
+// With few tiles the k of A's (the long side) is shared by a cluster: every CTA sums
+// its part of the steps, sends each other one its 32 columns of the sum, and
+// finishes its own 32 columns from the parts it was sent, added in the CTAs' order.
+constexpr int kSplit = 4;
+constexpr int kStaging = 32 * kChunk * 4;       // bytes of shared memory for 32 rows of 32 columns in fp32
+
+struct Counts {
+    int ahead;   // tiles whose C may be read
+    int taken;   // tiles the epilogue has begun
+    int stored[kEpilogueWarps];   // tiles each of its warps has stored
+    uint64_t received, sent;      // barriers: the parts of my columns are here; the parts I sent have been used
+};
+constexpr int kCountsBytes = 128;
+static_assert(sizeof(Counts) <= kCountsBytes, "the counts' room");
+
+// Staging: 32 x 32 of a warp, or, of a split tile, the parts that come in and the
+// ones that go out: 4 of 128 rows of 32 columns each.
+template <class S>
+constexpr int staging_bytes() { return S::SPLIT == 1 ? kEpilogueWarps * kStaging : 2 * S::SPLIT * 4 * kStaging; }
+template <class S>
+constexpr int own_smem()
+{
+    static_assert(smem_bytes<S>(staging_bytes<S>() + kCountsBytes) <= 227 * 1024, "the SM's shared memory");
+    return smem_bytes<S>(staging_bytes<S>() + kCountsBytes);
+}
 
 struct Steps {
     CUtensorMap x_gram[2], x_update[2], a_map, b_map;   // x_gram: of A = X X^T; x_update: of X' = B X
@@ -289,38 +312,76 @@ struct Tile {
     unsigned needs;          // of done[matrix]
 };
 
+// How many tiles a matrix has of a product, and how many CTAs finish one.
+__device__ __forceinline__ unsigned tiles_of(const Steps& q, Product p)
+{
+    return p == kUpdate ? q.tiles_m * q.tiles_n : q.side * (q.side + 1) / 2;
+}
 template <class S>
-__device__ __forceinline__ Tile tile_at(const Steps& q, unsigned t)
+__device__ __forceinline__ constexpr unsigned finishers(Product p) { return S::CTAS * (p == kGram ? S::SPLIT : 1); }
+
+// Tile `index` of a product, the matrices' one after another.
+template <class S>
+__device__ __forceinline__ Tile tile_of(const Steps& q, int step, Product product, unsigned index)
 {
     Tile r;
-    const unsigned gram = q.side * (q.side + 1) / 2, update = q.tiles_m * q.tiles_n, per = 2 * gram + update;
-    r.step = t / (per * q.batch);
-    t -= r.step * per * q.batch;
-    unsigned before = r.step * per;
+    r.step = step;
+    r.product = product;
+    const unsigned gram = tiles_of(q, kGram), update = tiles_of(q, kUpdate);
+    r.needs = step * (gram * (finishers<S>(kGram) + finishers<S>(kQuadratic)) + update * finishers<S>(kUpdate));
     int64_t k = q.m;
-    if (t < 2 * gram * q.batch) {
-        r.product = t < gram * q.batch ? kGram : kQuadratic;
-        if (r.product == kGram) k = q.rows + q.cols - q.m;
-        else t -= gram * q.batch, before += gram;
-        r.matrix = t / gram;
-        const unsigned idx = t - r.matrix * gram;
+    if (product == kUpdate) {
+        r.needs += gram * (finishers<S>(kGram) + finishers<S>(kQuadratic));
+        r.matrix = index / update;
+        const unsigned idx = index - r.matrix * update;
+        r.m0 = (int64_t)(idx / q.tiles_n) * S::kTile;
+        r.n0 = (int64_t)(idx % q.tiles_n) * S::kTile;
+    } else {
+        if (product == kGram) k = q.rows + q.cols - q.m;
+        else r.needs += gram * finishers<S>(kGram);
+        r.matrix = index / gram;
+        const unsigned idx = index - r.matrix * gram;
         unsigned i = (unsigned)((sqrtf(8.f * (float)idx + 1.f) - 1.f) * 0.5f);   // row i of the triangle starts at i (i + 1) / 2
         while (i * (i + 1) / 2 > idx) --i;
         while ((i + 1) * (i + 2) / 2 <= idx) ++i;
         r.m0 = (int64_t)i * S::kTile;
         r.n0 = (int64_t)(idx - i * (i + 1) / 2) * S::kTile;
-    } else {
-        r.product = kUpdate;
-        t -= 2 * gram * q.batch, before += 2 * gram;
-        r.matrix = t / update;
-        const unsigned idx = t - r.matrix * update;
-        r.m0 = (int64_t)(idx / q.tiles_n) * S::kTile;
-        r.n0 = (int64_t)(idx % q.tiles_n) * S::kTile;
     }
     r.k_steps = (int)((k + kStep - 1) / kStep);
-    r.needs = before * S::CTAS;
     return r;
 }
+
+// The tiles of one CTA, in the list's order.  Without a shared k they are dealt out
+// over the whole list; with one, A's tiles go to clusters and the others to CTAs,
+// product by product.
+template <class S>
+struct Walk {
+    const Steps& q;
+    int step;
+    int product;
+    unsigned index;   // of a tile among all matrices' of the product
+
+    __device__ explicit Walk(const Steps& steps) : q(steps), step(0), product(kGram), index(blockIdx.x / S::kCluster) { settle(); }
+    __device__ bool more() const { return step < q.steps; }
+    __device__ Tile tile() const { return tile_of<S>(q, step, (Product)product, index); }
+    __device__ void next()
+    {
+        index += S::SPLIT > 1 && product != kGram ? gridDim.x : gridDim.x / S::kCluster;
+        settle();
+    }
+
+private:
+    __device__ void settle()
+    {
+        while (step < q.steps) {
+            const unsigned count = q.batch * tiles_of(q, (Product)product);
+            if (index < count) return;
+            index -= count;
+            if (++product > kUpdate) product = kGram, ++step;
+            if (S::SPLIT > 1) index = product == kGram ? blockIdx.x / S::kCluster : blockIdx.x;
+        }
+    }
+};
 
 // Waits until a matrix has got so far; false when the limit ran out.
 __device__ __forceinline__ bool wait_done(const unsigned* done, unsigned needs, volatile int* gave_up)
@@ -358,7 +419,6 @@ __device__ __forceinline__ bool wait_count(const int* count, int least, volatile
             *gave_up = 1;
             return false;
         }
-        __nanosleep(40);   // the issue slots are the epilogue's
     }
     return true;
 }
@@ -376,13 +436,14 @@ __device__ __forceinline__ void set_count(int* count, int v)
 //   kGram       D = s^2 sum, s in the first step
 //   kQuadratic  D = cc sum + cb C + diagonal I
 //   kUpdate     D = s (sum + beta (C + C's low part))
-template <Product F>
-__device__ __forceinline__ bool finish(const Steps& q, const Tile& tile, const Part& part, float* mine, uint32_t rank, int* stored,
-                                       int tiles, volatile int* gave_up)
+template <class S, Product F, bool SHARED = (S::SPLIT > 1 && F == kGram)>
+__device__ __forceinline__ bool finish(const Steps& q, const Tile& tile, const Part& part, float* mine, uint32_t rank, unsigned parts,
+                                       uint32_t received, uint32_t turn_of, volatile int* gave_up)
 {
+    const int c0 = SHARED ? (int)rank * kChunk : part.c0, c1 = SHARED ? c0 + kChunk : part.c1;
     const int lane = threadIdx.x & 31, r0 = lane >> 2, p = lane & 3;
     const int64_t height = F == kUpdate ? q.rows : q.m, width = F == kUpdate ? q.cols : q.m, ld = F == kUpdate ? q.ld : q.ldm;
-    const int64_t m_first = tile.m0 + rank * kRows + part.row, left = height - m_first;
+    const int64_t m_first = tile.m0 + (S::CTAS == 2 ? rank * kRows : 0) + part.row, left = height - m_first;
     const int rows = left < 0 ? 0 : left > 32 ? 32 : (int)left;
     const int64_t of_matrix = tile.matrix * (F == kUpdate ? q.rows * q.ld : q.m * q.ldm);
     const int64_t at = of_matrix + (m_first + r0) * ld + tile.n0 + p * 8;
@@ -415,13 +476,18 @@ __device__ __forceinline__ bool finish(const Steps& q, const Tile& tile, const P
             if (F == kUpdate) l[i] = has && low ? __ldcg(reinterpret_cast<const uint4*>(low + i * 8 * ld + c)) : make_uint4(0, 0, 0, 0);
         }
     };
-    if (F != kGram) fetch(part.c0);
-    if (!tc::bar_wait_warp(part.full, part.phase, gave_up)) return false;
-    tc::fence_after();
-    for (int c = part.c0; c < part.c1; c += kChunk) {
+    if (F != kGram) fetch(c0);
+    if (!SHARED) {
+        if (!tc::bar_wait_warp(part.full, part.phase, gave_up)) return false;
+        tc::fence_after();
+    } else {
+        if (!tc::bar_wait_cluster(received, turn_of, gave_up)) return false;
+    }
+    for (int c = c0; c < c1; c += kChunk) {
+        if constexpr (!SHARED) {
         uint32_t v[32];
         tc::tmem_load32(part.tmem + c, v);
-        if (c + kChunk == part.c1) {
+        if (c + kChunk == c1) {
             tc::fence_before();
             if (lane == 0) tc::bar_arrive(part.empty);
         }
@@ -431,18 +497,29 @@ __device__ __forceinline__ bool finish(const Steps& q, const Tile& tile, const P
             *reinterpret_cast<uint4*>(mine + lane * kChunk + ((i ^ (lane & 7) ^ ((lane >> 3) << 1)) * 4)) =
                 make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         __syncwarp();
+        }
         const int64_t n = tile.n0 + c + p * 8;
         uint4 ch[4], cl[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) ch[i] = h[i], cl[i] = l[i];
-        if (F != kGram && c + kChunk < part.c1) fetch(c + kChunk);
+        if (F != kGram && c + kChunk < c1) fetch(c + kChunk);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = i * 8 + r0, turn = (r & 7) ^ ((r >> 3) << 1);
             float4* const px = reinterpret_cast<float4*>(mine + r * kChunk + (((2 * p) ^ turn) * 4));
             float4* const py = reinterpret_cast<float4*>(mine + r * kChunk + (((2 * p + 1) ^ turn) * 4));
-            const float4 x = *px, y = *py;
-            float o[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+            float o[8] = {};
+            if constexpr (!SHARED) {
+                const float4 x = *px, y = *py;
+                o[0] = x.x, o[1] = x.y, o[2] = x.z, o[3] = x.w, o[4] = y.x, o[5] = y.y, o[6] = y.z, o[7] = y.w;
+            } else {
+#pragma unroll
+                for (int k = 0; k < S::SPLIT; ++k)
+                    if (parts >> k & 1) {   // part k, 128 rows further on
+                        const float4 x = px[k * (4 * kStaging / 16)], y = py[k * (4 * kStaging / 16)];
+                        o[0] += x.x, o[1] += x.y, o[2] += x.z, o[3] += x.w, o[4] += y.x, o[5] += y.y, o[6] += y.z, o[7] += y.w;
+                    }
+            }
             if (F == kGram) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) o[j] *= s;
@@ -501,28 +578,53 @@ __device__ __forceinline__ bool finish(const Steps& q, const Tile& tile, const P
             __syncwarp();
         }
     }
-    // this warp's stores, for the warp that tells the other SMs of them
+    return true;
+}
+
+// A warp's rows of this CTA's part of the sum, two CTAs' columns of them, to those
+// CTAs.
+template <class S>
+__device__ __forceinline__ bool send_parts(const Block& b, Counts* counts, const Part& part, unsigned char* staging)
+{
+    const int lane = threadIdx.x & 31, half = part.c0 != 0;
+    if (!tc::bar_wait_warp(part.full, part.phase, b.gave_up)) return false;
+    tc::fence_after();
+    uint32_t v[2][32];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) tc::tmem_load32(part.tmem + (half * 2 + g) * kChunk, v[g]);
+    tc::fence_before();
     __syncwarp();
-    if (lane == 0) set_count(stored, tiles);
+    if (lane == 0) tc::bar_arrive(part.empty);
+    // a lane's 16 bytes at a time would cross to the other CTAs one by one (9 bytes a cycle); 4 KB copies do not
+    unsigned char* const out = staging + S::SPLIT * 4 * kStaging;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        unsigned char* const mine = out + ((half * 2 + g) * 4 + part.row / 32) * kStaging;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(mine + lane * kChunk * 4 + ((i ^ (lane & 7) ^ ((lane >> 3) << 1)) * 16)) =
+                make_uint4(v[g][4 * i], v[g][4 * i + 1], v[g][4 * i + 2], v[g][4 * i + 3]);
+    }
+    tc::fence_async();
+    __syncwarp();
+    if (lane < 2) {
+        const uint32_t to = half * 2 + lane;
+        tc::copy_cluster(tc::in_cta(tc::smem_addr(staging + (b.rank * 4 + part.row / 32) * kStaging), to),
+                         tc::smem_addr(out + (to * 4 + part.row / 32) * kStaging), kStaging, tc::in_cta(tc::smem_addr(&counts->received), to));
+    }
     return true;
 }
 
 // What the epilogue reads of C, asked for while the tile's products still run:
 // one warp goes a tile ahead, waits for the matrix and has the low parts of X
 // brought to L2 (the high parts come with the products' operands).
-struct Counts {
-    int ahead;   // tiles whose C may be read
-    int taken;   // tiles the epilogue has begun
-    int stored[kEpilogueWarps];   // tiles each of its warps has stored
-};
-
 template <class S>
-__device__ __forceinline__ void scout(const Steps& q, const Block& b, Counts* s, unsigned first, unsigned total, unsigned step)
+__device__ __forceinline__ void scout(const Steps& q, const Block& b, Counts* s)
 {
     const int lane = threadIdx.x & 31;
     int n = 0;
-    for (unsigned t = first; t < total; t += step, ++n) {
-        const Tile tile = tile_at<S>(q, t);
+    for (Walk<S> walk(q); walk.more(); walk.next(), ++n) {
+        const Tile tile = walk.tile();
         if (!__all_sync(0xffffffffu, wait_count(&s->taken, n - 1, b.gave_up))) return;
         if (tile.product != kGram) {
             if (!__all_sync(0xffffffffu, wait_done(q.done + tile.matrix, tile.needs, b.gave_up))) return;
@@ -531,7 +633,7 @@ __device__ __forceinline__ void scout(const Steps& q, const Block& b, Counts* s,
         if (tile.product == kUpdate && (tile.step || q.low_in)) {
             const int64_t width = q.ld - tile.n0 < S::kTile ? q.ld - tile.n0 : S::kTile;
             for (int r = lane; r < kRows; r += 32) {
-                const int64_t m = tile.m0 + b.rank * kRows + r;
+                const int64_t m = tile.m0 + (S::CTAS == 2 ? b.rank * kRows : 0) + r;
                 if (m < q.rows)
                     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
                                  ::"l"(q.x_low[tile.step & 1] + tile.matrix * q.rows * q.ld + m * q.ld + tile.n0), "r"((int)width * 2) : "memory");
@@ -540,29 +642,37 @@ __device__ __forceinline__ void scout(const Steps& q, const Block& b, Counts* s,
     }
 }
 
+// This CTA's part of a tile's steps: [from, to).
+template <class S>
+__device__ __forceinline__ void part_steps(const Tile& tile, int rank, int& from, int& to)
+{
+    const bool shared = S::SPLIT > 1 && tile.product == kGram;
+    from = shared ? tile.k_steps * rank / S::SPLIT : 0;
+    to = shared ? tile.k_steps * (rank + 1) / S::SPLIT : tile.k_steps;
+}
+
 template <class S>
 __global__ void __launch_bounds__(kThreads, 1) newton_schulz(const __grid_constant__ Steps q)
 {
     extern __shared__ __align__(1024) unsigned char dynamic[];
-    Block b = block_of(dynamic);
-    const int warp = threadIdx.x >> 5;
-    Counts* const counts = reinterpret_cast<Counts*>(b.own + kEpilogueWarps * kStaging);
+    Block b = block_of<S>(dynamic);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Counts* const counts = reinterpret_cast<Counts*>(b.own + staging_bytes<S>());
     if (threadIdx.x == 0) {
         counts->ahead = counts->taken = 0;
         for (int i = 0; i < kEpilogueWarps; ++i) counts->stored[i] = 0;
+        tc::bar_init(tc::smem_addr(&counts->received), 1);
+        tc::bar_init(tc::smem_addr(&counts->sent), 4 * S::SPLIT);
     }
     open<S>(b);
-    const unsigned total = q.steps * q.batch * (q.side * (q.side + 1) + q.tiles_m * q.tiles_n);
-    const unsigned first = blockIdx.x / S::CTAS, step = gridDim.x / S::CTAS;
 
     if (warp == 0 && tc::elect_one()) {
         uint32_t n = 0;
         bool ok = true;
-        for (unsigned t = first; ok && t < total; t += step) {
-            const Tile tile = tile_at<S>(q, t);
-            const int m = (int)tile.m0 + (int)b.rank * kRows, nn = (int)tile.n0 + (int)b.rank * kRows, z = tile.matrix;
-            ok = wait_done(q.done + tile.matrix, tile.needs, b.gave_up);
-            tc::fence_async();
+        for (Walk<S> walk(q); ok && walk.more(); walk.next()) {
+            const Tile tile = walk.tile();
+            const int shift = S::CTAS == 2 ? (int)b.rank * kRows : 0, z = tile.matrix;
+            const int m = (int)tile.m0 + shift, nn = (int)tile.n0 + shift;
             const CUtensorMap *ma = &q.a_map, *mb = &q.a_map;
             bool a_mn = false, b_mn = false;
             if (tile.product == kGram) {
@@ -573,24 +683,32 @@ __global__ void __launch_bounds__(kThreads, 1) newton_schulz(const __grid_consta
                 mb = q.tall ? &q.b_map : &q.x_update[tile.step & 1];
                 b_mn = !q.tall;
             }
-            for (int i = 0; ok && i < tile.k_steps; ++i, ++n) ok = copy_step<S>(b, n, false, ma, a_mn, m, z, mb, b_mn, nn, z, i * kStep);
+            tc::prefetch_map(ma);
+            tc::prefetch_map(mb);
+            int from, to;
+            part_steps<S>(tile, b.rank, from, to);
+            ok = wait_done(q.done + tile.matrix, tile.needs, b.gave_up);
+            tc::fence_async();
+            for (int i = from; ok && i < to; ++i, ++n) ok = copy_step<S>(b, n, false, ma, a_mn, m, z, mb, b_mn, nn, z, i * kStep);
         }
-        finish_copies(b, n, ok);
-    } else if (warp == 1 && b.rank == 0 && tc::elect_one()) {
+        finish_copies<S>(b, n, ok);
+    } else if (warp == 1 && (S::CTAS == 1 || b.rank == 0) && tc::elect_one()) {
         uint32_t n = 0, made = 0;
-        for (unsigned t = first; t < total; t += step) {
-            const Tile tile = tile_at<S>(q, t);
+        for (Walk<S> walk(q); walk.more(); walk.next()) {
+            const Tile tile = walk.tile();
+            int from, to;
+            part_steps<S>(tile, b.rank, from, to);
+            if (from == to) continue;
             const bool a_mn = tile.product == kGram && q.tall, b_mn = tile.product == kGram ? q.tall : tile.product == kUpdate && !q.tall;
-            if (!multiply<S>(b, made++, n, tile.k_steps, tc::instruction(false, a_mn, b_mn, S::kTile, S::kTile), a_mn, b_mn)) break;
-            n += tile.k_steps;
+            if (!multiply<S>(b, made++, n, to - from, tc::instruction(false, a_mn, b_mn, S::kTile, S::kTile), a_mn, b_mn)) break;
+            n += to - from;
         }
     } else if (warp == 2) {
         // a tile's stores, once all its warps have made them, are ordered before the matrix's count by one
         // thread: each warp waiting for its own to reach L2 would hold the epilogue up
-        const int lane = threadIdx.x & 31;
         int made = 0;
-        for (unsigned t = first; t < total; t += step) {
-            const Tile tile = tile_at<S>(q, t);
+        for (Walk<S> walk(q); walk.more(); walk.next()) {
+            const Tile tile = walk.tile();
             ++made;
             if (!__all_sync(0xffffffffu, wait_count(&counts->stored[lane % kEpilogueWarps], made, b.gave_up))) break;
             if (lane == 0) {
@@ -599,19 +717,52 @@ __global__ void __launch_bounds__(kThreads, 1) newton_schulz(const __grid_consta
             }
         }
     } else if (warp == 3) {
-        scout<S>(q, b, counts, first, total, step);
+        scout<S>(q, b, counts);
     } else if (warp >= 4) {
         int made = 0;
-        int* const stored = &counts->stored[warp - 4];
-        float* const mine = reinterpret_cast<float*>(b.own + (warp - 4) * kStaging);
-        for (unsigned t = first; t < total; t += step) {
-            const Tile tile = tile_at<S>(q, t);
-            const Part part = part_of<S>(b, made++);
-            if (threadIdx.x == 4 * 32) set_count(&counts->taken, made);
-            if (!__all_sync(0xffffffffu, wait_count(&counts->ahead, made, b.gave_up))) break;
-            const bool ok = tile.product == kGram        ? finish<kGram>(q, tile, part, mine, b.rank, stored, made, b.gave_up)
-                            : tile.product == kQuadratic ? finish<kQuadratic>(q, tile, part, mine, b.rank, stored, made, b.gave_up)
-                                                         : finish<kUpdate>(q, tile, part, mine, b.rank, stored, made, b.gave_up);
+        uint32_t accumulators = 0, shared_tiles = 0;
+        // (what comes from other CTAs may come at any time: a tile of one's own goes through the room for what goes out)
+        float* const mine = reinterpret_cast<float*>(b.own + (S::SPLIT > 1 ? S::SPLIT * 4 : 0) * kStaging + (warp - 4) * kStaging);
+        const auto stored = [&] {   // this warp's stores, for the warp that tells the other SMs of them
+            __syncwarp();
+            if (lane == 0) set_count(&counts->stored[warp - 4], made + 1);
+        };
+        for (Walk<S> walk(q); walk.more(); walk.next(), ++made) {
+            const Tile tile = walk.tile();
+            int from, to;
+            part_steps<S>(tile, b.rank, from, to);
+            const Part part = part_of<S>(b, accumulators);
+            if (from < to) ++accumulators;
+            if (threadIdx.x == 4 * 32) set_count(&counts->taken, made + 1);
+            bool ok = true;
+            if (S::SPLIT > 1 && tile.product == kGram) {
+                unsigned parts = 0;   // the CTAs that have one
+                for (int i = 0; i < S::SPLIT; ++i) {
+                    int f, t;
+                    part_steps<S>(tile, i, f, t);
+                    parts |= (unsigned)(f < t) << i;
+                }
+                const uint32_t turn = shared_tiles++ & 1;
+                if (threadIdx.x == 4 * 32) tc::bar_expect(tc::smem_addr(&counts->received), __popc(parts) * 4 * kStaging);
+                if (from < to) ok = send_parts<S>(b, counts, part, b.own);
+                if (ok && warp < 8) {
+                    ok = finish<S, kGram>(q, tile, part, reinterpret_cast<float*>(b.own + (warp & 3) * kStaging), b.rank, parts,
+                                          tc::smem_addr(&counts->received), turn, b.gave_up);
+                    if (ok) stored();
+                    if (ok && lane < S::SPLIT) tc::bar_arrive(tc::in_cta(tc::smem_addr(&counts->sent), lane));
+                } else if (ok) {
+                    stored();
+                }
+                // every CTA has used what came from here: the room for it is free again
+                ok = ok && tc::bar_wait_warp(tc::smem_addr(&counts->sent), turn, b.gave_up);
+            } else {
+                ok = tile.product == kGram || __all_sync(0xffffffffu, wait_count(&counts->ahead, made + 1, b.gave_up));
+                if (ok)
+                    ok = tile.product == kGram        ? finish<S, kGram>(q, tile, part, mine, b.rank, 1, 0, 0, b.gave_up)
+                         : tile.product == kQuadratic ? finish<S, kQuadratic>(q, tile, part, mine, b.rank, 1, 0, 0, b.gave_up)
+                                                      : finish<S, kUpdate>(q, tile, part, mine, b.rank, 1, 0, 0, b.gave_up);
+                if (ok) stored();
+            }
             if (!ok) break;
         }
     }
@@ -634,13 +785,13 @@ int launch_steps(Steps& q, cudaStream_t st)
     if (tiles > INT_MAX) return EMB_ERR_INVALID_ARG;
     auto* const kernel = newton_schulz<S>;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(S::CTAS);
+    cfg.gridDim = dim3(S::kCluster);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = own_smem<S>();
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {(unsigned)S::CTAS, 1, 1};
+    attr[0].val.clusterDim = {(unsigned)S::kCluster, 1, 1};
     attr[1].id = cudaLaunchAttributeCooperative;
     attr[1].val.cooperative = 1;
     cfg.attrs = attr;
@@ -648,7 +799,7 @@ int launch_steps(Steps& q, cudaStream_t st)
     static std::atomic<int> resident[kMaxDevices];   // clusters that run at the same time
     int clusters = resident[dev.number].load(std::memory_order_relaxed);
     if (!clusters) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, own_smem<S>()) != cudaSuccess ||
             cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess || clusters < 1) {
             cudaGetLastError();
             return EMB_ERR_CUDA;
@@ -656,7 +807,7 @@ int launch_steps(Steps& q, cudaStream_t st)
         resident[dev.number].store(clusters, std::memory_order_relaxed);
     }
     const int64_t most = q.batch * std::max<int64_t>((int64_t)q.side * (q.side + 1) / 2, (int64_t)q.tiles_m * q.tiles_n);
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>(clusters, most) * S::CTAS);
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(clusters, most) * S::kCluster);
     cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, kernel, q) != cudaSuccess) {
         cudaGetLastError();
@@ -665,22 +816,31 @@ int launch_steps(Steps& q, cudaStream_t st)
     return EMB_OK;
 }
 
-// Rounds of tiles a step takes, times a tile's products: a pair's tile has four
-// times those of a single CTA's on twice its SMs.
-int64_t rounds(const Steps& q, int64_t tile, int64_t units)
+constexpr int kFixed = 14, kExchange = 12;
+
+// How long a step takes, in 64-wide steps of a single CTA's tile: rounds of tiles
+// times their k, and what each of the three products costs whatever its k (its
+// epilogue, and the way to the next one's copies over L2).
+int64_t step_time(const Steps& q, int64_t tile, int64_t units, int64_t split)
 {
     const auto along = [&](int64_t v) { return (v + tile - 1) / tile; };
+    const auto rounds = [&](int64_t tiles, int64_t at_once, int64_t k) { return (tiles + at_once - 1) / at_once * ((k + kStep - 1) / kStep + kFixed); };
     const int64_t gram = q.batch * along(q.m) * (along(q.m) + 1) / 2, update = q.batch * along(q.rows) * along(q.cols);
     const int64_t gram_k = q.rows + q.cols - q.m;
-    return (gram + units - 1) / units * (gram_k + q.m) + (update + units - 1) / units * q.m;
+    return (split == 1 ? rounds(gram, units, gram_k) : rounds(gram, units / split, gram_k / split) + kExchange) + rounds(gram, units, q.m) +
+           rounds(update, units, q.m);
 }
 
 int run_steps(Steps& q, cudaStream_t st)
 {
-    // a pair's tile takes twice a single CTA's time, which the single ones' twice as many bytes a product eat up again
     const Device dev = device();
     if (!dev.sms) return EMB_ERR_CUDA;
-    return 2 * rounds(q, 256, dev.sms / 2) <= rounds(q, 128, dev.sms) * 5 / 4 ? launch_steps<Shape<2>>(q, st) : launch_steps<Shape<1>>(q, st);
+    // a pair's tile takes twice a single CTA's time, which the single ones' twice as many bytes a product eat up again
+    const int64_t pairs = 2 * step_time(q, 2 * kRows, dev.sms / 2, 1), single = step_time(q, kRows, dev.sms, 1) * 5 / 4;
+    const int64_t split = step_time(q, kRows, dev.sms, kSplit) * 5 / 4;
+    if (split < pairs && split < single)
+        return launch_steps<Shape<1, kSplit>>(q, st);
+    return pairs <= single ? launch_steps<Shape<2>>(q, st) : launch_steps<Shape<1>>(q, st);
 }
 
 bool sizes_valid(int64_t batch, int64_t rows, int64_t cols)

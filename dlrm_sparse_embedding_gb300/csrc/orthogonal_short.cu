@@ -53,7 +53,7 @@ constexpr int kWarps = 16;                       // of the epilogue: four to eac
 constexpr int kStepsThreads = 128 + 32 * kWarps;
 
 struct Control {
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t done[2];    // the products into the first (second) pair of accumulators
     uint64_t drained[2]; // the epilogue's warps have added that part of A0's sum up
     uint64_t ready;      // the epilogue's warps have written what the next product reads
@@ -107,7 +107,7 @@ __device__ __forceinline__ void multiply_matrices(uint32_t tmem, const Matrix& x
 }
 
 constexpr int kStepsSmem = 1024 + 6 * kMatrix + 512;
-static_assert(kStages * 2 * kOperand == 6 * kMatrix, "the ring of A0's sum is the matrices' room");
+static_assert(kMaxStages * 2 * kOperand == 6 * kMatrix, "the ring of A0's sum is the matrices' room");
 static_assert(sizeof(Control) <= 512 && kStepsSmem <= 227 * 1024, "the SM's shared memory");
 
 __global__ void __launch_bounds__(kStepsThreads, 1) short_steps(const __grid_constant__ Short q)
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kStepsThreads, 1) short_steps(const __grid_con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, z = blockIdx.x;
     volatile int* const gave_up = &ctl->gave_up;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < kMaxStages; ++i) {
             tc::bar_init(tc::smem_addr(&ctl->full[i]), 1);
             tc::bar_init(tc::smem_addr(&ctl->empty[i]), 1);
         }
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kStepsThreads, 1) short_steps(const __grid_con
         // X's steps: the high part in the first half of a stage, the low part in the second
         bool ok = true;
         for (int i = 0; ok && i < q.k_steps; ++i) {
-            const Slot s(i);
+            const Slot<kMaxStages> s(i);
             ok = tc::bar_wait(tc::smem_addr(&ctl->empty[s.stage]), s.phase ^ 1, gave_up);
             if (!ok) break;
             const uint32_t to = tc::smem_addr(base + s.stage * 2 * kOperand), bar = tc::smem_addr(&ctl->full[s.stage]);
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kStepsThreads, 1) short_steps(const __grid_con
             return ok;
         };
         for (int i = 0; ok && i < q.k_steps; ++i) {
-            const Slot s(i);
+            const Slot<kMaxStages> s(i);
             const int chain = i / kChain, pair = chain & 1;
             if (i % kChain == 0 && chain >= 2) ok = tc::bar_wait(tc::smem_addr(&ctl->drained[pair]), ((chain >> 1) & 1) ^ 1, gave_up);
             ok = ok && tc::bar_wait(tc::smem_addr(&ctl->full[s.stage]), s.phase, gave_up);

@@ -23,23 +23,27 @@ constexpr int kEpilogueWarps = 8;               // two to each quarter of the ac
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;   // warps: copy, products, tails, (none), epilogue
 constexpr int kBlockBytes = 64 * 128;           // an mn-major block: 64 k of 64 m
 constexpr int kOperand = kRows * 128;           // bytes of one operand a stage
-constexpr int kStages = 6;
+constexpr int kMaxStages = 6;
 constexpr int kChunk = 32;                      // columns an epilogue warp takes at once
 constexpr int kMaxDevices = 64;
 
 // Pairs move half the bytes of single CTAs for the same products; these fill the
-// GPU with less work.  Either way a CTA holds 128 rows of A and 128 of B.
-template <int CTAS_>
+// GPU with less work; and where even that is not enough, SPLIT CTAs share a tile's
+// k.  Each way a CTA holds 128 rows of A and 128 of B.
+template <int CTAS_, int SPLIT_ = 1>
 struct Shape {
-    static constexpr int CTAS = CTAS_;
+    static constexpr int CTAS = CTAS_, SPLIT = SPLIT_;
+    static constexpr int kCluster = CTAS * SPLIT;
     static constexpr int kTile = kRows * CTAS;       // of D, both ways
+    static constexpr int kStages = SPLIT == 1 ? kMaxStages : 3;
     static constexpr uint32_t kColumns = 2 * kTile;  // two accumulators
     static constexpr uint32_t kBytes = CTAS * 2 * kOperand;   // a stage's, over the pair
+    static_assert(CTAS == 1 || SPLIT == 1, "pairs do not share a tile's k");
 };
 
 struct Ring {
-    uint64_t full[kStages], empty[kStages];
-    uint64_t part[kStages], peer_part[kStages];   // a step whose rows past the group are still to be zeroed; the other CTA's is done
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t part[kMaxStages], peer_part[kMaxStages];   // a step whose rows past the group are still to be zeroed; the other CTA's is done
     uint64_t acc_full[2], acc_empty[2];
     uint32_t tmem;
     int gave_up;
@@ -48,7 +52,8 @@ constexpr int kRingBytes = 512;
 static_assert(sizeof(Ring) <= kRingBytes, "the ring's room");
 
 // Shared memory: the stages on a 1024-byte boundary, the ring, then the kernel's own.
-constexpr int smem_bytes(int own) { return 1024 + 2 * kStages * kOperand + kRingBytes + own; }
+template <class S>
+constexpr int smem_bytes(int own) { return 1024 + 2 * S::kStages * kOperand + kRingBytes + own; }
 
 struct Block {
     unsigned char* stage_a;
@@ -59,12 +64,13 @@ struct Block {
     volatile int* gave_up;
 };
 
+template <class S>
 __device__ __forceinline__ Block block_of(unsigned char* dynamic)
 {
     Block b;
     b.stage_a = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dynamic) + 1023) & ~uintptr_t(1023));
-    b.stage_b = b.stage_a + kStages * kOperand;
-    b.ring = reinterpret_cast<Ring*>(b.stage_b + kStages * kOperand);
+    b.stage_b = b.stage_a + S::kStages * kOperand;
+    b.ring = reinterpret_cast<Ring*>(b.stage_b + S::kStages * kOperand);
     b.own = reinterpret_cast<unsigned char*>(b.ring) + kRingBytes;
     b.gave_up = &b.ring->gave_up;
     return b;
@@ -75,9 +81,9 @@ template <class S>
 __device__ __forceinline__ void open(Block& b)
 {
     const int warp = threadIdx.x >> 5;
-    b.rank = S::CTAS == 2 ? tc::cluster_rank() : 0;
+    b.rank = S::kCluster > 1 ? tc::cluster_rank() : 0;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < S::kStages; ++i) {
             tc::bar_init(tc::smem_addr(&b.ring->full[i]), 1);
             tc::bar_init(tc::smem_addr(&b.ring->empty[i]), 1);
             tc::bar_init(tc::smem_addr(&b.ring->part[i]), 1);
@@ -93,7 +99,7 @@ __device__ __forceinline__ void open(Block& b)
     if (warp == 2) tc::tmem_alloc<S::CTAS>(tc::smem_addr(&b.ring->tmem), S::kColumns);
     tc::fence_before();
     __syncthreads();
-    if constexpr (S::CTAS == 2) tc::cluster_sync();
+    if constexpr (S::kCluster > 1) tc::cluster_sync();
     tc::fence_after();
     b.tmem = b.ring->tmem;
 }
@@ -105,15 +111,16 @@ __device__ __forceinline__ void close(const Block& b, int* status)
     __syncthreads();
     if (threadIdx.x == 0 && *b.gave_up && status) atomicOr(status, ERRBIT_TIMEOUT);
     tc::fence_before();
-    if constexpr (S::CTAS == 2) tc::cluster_sync();
+    if constexpr (S::kCluster > 1) tc::cluster_sync();
     tc::fence_after();
     if ((threadIdx.x >> 5) == 2) tc::tmem_free<S::CTAS>(b.tmem, S::kColumns);
 }
 
 // Where the n-th step of a role stands in the ring.
+template <int STAGES>
 struct Slot {
     uint32_t stage, phase;
-    __device__ explicit Slot(uint32_t n) : stage(n % kStages), phase((n / kStages) & 1) {}
+    __device__ explicit Slot(uint32_t n) : stage(n % STAGES), phase((n / STAGES) & 1) {}
 };
 
 // Copy this CTA's part of one step: 128 rows (columns, if mn-major) of each
@@ -123,7 +130,7 @@ template <class S>
 __device__ __forceinline__ bool copy_step(const Block& b, uint32_t step, bool part, const CUtensorMap* map_a, bool a_mn, int m, int za,
                                           const CUtensorMap* map_b, bool b_mn, int n, int zb, int k)
 {
-    const Slot s(step);
+    const Slot<S::kStages> s(step);
     if (!tc::bar_wait(tc::smem_addr(&b.ring->empty[s.stage]), s.phase ^ 1, b.gave_up)) return false;
     const uint32_t to_a = tc::smem_addr(b.stage_a + s.stage * kOperand), to_b = tc::smem_addr(b.stage_b + s.stage * kOperand);
     uint32_t bar;
@@ -132,8 +139,9 @@ __device__ __forceinline__ bool copy_step(const Block& b, uint32_t step, bool pa
         tc::bar_expect(bar, S::kBytes / S::CTAS);
     } else {
         // the pair's first CTA expects both CTAs' bytes; the second one's may come first
-        bar = tc::in_cta(tc::smem_addr(&b.ring->full[s.stage]), 0);
-        if (b.rank == 0) tc::bar_expect(tc::smem_addr(&b.ring->full[s.stage]), S::kBytes);
+        bar = tc::smem_addr(&b.ring->full[s.stage]);
+        if (S::CTAS == 1 || b.rank == 0) tc::bar_expect(bar, S::kBytes);
+        if (S::CTAS == 2) bar = tc::in_cta(bar, 0);
     }
     if (a_mn) {
         tc::load_box<S::CTAS>(to_a, map_a, bar, m, k, za);
@@ -153,10 +161,11 @@ __device__ __forceinline__ bool copy_step(const Block& b, uint32_t step, bool pa
 // After the last of `steps` copies: the products of every stage are done, here
 // and in the pair's other CTA, before either ends.  If a wait gave up, what was
 // copied last lands before the block ends.
+template <class S>
 __device__ __forceinline__ void finish_copies(const Block& b, uint32_t steps, bool ok)
 {
-    for (uint32_t i = steps < kStages ? 0 : steps - kStages; ok && i < steps; ++i) {
-        const Slot s(i);
+    for (uint32_t i = steps < S::kStages ? 0 : steps - S::kStages; ok && i < steps; ++i) {
+        const Slot<S::kStages> s(i);
         ok = tc::bar_wait(tc::smem_addr(&b.ring->empty[s.stage]), s.phase, b.gave_up);
     }
     if (!ok) {
@@ -175,7 +184,7 @@ __device__ __forceinline__ bool multiply(const Block& b, uint32_t tile, uint32_t
     tc::fence_after();
     const uint32_t da = tc::operand_step(a_mn), db = tc::operand_step(b_mn);
     for (int i = 0; i < steps; ++i, ++step) {
-        const Slot s(step);
+        const Slot<S::kStages> s(step);
         if (!tc::bar_wait(tc::smem_addr(&b.ring->full[s.stage]), s.phase, b.gave_up)) return false;
         tc::fence_after();
         const uint64_t x = tc::operand(tc::smem_addr(b.stage_a + s.stage * kOperand), a_mn, kBlockBytes);
@@ -204,7 +213,8 @@ __device__ __forceinline__ Part part_of(const Block& b, uint32_t tile)
     p.tmem = b.tmem + acc * S::kTile + ((uint32_t)(w * 32) << 16);
     p.full = tc::smem_addr(&b.ring->acc_full[acc]);
     p.phase = (tile >> 1) & 1;
-    p.empty = tc::in_cta(tc::smem_addr(&b.ring->acc_empty[acc]), 0);
+    p.empty = tc::smem_addr(&b.ring->acc_empty[acc]);
+    if (S::CTAS == 2) p.empty = tc::in_cta(p.empty, 0);
     p.row = w * 32;
     p.c0 = (warp - 4) / 4 * (S::kTile / 2);
     p.c1 = p.c0 + S::kTile / 2;

@@ -13,7 +13,7 @@ namespace {
 using namespace core;
 
 constexpr int kStaging = 32 * kChunk * 2;       // bytes of shared memory an epilogue warp takes its columns through
-constexpr int kSmem = smem_bytes(kEpilogueWarps * kStaging + 2 * (kMaxExperts + 2) * (int)sizeof(int));
+constexpr int kSmem = smem_bytes<Shape<1>>(kEpilogueWarps * kStaging + 2 * (kMaxExperts + 2) * (int)sizeof(int));
 static_assert(kSmem <= 227 * 1024, "the SM's shared memory");
 
 struct Tile {
@@ -152,7 +152,7 @@ template <class S, bool A_MN, bool B_MN, bool K_GROUPED>
 __global__ void __launch_bounds__(kThreads, 1) expert_products(const __grid_constant__ Problems q)
 {
     extern __shared__ __align__(1024) unsigned char dynamic[];
-    Block b = block_of(dynamic);
+    Block b = block_of<S>(dynamic);
     unsigned char* const staging = b.own;
     int* const start = reinterpret_cast<int*>(staging + kEpilogueWarps * kStaging);
     int* const rows = start + kMaxExperts + 2;
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_products(const __grid_cons
                 ok = copy_step<S>(b, n, K_GROUPED && k + kStep > tile.k_end, &q.a, A_MN, m, 0, &q.b, B_MN, nn, K_GROUPED ? 0 : tile.problem, (int)k);
             }
         }
-        finish_copies(b, n, ok);
+        finish_copies<S>(b, n, ok);
     } else if (warp == 1 && b.rank == 0 && tc::elect_one()) {
         const uint32_t instr = tc::instruction(q.p.dtype == EMB_BF16, A_MN, B_MN, S::kTile, S::kTile);
         uint32_t n = 0, made = 0;
@@ -193,16 +193,16 @@ __global__ void __launch_bounds__(kThreads, 1) expert_products(const __grid_cons
         }
     } else if (warp == 2 && K_GROUPED) {
         // zero the rows past a group in its last step, then hand the step on
-        uint32_t n = 0, turns[kStages] = {};
+        uint32_t n = 0, turns[S::kStages] = {};
         bool ok = true;
         for (int64_t t = first; ok && t < total; t += step) {
             const Tile tile = list.at(t);
             const int left = (int)((tile.k_end - tile.k0) % kStep);
             if (tile.steps && left) {
-                const uint32_t s = (n + tile.steps - 1) % kStages;
+                const uint32_t s = (n + tile.steps - 1) % S::kStages;
                 uint32_t turn = 0;
 #pragma unroll
-                for (int i = 0; i < kStages; ++i)
+                for (int i = 0; i < S::kStages; ++i)
                     if (i == (int)s) turn = turns[i]++;
                 ok = tc::bar_wait_warp(tc::smem_addr(&b.ring->part[s]), turn & 1, b.gave_up);
                 if (ok) {

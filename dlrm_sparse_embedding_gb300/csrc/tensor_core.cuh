@@ -92,6 +92,32 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     return true;
 }
 
+// bar_wait_warp for what other CTAs of the cluster stored here.
+__device__ __forceinline__ bool bar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* gave_up)
+{
+    const auto reached = [&] {
+        uint32_t ok;
+        asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\nselp.b32 %0, 1, 0, p;\n}"
+                     : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+        return ok != 0;
+    };
+    bool ok = reached();
+    const uint64_t start = now_ns();
+    while (!ok) {
+        if (*gave_up) break;
+        if (now_ns() - start > kWaitLimitNs) *gave_up = 1;
+        ok = reached();
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+// `bytes` of this CTA's shared memory to another one's; they count on its barrier `bar`.
+__device__ __forceinline__ void copy_cluster(uint32_t to, uint32_t from, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(to), "r"(from), "r"(bytes), "r"(bar) : "memory");
+}
+
 // The same by a whole warp, with one answer for all its lanes.
 __device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity, volatile int* gave_up)
 {
