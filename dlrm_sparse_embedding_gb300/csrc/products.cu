@@ -5,6 +5,8 @@
 // in its row.  Where they are k (a weight's gradient), the last step's rows past
 // the group are zeroed in shared memory, in both operands, before it is
 // multiplied: 0 times an infinity or a NaN of the next group would not be 0.
+#include <algorithm>
+
 #include "product_core.cuh"
 
 namespace emb {
@@ -281,6 +283,18 @@ int launch_shape(Problems& q, cudaStream_t st)
     return q.p.b_mn ? launch<S, false, true, false>(q, st) : launch<S, false, false, false>(q, st);
 }
 
+// About how long a product takes with tiles of `tile` on `units` CTAs or pairs, in
+// 64-wide steps: a step takes either the same, it is bound by its 32 KB from L2,
+// and `fixed` more go by at a tile's ends.  How the rows are dealt out to the groups
+// is not known here: a group is taken to end in the middle of a tile.
+double estimate(const ProductArgs& p, int tile, int units, int fixed)
+{
+    const auto along = [&](int64_t v) { return (double)((v + tile - 1) / tile); };
+    const double rows = (double)(p.k_grouped ? p.k : p.m) / p.experts, steps = (p.k_grouped ? rows : (double)p.k) / kStep;
+    const double tiles_m = p.k_grouped ? along(p.m) : std::max(1.0, rows / tile + 0.5);
+    return std::max(1.0, p.experts * tiles_m * along(p.n) / units) * (steps + fixed);
+}
+
 }  // namespace
 
 int launch_product(const ProductArgs& p, cudaStream_t st)
@@ -288,10 +302,12 @@ int launch_product(const ProductArgs& p, cudaStream_t st)
     if (!p.k_grouped && !p.b_mn && p.m <= kFewRows) return launch_few_rows(p, st);
     Problems q;
     q.p = p;
-    // pairs where they have work for the whole GPU and groups are not mostly smaller than half their tile
-    const int64_t big = ((p.m + 255) / 256) * ((p.n + 255) / 256) * (p.k_grouped ? p.experts : 1);
-    if (big >= 76 && (p.k_grouped || p.m >= 128 * (int64_t)p.experts)) return launch_shape<Shape<2>>(q, st);
-    return launch_shape<Shape<1>>(q, st);
+    const int sms = device().sms;
+    if (!sms) return EMB_ERR_CUDA;
+    // Measured, single CTAs and pairs: 2488 rows, 12 groups, 1032 x 776: 17.0 and 12.0 us (1.2 rounds of tiles against 0.8);
+    // 192 rows, 64 groups, 1024 x 2048: 44.2 and 47.1 us (one tile a group either way); a weight's gradient of 4096 rows,
+    // 16 groups, 3328 x 1024: 45.9 and 33.5 us; 512 rows, 8 groups, 512 x 512: 5.2 and 7.2 us.
+    return estimate(p, 2 * kRows, sms / 2, 10) < estimate(p, kRows, sms, 6) ? launch_shape<Shape<2>>(q, st) : launch_shape<Shape<1>>(q, st);
 }
 
 }  // namespace emb
