@@ -249,9 +249,8 @@ int start(const Input& q, const T* g, int64_t batch, cudaStream_t st)
 // ---------------------------------------------------------------------------
 // the steps
 // ---------------------------------------------------------------------------
-// All products of all steps are one list of tiles for one persistent grid: step
-// by step, in a step A's, B's and then X's tiles, in each the matrices one after
-// another.  A tile needs its own matrix's earlier tiles and no other's, so
+// All products of all steps are one list of tiles for one persistent grid (see
+// Walk).  A tile needs its own matrix's earlier tiles and no other's, so
 // matrices run into each other's products instead of waiting at 3 x steps
 // launches; a counter a matrix says how far it is.  CTAs take tiles in the
 // list's order, and the launch is cooperative, so what a tile waits for is done
@@ -351,9 +350,12 @@ __device__ __forceinline__ Tile tile_of(const Steps& q, int step, Product produc
     return r;
 }
 
-// The tiles of one CTA, in the list's order.  Without a shared k they are dealt out
-// over the whole list; with one, A's tiles go to clusters and the others to CTAs,
-// product by product.
+// The tiles of one CTA, in the list's order: step by step, in a step A's, B's and
+// then X's, in each the matrices one after another.  Without a shared k they are
+// dealt out over the whole list; with one, A's tiles go to clusters and the others
+// to CTAs, product by product.  (Half the matrices half a step behind the others, so
+// that products bound by memory and by the tensor cores run side by side, measured
+// the same: 1044 us for 16 of 1024 x 3328, against 1016.)
 template <class S>
 struct Walk {
     const Steps& q;
@@ -615,9 +617,10 @@ __device__ __forceinline__ bool send_parts(const Block& b, Counts* counts, const
     return true;
 }
 
-// What the epilogue reads of C, asked for while the tile's products still run:
-// one warp goes a tile ahead, waits for the matrix and has the low parts of X
-// brought to L2 (the high parts come with the products' operands).
+// One warp goes two tiles ahead of the epilogue: it waits until the tile's matrix is
+// far enough, for the copies and the epilogue alike (each would wait 2000 cycles a
+// tile for L2's answer and the fence), and has the low parts of X brought to L2 (the
+// high parts come with the products' operands).
 template <class S>
 __device__ __forceinline__ void scout(const Steps& q, const Block& b, Counts* s)
 {
@@ -625,11 +628,12 @@ __device__ __forceinline__ void scout(const Steps& q, const Block& b, Counts* s)
     int n = 0;
     for (Walk<S> walk(q); walk.more(); walk.next(), ++n) {
         const Tile tile = walk.tile();
-        if (!__all_sync(0xffffffffu, wait_count(&s->taken, n - 1, b.gave_up))) return;
-        if (tile.product != kGram) {
-            if (!__all_sync(0xffffffffu, wait_done(q.done + tile.matrix, tile.needs, b.gave_up))) return;
+        if (!__all_sync(0xffffffffu, wait_count(&s->taken, n - 2, b.gave_up))) return;
+        if (!__all_sync(0xffffffffu, wait_done(q.done + tile.matrix, tile.needs, b.gave_up))) return;
+        if (lane == 0) {
+            tc::fence_async();   // the copies to come read what other SMs' plain stores wrote
+            set_count(&s->ahead, n + 1);
         }
-        if (lane == 0) set_count(&s->ahead, n + 1);
         if (tile.product == kUpdate && (tile.step || q.low_in)) {
             const int64_t width = q.ld - tile.n0 < S::kTile ? q.ld - tile.n0 : S::kTile;
             for (int r = lane; r < kRows; r += 32) {
@@ -668,6 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) newton_schulz(const __grid_consta
 
     if (warp == 0 && tc::elect_one()) {
         uint32_t n = 0;
+        int begun = 0;
         bool ok = true;
         for (Walk<S> walk(q); ok && walk.more(); walk.next()) {
             const Tile tile = walk.tile();
@@ -687,8 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1) newton_schulz(const __grid_consta
             tc::prefetch_map(mb);
             int from, to;
             part_steps<S>(tile, b.rank, from, to);
-            ok = wait_done(q.done + tile.matrix, tile.needs, b.gave_up);
-            tc::fence_async();
+            ok = wait_count(&counts->ahead, ++begun, b.gave_up);
             for (int i = from; ok && i < to; ++i, ++n) ok = copy_step<S>(b, n, false, ma, a_mn, m, z, mb, b_mn, nn, z, i * kStep);
         }
         finish_copies<S>(b, n, ok);
@@ -756,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) newton_schulz(const __grid_consta
                 // every CTA has used what came from here: the room for it is free again
                 ok = ok && tc::bar_wait_warp(tc::smem_addr(&counts->sent), turn, b.gave_up);
             } else {
-                ok = tile.product == kGram || __all_sync(0xffffffffu, wait_count(&counts->ahead, made + 1, b.gave_up));
+                ok = __all_sync(0xffffffffu, wait_count(&counts->ahead, made + 1, b.gave_up));
                 if (ok)
                     ok = tile.product == kGram        ? finish<S, kGram>(q, tile, part, mine, b.rank, 1, 0, 0, b.gave_up)
                          : tile.product == kQuadratic ? finish<S, kQuadratic>(q, tile, part, mine, b.rank, 1, 0, 0, b.gave_up)
