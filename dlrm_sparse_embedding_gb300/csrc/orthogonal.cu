@@ -559,7 +559,7 @@ __device__ __forceinline__ bool finish(const Steps& q, const Tile& tile, const P
                 uint4 top, rest;
                 split8(o, top, rest);
                 *reinterpret_cast<uint4*>(d + i * 8 * ld + c) = top;
-                *reinterpret_cast<uint4*>(d_low + i * 8 * ld + c) = rest;
+                __stcs(reinterpret_cast<uint4*>(d_low + i * 8 * ld + c), rest);
             } else {
                 *reinterpret_cast<uint4*>(d + i * 8 * ld + c) = pack8<__half>(o);
             }
