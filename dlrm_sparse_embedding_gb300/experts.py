@@ -20,16 +20,10 @@ MAX_EXPERTS = 1024
 MAX_EXPERTS_PER_TOKEN = 64
 
 
-def on_stream(call):
-    """Gives `call` a `stream` argument: with one, it runs, and what it returns is
-    allocated, on that stream instead of the current one."""
-    @functools.wraps(call)
-    def run(*args, stream=None, **kwargs):
-        if stream is None:
-            return call(*args, **kwargs)
-        with torch.cuda.stream(stream):
-            return call(*args, **kwargs)
-    return run
+def _on(stream, call, *args):
+    """`call` on another stream: what it returns is allocated for that stream."""
+    with torch.cuda.stream(stream):
+        return call(*args)
 
 
 def _stream(device: torch.device) -> int:
@@ -37,32 +31,37 @@ def _stream(device: torch.device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _matrix(t, name: str, rows: int, width: Optional[int] = None, dtype=None, device=None) -> int:
-    """Checks a [rows, width] matrix with contiguous rows; returns its row stride."""
+def _matrix(t, name: str, rows: int, device, width: Optional[int] = None):
+    """Checks a [rows, width] matrix with contiguous rows on `device`; returns its
+    address, type code, row stride and width."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError("%s must be a 2-d torch tensor" % name)
-    if t.dtype not in _DTYPE_CODE:
+    code = _DTYPE_CODE.get(t.dtype)
+    if code is None:
         raise ValueError("%s must be float32, float16 or bfloat16, got %s" % (name, t.dtype))
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
     n, w = t.shape
-    if n != rows or (width is not None and w != width) or w < 1:
+    if n != rows or w < 1 or (width is not None and w != width):
         raise ValueError("%s must have shape (%d, %s), got %s" % (name, rows, width or "width", tuple(t.shape)))
-    if device is not None and t.device != device:
+    if t.device != device:
         raise ValueError("%s is on %s, the plan on %s" % (name, t.device, device))
     s, c = t.stride()
     if n <= 1:
         s = w
-    if (c != 1 and w > 1) or s < w:
+    if s < w or (c != 1 and w > 1):
         raise ValueError("%s must have contiguous rows that do not overlap" % name)
-    return s
+    return t.data_ptr(), code, s, w
 
 
-def _dtype(dtype, default) -> torch.dtype:
-    dtype = default if dtype is None else dtype
-    if dtype not in _DTYPE_CODE:
+def _dtype(dtype) -> int:
+    code = _DTYPE_CODE.get(dtype)
+    if code is None:
         raise ValueError("dtype must be float32, float16 or bfloat16, got %s" % (dtype,))
-    return dtype
+    return code
+
+
+def _indices(t, name: str, dims: int) -> None:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %d-d int32 tensor" % (name, dims))
 
 
 class ExpertPlan:
@@ -76,12 +75,13 @@ class ExpertPlan:
     __slots__ = ("offsets", "src", "pos", "tokens", "k", "experts", "assignments", "device", "_c", "_ref")
 
     def __init__(self, offsets: torch.Tensor, src: torch.Tensor, pos: torch.Tensor):
-        for t, name, dims in ((offsets, "offsets", 1), (src, "src", 1), (pos, "pos", 2)):
-            if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous():
-                raise ValueError("%s must be a contiguous %d-d int32 tensor" % (name, dims))
-        for t, name in ((offsets, "offsets"), (src, "src"), (pos, "pos")):
-            if not t.is_cuda or t.device != offsets.device:
-                raise ValueError("%s must be a CUDA tensor on the plan's device" % name)
+        _indices(offsets, "offsets", 1)
+        _indices(src, "src", 1)
+        _indices(pos, "pos", 2)
+        device = offsets.device
+        if not (offsets.is_cuda and src.device == device and pos.device == device):
+            raise ValueError("offsets, src and pos must be CUDA tensors on one device, got %s, %s and %s"
+                             % (device, src.device, pos.device))
         T, k = pos.shape
         E = offsets.shape[0] - 1
         if not 1 <= k <= MAX_EXPERTS_PER_TOKEN or not 1 <= E <= MAX_EXPERTS:
@@ -89,7 +89,7 @@ class ExpertPlan:
                              % (MAX_EXPERTS, MAX_EXPERTS_PER_TOKEN, E, k))
         if src.shape[0] != T * k:
             raise ValueError("src holds %d assignments, pos %d" % (src.shape[0], T * k))
-        self._set(offsets, src, pos, T, k, E, offsets.device)
+        self._set(offsets, src, pos, T, k, E, device)
 
     def _set(self, offsets, src, pos, T, k, E, device):
         self.offsets, self.src, self.pos = offsets, src, pos
@@ -112,13 +112,14 @@ def _sort_workspace(tokens: int, k: int, experts: int) -> int:
     return n.value
 
 
-@on_stream
-def expert_sort(ids: torch.Tensor, num_experts: int) -> ExpertPlan:
+def expert_sort(ids: torch.Tensor, num_experts: int, stream=None) -> ExpertPlan:
     """The plan of int32 or int64 ids [tokens, k] of experts in [0, num_experts).
 
     A stable sort: within an expert, assignments stay in order.  -1 marks an
     assignment without an expert; any other id outside the range is treated the
     same way and reported by dense_status()."""
+    if stream is not None:
+        return _on(stream, expert_sort, ids, num_experts)
     if not isinstance(ids, torch.Tensor) or ids.dtype not in (torch.int32, torch.int64):
         raise ValueError("ids must be an int32 or int64 tensor")
     if ids.dim() != 2 or not ids.is_contiguous():
@@ -141,79 +142,88 @@ def expert_sort(ids: torch.Tensor, num_experts: int) -> ExpertPlan:
     return plan
 
 
-@on_stream
-def expert_dispatch(plan: ExpertPlan, x: torch.Tensor, dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+def expert_dispatch(plan: ExpertPlan, x: torch.Tensor, dtype: Optional[torch.dtype] = None,
+                    stream=None) -> torch.Tensor:
     """Rows [tokens * k, width] in expert order of x [tokens, width], in `dtype`
     (default x's); the rows after the last group are zero."""
-    plan = _plan(plan)
-    stride = _matrix(x, "x", plan.tokens, device=plan.device)
-    dtype = _dtype(dtype, x.dtype)
-    width = x.shape[1]
-    rows = torch.empty((plan.assignments, width), dtype=dtype, device=plan.device)
-    check(lib.emb_expert_dispatch(plan._ref, x.data_ptr(), _DTYPE_CODE[x.dtype], stride, width, rows.data_ptr(),
-                                  _DTYPE_CODE[dtype], _stream(plan.device)), "emb_expert_dispatch")
+    if stream is not None:
+        return _on(stream, expert_dispatch, plan, x, dtype)
+    device = _plan(plan).device
+    ptr, code, stride, width = _matrix(x, "x", plan.tokens, device)
+    dtype = dtype or x.dtype
+    out_code = _dtype(dtype)
+    rows = torch.empty((plan.assignments, width), dtype=dtype, device=device)
+    check(lib.emb_expert_dispatch(plan._ref, ptr, code, stride, width, rows.data_ptr(), out_code, _stream(device)),
+          "emb_expert_dispatch")
     return rows
 
 
-@on_stream
-def expert_dispatch_grad(plan: ExpertPlan, grad_rows: torch.Tensor, dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+def expert_dispatch_grad(plan: ExpertPlan, grad_rows: torch.Tensor, dtype: Optional[torch.dtype] = None,
+                         stream=None) -> torch.Tensor:
     """Gradient [tokens, width] of expert_dispatch's x, in `dtype` (default grad_rows's)."""
-    plan = _plan(plan)
-    stride = _matrix(grad_rows, "grad_rows", plan.assignments, device=plan.device)
-    dtype = _dtype(dtype, grad_rows.dtype)
-    width = grad_rows.shape[1]
-    grad_x = torch.empty((plan.tokens, width), dtype=dtype, device=plan.device)
-    check(lib.emb_expert_dispatch_grad(plan._ref, grad_rows.data_ptr(), _DTYPE_CODE[grad_rows.dtype], stride, width,
-                                       grad_x.data_ptr(), _DTYPE_CODE[dtype], _stream(plan.device)),
-          "emb_expert_dispatch_grad")
+    if stream is not None:
+        return _on(stream, expert_dispatch_grad, plan, grad_rows, dtype)
+    device = _plan(plan).device
+    ptr, code, stride, width = _matrix(grad_rows, "grad_rows", plan.assignments, device)
+    dtype = dtype or grad_rows.dtype
+    out_code = _dtype(dtype)
+    grad_x = torch.empty((plan.tokens, width), dtype=dtype, device=device)
+    check(lib.emb_expert_dispatch_grad(plan._ref, ptr, code, stride, width, grad_x.data_ptr(), out_code,
+                                       _stream(device)), "emb_expert_dispatch_grad")
     return grad_x
 
 
-def _weights(plan, weights) -> None:
+def _weights(plan, weights) -> int:
     if (not isinstance(weights, torch.Tensor) or weights.dtype != torch.float32 or not weights.is_contiguous()
-            or tuple(weights.shape) != (plan.tokens, plan.k)):
+            or weights.shape != plan.pos.shape):
         raise ValueError("weights must be contiguous float32 [%d, %d]" % (plan.tokens, plan.k))
     if weights.device != plan.device:
         raise ValueError("weights is on %s, the plan on %s" % (weights.device, plan.device))
+    return weights.data_ptr()
 
 
-@on_stream
-def expert_combine(plan: ExpertPlan, rows: torch.Tensor, weights: torch.Tensor, dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+def expert_combine(plan: ExpertPlan, rows: torch.Tensor, weights: torch.Tensor, dtype: Optional[torch.dtype] = None,
+                   stream=None) -> torch.Tensor:
     """[tokens, width]: each token's rows, weighted by float32 weights [tokens, k]
     and added in fp32, in `dtype` (default rows's)."""
-    plan = _plan(plan)
-    stride = _matrix(rows, "rows", plan.assignments, device=plan.device)
-    _weights(plan, weights)
-    dtype = _dtype(dtype, rows.dtype)
-    width = rows.shape[1]
-    out = torch.empty((plan.tokens, width), dtype=dtype, device=plan.device)
-    check(lib.emb_expert_combine(plan._ref, rows.data_ptr(), _DTYPE_CODE[rows.dtype], stride, weights.data_ptr(),
-                                 width, out.data_ptr(), _DTYPE_CODE[dtype], _stream(plan.device)), "emb_expert_combine")
+    if stream is not None:
+        return _on(stream, expert_combine, plan, rows, weights, dtype)
+    device = _plan(plan).device
+    ptr, code, stride, width = _matrix(rows, "rows", plan.assignments, device)
+    weights_ptr = _weights(plan, weights)
+    dtype = dtype or rows.dtype
+    out_code = _dtype(dtype)
+    out = torch.empty((plan.tokens, width), dtype=dtype, device=device)
+    check(lib.emb_expert_combine(plan._ref, ptr, code, stride, weights_ptr, width, out.data_ptr(), out_code,
+                                 _stream(device)), "emb_expert_combine")
     return out
 
 
-@on_stream
-def expert_combine_grad(plan: ExpertPlan, grad_out: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor):
+def expert_combine_grad(plan: ExpertPlan, grad_out: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor,
+                        stream=None):
     """(grad_rows in rows's dtype, grad_weights float32 [tokens, k]) of expert_combine."""
-    plan = _plan(plan)
-    stride = _matrix(rows, "rows", plan.assignments, device=plan.device)
-    width = rows.shape[1]
-    grad_stride = _matrix(grad_out, "grad_out", plan.tokens, width, device=plan.device)
-    _weights(plan, weights)
-    grad_rows = torch.empty((plan.assignments, width), dtype=rows.dtype, device=plan.device)
-    grad_weights = torch.empty((plan.tokens, plan.k), dtype=torch.float32, device=plan.device)
-    check(lib.emb_expert_combine_grad(plan._ref, grad_out.data_ptr(), _DTYPE_CODE[grad_out.dtype], grad_stride,
-                                      rows.data_ptr(), _DTYPE_CODE[rows.dtype], stride, weights.data_ptr(), width,
-                                      grad_rows.data_ptr(), grad_weights.data_ptr(), _stream(plan.device)),
+    if stream is not None:
+        return _on(stream, expert_combine_grad, plan, grad_out, rows, weights)
+    device = _plan(plan).device
+    ptr, code, stride, width = _matrix(rows, "rows", plan.assignments, device)
+    grad_ptr, grad_code, grad_stride, _ = _matrix(grad_out, "grad_out", plan.tokens, device, width)
+    weights_ptr = _weights(plan, weights)
+    grad_rows = torch.empty((plan.assignments, width), dtype=rows.dtype, device=device)
+    grad_weights = torch.empty((plan.tokens, plan.k), dtype=torch.float32, device=device)
+    check(lib.emb_expert_combine_grad(plan._ref, grad_ptr, grad_code, grad_stride, ptr, code, stride, weights_ptr, width,
+                                      grad_rows.data_ptr(), grad_weights.data_ptr(), _stream(device)),
           "emb_expert_combine_grad")
     return grad_rows, grad_weights
 
 
-def _linear(plan, t, name, width, dtype) -> int:
-    s = _matrix(t, name, plan.assignments, width, dtype, plan.device)
-    if s % 8 or t.data_ptr() % 16:
+def _operand(plan, t, name, width, code):
+    """_matrix for an operand of the products; returns its address and row stride."""
+    ptr, c, stride, _ = _matrix(t, name, plan.assignments, plan.device, width)
+    if c != code:
+        raise ValueError("%s must have weight's dtype, got %s" % (name, t.dtype))
+    if stride % 8 or ptr % 16:
         raise ValueError("%s must be 16-byte aligned with a row stride that is a multiple of 8" % name)
-    return s
+    return ptr, stride
 
 
 def _weight(plan, weight):
@@ -222,48 +232,49 @@ def _weight(plan, weight):
     if weight.dim() != 3 or weight.shape[0] != plan.experts or not weight.is_contiguous():
         raise ValueError("weight must be contiguous [%d, out, in], got %s" % (plan.experts, tuple(weight.shape)))
     _, N, K = weight.shape
-    if N % 8 or K % 8 or N < 8 or K < 8 or weight.data_ptr() % 16:
+    ptr = weight.data_ptr()
+    if N % 8 or K % 8 or N < 8 or K < 8 or ptr % 16:
         raise ValueError("weight's out and in widths must be multiples of 8 and its memory 16-byte aligned, got %s"
                          % (tuple(weight.shape),))
     if weight.device != plan.device:
         raise ValueError("weight is on %s, the plan on %s" % (weight.device, plan.device))
-    return N, K
+    return ptr, _DTYPE_CODE[weight.dtype], N, K
 
 
-@on_stream
-def expert_linear(plan: ExpertPlan, rows: torch.Tensor, weight: torch.Tensor) -> torch.Tensor:
+def expert_linear(plan: ExpertPlan, rows: torch.Tensor, weight: torch.Tensor, stream=None) -> torch.Tensor:
     """[tokens * k, out]: each expert's rows times the transpose of its own
     weight [out, in] of ``weight`` [E, out, in]; float16 or bfloat16, fp32 sums.
     Rows after the last group are not read; their products are zero."""
-    plan = _plan(plan)
-    N, K = _weight(plan, weight)
-    stride = _linear(plan, rows, "rows", K, weight.dtype)
-    y = torch.empty((plan.assignments, N), dtype=weight.dtype, device=plan.device)
-    check(lib.emb_expert_linear(plan._ref, rows.data_ptr(), stride, weight.data_ptr(), K, N,
-                                _DTYPE_CODE[weight.dtype], y.data_ptr(), _stream(plan.device)), "emb_expert_linear")
+    if stream is not None:
+        return _on(stream, expert_linear, plan, rows, weight)
+    device = _plan(plan).device
+    weight_ptr, code, N, K = _weight(plan, weight)
+    ptr, stride = _operand(plan, rows, "rows", K, code)
+    y = torch.empty((plan.assignments, N), dtype=weight.dtype, device=device)
+    check(lib.emb_expert_linear(plan._ref, ptr, stride, weight_ptr, K, N, code, y.data_ptr(), _stream(device)),
+          "emb_expert_linear")
     return y
 
 
-@on_stream
 def expert_linear_grad(plan: ExpertPlan, grad_y: torch.Tensor, rows: Optional[torch.Tensor], weight: torch.Tensor,
-                       need_rows: bool = True, need_weight: bool = True):
+                       need_rows: bool = True, need_weight: bool = True, stream=None):
     """(grad_rows, grad_weight) of expert_linear; None in the place of one that is not needed."""
-    plan = _plan(plan)
-    N, K = _weight(plan, weight)
-    grad_stride = _linear(plan, grad_y, "grad_y", N, weight.dtype)
-    code = _DTYPE_CODE[weight.dtype]
-    grad_rows = grad_weight = None
+    if stream is not None:
+        return _on(stream, expert_linear_grad, plan, grad_y, rows, weight, need_rows, need_weight)
+    device = _plan(plan).device
+    weight_ptr, code, N, K = _weight(plan, weight)
+    grad_ptr, grad_stride = _operand(plan, grad_y, "grad_y", N, code)
     if need_weight:
-        stride = _linear(plan, rows, "rows", K, weight.dtype)
+        ptr, stride = _operand(plan, rows, "rows", K, code)
+    grad_rows = grad_weight = None
     if need_rows:
-        grad_rows = torch.empty((plan.assignments, K), dtype=weight.dtype, device=plan.device)
-        check(lib.emb_expert_linear_grad_rows(plan._ref, grad_y.data_ptr(), grad_stride, weight.data_ptr(), K, N,
-                                              code, grad_rows.data_ptr(), _stream(plan.device)),
-              "emb_expert_linear_grad_rows")
+        grad_rows = torch.empty((plan.assignments, K), dtype=weight.dtype, device=device)
+        check(lib.emb_expert_linear_grad_rows(plan._ref, grad_ptr, grad_stride, weight_ptr, K, N, code,
+                                              grad_rows.data_ptr(), _stream(device)), "emb_expert_linear_grad_rows")
     if need_weight:
         grad_weight = torch.empty_like(weight)
-        check(lib.emb_expert_linear_grad_weight(plan._ref, grad_y.data_ptr(), grad_stride, rows.data_ptr(), stride,
-                                                K, N, code, grad_weight.data_ptr(), _stream(plan.device)),
+        check(lib.emb_expert_linear_grad_weight(plan._ref, grad_ptr, grad_stride, ptr, stride, K, N, code,
+                                                grad_weight.data_ptr(), _stream(device)),
               "emb_expert_linear_grad_weight")
     return grad_rows, grad_weight
 

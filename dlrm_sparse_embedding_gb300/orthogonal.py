@@ -8,7 +8,7 @@ from typing import Optional, Tuple
 import torch
 
 from ._lib import check, lib
-from .experts import _DTYPE_CODE, _stream, on_stream
+from .experts import _DTYPE_CODE, _on, _stream
 
 #: K. Jordan et al., "Muon" (2024)
 COEFFICIENTS = (3.4445, -4.7750, 2.0315)
@@ -21,9 +21,8 @@ def _workspace(batch: int, rows: int, cols: int) -> int:
     return n.value
 
 
-@on_stream
 def orthogonalize(update: torch.Tensor, steps: int = 5, coefficients: Tuple[float, float, float] = COEFFICIENTS,
-                  eps: float = 1e-7, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                  eps: float = 1e-7, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """bfloat16 [..., rows, cols]: each matrix of `update` (float32, float16 or
     bfloat16) with its singular values driven towards 1, by `steps` steps
     X <- a X + (b A + c A A) X, A = X X^T, from X = update / (|update|_F + eps).
@@ -31,6 +30,8 @@ def orthogonalize(update: torch.Tensor, steps: int = 5, coefficients: Tuple[floa
     update: [rows, cols] or [batch, rows, cols] with contiguous rows, rows and
     cols up to 65536; steps 1 to 32.  out, if given, is contiguous bfloat16 of
     update's shape and may not overlap it."""
+    if stream is not None:
+        return _on(stream, orthogonalize, update, steps, coefficients, eps, out)
     if not isinstance(update, torch.Tensor) or update.dim() not in (2, 3):
         raise ValueError("update must be a 2-d or 3-d torch tensor")
     if update.dtype not in _DTYPE_CODE:
