@@ -195,8 +195,8 @@ __device__ __forceinline__ void put_scaled(const Input& q, const T* g, double su
             l[i] = kLowScale * (h[i] - __half2float(__float2half_rn(h[i])));
         }
         if constexpr (V == 8) {
-            *reinterpret_cast<uint4*>(q.x + at + row * q.ld + c) = pack8<__half>(h);
-            if (sizeof(T) == 4) *reinterpret_cast<uint4*>(q.x_low + at + row * q.ld + c) = pack8<__half>(l);
+            *reinterpret_cast<uint4*>(q.x + at + row * q.ld + c) = core::pack8<__half>(h);
+            if (sizeof(T) == 4) *reinterpret_cast<uint4*>(q.x_low + at + row * q.ld + c) = core::pack8<__half>(l);
         } else {
             q.x[at + row * q.ld + c] = __float2half_rn(h[0]);
             if (sizeof(T) == 4) q.x_low[at + row * q.ld + c] = __float2half_rn(l[0]);
@@ -510,38 +510,45 @@ __device__ __forceinline__ bool finish(const Steps& q, const Tile& tile, const P
             const int r = i * 8 + r0, turn = (r & 7) ^ ((r >> 3) << 1);
             float4* const px = reinterpret_cast<float4*>(mine + r * kChunk + (((2 * p) ^ turn) * 4));
             float4* const py = reinterpret_cast<float4*>(mine + r * kChunk + (((2 * p + 1) ^ turn) * 4));
-            float o[8] = {};
+            float2 o[4] = {};
             if constexpr (!SHARED) {
                 const float4 x = *px, y = *py;
-                o[0] = x.x, o[1] = x.y, o[2] = x.z, o[3] = x.w, o[4] = y.x, o[5] = y.y, o[6] = y.z, o[7] = y.w;
+                o[0] = make_float2(x.x, x.y), o[1] = make_float2(x.z, x.w), o[2] = make_float2(y.x, y.y), o[3] = make_float2(y.z, y.w);
             } else {
 #pragma unroll
                 for (int k = 0; k < S::SPLIT; ++k)
                     if (parts >> k & 1) {   // part k, 128 rows further on
                         const float4 x = px[k * (4 * kStaging / 16)], y = py[k * (4 * kStaging / 16)];
-                        o[0] += x.x, o[1] += x.y, o[2] += x.z, o[3] += x.w, o[4] += y.x, o[5] += y.y, o[6] += y.z, o[7] += y.w;
+                        o[0] = add2(o[0], make_float2(x.x, x.y)), o[1] = add2(o[1], make_float2(x.z, x.w));
+                        o[2] = add2(o[2], make_float2(y.x, y.y)), o[3] = add2(o[3], make_float2(y.z, y.w));
                     }
             }
             if (F == kGram) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] *= s;
+                for (int j = 0; j < 4; ++j) o[j] = mul2(both(s), o[j]);
             } else {
-                float cv[8];
-                unpack8(ch[i], cv);
+                float2 cv[4];
                 if (F == kUpdate) {
-                    float lv[8];
-                    unpack8(cl[i], lv);
+                    join8(ch[i], cl[i], cv);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) o[j] = s * __fmaf_rn(beta, __fmaf_rn(1.f / kLowScale, lv[j], cv[j]), o[j]);
+                    for (int j = 0; j < 4; ++j) o[j] = mul2(both(s), fma2(both(beta), cv[j], o[j]));
                 } else {
-                    const int64_t on = m_first + r - n;   // which of them is on the diagonal
+                    unpack8(ch[i], cv);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) o[j] = __fmaf_rn(beta, cv[j], q.cc * o[j]) + (on == j ? diagonal : 0.f);
+                    for (int j = 0; j < 4; ++j) o[j] = fma2(both(beta), cv[j], mul2(both(q.cc), o[j]));
+                    const int64_t on = m_first + r - n;   // which of them is on the diagonal
+                    if (diagonal != 0.f && on >= 0 && on < 8) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (on == 2 * j) o[j].x += diagonal;
+                            if (on == 2 * j + 1) o[j].y += diagonal;
+                        }
+                    }
                 }
             }
             if (F != kUpdate && tile.m0 != tile.n0) {   // for the transpose below
-                *px = make_float4(o[0], o[1], o[2], o[3]);
-                *py = make_float4(o[4], o[5], o[6], o[7]);
+                *px = make_float4(o[0].x, o[0].y, o[1].x, o[1].y);
+                *py = make_float4(o[2].x, o[2].y, o[3].x, o[3].y);
             }
             if (n >= width || r >= rows) continue;
             if (last) {
@@ -551,7 +558,7 @@ __device__ __forceinline__ bool finish(const Steps& q, const Tile& tile, const P
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        if (n + j < width) to[j] = __float2bfloat16_rn(o[j]);
+                        if (n + j < width) to[j] = __float2bfloat16_rn(j & 1 ? o[j / 2].y : o[j / 2].x);
                 }
                 continue;
             }
@@ -607,7 +614,7 @@ __device__ __forceinline__ bool send_parts(const Block& b, Counts* counts, const
             *reinterpret_cast<uint4*>(mine + lane * kChunk * 4 + ((i ^ (lane & 7) ^ ((lane >> 3) << 1)) * 16)) =
                 make_uint4(v[g][4 * i], v[g][4 * i + 1], v[g][4 * i + 2], v[g][4 * i + 3]);
     }
-    tc::fence_async();
+    tc::fence_async_shared();
     __syncwarp();
     if (lane < 2) {
         const uint32_t to = half * 2 + lane;

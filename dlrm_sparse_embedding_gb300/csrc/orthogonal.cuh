@@ -26,29 +26,51 @@ struct StepsArgs {
 
 int run_short(const StepsArgs& p, cudaStream_t st);
 
-__device__ __forceinline__ void unpack8(const uint4& p, float (&v)[8])
+// Two fp32 products and sums at once, each rounded once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
+          "l"(*reinterpret_cast<unsigned long long*>(&c)));
+    return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Eight fp16 numbers as four pairs.
+__device__ __forceinline__ void unpack8(const uint4& p, float2 (&v)[4])
 {
     const uint32_t w[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        v[2 * i] = f.x, v[2 * i + 1] = f.y;
-    }
+    for (int i = 0; i < 4; ++i) v[i] = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
 }
 
-// v as two fp16 numbers each, two at a time.
-__device__ __forceinline__ void split8(const float (&v)[8], uint4& high, uint4& low)
+template <class T>
+__device__ __forceinline__ uint4 pack8(const float2 (&v)[4])
 {
-    high = core::pack8<__half>(v);
-    const uint32_t h[4] = {high.x, high.y, high.z, high.w};
-    uint32_t l[4];
+    return make_uint4(core::pack2<T>(v[0].x, v[0].y), core::pack2<T>(v[1].x, v[1].y), core::pack2<T>(v[2].x, v[2].y), core::pack2<T>(v[3].x, v[3].y));
+}
+
+// h + l / kLowScale
+__device__ __forceinline__ void join8(const uint4& high, const uint4& low, float2 (&v)[4])
+{
+    float2 l[4];
+    unpack8(high, v);
+    unpack8(low, l);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 off = sub2(make_float2(v[2 * i], v[2 * i + 1]), __half22float2(*reinterpret_cast<const __half2*>(&h[i])));
-        const float2 up = mul2(off, make_float2(kLowScale, kLowScale));
-        l[i] = core::pack2<__half>(up.x, up.y);
-    }
-    low = make_uint4(l[0], l[1], l[2], l[3]);
+    for (int i = 0; i < 4; ++i) v[i] = fma2(both(1.f / kLowScale), l[i], v[i]);
+}
+
+// v as two fp16 numbers each.
+__device__ __forceinline__ void split8(const float2 (&v)[4], uint4& high, uint4& low)
+{
+    high = pack8<__half>(v);
+    float2 h[4], l[4];
+    unpack8(high, h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) l[i] = mul2(sub2(v[i], h[i]), both(kLowScale));
+    low = pack8<__half>(l);
 }
 
 }  // namespace emb

@@ -67,20 +67,16 @@ struct Matrix {
     unsigned char *high, *low;
 
     __device__ static uint32_t at(int row, int col) { return (col >> 6) * (kMatrix / 2) + row * 128 + ((((col >> 3) & 7) ^ (row & 7)) << 4); }
-    __device__ void store(int row, int col, const float (&v)[8]) const
+    __device__ void store(int row, int col, const float2 (&v)[4]) const
     {
         uint4 h, l;
         split8(v, h, l);
         *reinterpret_cast<uint4*>(high + at(row, col)) = h;
         *reinterpret_cast<uint4*>(low + at(row, col)) = l;
     }
-    __device__ void load(int row, int col, float (&v)[8]) const
+    __device__ void load(int row, int col, float2 (&v)[4]) const
     {
-        float l[8];
-        unpack8(*reinterpret_cast<const uint4*>(high + at(row, col)), v);
-        unpack8(*reinterpret_cast<const uint4*>(low + at(row, col)), l);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __fmaf_rn(1.f / kLowScale, l[j], v[j]);
+        join8(*reinterpret_cast<const uint4*>(high + at(row, col)), *reinterpret_cast<const uint4*>(low + at(row, col)), v);
     }
 };
 
@@ -207,6 +203,7 @@ __global__ void __launch_bounds__(kStepsThreads, 1) short_steps(const __grid_con
     } else if (warp >= 4) {
         // a lane has 32 columns of a row
         const int row = (warp & 3) * 32 + lane, c0 = (warp - 4) / 4 * 32;
+        const bool diagonal = c0 == (warp & 3) * 32;
         const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         uint32_t dones[2] = {};
         bool ok = true;
@@ -216,29 +213,28 @@ __global__ void __launch_bounds__(kStepsThreads, 1) short_steps(const __grid_con
             return ok;
         };
         // every eight columns of a pair of accumulators, added up
-        const auto each = [&](int pair, bool has_low, auto f) {
+        const auto each = [&](int pair, auto f) {
             uint32_t v[32], l[32];
             tc::tmem_load32(mine + pair * 2 * kRows + c0, v);
-            if (has_low) tc::tmem_load32(mine + pair * 2 * kRows + kRows + c0, l);
+            tc::tmem_load32(mine + pair * 2 * kRows + kRows + c0, l);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float o[8];
+                float2 o[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    o[j] = __uint_as_float(v[8 * i + j]);
-                    if (has_low) o[j] = __fmaf_rn(1.f / kLowScale, __uint_as_float(l[8 * i + j]), o[j]);
-                }
+                for (int j = 0; j < 4; ++j)
+                    o[j] = fma2(both(1.f / kLowScale), make_float2(__uint_as_float(l[8 * i + 2 * j]), __uint_as_float(l[8 * i + 2 * j + 1])),
+                                make_float2(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1])));
                 f(c0 + 8 * i, o);
             }
         };
         const auto written = [&] {
-            tc::fence_async();
+            tc::fence_async_shared();
             tc::fence_before();
             __syncwarp();
             if (lane == 0) tc::bar_arrive(tc::smem_addr(&ctl->ready));
         };
-        const auto to_matrix = [&](const Matrix& m) { return [&m, row](int col, const float (&o)[8]) { m.store(row, col, o); }; };
-        const auto to_memory = [&](int col, const float (&o)[8]) {
+        const auto to_matrix = [&](const Matrix& m) { return [&m, row](int col, const float2 (&o)[4]) { m.store(row, col, o); }; };
+        const auto to_memory = [&](int col, const float2 (&o)[4]) {
             uint4 h, l;
             split8(o, h, l);
             const int64_t at = ((int64_t)z * kShort + row) * kShort + col;
@@ -268,9 +264,9 @@ __global__ void __launch_bounds__(kStepsThreads, 1) short_steps(const __grid_con
             if (ok) {
 #pragma unroll
                 for (int c = 0; c < 32; c += 8) {
-                    float o[8];
+                    float2 o[4];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) o[j] = s * sum[c + j];
+                    for (int j = 0; j < 4; ++j) o[j] = mul2(both(s), make_float2(sum[c + 2 * j], sum[c + 2 * j + 1]));
                     A.store(row, c0 + c, o);
                 }
                 written();
@@ -279,11 +275,18 @@ __global__ void __launch_bounds__(kStepsThreads, 1) short_steps(const __grid_con
         for (int i = 0; ok && i < q.steps; ++i) {
             const bool more = i + 1 < q.steps;
             if (!wait_done(0)) break;
-            each(0, true, [&](int col, float (&o)[8]) {
-                float a[8];
+            each(0, [&](int col, float2 (&o)[4]) {
+                float2 a[4];
                 A.load(row, col, a);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = __fmaf_rn(q.b, a[j], q.c * o[j]) + (col + j == row ? q.a : 0.f);
+                for (int j = 0; j < 4; ++j) o[j] = fma2(both(q.b), a[j], mul2(both(q.c), o[j]));
+                if (diagonal) {   // a lane's own row is on it somewhere in these columns
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (col + 2 * j == row) o[j].x += q.a;
+                        if (col + 2 * j + 1 == row) o[j].y += q.a;
+                    }
+                }
                 Q.store(row, col, o);
                 if (i == 0 && more) W.store(row, col, o);
                 if (i == 0 && !more) to_memory(col, o);
@@ -291,17 +294,17 @@ __global__ void __launch_bounds__(kStepsThreads, 1) short_steps(const __grid_con
             written();
             if (more) {
                 if (!wait_done(0)) break;
-                each(0, true, to_matrix(A));
+                each(0, to_matrix(A));
                 written();
             }
             if (i) {
                 if (!wait_done(1)) break;
-                if (more) each(1, true, to_matrix(W));
-                else each(1, true, to_memory);
+                if (more) each(1, to_matrix(W));
+                else each(1, to_memory);
             }
             if (more) {
                 if (!wait_done(0)) break;
-                each(0, true, to_matrix(A));
+                each(0, to_matrix(A));
                 written();
             }
         }
@@ -406,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) short_apply(const __grid_constant
                 if (m >= q.rows || n >= q.cols) continue;
                 const float4 x = *reinterpret_cast<const float4*>(mine + r * kChunk + (((2 * p) ^ (r & 7)) * 4));
                 const float4 y = *reinterpret_cast<const float4*>(mine + r * kChunk + (((2 * p + 1) ^ (r & 7)) * 4));
-                const float o[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                const float2 o[4] = {{x.x, x.y}, {x.z, x.w}, {y.x, y.y}, {y.z, y.w}};
                 if (q.x_out) {
                     const int64_t at = (z * q.rows + m) * q.ld + n;
                     uint4 high, rest;
@@ -421,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) short_apply(const __grid_constant
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        if (n + j < q.cols) to[j] = __float2bfloat16_rn(o[j]);
+                        if (n + j < q.cols) to[j] = __float2bfloat16_rn(j & 1 ? o[j / 2].y : o[j / 2].x);
                 }
             }
             __syncwarp();

@@ -146,6 +146,8 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map)
 
 // Shared-memory writes of this thread before async reads (copies, products) ordered after it.
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+// The same for shared memory alone.
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------
 // tensor memory
