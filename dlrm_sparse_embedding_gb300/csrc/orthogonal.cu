@@ -27,6 +27,7 @@
 // rest of the norm goes into the first step's factors.
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <type_traits>
 
 #include "orthogonal.cuh"
@@ -261,9 +262,10 @@ int start(const Input& q, const T* g, int64_t batch, cudaStream_t st)
 enum Product { kGram, kQuadratic, kUpdate };
 
 //
-// With few tiles the k of A's (the long side) is shared by a cluster: every CTA sums
-// its part of the steps, sends each other one its 32 columns of the sum, and
-// finishes its own 32 columns from the parts it was sent, added in the CTAs' order.
+// With few tiles they are 64 columns wide, and the k of A's (the long side) is
+// shared by a cluster: every CTA sums its part of the steps, sends each other one its
+// 32 rows of the sum, and finishes its own 32 rows from the parts it was sent, added
+// in the CTAs' order.
 constexpr int kSplit = 4;
 constexpr int kStaging = 32 * kChunk * 4;       // bytes of shared memory for 32 rows of 32 columns in fp32
 
@@ -276,10 +278,12 @@ struct Counts {
 constexpr int kCountsBytes = 128;
 static_assert(sizeof(Counts) <= kCountsBytes, "the counts' room");
 
-// Staging: 32 x 32 of a warp, or, of a split tile, the parts that come in and the
-// ones that go out: 4 of 128 rows of 32 columns each.
+// Staging: 32 x 32 of a warp, and where tiles are shared as much again for the parts
+// that come in: 32 rows of 64 columns of each CTA.
 template <class S>
-constexpr int staging_bytes() { return S::SPLIT == 1 ? kEpilogueWarps * kStaging : 2 * S::SPLIT * 4 * kStaging; }
+constexpr int staging_bytes() { return (S::SPLIT == 1 ? 1 : 2) * kEpilogueWarps * kStaging; }
+using Few = Shape<1, kSplit, 64>;
+static_assert(kSplit * 2 == kEpilogueWarps && kSplit * 32 == kRows, "a CTA of a cluster finishes a quarter of a tile's rows");
 template <class S>
 constexpr int own_smem()
 {
@@ -288,17 +292,20 @@ constexpr int own_smem()
 }
 
 struct Steps {
-    CUtensorMap x_gram[2], x_update[2], a_map, b_map;   // x_gram: of A = X X^T; x_update: of X' = B X
+    // operands: x_gram of A = X X^T, x_update of X' = B X (or X B), the `n` ones in the place of B
+    CUtensorMap x_gram[2], x_gram_n[2], x_update[2], a_map, a_map_n, b_map;
     __half *x[2], *x_low[2], *a, *b;
     __nv_bfloat16* out;
     const float* scale;
     unsigned* done;          // of each matrix: CTAs that have finished a tile
     int64_t rows, cols, ld, ldm, m;
+    int64_t long_stride, short_stride;   // between matrices: of X, of A and B
     unsigned batch;
     int steps;
     bool tall;
     float ca, cb, cc;
-    unsigned side, tiles_m, tiles_n;   // tiles along A; of X
+    unsigned squares;        // tiles of A on and below the diagonal
+    unsigned tiles_m, tiles_n;   // of X
     bool low_in;             // the first X has a low part
     int* status;
 };
@@ -314,7 +321,7 @@ struct Tile {
 // How many tiles a matrix has of a product, and how many CTAs finish one.
 __device__ __forceinline__ unsigned tiles_of(const Steps& q, Product p)
 {
-    return p == kUpdate ? q.tiles_m * q.tiles_n : q.side * (q.side + 1) / 2;
+    return p == kUpdate ? q.tiles_m * q.tiles_n : q.squares;
 }
 template <class S>
 __device__ __forceinline__ constexpr unsigned finishers(Product p) { return S::CTAS * (p == kGram ? S::SPLIT : 1); }
@@ -334,17 +341,18 @@ __device__ __forceinline__ Tile tile_of(const Steps& q, int step, Product produc
         r.matrix = index / update;
         const unsigned idx = index - r.matrix * update;
         r.m0 = (int64_t)(idx / q.tiles_n) * S::kTile;
-        r.n0 = (int64_t)(idx % q.tiles_n) * S::kTile;
+        r.n0 = (int64_t)(idx % q.tiles_n) * S::kCols;
     } else {
         if (product == kGram) k = q.rows + q.cols - q.m;
         else r.needs += gram * finishers<S>(kGram);
         r.matrix = index / gram;
         const unsigned idx = index - r.matrix * gram;
-        unsigned i = (unsigned)((sqrtf(8.f * (float)idx + 1.f) - 1.f) * 0.5f);   // row i of the triangle starts at i (i + 1) / 2
-        while (i * (i + 1) / 2 > idx) --i;
-        while ((i + 1) * (i + 2) / 2 <= idx) ++i;
+        constexpr unsigned kWide = S::kTile / S::kCols;   // row i of the triangle starts at kWide i (i + 1) / 2
+        unsigned i = (unsigned)((sqrtf(8.f / kWide * (float)idx + 1.f) - 1.f) * 0.5f);
+        while (kWide * i * (i + 1) / 2 > idx) --i;
+        while (kWide * (i + 1) * (i + 2) / 2 <= idx) ++i;
         r.m0 = (int64_t)i * S::kTile;
-        r.n0 = (int64_t)(idx - i * (i + 1) / 2) * S::kTile;
+        r.n0 = (int64_t)(idx - kWide * i * (i + 1) / 2) * S::kCols;
     }
     r.k_steps = (int)((k + kStep - 1) / kStep);
     return r;
@@ -442,10 +450,10 @@ template <class S, Product F, bool SHARED = (S::SPLIT > 1 && F == kGram)>
 __device__ __forceinline__ bool finish(const Steps& q, const Tile& tile, const Part& part, float* mine, uint32_t rank, unsigned parts,
                                        uint32_t received, uint32_t turn_of, volatile int* gave_up)
 {
-    const int c0 = SHARED ? (int)rank * kChunk : part.c0, c1 = SHARED ? c0 + kChunk : part.c1;
+    const int c0 = part.c0, c1 = part.c1;
     const int lane = threadIdx.x & 31, r0 = lane >> 2, p = lane & 3;
     const int64_t height = F == kUpdate ? q.rows : q.m, width = F == kUpdate ? q.cols : q.m, ld = F == kUpdate ? q.ld : q.ldm;
-    const int64_t m_first = tile.m0 + (S::CTAS == 2 ? rank * kRows : 0) + part.row, left = height - m_first;
+    const int64_t m_first = tile.m0 + (S::CTAS == 2 ? rank * kRows : 0) + (SHARED ? rank * 32 : part.row), left = height - m_first;
     const int rows = left < 0 ? 0 : left > 32 ? 32 : (int)left;
     const int64_t of_matrix = tile.matrix * (F == kUpdate ? q.rows * q.ld : q.m * q.ldm);
     const int64_t at = of_matrix + (m_first + r0) * ld + tile.n0 + p * 8;
@@ -517,8 +525,8 @@ __device__ __forceinline__ bool finish(const Steps& q, const Tile& tile, const P
             } else {
 #pragma unroll
                 for (int k = 0; k < S::SPLIT; ++k)
-                    if (parts >> k & 1) {   // part k, 128 rows further on
-                        const float4 x = px[k * (4 * kStaging / 16)], y = py[k * (4 * kStaging / 16)];
+                    if (parts >> k & 1) {   // part k, 64 columns of 32 rows further on
+                        const float4 x = px[k * (2 * kStaging / 16)], y = py[k * (2 * kStaging / 16)];
                         o[0] = add2(o[0], make_float2(x.x, x.y)), o[1] = add2(o[1], make_float2(x.z, x.w));
                         o[2] = add2(o[2], make_float2(y.x, y.y)), o[3] = add2(o[3], make_float2(y.z, y.w));
                     }
@@ -546,7 +554,7 @@ __device__ __forceinline__ bool finish(const Steps& q, const Tile& tile, const P
                     }
                 }
             }
-            if (F != kUpdate && tile.m0 != tile.n0) {   // for the transpose below
+            if (F != kUpdate && tile.n0 + S::kCols <= tile.m0) {   // for the transpose below
                 *px = make_float4(o[0].x, o[0].y, o[1].x, o[1].y);
                 *py = make_float4(o[2].x, o[2].y, o[3].x, o[3].y);
             }
@@ -572,7 +580,7 @@ __device__ __forceinline__ bool finish(const Steps& q, const Tile& tile, const P
             }
         }
         __syncwarp();
-        if (F != kUpdate && tile.m0 != tile.n0) {
+        if (F != kUpdate && tile.n0 + S::kCols <= tile.m0) {
             // column n of these 32 rows is 32 elements of row n of the other triangle: four lanes store 64 bytes of it
             __half* const t = (F == kGram ? q.a : q.b) + of_matrix + (tile.n0 + c + r0) * ld + m_first + p * 8;
 #pragma unroll
@@ -590,37 +598,30 @@ __device__ __forceinline__ bool finish(const Steps& q, const Tile& tile, const P
     return true;
 }
 
-// A warp's rows of this CTA's part of the sum, two CTAs' columns of them, to those
-// CTAs.
+// A warp's 32 rows and columns of this CTA's part of the sum, to the CTA of those
+// rows.
 template <class S>
-__device__ __forceinline__ bool send_parts(const Block& b, Counts* counts, const Part& part, unsigned char* staging)
+__device__ __forceinline__ bool send_part(const Block& b, Counts* counts, const Part& part, float* mine, unsigned char* received)
 {
-    const int lane = threadIdx.x & 31, half = part.c0 != 0;
+    const int lane = threadIdx.x & 31;
+    const uint32_t to = part.row / 32, half = part.c0 / kChunk;
     if (!tc::bar_wait_warp(part.full, part.phase, b.gave_up)) return false;
     tc::fence_after();
-    uint32_t v[2][32];
-#pragma unroll
-    for (int g = 0; g < 2; ++g) tc::tmem_load32(part.tmem + (half * 2 + g) * kChunk, v[g]);
+    uint32_t v[32];
+    tc::tmem_load32(part.tmem + part.c0, v);
     tc::fence_before();
     __syncwarp();
     if (lane == 0) tc::bar_arrive(part.empty);
-    // a lane's 16 bytes at a time would cross to the other CTAs one by one (9 bytes a cycle); 4 KB copies do not
-    unsigned char* const out = staging + S::SPLIT * 4 * kStaging;
+    // a lane's 16 bytes at a time would cross to the other CTAs one by one (9 bytes a cycle); a 4 KB copy does not
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-        unsigned char* const mine = out + ((half * 2 + g) * 4 + part.row / 32) * kStaging;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint4*>(mine + lane * kChunk * 4 + ((i ^ (lane & 7) ^ ((lane >> 3) << 1)) * 16)) =
-                make_uint4(v[g][4 * i], v[g][4 * i + 1], v[g][4 * i + 2], v[g][4 * i + 3]);
-    }
+    for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<uint4*>(mine + lane * kChunk + ((i ^ (lane & 7) ^ ((lane >> 3) << 1)) * 4)) =
+            make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     tc::fence_async_shared();
     __syncwarp();
-    if (lane < 2) {
-        const uint32_t to = half * 2 + lane;
-        tc::copy_cluster(tc::in_cta(tc::smem_addr(staging + (b.rank * 4 + part.row / 32) * kStaging), to),
-                         tc::smem_addr(out + (to * 4 + part.row / 32) * kStaging), kStaging, tc::in_cta(tc::smem_addr(&counts->received), to));
-    }
+    if (lane == 0)
+        tc::copy_cluster(tc::in_cta(tc::smem_addr(received + (b.rank * 2 + half) * kStaging), to), tc::smem_addr(mine), kStaging,
+                         tc::in_cta(tc::smem_addr(&counts->received), to));
     return true;
 }
 
@@ -642,7 +643,7 @@ __device__ __forceinline__ void scout(const Steps& q, const Block& b, Counts* s)
             set_count(&s->ahead, n + 1);
         }
         if (tile.product == kUpdate && (tile.step || q.low_in)) {
-            const int64_t width = q.ld - tile.n0 < S::kTile ? q.ld - tile.n0 : S::kTile;
+            const int64_t width = q.ld - tile.n0 < S::kCols ? q.ld - tile.n0 : S::kCols;
             for (int r = lane; r < kRows; r += 32) {
                 const int64_t m = tile.m0 + (S::CTAS == 2 ? b.rank * kRows : 0) + r;
                 if (m < q.rows)
@@ -673,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) newton_schulz(const __grid_consta
         counts->ahead = counts->taken = 0;
         for (int i = 0; i < kEpilogueWarps; ++i) counts->stored[i] = 0;
         tc::bar_init(tc::smem_addr(&counts->received), 1);
-        tc::bar_init(tc::smem_addr(&counts->sent), 4 * S::SPLIT);
+        tc::bar_init(tc::smem_addr(&counts->sent), 2 * S::SPLIT);
     }
     open<S>(b);
 
@@ -685,10 +686,11 @@ __global__ void __launch_bounds__(kThreads, 1) newton_schulz(const __grid_consta
             const Tile tile = walk.tile();
             const int shift = S::CTAS == 2 ? (int)b.rank * kRows : 0, z = tile.matrix;
             const int m = (int)tile.m0 + shift, nn = (int)tile.n0 + shift;
-            const CUtensorMap *ma = &q.a_map, *mb = &q.a_map;
+            const CUtensorMap *ma = &q.a_map, *mb = &q.a_map_n;
             bool a_mn = false, b_mn = false;
             if (tile.product == kGram) {
-                ma = mb = &q.x_gram[tile.step & 1];
+                ma = &q.x_gram[tile.step & 1];
+                mb = &q.x_gram_n[tile.step & 1];
                 a_mn = b_mn = q.tall;
             } else if (tile.product == kUpdate) {
                 ma = q.tall ? &q.x_update[tile.step & 1] : &q.b_map;
@@ -711,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) newton_schulz(const __grid_consta
             part_steps<S>(tile, b.rank, from, to);
             if (from == to) continue;
             const bool a_mn = tile.product == kGram && q.tall, b_mn = tile.product == kGram ? q.tall : tile.product == kUpdate && !q.tall;
-            if (!multiply<S>(b, made++, n, to - from, tc::instruction(false, a_mn, b_mn, S::kTile, S::kTile), a_mn, b_mn)) break;
+            if (!multiply<S>(b, made++, n, to - from, tc::instruction(false, a_mn, b_mn, S::kTile, S::kCols), a_mn, b_mn)) break;
             n += to - from;
         }
     } else if (warp == 2) {
@@ -732,8 +734,8 @@ __global__ void __launch_bounds__(kThreads, 1) newton_schulz(const __grid_consta
     } else if (warp >= 4) {
         int made = 0;
         uint32_t accumulators = 0, shared_tiles = 0;
-        // (what comes from other CTAs may come at any time: a tile of one's own goes through the room for what goes out)
-        float* const mine = reinterpret_cast<float*>(b.own + (S::SPLIT > 1 ? S::SPLIT * 4 : 0) * kStaging + (warp - 4) * kStaging);
+        float* const mine = reinterpret_cast<float*>(b.own + (warp - 4) * kStaging);
+        unsigned char* const in = b.own + kEpilogueWarps * kStaging;   // shared tiles: what comes from other CTAs, at any time
         const auto stored = [&] {   // this warp's stores, for the warp that tells the other SMs of them
             __syncwarp();
             if (lane == 0) set_count(&counts->stored[warp - 4], made + 1);
@@ -754,10 +756,10 @@ __global__ void __launch_bounds__(kThreads, 1) newton_schulz(const __grid_consta
                     parts |= (unsigned)(f < t) << i;
                 }
                 const uint32_t turn = shared_tiles++ & 1;
-                if (threadIdx.x == 4 * 32) tc::bar_expect(tc::smem_addr(&counts->received), __popc(parts) * 4 * kStaging);
-                if (from < to) ok = send_parts<S>(b, counts, part, b.own);
-                if (ok && warp < 8) {
-                    ok = finish<S, kGram>(q, tile, part, reinterpret_cast<float*>(b.own + (warp & 3) * kStaging), b.rank, parts,
+                if (threadIdx.x == 4 * 32) tc::bar_expect(tc::smem_addr(&counts->received), __popc(parts) * 2 * kStaging);
+                if (from < to) ok = send_part<S>(b, counts, part, mine, in);
+                if (ok && (warp & 3) == 0) {   // a warp for each 32 of the columns
+                    ok = finish<S, kGram>(q, tile, part, reinterpret_cast<float*>(in + part.c0 / kChunk * kStaging), b.rank, parts,
                                           tc::smem_addr(&counts->received), turn, b.gave_up);
                     if (ok) stored();
                     if (ok && lane < S::SPLIT) tc::bar_arrive(tc::in_cta(tc::smem_addr(&counts->sent), lane));
@@ -780,8 +782,14 @@ __global__ void __launch_bounds__(kThreads, 1) newton_schulz(const __grid_consta
     close<S>(b, q.status);
 }
 
-// Tiles of a matrix a step.
-__host__ __device__ inline int64_t steps_tiles(const Steps& q) { return (int64_t)q.side * (q.side + 1) + (int64_t)q.tiles_m * q.tiles_n; }
+int64_t along(int64_t v, int64_t tile) { return (v + tile - 1) / tile; }
+
+// Tiles of rows x cols that cover a square's diagonal and what is below it.
+int64_t squares(int64_t m, int64_t rows, int64_t cols)
+{
+    const int64_t n = along(m, rows), wide = rows / cols;
+    return wide * n * (n + 1) / 2 - (wide * n - along(m, cols));
+}
 
 template <class S>
 int launch_steps(Steps& q, cudaStream_t st)
@@ -789,11 +797,25 @@ int launch_steps(Steps& q, cudaStream_t st)
     const Device dev = device();
     q.status = dense_status_word();
     if (!dev.sms || !q.status) return EMB_ERR_CUDA;
-    q.side = (unsigned)((q.m + S::kTile - 1) / S::kTile);
-    q.tiles_m = (unsigned)((q.rows + S::kTile - 1) / S::kTile);
-    q.tiles_n = (unsigned)((q.cols + S::kTile - 1) / S::kTile);
-    const int64_t tiles = (int64_t)steps_tiles(q) * q.batch * q.steps;
+    q.squares = (unsigned)squares(q.m, S::kTile, S::kCols);
+    q.tiles_m = (unsigned)along(q.rows, S::kTile);
+    q.tiles_n = (unsigned)along(q.cols, S::kCols);
+    const int64_t update = (int64_t)q.tiles_m * q.tiles_n, tiles = (2 * (int64_t)q.squares + update) * q.batch * q.steps;
     if (tiles > INT_MAX) return EMB_ERR_INVALID_ARG;
+    // A's products run along the long side: X is k-major in them where its rows are long, and in the update where not
+    const auto map = [&](CUtensorMap* m, const __half* x, bool mn_major, int held) {
+        return make_map(m, EMB_F16, x, mn_major, q.cols, q.rows, q.batch, q.ld, q.long_stride, held);
+    };
+    const auto short_map = [&](CUtensorMap* m, const __half* a, int held) {
+        return make_map(m, EMB_F16, a, false, q.m, q.m, q.batch, q.ldm, q.short_stride, held);
+    };
+    for (int i = 0; i < 2; ++i)
+        if (!map(&q.x_gram[i], q.x[i], q.tall, kRows) || !map(&q.x_gram_n[i], q.x[i], q.tall, S::kColsHeld) ||
+            !map(&q.x_update[i], q.x[i], !q.tall, kRows))
+            return EMB_ERR_CUDA;
+    // B is the first operand, or the second where the matrix is tall
+    if (!short_map(&q.a_map, q.a, kRows) || !short_map(&q.a_map_n, q.a, S::kColsHeld) || !short_map(&q.b_map, q.b, q.tall ? S::kColsHeld : kRows))
+        return EMB_ERR_CUDA;
     auto* const kernel = newton_schulz<S>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(S::kCluster);
@@ -817,7 +839,7 @@ int launch_steps(Steps& q, cudaStream_t st)
         }
         resident[dev.number].store(clusters, std::memory_order_relaxed);
     }
-    const int64_t most = q.batch * std::max<int64_t>((int64_t)q.side * (q.side + 1) / 2, (int64_t)q.tiles_m * q.tiles_n);
+    const int64_t most = q.batch * std::max<int64_t>(q.squares, update);
     cfg.gridDim = dim3((unsigned)std::min<int64_t>(clusters, most) * S::kCluster);
     cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, kernel, q) != cudaSuccess) {
@@ -827,31 +849,34 @@ int launch_steps(Steps& q, cudaStream_t st)
     return EMB_OK;
 }
 
-constexpr int kFixed = 14, kExchange = 12;
-
-// How long a step takes, in 64-wide steps of a single CTA's tile: rounds of tiles
-// times their k, and what each of the three products costs whatever its k (its
-// epilogue, and the way to the next one's copies over L2).
-int64_t step_time(const Steps& q, int64_t tile, int64_t units, int64_t split)
+// About how long a step takes, in us.  A product starts `start` after the one before
+// it (epilogue, the way over L2, the first copies) and takes `first` for each 64 of
+// its k; where it has more tiles than run at once, every further round takes `more`
+// for each 64 of k, or an epilogue.
+template <class S>
+double step_time(const Steps& q, int sms, double start, double first, double more, double epilogue)
 {
-    const auto along = [&](int64_t v) { return (v + tile - 1) / tile; };
-    const auto rounds = [&](int64_t tiles, int64_t at_once, int64_t k) { return (tiles + at_once - 1) / at_once * ((k + kStep - 1) / kStep + kFixed); };
-    const int64_t gram = q.batch * along(q.m) * (along(q.m) + 1) / 2, update = q.batch * along(q.rows) * along(q.cols);
-    const int64_t gram_k = q.rows + q.cols - q.m;
-    return (split == 1 ? rounds(gram, units, gram_k) : rounds(gram, units / split, gram_k / split) + kExchange) + rounds(gram, units, q.m) +
-           rounds(update, units, q.m);
+    const double units = sms / S::CTAS;
+    const auto product = [&](int64_t tiles, double at_once, double k) {
+        k = std::ceil(k / kStep);
+        return start + first * k + (std::ceil(tiles / at_once) - 1) * std::max(epilogue, more * k);
+    };
+    const int64_t gram = q.batch * squares(q.m, S::kTile, S::kCols), update = q.batch * along(q.rows, S::kTile) * along(q.cols, S::kCols);
+    return product(gram, units / S::SPLIT, (double)(q.rows + q.cols - q.m) / S::SPLIT) + product(gram, units, (double)q.m) +
+           product(update, units, (double)q.m);
 }
 
+// Measured, single CTAs, pairs and shared 64-wide tiles: one 1777 x 519 matrix 189, 232 and 126 us; one 256 x 1024 116, 138
+// and 87; two 1024 x 1024 147, 204 and 164; 24 of 300 x 500 178, 215 and 289; one 3325 x 3001 667, 711 and 1119; 16 of
+// 1024 x 3328 1052, 896 and 2066.  The numbers below are fitted to these and eleven more.
 int run_steps(Steps& q, cudaStream_t st)
 {
-    const Device dev = device();
-    if (!dev.sms) return EMB_ERR_CUDA;
-    // a pair's tile takes twice a single CTA's time, which the single ones' twice as many bytes a product eat up again
-    const int64_t pairs = 2 * step_time(q, 2 * kRows, dev.sms / 2, 1), single = step_time(q, kRows, dev.sms, 1) * 5 / 4;
-    const int64_t split = step_time(q, kRows, dev.sms, kSplit) * 5 / 4;
-    if (split < pairs && split < single)
-        return launch_steps<Shape<1, kSplit>>(q, st);
-    return pairs <= single ? launch_steps<Shape<2>>(q, st) : launch_steps<Shape<1>>(q, st);
+    const int sms = device().sms;
+    if (!sms) return EMB_ERR_CUDA;
+    const double single = step_time<Shape<1>>(q, sms, 5.5, 0.3, 0.19, 5), pairs = step_time<Shape<2>>(q, sms, 8.2, 0.29, 0.29, 8);
+    const double few = step_time<Few>(q, sms, 5, 0.25, 0.25, 4);
+    if (few < pairs && few < single) return launch_steps<Few>(q, st);
+    return pairs < single ? launch_steps<Shape<2>>(q, st) : launch_steps<Shape<1>>(q, st);
 }
 
 bool sizes_valid(int64_t batch, int64_t rows, int64_t cols)
@@ -925,13 +950,6 @@ extern "C" int emb_orthogonalize(const void* update, int32_t dtype, int64_t batc
     q.out = p.out;
     q.scale = p.scale;
     q.done = reinterpret_cast<unsigned*>(ws + l.done);
-    // A's products run along the long side: X is k-major in them where its rows are long, and in the update where not
-    for (int i = 0; i < 2; ++i)
-        if (!make_map(&q.x_gram[i], EMB_F16, q.x[i], q.tall, cols, rows, batch, l.ld, l.x_elems) ||
-            !make_map(&q.x_update[i], EMB_F16, q.x[i], !q.tall, cols, rows, batch, l.ld, l.x_elems))
-            return EMB_ERR_CUDA;
-    if (!make_map(&q.a_map, EMB_F16, q.a, false, l.m, l.m, batch, l.ldm, l.a_elems) ||
-        !make_map(&q.b_map, EMB_F16, q.b, false, l.m, l.m, batch, l.ldm, l.a_elems))
-        return EMB_ERR_CUDA;
+    q.short_stride = l.a_elems, q.long_stride = l.x_elems;
     return run_steps(q, st);
 }

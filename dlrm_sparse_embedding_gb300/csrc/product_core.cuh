@@ -28,17 +28,21 @@ constexpr int kChunk = 32;                      // columns an epilogue warp take
 constexpr int kMaxDevices = 64;
 
 // Pairs move half the bytes of single CTAs for the same products; these fill the
-// GPU with less work; and where even that is not enough, SPLIT CTAs share a tile's
-// k.  Each way a CTA holds 128 rows of A and 128 of B.
-template <int CTAS_, int SPLIT_ = 1>
+// GPU with less work; and where even that is not enough, tiles are half as wide and
+// SPLIT CTAs share a long k.
+template <int CTAS_, int SPLIT_ = 1, int COLS_ = kRows * CTAS_>
 struct Shape {
     static constexpr int CTAS = CTAS_, SPLIT = SPLIT_;
     static constexpr int kCluster = CTAS * SPLIT;
-    static constexpr int kTile = kRows * CTAS;       // of D, both ways
-    static constexpr int kStages = SPLIT == 1 ? kMaxStages : 3;
-    static constexpr uint32_t kColumns = 2 * kTile;  // two accumulators
-    static constexpr uint32_t kBytes = CTAS * 2 * kOperand;   // a stage's, over the pair
+    static constexpr int kTile = kRows * CTAS, kCols = COLS_;   // of D
+    static constexpr int kColsHeld = kCols / CTAS;   // rows of B a CTA holds a step
+    static constexpr int kStages = kMaxStages;
+    static constexpr int kOperandB = kColsHeld * 128;
+    static constexpr int kStageBytes = kOperand + kOperandB;
+    static constexpr uint32_t kColumns = 2 * kCols;   // two accumulators
+    static constexpr uint32_t kBytes = CTAS * kStageBytes;   // a stage's, over the pair
     static_assert(CTAS == 1 || SPLIT == 1, "pairs do not share a tile's k");
+    static_assert(kColsHeld % 64 == 0, "whole mn-major blocks");
 };
 
 struct Ring {
@@ -53,7 +57,7 @@ static_assert(sizeof(Ring) <= kRingBytes, "the ring's room");
 
 // Shared memory: the stages on a 1024-byte boundary, the ring, then the kernel's own.
 template <class S>
-constexpr int smem_bytes(int own) { return 1024 + 2 * S::kStages * kOperand + kRingBytes + own; }
+constexpr int smem_bytes(int own) { return 1024 + S::kStages * S::kStageBytes + kRingBytes + own; }
 
 struct Block {
     unsigned char* stage_a;
@@ -70,7 +74,7 @@ __device__ __forceinline__ Block block_of(unsigned char* dynamic)
     Block b;
     b.stage_a = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dynamic) + 1023) & ~uintptr_t(1023));
     b.stage_b = b.stage_a + S::kStages * kOperand;
-    b.ring = reinterpret_cast<Ring*>(b.stage_b + S::kStages * kOperand);
+    b.ring = reinterpret_cast<Ring*>(b.stage_b + S::kStages * S::kOperandB);
     b.own = reinterpret_cast<unsigned char*>(b.ring) + kRingBytes;
     b.gave_up = &b.ring->gave_up;
     return b;
@@ -123,8 +127,8 @@ struct Slot {
     __device__ explicit Slot(uint32_t n) : stage(n % STAGES), phase((n / STAGES) & 1) {}
 };
 
-// Copy this CTA's part of one step: 128 rows (columns, if mn-major) of each
-// operand from m and n on.  `part`: the step is not whole yet when it has
+// Copy this CTA's part of one step: its rows (columns, if mn-major) of each operand
+// from m and n on.  `part`: the step is not whole yet when it has
 // arrived, and goes through ring->part.
 template <class S>
 __device__ __forceinline__ bool copy_step(const Block& b, uint32_t step, bool part, const CUtensorMap* map_a, bool a_mn, int m, int za,
@@ -132,7 +136,7 @@ __device__ __forceinline__ bool copy_step(const Block& b, uint32_t step, bool pa
 {
     const Slot<S::kStages> s(step);
     if (!tc::bar_wait(tc::smem_addr(&b.ring->empty[s.stage]), s.phase ^ 1, b.gave_up)) return false;
-    const uint32_t to_a = tc::smem_addr(b.stage_a + s.stage * kOperand), to_b = tc::smem_addr(b.stage_b + s.stage * kOperand);
+    const uint32_t to_a = tc::smem_addr(b.stage_a + s.stage * kOperand), to_b = tc::smem_addr(b.stage_b + s.stage * S::kOperandB);
     uint32_t bar;
     if (part) {
         bar = tc::smem_addr(&b.ring->part[s.stage]);
@@ -151,7 +155,7 @@ __device__ __forceinline__ bool copy_step(const Block& b, uint32_t step, bool pa
     }
     if (b_mn) {
         tc::load_box<S::CTAS>(to_b, map_b, bar, n, k, zb);
-        tc::load_box<S::CTAS>(to_b + kBlockBytes, map_b, bar, n + 64, k, zb);
+        if (S::kColsHeld > 64) tc::load_box<S::CTAS>(to_b + kBlockBytes, map_b, bar, n + 64, k, zb);
     } else {
         tc::load_box<S::CTAS>(to_b, map_b, bar, k, n, zb);
     }
@@ -188,9 +192,9 @@ __device__ __forceinline__ bool multiply(const Block& b, uint32_t tile, uint32_t
         if (!tc::bar_wait(tc::smem_addr(&b.ring->full[s.stage]), s.phase, b.gave_up)) return false;
         tc::fence_after();
         const uint64_t x = tc::operand(tc::smem_addr(b.stage_a + s.stage * kOperand), a_mn, kBlockBytes);
-        const uint64_t y = tc::operand(tc::smem_addr(b.stage_b + s.stage * kOperand), b_mn, kBlockBytes);
+        const uint64_t y = tc::operand(tc::smem_addr(b.stage_b + s.stage * S::kOperandB), b_mn, kBlockBytes);
 #pragma unroll
-        for (int j = 0; j < kStep / 16; ++j) tc::mma<S::CTAS>(b.tmem + acc * S::kTile, x + j * da, y + j * db, instr, i > 0 || j > 0);
+        for (int j = 0; j < kStep / 16; ++j) tc::mma<S::CTAS>(b.tmem + acc * S::kCols, x + j * da, y + j * db, instr, i > 0 || j > 0);
         tc::commit<S::CTAS>(tc::smem_addr(&b.ring->empty[s.stage]));
     }
     tc::commit<S::CTAS>(tc::smem_addr(&b.ring->acc_full[acc]));
@@ -210,14 +214,14 @@ __device__ __forceinline__ Part part_of(const Block& b, uint32_t tile)
     const int warp = threadIdx.x >> 5, w = warp & 3;
     const uint32_t acc = tile & 1;
     Part p;
-    p.tmem = b.tmem + acc * S::kTile + ((uint32_t)(w * 32) << 16);
+    p.tmem = b.tmem + acc * S::kCols + ((uint32_t)(w * 32) << 16);
     p.full = tc::smem_addr(&b.ring->acc_full[acc]);
     p.phase = (tile >> 1) & 1;
     p.empty = tc::smem_addr(&b.ring->acc_empty[acc]);
     if (S::CTAS == 2) p.empty = tc::in_cta(p.empty, 0);
     p.row = w * 32;
-    p.c0 = (warp - 4) / 4 * (S::kTile / 2);
-    p.c1 = p.c0 + S::kTile / 2;
+    p.c0 = (warp - 4) / 4 * (S::kCols / 2);
+    p.c1 = p.c0 + S::kCols / 2;
     return p;
 }
 
@@ -265,16 +269,16 @@ inline Encode encoder()
 }
 
 // A stack of matrices in memory, copied in boxes of 64 columns: the operand's
-// 128 rows at a time where its k runs along memory, 64 k at a time where not.
+// `held` rows at a time where its k runs along memory, 64 k at a time where not.
 // What lies outside a matrix is read as zeros.
 inline bool make_map(CUtensorMap* map, int dtype, const void* p, bool mn_major, int64_t cols, int64_t nrows, int64_t stack, int64_t ld,
-                     int64_t stack_stride)
+                     int64_t stack_stride, int held = kRows)
 {
     const Encode encode = encoder();
     if (!encode) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)nrows, (cuuint64_t)stack};
     const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(stack > 1 ? stack_stride : ld) * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)(mn_major ? kStep : kRows), 1}, ones[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, (cuuint32_t)(mn_major ? kStep : held), 1}, ones[3] = {1, 1, 1};
     return encode(map, dtype == EMB_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(p), dims, strides,
                   box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
