@@ -91,29 +91,34 @@ __device__ __forceinline__ double block_sum(double of_warp, double* room)
     return threadIdx.x < 32 ? warp_sum(threadIdx.x < blockDim.x / 32 ? room[threadIdx.x] : 0.0) : 0.0;
 }
 
-// Calls f(row, first column, the V values there) for the elements of a matrix
-// that are this warp's: rows are dealt out warp by warp, in pieces of 32 V
-// columns.
-template <int V, class T, class F>
+// Calls f(row, first column, the 8 values there) for the elements of a matrix that
+// are this warp's: rows are dealt out warp by warp, in pieces of 256 columns.  WIDE:
+// rows are whole vectors of 16 bytes; else they are read one element at a time, and
+// zeros follow a row's last one.
+template <bool WIDE, class T, class F>
 __device__ __forceinline__ void each_piece(const T* g, int64_t row_stride, int64_t rows, int64_t cols, F f)
 {
     const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
-    const int64_t pieces = (cols + 32 * V - 1) / (32 * V), step = (int64_t)gridDim.x * warps;
-    int64_t u = (int64_t)blockIdx.x * warps + (threadIdx.x >> 5);
+    const int64_t pieces = (cols + 255) / 256, step = (int64_t)gridDim.x * warps;
+    const int64_t u = (int64_t)blockIdx.x * warps + (threadIdx.x >> 5);
     int64_t row = u / pieces, piece = u - row * pieces;
     const int64_t row_step = step / pieces, piece_step = step - row_step * pieces;
-    constexpr int kAhead = 4;   // loads on their way at once
+    using Word = typename std::conditional<WIDE, uint4, T>::type;
+    constexpr int kWords = 8 * sizeof(T) / sizeof(Word);
+    constexpr int kAhead = WIDE ? 4 : 2;   // pieces on their way at once
     while (row < rows) {
-        using Word = typename std::conditional<V == 1, T, uint4>::type;
-        constexpr int kWords = V * sizeof(T) / sizeof(Word);
         Word w[kAhead][kWords];
         int64_t at_row[kAhead], at_col[kAhead];
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) {
-            at_row[a] = row, at_col[a] = (piece * 32 + lane) * V;
+            at_row[a] = row, at_col[a] = (piece * 32 + lane) * 8;
             if (row < rows && at_col[a] < cols) {
+                const Word* const p = reinterpret_cast<const Word*>(g + row * row_stride + at_col[a]);
 #pragma unroll
-                for (int i = 0; i < kWords; ++i) w[a][i] = reinterpret_cast<const Word*>(g + row * row_stride + at_col[a])[i];
+                for (int i = 0; i < kWords; ++i) {
+                    if constexpr (WIDE) w[a][i] = p[i];
+                    else w[a][i] = at_col[a] + i < cols ? p[i] : from_float<T>(0.f);
+                }
             } else {
                 at_row[a] = rows;
             }
@@ -123,9 +128,9 @@ __device__ __forceinline__ void each_piece(const T* g, int64_t row_stride, int64
 #pragma unroll
         for (int a = 0; a < kAhead; ++a)
             if (at_row[a] < rows) {
-                float v[V];
+                float v[8];
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[i] = to_float<T>(reinterpret_cast<const T*>(w[a])[i]);
+                for (int i = 0; i < 8; ++i) v[i] = to_float<T>(reinterpret_cast<const T*>(w[a])[i]);
                 f(at_row[a], at_col[a], v);
             }
     }
@@ -133,22 +138,22 @@ __device__ __forceinline__ void each_piece(const T* g, int64_t row_stride, int64
 
 // This warp's sum of squares, in every lane: fp32, a thread has some dozens of
 // elements; in double again where the squares could leave fp32's range.
-template <int V, class T>
+template <bool WIDE, class T>
 __device__ __forceinline__ double squares(const T* g, int64_t row_stride, int64_t rows, int64_t cols)
 {
     float s = 0.f, top = 0.f;
-    each_piece<V, T>(g, row_stride, rows, cols, [&](int64_t, int64_t, const float (&v)[V]) {
+    each_piece<WIDE, T>(g, row_stride, rows, cols, [&](int64_t, int64_t, const float (&v)[8]) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < 8; ++i) {
             s = __fmaf_rn(v[i], v[i], s);
             top = fmaxf(top, fabsf(v[i]));
         }
     });
     if (__any_sync(0xffffffffu, top > 1e15f || (top < 1e-15f && top > 0.f))) {
         double d = 0;
-        each_piece<V, T>(g, row_stride, rows, cols, [&](int64_t, int64_t, const float (&v)[V]) {
+        each_piece<WIDE, T>(g, row_stride, rows, cols, [&](int64_t, int64_t, const float (&v)[8]) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) d = fma((double)v[i], (double)v[i], d);
+            for (int i = 0; i < 8; ++i) d = fma((double)v[i], (double)v[i], d);
         });
         return warp_sum(d);
     }
@@ -171,7 +176,7 @@ struct Input {
 // X = G 2^e as a sum of two fp16 (for 16-bit G one: its 8 or 11 bits fit, but for
 // entries below 2^-24 of the norm), and the factor that makes it G / (|G| + eps).
 // Thread 0 has the sum of squares.
-template <int V, class T>
+template <bool WIDE, class T>
 __device__ __forceinline__ void put_scaled(const Input& q, const T* g, double sum_of_squares)
 {
     __shared__ float factor;
@@ -188,35 +193,31 @@ __device__ __forceinline__ void put_scaled(const Input& q, const T* g, double su
     __syncthreads();
     const float up = factor;
     const int64_t at = (int64_t)blockIdx.y * q.rows * q.ld;
-    each_piece<V, T>(g, q.row_stride, q.rows, q.cols, [&](int64_t row, int64_t c, const float (&v)[V]) {
-        float h[V], l[V];
+    each_piece<WIDE, T>(g, q.row_stride, q.rows, q.cols, [&](int64_t row, int64_t c, const float (&v)[8]) {
+        float h[8], l[8];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < 8; ++i) {
             h[i] = up * v[i];
             l[i] = kLowScale * (h[i] - __half2float(__float2half_rn(h[i])));
         }
-        if constexpr (V == 8) {
-            *reinterpret_cast<uint4*>(q.x + at + row * q.ld + c) = core::pack8<__half>(h);
-            if (sizeof(T) == 4) *reinterpret_cast<uint4*>(q.x_low + at + row * q.ld + c) = core::pack8<__half>(l);
-        } else {
-            q.x[at + row * q.ld + c] = __float2half_rn(h[0]);
-            if (sizeof(T) == 4) q.x_low[at + row * q.ld + c] = __float2half_rn(l[0]);
-        }
+        // rows of X start at 16 bytes and have room for whole vectors
+        *reinterpret_cast<uint4*>(q.x + at + row * q.ld + c) = core::pack8<__half>(h);
+        if (sizeof(T) == 4) *reinterpret_cast<uint4*>(q.x_low + at + row * q.ld + c) = core::pack8<__half>(l);
     });
 }
 
 // Sums of squares, in blocks of a fixed order, then X.
-template <int V, class T>
+template <bool WIDE, class T>
 __global__ void __launch_bounds__(kNormThreads) norm_partials(Input q, const T* __restrict__ g)
 {
     __shared__ double warp_sums[kNormThreads / 32];
     let_next_begin();
     wait_for_earlier();
-    const double d = block_sum(squares<V, T>(g + blockIdx.y * q.batch_stride, q.row_stride, q.rows, q.cols), warp_sums);
+    const double d = block_sum(squares<WIDE, T>(g + blockIdx.y * q.batch_stride, q.row_stride, q.rows, q.cols), warp_sums);
     if (threadIdx.x == 0) q.partial[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = d;
 }
 
-template <int V, class T>
+template <bool WIDE, class T>
 __global__ void __launch_bounds__(kNormThreads) scale_in(Input q, const T* __restrict__ g)
 {
     __shared__ double warp_sums[kNormThreads / 32];
@@ -224,27 +225,27 @@ __global__ void __launch_bounds__(kNormThreads) scale_in(Input q, const T* __res
     let_next_begin();
     wait_for_earlier();
     const double d = (int)threadIdx.x < q.norm_blocks ? q.partial[(int64_t)blockIdx.y * q.norm_blocks + threadIdx.x] : 0.0;
-    put_scaled<V, T>(q, g + blockIdx.y * q.batch_stride, block_sum(warp_sum(d), warp_sums));
+    put_scaled<WIDE, T>(q, g + blockIdx.y * q.batch_stride, block_sum(warp_sum(d), warp_sums));
 }
 
 // Both by one block a matrix.
-template <int V, class T>
+template <bool WIDE, class T>
 __global__ void __launch_bounds__(kOneBlockThreads) norm_and_scale(Input q, const T* __restrict__ g)
 {
     __shared__ double warp_sums[kOneBlockThreads / 32];
     let_next_begin();
     wait_for_earlier();
     const T* const mine = g + blockIdx.y * q.batch_stride;
-    put_scaled<V, T>(q, mine, block_sum(squares<V, T>(mine, q.row_stride, q.rows, q.cols), warp_sums));
+    put_scaled<WIDE, T>(q, mine, block_sum(squares<WIDE, T>(mine, q.row_stride, q.rows, q.cols), warp_sums));
 }
 
-template <int V, class T>
+template <bool WIDE, class T>
 int start(const Input& q, const T* g, int64_t batch, cudaStream_t st)
 {
-    if (q.rows * q.cols <= kOneBlock) return launch_next(norm_and_scale<V, T>, dim3(1, (unsigned)batch), kOneBlockThreads, 0, st, 1, q, g);
+    if (q.rows * q.cols <= kOneBlock) return launch_next(norm_and_scale<WIDE, T>, dim3(1, (unsigned)batch), kOneBlockThreads, 0, st, 1, q, g);
     const dim3 grid(q.norm_blocks, (unsigned)batch);
-    if (int rc = launch_next(norm_partials<V, T>, grid, kNormThreads, 0, st, 1, q, g)) return rc;
-    return launch_next(scale_in<V, T>, grid, kNormThreads, 0, st, 1, q, g);
+    if (int rc = launch_next(norm_partials<WIDE, T>, grid, kNormThreads, 0, st, 1, q, g)) return rc;
+    return launch_next(scale_in<WIDE, T>, grid, kNormThreads, 0, st, 1, q, g);
 }
 
 // ---------------------------------------------------------------------------
@@ -922,7 +923,7 @@ extern "C" int emb_orthogonalize(const void* update, int32_t dtype, int64_t batc
     const auto begin = [&](auto t) {
         using T = decltype(t);
         const T* const g = static_cast<const T*>(update);
-        return wide ? start<8, T>(in, g, batch, st) : start<1, T>(in, g, batch, st);
+        return wide ? start<true, T>(in, g, batch, st) : start<false, T>(in, g, batch, st);
     };
     const int rc = dtype == EMB_F32 ? begin(float()) : dtype == EMB_F16 ? begin(__half()) : begin(__nv_bfloat16());
     if (rc != EMB_OK) return rc;
