@@ -5,7 +5,10 @@
 // so the long side is needed at both ends only, and in between a CTA keeps its
 // matrix's A, Q and W in shared memory: a step is a few products of 128 x 128,
 // with no other SM to wait for.  What bounds it is the chain: 14 products of
-// five steps, each of which needs the one before.
+// five steps, each of which needs the one before, 1600 cycles of tensor cores (24
+// instructions of 128 x 128 x 16) and about as many of epilogue.  32 matrices of 128 x
+// 256 take 45 us with the norm before and W X0 after it, 35 of them in this kernel;
+// as products over memory, three a step, they took 106.
 //
 // W's eigenvalues grow by up to a a step where X's singular values are small,
 // and their rounding must not reach the large ones.  So A, Q and W are held as

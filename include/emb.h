@@ -6,6 +6,9 @@
  *   emb_backward_update  dedup of the touched rows, per-row gradient reduction
  *                        and the SGD / Adagrad update, in place
  *   emb_unique           the stand-alone dedup primitive
+ * and, further down, the dense side's operators: an expert layer (sort,
+ * dispatch, products, combine, and their gradients) and orthogonalised updates
+ * for its weights.
  *
  * The operations are the ones the GTC 2022 "Merlin HugeCTR" slides name
  * (slides "COMMON EMBEDDING PRIMITIVES" and "HUGECTR EMBEDDING LAYER": table
