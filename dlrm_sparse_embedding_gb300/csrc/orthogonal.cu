@@ -322,7 +322,8 @@ struct Tile {
     Product product;
     int step, matrix;
     int64_t m0, n0;
-    int k_steps;
+    int64_t k;
+    int k_steps;             // of 64
     unsigned needs;          // of done[matrix]
 };
 
@@ -362,6 +363,7 @@ __device__ __forceinline__ Tile tile_of(const Steps& q, int step, Product produc
         r.m0 = (int64_t)i * S::kTile;
         r.n0 = (int64_t)(idx - kWide * i * (i + 1) / 2) * S::kCols;
     }
+    r.k = k;
     r.k_steps = (int)((k + kStep - 1) / kStep);
     return r;
 }
@@ -721,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1) newton_schulz(const __grid_consta
             part_steps<S>(tile, b.rank, from, to);
             if (from == to) continue;
             const bool a_mn = tile.product == kGram && q.tall, b_mn = tile.product == kGram ? q.tall : tile.product == kUpdate && !q.tall;
-            if (!multiply<S>(b, made++, n, to - from, tc::instruction(false, a_mn, b_mn, S::kTile, S::kCols), a_mn, b_mn)) break;
+            if (!multiply<S>(b, made++, n, min(tile.k, (int64_t)to * kStep) - (int64_t)from * kStep, tc::instruction(false, a_mn, b_mn, S::kTile, S::kCols), a_mn, b_mn)) break;
             n += to - from;
         }
     } else if (warp == 2) {

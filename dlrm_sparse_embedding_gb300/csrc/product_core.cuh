@@ -178,11 +178,12 @@ __device__ __forceinline__ void finish_copies(const Block& b, uint32_t steps, bo
     }
 }
 
-// Multiply `steps` steps into accumulator number `tile` (the count of tiles so
-// far); step is the count of steps before them.
+// Multiply k (> 0) into accumulator number `tile` (the count of tiles so far); step
+// is the count of steps before.  Of the last step, only the 16s that k reaches.
 template <class S>
-__device__ __forceinline__ bool multiply(const Block& b, uint32_t tile, uint32_t step, int steps, uint32_t instr, bool a_mn, bool b_mn)
+__device__ __forceinline__ bool multiply(const Block& b, uint32_t tile, uint32_t step, int64_t k, uint32_t instr, bool a_mn, bool b_mn)
 {
+    const int steps = (int)((k + kStep - 1) / kStep), last = (int)(k - (int64_t)(steps - 1) * kStep + 15) / 16;
     const uint32_t acc = tile & 1;
     if (!tc::bar_wait(tc::smem_addr(&b.ring->acc_empty[acc]), ((tile >> 1) & 1) ^ 1, b.gave_up)) return false;
     tc::fence_after();
@@ -193,8 +194,12 @@ __device__ __forceinline__ bool multiply(const Block& b, uint32_t tile, uint32_t
         tc::fence_after();
         const uint64_t x = tc::operand(tc::smem_addr(b.stage_a + s.stage * kOperand), a_mn, kBlockBytes);
         const uint64_t y = tc::operand(tc::smem_addr(b.stage_b + s.stage * S::kOperandB), b_mn, kBlockBytes);
+        if (i + 1 < steps) {
 #pragma unroll
-        for (int j = 0; j < kStep / 16; ++j) tc::mma<S::CTAS>(b.tmem + acc * S::kCols, x + j * da, y + j * db, instr, i > 0 || j > 0);
+            for (int j = 0; j < kStep / 16; ++j) tc::mma<S::CTAS>(b.tmem + acc * S::kCols, x + j * da, y + j * db, instr, i > 0 || j > 0);
+        } else {
+            for (int j = 0; j < last; ++j) tc::mma<S::CTAS>(b.tmem + acc * S::kCols, x + j * da, y + j * db, instr, i > 0 || j > 0);
+        }
         tc::commit<S::CTAS>(tc::smem_addr(&b.ring->empty[s.stage]));
     }
     tc::commit<S::CTAS>(tc::smem_addr(&b.ring->acc_full[acc]));

@@ -44,9 +44,9 @@ struct Problems {
 
 // The list of tiles.  m-grouped problems have as many tiles as their rows need,
 // one problem after another, and last the rows without an expert.  k-grouped ones
-// come longest first: CTAs take tiles in turn, and what one gets more than another
-// is then less than one tile (in the plan's order the tensor cores of some were busy
-// 55% of the time, of others 87%).
+// come longest first and are dealt out back and forth, so that all CTAs get about as
+// many steps (in the plan's order the tensor cores of some were busy 55% of the
+// time, of others 87%).
 template <class S, bool K_GROUPED>
 struct List {
     const Problems& q;
@@ -83,6 +83,14 @@ struct List {
         r.steps = (int)((r.k_end - r.k0 + kStep - 1) / kStep);
         return r;
     }
+};
+
+// Which tiles of the list a CTA (a pair) takes: one a round.  Where rounds go from
+// the longest groups to the shortest, every other round is dealt out backwards.
+template <bool BACK_AND_FORTH>
+struct Turns {
+    int64_t count, mine;
+    __device__ int64_t at(int64_t round) const { return round * count + (BACK_AND_FORTH && (round & 1) ? count - 1 - mine : mine); }
 };
 
 // Both tables, by the first warp: rows is the plan's offsets made sound, start the
@@ -195,13 +203,14 @@ __global__ void __launch_bounds__(kThreads, 1) expert_products(const __grid_cons
     }
 
     const List<S, K_GROUPED> list{q, start, rows};
-    const int64_t total = list.total(), first = blockIdx.x / S::CTAS, step = gridDim.x / S::CTAS;
+    const int64_t total = list.total();
+    const Turns<K_GROUPED> turns{(int64_t)gridDim.x / S::CTAS, (int64_t)blockIdx.x / S::CTAS};
 
     if (warp == 0 && tc::elect_one()) {
         uint32_t n = 0;
         bool ok = true;
-        for (int64_t t = first; ok && t < total; t += step) {
-            const Tile tile = list.at(t);
+        for (int64_t turn = 0; ok && turns.at(turn) < total; ++turn) {
+            const Tile tile = list.at(turns.at(turn));
             const int m = (int)tile.m0 + (int)b.rank * kRows, nn = (int)tile.n0 + (int)b.rank * kRows;
             for (int i = 0; ok && i < tile.steps; ++i, ++n) {
                 const int64_t k = tile.k0 + i * kStep;
@@ -212,30 +221,31 @@ __global__ void __launch_bounds__(kThreads, 1) expert_products(const __grid_cons
     } else if (warp == 1 && b.rank == 0 && tc::elect_one()) {
         const uint32_t instr = tc::instruction(q.p.dtype == EMB_BF16, A_MN, B_MN, S::kTile, S::kTile);
         uint32_t n = 0, made = 0;
-        for (int64_t t = first; t < total; t += step) {
-            const Tile tile = list.at(t);
+        for (int64_t turn = 0; turns.at(turn) < total; ++turn) {
+            const Tile tile = list.at(turns.at(turn));
             if (!tile.steps) continue;
-            if (!multiply<S>(b, made++, n, tile.steps, instr, A_MN, B_MN)) break;
+            if (!multiply<S>(b, made++, n, tile.k_end - tile.k0, instr, A_MN, B_MN)) break;
             n += tile.steps;
         }
     } else if (warp == 2 && K_GROUPED) {
         // zero the rows past a group in its last step, then hand the step on
-        uint32_t n = 0, turns[S::kStages] = {};
+        uint32_t n = 0, times[S::kStages] = {};
         bool ok = true;
-        for (int64_t t = first; ok && t < total; t += step) {
-            const Tile tile = list.at(t);
+        for (int64_t turn = 0; ok && turns.at(turn) < total; ++turn) {
+            const Tile tile = list.at(turns.at(turn));
             const int left = (int)((tile.k_end - tile.k0) % kStep);
             if (tile.steps && left) {
                 const uint32_t s = (n + tile.steps - 1) % S::kStages;
-                uint32_t turn = 0;
+                uint32_t time = 0;   // how many times this stage held such a step before
 #pragma unroll
                 for (int i = 0; i < S::kStages; ++i)
-                    if (i == (int)s) turn = turns[i]++;
-                ok = tc::bar_wait_warp(tc::smem_addr(&b.ring->part[s]), turn & 1, b.gave_up);
+                    if (i == (int)s) time = times[i]++;
+                ok = tc::bar_wait_warp(tc::smem_addr(&b.ring->part[s]), time & 1, b.gave_up);
                 if (ok) {
                     const uint4 zero = make_uint4(0, 0, 0, 0);
+                    const int end = (left + 15) / 16 * 16 * 128;   // what is multiplied
                     for (int j = 0; j < 2; ++j)
-                        for (int i = j * kBlockBytes + left * 128 + lane * 16; i < (j + 1) * kBlockBytes; i += 512) {
+                        for (int i = j * kBlockBytes + left * 128 + lane * 16; i < j * kBlockBytes + end; i += 512) {
                             *reinterpret_cast<uint4*>(b.stage_a + s * kOperand + i) = zero;
                             *reinterpret_cast<uint4*>(b.stage_b + s * kOperand + i) = zero;
                         }
@@ -244,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_products(const __grid_cons
                     if (b.rank) {
                         if (lane == 0) tc::bar_arrive(tc::in_cta(tc::smem_addr(&b.ring->peer_part[s]), 0));
                     } else {
-                        if (S::CTAS == 2) ok = tc::bar_wait_warp(tc::smem_addr(&b.ring->peer_part[s]), turn & 1, b.gave_up);
+                        if (S::CTAS == 2) ok = tc::bar_wait_warp(tc::smem_addr(&b.ring->peer_part[s]), time & 1, b.gave_up);
                         if (ok && lane == 0) tc::bar_arrive(tc::smem_addr(&b.ring->full[s]));
                     }
                 }
@@ -254,8 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_products(const __grid_cons
     } else if (warp >= 4) {
         uint32_t made = 0;
         unsigned char* const mine = staging + (warp - 4) * kStaging;
-        for (int64_t t = first; t < total; t += step) {
-            const Tile tile = list.at(t);
+        for (int64_t turn = 0; turns.at(turn) < total; ++turn) {
+            const Tile tile = list.at(turns.at(turn));
             const Part part = part_of<S>(b, made);
             if (tile.steps) {
                 ++made;
