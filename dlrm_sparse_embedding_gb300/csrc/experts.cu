@@ -182,7 +182,23 @@ size_t place_smem(int E)
 // ---------------------------------------------------------------------------
 // V consecutive elements: 8 (moved 16 bytes at a time) where everything is
 // aligned for it, else 1.  They are kept as they are in memory until they are
-// used: a load in flight costs no more registers than its bytes.
+// used: a load in flight costs no more registers than its bytes.  Rows are read and
+// written once, so vectors pass as streams, which leave L2 first (gradients and
+// weighted sum of 32768 x 4 x 2048 together 299 us without, 273 with).
+template <class W>
+__device__ __forceinline__ W load_word(const W* p)
+{
+    if constexpr (sizeof(W) == 16) return __ldcs(p);
+    else return *p;
+}
+
+template <class W>
+__device__ __forceinline__ void store_word(W* p, const W& v)
+{
+    if constexpr (sizeof(W) == 16) __stcs(p, v);
+    else *p = v;
+}
+
 template <int V, class T>
 struct Raw {
     using Word = typename std::conditional<V == 1, T, uint4>::type;
@@ -192,7 +208,7 @@ struct Raw {
     __device__ __forceinline__ void load(const T* p)
     {
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const Word*>(p)[i];
+        for (int i = 0; i < kWords; ++i) w[i] = load_word(reinterpret_cast<const Word*>(p) + i);
     }
     __device__ __forceinline__ float operator[](int i) const { return to_float<T>(reinterpret_cast<const T*>(w)[i]); }
 };
@@ -205,7 +221,7 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[V])
 #pragma unroll
     for (int i = 0; i < V; ++i) reinterpret_cast<T*>(r.w)[i] = from_float<T>(v[i]);
 #pragma unroll
-    for (int i = 0; i < Raw<V, T>::kWords; ++i) reinterpret_cast<Word*>(p)[i] = r.w[i];
+    for (int i = 0; i < Raw<V, T>::kWords; ++i) store_word(reinterpret_cast<Word*>(p) + i, r.w[i]);
 }
 
 constexpr int kRowThreads = 256;
