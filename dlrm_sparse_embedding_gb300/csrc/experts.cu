@@ -272,17 +272,17 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_rows(emb_expert_plan pla
 }
 
 // out[t] = sum_j w[t, j] rows[pos[t, j]]; without weights, the plain sum (the
-// dispatch's gradient).  Bound by memory: a lane has kInFlight loads on their
-// way, ROWS rows' pieces of kInFlight / ROWS vectors (one row after another, four
-// loads each: 105 us where this takes 77, and 181 where it takes 102).
-constexpr int kInFlight = 8;
+// dispatch's gradient).  Bound by memory: ROWS rows' pieces of kSumUnroll vectors
+// are on their way at once (one row after another, four vectors each: 105 us where
+// this takes 67, and 181 where it takes 90; eight vectors a lane for 2 rows: 77).
+constexpr int kSumUnroll = 2;
 
 template <int V, class R, class O, bool WEIGHTED, int ROWS>
 __global__ void __launch_bounds__(kRowThreads) gather_sum(emb_expert_plan plan, const R* __restrict__ rows,
                                                           int64_t rows_stride, const float* __restrict__ weights,
                                                           int64_t width, int64_t pieces, O* __restrict__ out)
 {
-    constexpr int U = kInFlight / ROWS;
+    constexpr int U = kSumUnroll;
     const int lane = threadIdx.x & 31, P = (int)(plan.tokens * plan.k);
     let_next_begin();
     wait_for_earlier();
@@ -430,7 +430,7 @@ int launch_gather_sum(const emb_expert_plan& plan, const void* rows, int rows_dt
             using R = decltype(r);
             using O = decltype(o);
             const int at_once = plan.k <= 1 ? 1 : plan.k <= 2 ? 2 : 4;
-            const int64_t pieces = pieces_of(width, w8 ? 8 : 1, kInFlight / at_once);
+            const int64_t pieces = pieces_of(width, w8 ? 8 : 1, kSumUnroll);
             const unsigned blocks = row_blocks(plan.tokens * pieces);
             const auto go = [&](auto kernel) {
                 return launch_next(kernel, blocks, kRowThreads, 0, st, 1, plan, (const R*)rows, stride, weights, width, pieces, (O*)out);
