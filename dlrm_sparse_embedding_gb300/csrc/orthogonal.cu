@@ -39,6 +39,7 @@ using namespace core;
 
 constexpr int kNormThreads = 256;
 constexpr int kMaxNormBlocks = 256;   // per matrix
+constexpr int kNormBlocks = 4 * 152;  // of all: four an SM (16 of 1024 x 3328: both passes 51 us, 55 with eight and 68 with 27)
 constexpr int kOneBlockThreads = 1024;
 constexpr int64_t kOneBlock = 8 * 8 * kOneBlockThreads;   // elements that one block reads twice sooner than two launches pass
 constexpr float kRange = 256.f;       // the scaled norm is in [kRange, 2 kRange)
@@ -57,7 +58,8 @@ Layout layout_of(int64_t batch, int64_t rows, int64_t cols)
     l.ldm = (l.m + 7) / 8 * 8;
     l.x_elems = rows * l.ld;
     l.a_elems = l.m <= kShort ? kShort * kShort : l.m * l.ldm;   // W's two parts, for short sides
-    l.norm_blocks = (int)std::min<int64_t>(kMaxNormBlocks, (rows * cols + 8 * kNormThreads - 1) / (8 * kNormThreads));
+    const int64_t share = std::max<int64_t>(1, kNormBlocks / std::max<int64_t>(batch, 1));   // of a matrix
+    l.norm_blocks = (int)std::min<int64_t>({kMaxNormBlocks, share, (rows * cols + 8 * kNormThreads - 1) / (8 * kNormThreads)});
     size_t at = 0;
     const auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -252,7 +254,7 @@ int start(const Input& q, const T* g, int64_t batch, cudaStream_t st)
 // the steps
 // ---------------------------------------------------------------------------
 // 16 matrices of 1024 x 3328 take 980 us for five steps, 940 TFLOP/s of what symmetry
-// leaves: reading G twice and writing X takes 68 us of them, and of the rest the
+// leaves: reading G twice and writing X takes 51 us of them, and of the rest the
 // tensor cores are busy 52%, DRAM 63% (3.7 GB): A's products (33
 // thousand cycles a tile, 27 of them products) run beside nothing that uses memory,
 // the update (16 and 8) beside 512 KB of X a tile.  One of 1777 x 519 takes 123 us,
