@@ -61,8 +61,8 @@ __global__ void __launch_bounds__(kPlaceThreads) expert_count(const ID* __restri
     wait_for_earlier();
     for (int e = threadIdx.x; e <= E; e += kPlaceThreads) cnt[e] = 0;
     __syncthreads();
-    const int lo = blockIdx.x * chunk, hi = min((int64_t)P, (int64_t)lo + chunk);
-    for (int a = lo + threadIdx.x; a < hi; a += kPlaceThreads) atomicAdd(&cnt[bucket_of(ids, a, E, nullptr)], 1);
+    const int64_t lo = (int64_t)blockIdx.x * chunk, hi = min((int64_t)P, lo + chunk);
+    for (int64_t a = lo + threadIdx.x; a < hi; a += kPlaceThreads) atomicAdd(&cnt[bucket_of(ids, a, E, nullptr)], 1);
     __syncthreads();
     for (int e = threadIdx.x; e <= E; e += kPlaceThreads) counts[(int64_t)e * gridDim.x + blockIdx.x] = cnt[e];
 }
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kPlaceThreads) expert_place(const ID* __restri
     int* const warp_sums = base + (E + 1);
     unsigned short* const of_warp = reinterpret_cast<unsigned short*>(warp_sums + 32);
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
-    const int lo = blockIdx.x * chunk, hi = min((int64_t)P, (int64_t)lo + chunk);
+    const int64_t lo = (int64_t)blockIdx.x * chunk, hi = min((int64_t)P, lo + chunk);
 
     for (int i = t; i < (E + 1) * kPlaceWarps; i += kPlaceThreads) of_warp[i] = 0;
     let_next_begin();
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kPlaceThreads) expert_place(const ID* __restri
     } else {
         for (int e = t; e <= E; e += kPlaceThreads) next[e] = 0, base[e] = 0;
         __syncthreads();
-        for (int a = lo + t; a < hi; a += kPlaceThreads) atomicAdd(&next[bucket_of(ids, a, E, nullptr)], 1);
+        for (int64_t a = lo + t; a < hi; a += kPlaceThreads) atomicAdd(&next[bucket_of(ids, a, E, nullptr)], 1);
     }
     __syncthreads();
     block_exclusive_scan(next, E + 1, warp_sums);
@@ -140,8 +140,8 @@ __global__ void __launch_bounds__(kPlaceThreads) expert_place(const ID* __restri
 
     // kPlaceThreads assignments a round, in order: an assignment's row is its
     // bucket's next one, plus those of earlier warps, plus those of lower lanes
-    for (int start = lo; start < hi; start += kPlaceThreads) {
-        const int a = start + t;
+    for (int64_t start = lo; start < hi; start += kPlaceThreads) {
+        const int64_t a = start + t;
         const bool has = a < hi;
         const int e = has ? bucket_of(ids, a, E, status) : E + 1;
         const unsigned same = __match_any_sync(0xffffffffu, e);
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kPlaceThreads) expert_place(const ID* __restri
         if (has) {
             const int row = base[e] + of_warp[e * kPlaceWarps + w] + rank;
             pos[a] = e < E ? row : -1;
-            src[row] = e < E ? a : -1;
+            src[row] = e < E ? (int32_t)a : -1;
         }
         if (start + kPlaceThreads < hi) {
             __syncthreads();

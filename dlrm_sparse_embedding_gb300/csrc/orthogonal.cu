@@ -639,8 +639,8 @@ __device__ __forceinline__ bool send_part(const Block& b, Counts* counts, const 
 
 // One warp goes two tiles ahead of the epilogue: it waits until the tile's matrix is
 // far enough, for the copies and the epilogue alike (each would wait 2000 cycles a
-// tile for L2's answer and the fence), and has the low parts of X brought to L2 (the
-// high parts come with the products' operands).
+// tile for L2's answer and the fence).  (Having X brought to L2 here as well gave
+// nothing for its low part and cost a tenth for its high one.)
 template <class S>
 __device__ __forceinline__ void scout(const Steps& q, const Block& b, Counts* s)
 {
@@ -653,15 +653,6 @@ __device__ __forceinline__ void scout(const Steps& q, const Block& b, Counts* s)
         if (lane == 0) {
             tc::fence_async();   // the copies to come read what other SMs' plain stores wrote
             set_count(&s->ahead, n + 1);
-        }
-        if (tile.product == kUpdate && (tile.step || q.low_in)) {
-            const int64_t width = q.ld - tile.n0 < S::kCols ? q.ld - tile.n0 : S::kCols;
-            for (int r = lane; r < kRows; r += 32) {
-                const int64_t m = tile.m0 + (S::CTAS == 2 ? b.rank * kRows : 0) + r;
-                if (m < q.rows)
-                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
-                                 ::"l"(q.x_low[tile.step & 1] + tile.matrix * q.rows * q.ld + m * q.ld + tile.n0), "r"((int)width * 2) : "memory");
-            }
         }
     }
 }

@@ -15,6 +15,7 @@
 // the group are zeroed in shared memory, in both operands, before it is
 // multiplied: 0 times an infinity or a NaN of the next group would not be 0.
 #include <algorithm>
+#include <climits>
 
 #include "product_core.cuh"
 
@@ -76,7 +77,7 @@ struct List {
                 if (start[mid] <= row_tile) lo = mid; else hi = mid - 1;
             }
             r.problem = lo;
-            r.m0 = rows[lo] + (row_tile - start[lo]) * S::kTile;
+            r.m0 = rows[lo] + (int64_t)(row_tile - start[lo]) * S::kTile;
             r.m_end = rows[lo + 1];
             r.k0 = 0, r.k_end = lo == q.p.experts ? 0 : q.p.k;
         }
@@ -118,7 +119,7 @@ __device__ void make_tables(const Problems& q, int* start, int* rows)
         __syncwarp();
         for (int base = 0; base <= E; base += 32) {
             const int e = base + lane;
-            const int mine = e <= E ? (rows[e + 1] - rows[e] + S::kTile - 1) / S::kTile : 0;
+            const int mine = e <= E ? (int)(((int64_t)rows[e + 1] - rows[e] + S::kTile - 1) / S::kTile) : 0;
             int s = mine;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -211,9 +212,10 @@ __global__ void __launch_bounds__(kThreads, 1) expert_products(const __grid_cons
         bool ok = true;
         for (int64_t turn = 0; ok && turns.at(turn) < total; ++turn) {
             const Tile tile = list.at(turns.at(turn));
-            const int m = (int)tile.m0 + (int)b.rank * kRows, nn = (int)tile.n0 + (int)b.rank * kRows;
+            // (a coordinate past the rows is read as zeros, and so is the largest one)
+            const int m = (int)min(tile.m0 + b.rank * kRows, (int64_t)INT_MAX), nn = (int)tile.n0 + (int)b.rank * kRows;
             for (int i = 0; ok && i < tile.steps; ++i, ++n) {
-                const int64_t k = tile.k0 + i * kStep;
+                const int64_t k = tile.k0 + (int64_t)i * kStep;
                 ok = copy_step<S>(b, n, K_GROUPED && k + kStep > tile.k_end, &q.a, A_MN, m, 0, &q.b, B_MN, nn, K_GROUPED ? 0 : tile.problem, (int)k);
             }
         }

@@ -74,7 +74,9 @@ __device__ __forceinline__ uint64_t now_ns()
     return t;
 }
 
-constexpr uint64_t kWaitLimitNs = 2000000000;   // no wait of a working kernel comes near it
+// No wait of a working kernel comes near it: the longest is for one tile's products,
+// half a second for every 10^8 of k.
+constexpr uint64_t kWaitLimitNs = 20000000000;
 
 // Waits for the phase; false when the limit ran out, here or in another wait
 // of the block (`gave_up`).
