@@ -32,6 +32,7 @@ struct Tile {
     int problem;         // the weight's index
     int64_t m0, m_end;   // rows of D
     int64_t n0;
+    int cols;
     int64_t k0, k_end;
     int steps;
 };
@@ -53,17 +54,26 @@ struct List {
     const Problems& q;
     const int* start;    // first row tile of each group, the tail's and the end; k-grouped: the groups, longest first
     const int* rows;     // first row of each group, the tail's and the end; both in shared memory
+    int64_t whole, total;   // tiles that are, and all of them
 
-    __device__ int64_t total() const
+    // `at_once`: CTAs or pairs.  Where the last round would keep at most half of them,
+    // its tiles are halves: a pair's step is bound by its products, which halve.
+    __device__ List(const Problems& problems, const int* start_, const int* rows_, int64_t at_once) : q(problems), start(start_), rows(rows_)
     {
-        return (K_GROUPED ? (int64_t)q.p.experts * q.tiles_m : (int64_t)start[q.p.experts + 1]) * q.tiles_n;
+        total = (K_GROUPED ? (int64_t)q.p.experts * q.tiles_m : (int64_t)start[q.p.experts + 1]) * q.tiles_n;
+        const int64_t last = total % at_once;
+        whole = S::CTAS == 2 && 2 * last <= at_once ? total - last : total;
+        total += total - whole;
     }
 
     __device__ Tile at(int64_t t) const
     {
         Tile r;
+        const int64_t half = t < whole ? 0 : (t - whole) & 1;
+        r.cols = t < whole ? S::kCols : S::kCols / 2;
+        if (t >= whole) t = whole + (t - whole) / 2;
         const int64_t row_tile = t / q.tiles_n;
-        r.n0 = (t - row_tile * q.tiles_n) * S::kTile;
+        r.n0 = (t - row_tile * q.tiles_n) * S::kTile + half * (S::kCols / 2);
         if constexpr (K_GROUPED) {
             const int64_t place = row_tile / q.tiles_m;
             r.problem = start[place];
@@ -81,6 +91,7 @@ struct List {
             r.m_end = rows[lo + 1];
             r.k0 = 0, r.k_end = lo == q.p.experts ? 0 : q.p.k;
         }
+        if (r.n0 >= q.p.n) r.k_end = r.k0;   // half a tile past the columns: nothing to store
         r.steps = (int)((r.k_end - r.k0 + kStep - 1) / kStep);
         return r;
     }
@@ -203,9 +214,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_products(const __grid_cons
         __syncthreads();
     }
 
-    const List<S, K_GROUPED> list{q, start, rows};
-    const int64_t total = list.total();
     const Turns<K_GROUPED> turns{(int64_t)gridDim.x / S::CTAS, (int64_t)blockIdx.x / S::CTAS};
+    const List<S, K_GROUPED> list(q, start, rows, turns.count);
+    const int64_t total = list.total;
 
     if (warp == 0 && tc::elect_one()) {
         uint32_t n = 0;
@@ -213,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_products(const __grid_cons
         for (int64_t turn = 0; ok && turns.at(turn) < total; ++turn) {
             const Tile tile = list.at(turns.at(turn));
             // (a coordinate past the rows is read as zeros, and so is the largest one)
-            const int m = (int)min(tile.m0 + b.rank * kRows, (int64_t)INT_MAX), nn = (int)tile.n0 + (int)b.rank * kRows;
+            const int m = (int)min(tile.m0 + b.rank * kRows, (int64_t)INT_MAX), nn = (int)tile.n0 + (int)b.rank * (tile.cols / S::CTAS);
             for (int i = 0; ok && i < tile.steps; ++i, ++n) {
                 const int64_t k = tile.k0 + (int64_t)i * kStep;
                 ok = copy_step<S>(b, n, K_GROUPED && k + kStep > tile.k_end, &q.a, A_MN, m, 0, &q.b, B_MN, nn, K_GROUPED ? 0 : tile.problem, (int)k);
@@ -221,11 +232,11 @@ __global__ void __launch_bounds__(kThreads, 1) expert_products(const __grid_cons
         }
         finish_copies<S>(b, n, ok);
     } else if (warp == 1 && b.rank == 0 && tc::elect_one()) {
-        const uint32_t instr = tc::instruction(q.p.dtype == EMB_BF16, A_MN, B_MN, S::kTile, S::kTile);
         uint32_t n = 0, made = 0;
         for (int64_t turn = 0; turns.at(turn) < total; ++turn) {
             const Tile tile = list.at(turns.at(turn));
             if (!tile.steps) continue;
+            const uint32_t instr = tc::instruction(q.p.dtype == EMB_BF16, A_MN, B_MN, S::kTile, tile.cols);
             if (!multiply<S>(b, made++, n, tile.k_end - tile.k0, instr, A_MN, B_MN)) break;
             n += tile.steps;
         }
@@ -268,7 +279,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_products(const __grid_cons
         unsigned char* const mine = staging + (warp - 4) * kStaging;
         for (int64_t turn = 0; turns.at(turn) < total; ++turn) {
             const Tile tile = list.at(turns.at(turn));
-            const Part part = part_of<S>(b, made);
+            Part part = part_of<S>(b, made);
+            if (tile.cols < S::kCols) part.c0 /= 2, part.c1 = part.c0 + tile.cols / 2;
             if (tile.steps) {
                 ++made;
                 if (!tc::bar_wait_warp(part.full, part.phase, b.gave_up)) break;
@@ -300,7 +312,7 @@ int launch(Problems& q, cudaStream_t st)
     q.tiles_m = (int)((p.m + S::kTile - 1) / S::kTile);
     // m-grouped: every group may add a partly filled tile, and the tail one
     const int64_t tiles = (K_GROUPED ? (int64_t)q.tiles_m * p.experts : q.tiles_m + p.experts + 1) * q.tiles_n;
-    const int blocks = (int)(tiles < dev.sms / S::CTAS ? tiles : dev.sms / S::CTAS) * S::CTAS;
+    const int blocks = (int)std::min<int64_t>(tiles * S::CTAS, dev.sms / S::CTAS) * S::CTAS;   // pairs: two halves of a tile
     auto* const kernel = expert_products<S, A_MN, B_MN, K_GROUPED>;
     static std::atomic<bool> sized[kMaxDevices];
     if (!sized[dev.number].load(std::memory_order_relaxed)) {

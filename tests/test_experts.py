@@ -246,6 +246,23 @@ def test_linear_and_its_gradients(T, k, E, K, N, dropped, dtype, extra, skew):
 
 
 @gpu
+@pytest.mark.parametrize("T,k,E,K,N", [(20000, 1, 3, 136, 2056), (9000, 2, 7, 1032, 776), (30000, 2, 200, 72, 264), (3, 2, 1024, 64, 4096)])
+def test_linear_in_many_tiles(T, k, E, K, N):
+    # pairs and single CTAs, several rounds of tiles, last rounds of halves
+    plan, off, x, gy, w = linear_case(T, k, E, K, N, 0.05, BF, skew=E < 100)
+    y = emb.expert_linear(plan, x, w)
+    dx, dw = emb.expert_linear_grad(plan, gy, x, w)
+    for e in range(0, E, max(1, E // 7)):
+        a, b = off[e], off[e + 1]
+        xe, ge, we = x[a:b].double(), gy[a:b].double(), w[e].double()
+        for got, p, q, n in ((y[a:b], xe, we.t(), K), (dx[a:b], ge, we, N), (dw[e], ge.t(), xe, b - a)):
+            ref, total = p @ q, p.abs() @ q.abs()
+            check_close(got, ref, out_bound(ref, BF, total, n, 2.0 ** -23))
+    assert not y[off[-1]:].any() and not dx[off[-1]:].any()
+    assert emb.dense_status() == emb.EMB_OK
+
+
+@gpu
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("T", [6, 500])
 def test_linear_keeps_groups_apart_whatever_they_hold(dtype, T):

@@ -75,6 +75,33 @@ def test_against_64_bits(batch, rows, cols, kind, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("batch,rows,cols", [(24, 300, 500), (12, 1024, 2600), (2, 2600, 700), (40, 130, 65), (300, 20, 90)])
+def test_many_tiles_at_once(batch, rows, cols):
+    # several rounds of tiles of each width, matrices that run into each other's products
+    G = matrices(batch, batch, rows, cols, "decay", BF)
+    got, ref = emb.orthogonalize(G), plain(G)
+    assert max(off(got[i], ref[i]) for i in range(batch)) <= BOUND
+    assert torch.equal(got, emb.orthogonalize(G))      # and the same again
+    assert emb.dense_status() == emb.EMB_OK
+
+
+@gpu
+def test_a_graph_captures_the_steps():
+    for rows, cols in ((100, 300), (300, 200)):
+        G = matrices(1, 2, rows, cols, "flat", F32)
+        emb.orthogonalize(G)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = emb.orthogonalize(G)
+        G.copy_(matrices(2, 2, rows, cols, "decay", F32))
+        for _ in range(2):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, emb.orthogonalize(G))
+
+
+@gpu
 @pytest.mark.parametrize("steps", [1, 2, 3, 8])
 @pytest.mark.parametrize("rows,cols", [(96, 200), (200, 96)])
 def test_steps_and_coefficients(steps, rows, cols):
