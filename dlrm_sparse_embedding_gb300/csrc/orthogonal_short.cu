@@ -13,12 +13,14 @@
 // W's eigenvalues grow by up to a a step where X's singular values are small,
 // and their rounding must not reach the large ones.  So A, Q and W are held as
 // two fp16 numbers, 22 bits, each product is three (the low parts' own product
-// is below the last bit), and after W may have grown kGrowth-fold X is written
-// back and the rest of the steps starts over from it.  Emulated in 64 bits over
-// 1 x 1 to 128 x 256 matrices of flat, 1/i, 1/i^2, low-rank and rank-1 spectra
-// and 3 to 12 steps, the result is 1e-6 to 9e-4 off, less than the output's
-// rounding to bf16 (1.7e-3).  (One fp16 number for each would be far off: with
-// so few singular values a rounding has few others to average with.)
+// is below the last bit), and W may grow kGrowth-fold (five steps of a = 3.44);
+// more steps are done in passes of kGrowthMany (three), with X written back in
+// between, because what one pass loses the next ones multiply.  Emulated in 64 bits
+// over 1 x 1 to 128 x 256 matrices of flat, 1/i, 1/i^2, low-rank and rank-1 spectra,
+// the result is 1e-6 to 4e-4 off after five steps, less than the output's rounding to
+// bf16 (1.7e-3), and 1e-5 after nine (in passes of five and four: up to 1e-3, six
+// at once: 5e-3).  (One fp16 number for each would be far off: with so few singular
+// values a rounding has few others to average with.)
 #include <cmath>
 
 #include "orthogonal.cuh"
@@ -28,7 +30,7 @@ namespace {
 
 using namespace core;
 
-constexpr float kGrowth = 600.f;
+constexpr float kGrowth = 600.f, kGrowthMany = 50.f;
 // The tensor cores truncate where fp32 rounds: over 5000 columns A0 was 2e-5 off,
 // which W's growth made 6e-3 of the result.  After so many steps of 64 columns
 // the accumulator's sum goes on in registers.
@@ -446,13 +448,14 @@ __global__ void __launch_bounds__(kThreads, 1) short_apply(const __grid_constant
     if (warp == 2) tc::tmem_free<1>(tmem, 2 * kRows);
 }
 
-// Steps until W may have grown kGrowth-fold.
-int steps_a_pass(float a)
+// Most steps of a pass.
+int steps_a_pass(int steps, float a)
 {
-    const float grow = std::fabs(a);
-    if (!(grow > 1.f)) return 32;
-    const int n = (int)(std::log(kGrowth) / std::log(grow));
-    return n < 1 ? 1 : n > 32 ? 32 : n;
+    const auto until = [&](float growth) {   // W may have grown so much
+        const float n = std::log(growth) / std::log(std::fabs(a));
+        return !(std::fabs(a) > 1.f) || n > 32.f ? 32 : n < 1.f ? 1 : (int)n;
+    };
+    return steps <= until(kGrowth) ? steps : until(kGrowthMany);
 }
 
 }  // namespace
@@ -483,7 +486,7 @@ int run_short(const StepsArgs& p, cudaStream_t st)
     if (!make_map(&q.w_map, EMB_F16, p.w, false, kShort, kShort, p.batch, kShort, kShort * kShort) ||
         !make_map(&q.w_low_map, EMB_F16, p.w_low, false, kShort, kShort, p.batch, kShort, kShort * kShort))
         return EMB_ERR_CUDA;
-    const int most = steps_a_pass(p.a), passes = (p.steps + most - 1) / most;
+    const int most = steps_a_pass(p.steps, p.a), passes = (p.steps + most - 1) / most;
     int done = 0;
     for (int i = 0; i < passes; ++i) {
         const int from = i & 1;
