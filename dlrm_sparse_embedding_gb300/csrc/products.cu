@@ -1,9 +1,9 @@
 // The experts' products on the tensor cores: D = A B^T for each group of rows.
 //
 // Bound by the tensor cores where groups are long: three products of 65536 rows,
-// 1024 x 4096, 32 groups take 315, 301 and 324 us (forward, gradients of the rows and
-// of the weights: 1.71, 1.79 and 1.66 PFLOP/s, the tensor cores busy 91, 92 and 80%
-// of the time), and one dense product of the same size by the vendor's library 275 us. Tiles
+// 1024 x 4096, 32 groups take 319, 309 and 308 us (forward, gradients of the rows and
+// of the weights: 1.69, 1.74 and 1.75 PFLOP/s, the tensor cores busy 89, 93 and 86%
+// of the time), and one dense product of that size by the vendor's library 280 us.  Tiles
 // of 256 x 256 by pairs of CTAs are what lets them: a step of 64 k takes 512 cycles
 // of products and moves 32 KB to each SM; 128 x 128 would move as much in half the
 // cycles.  Where groups are short it is bound by the weights' bytes: 192 rows, 64
