@@ -255,9 +255,9 @@ int start(const Input& q, const T* g, int64_t batch, cudaStream_t st)
 // ---------------------------------------------------------------------------
 // 16 matrices of 1024 x 3328 take 966 us for five steps, 955 TFLOP/s of what symmetry
 // leaves: reading G twice and writing X takes 51 us of them, and of the rest the
-// tensor cores are busy 52%, DRAM 63% (3.7 GB): A's products (33
-// thousand cycles a tile, 27 of them products) run beside nothing that uses memory,
-// the update (16 and 8) beside 512 KB of X a tile.  One of 1777 x 519 takes 121 us,
+// tensor cores are busy 52%, DRAM 63% (3.7 GB): A's products (33 thousand cycles a
+// tile, 27 of them products) run beside nothing that uses memory, the update (16 and
+// 8) beside 512 KB of X a tile.  One of 1777 x 519 takes 121 us,
 // bound by the chain of 15 products: 7 us each, of which the products are 1 to 2.
 //
 // All products of all steps are one list of tiles for one persistent grid (see
@@ -269,13 +269,13 @@ int start(const Input& q, const T* g, int64_t batch, cudaStream_t st)
 //
 // A and B are symmetric: only the tiles on and below the diagonal are computed,
 // the others are written as their transposes.
-enum Product { kGram, kQuadratic, kUpdate };
-
 //
 // With few tiles they are 64 columns wide, and the k of A's (the long side) is
 // shared by a cluster: every CTA sums its part of the steps, sends each other one its
 // 32 rows of the sum, and finishes its own 32 rows from the parts it was sent, added
 // in the CTAs' order.
+enum Product { kGram, kQuadratic, kUpdate };   // A = X X^T, B = b A + c A A, X' = a X + B X
+
 constexpr int kSplit = 4;
 constexpr int kStaging = 32 * kChunk * 4;       // bytes of shared memory for 32 rows of 32 columns in fp32
 
@@ -283,7 +283,7 @@ struct Counts {
     int ahead;   // tiles whose C may be read
     int taken;   // tiles the epilogue has begun
     int stored[kEpilogueWarps];   // tiles each of its warps has stored
-    uint64_t received, sent;      // barriers: the parts of my columns are here; the parts I sent have been used
+    uint64_t received, sent;      // barriers: the parts of this CTA's rows are here; the parts it sent have been used
 };
 constexpr int kCountsBytes = 128;
 static_assert(sizeof(Counts) <= kCountsBytes, "the counts' room");
@@ -507,18 +507,18 @@ __device__ __forceinline__ bool finish(const Steps& q, const Tile& tile, const P
     }
     for (int c = c0; c < c1; c += kChunk) {
         if constexpr (!SHARED) {
-        uint32_t v[32];
-        tc::tmem_load32(part.tmem + c, v);
-        if (c + kChunk == c1) {
-            tc::fence_before();
-            if (lane == 0) tc::bar_arrive(part.empty);
-        }
-        // 16-byte piece i of row r is at i ^ (r & 7) ^ 2 (r >> 3): rows, and columns of eight rows, without conflicts
+            uint32_t v[32];
+            tc::tmem_load32(part.tmem + c, v);
+            if (c + kChunk == c1) {
+                tc::fence_before();
+                if (lane == 0) tc::bar_arrive(part.empty);
+            }
+            // 16-byte piece i of row r is at i ^ (r & 7) ^ 2 (r >> 3): rows, and columns of eight rows, without conflicts
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint4*>(mine + lane * kChunk + ((i ^ (lane & 7) ^ ((lane >> 3) << 1)) * 4)) =
-                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        __syncwarp();
+            for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4*>(mine + lane * kChunk + ((i ^ (lane & 7) ^ ((lane >> 3) << 1)) * 4)) =
+                    make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            __syncwarp();
         }
         const int64_t n = tile.n0 + c + p * 8;
         uint4 ch[4], cl[4];
@@ -716,7 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1) newton_schulz(const __grid_consta
             part_steps<S>(tile, b.rank, from, to);
             if (from == to) continue;
             const bool a_mn = tile.product == kGram && q.tall, b_mn = tile.product == kGram ? q.tall : tile.product == kUpdate && !q.tall;
-            if (!multiply<S>(b, made++, n, min(tile.k, (int64_t)to * kStep) - (int64_t)from * kStep, tc::instruction(false, a_mn, b_mn, S::kTile, S::kCols), a_mn, b_mn)) break;
+            const uint32_t instr = tc::instruction(false, a_mn, b_mn, S::kTile, S::kCols);
+            if (!multiply<S>(b, made++, n, min(tile.k, (int64_t)to * kStep) - (int64_t)from * kStep, instr, a_mn, b_mn)) break;
             n += to - from;
         }
     } else if (warp == 2) {
