@@ -3,7 +3,9 @@ each expert's weights and added back, with the gradients.
 
 Argument checks and marshalling only; the work is in libemb.so.  Tensors are on
 the current CUDA device.  Every call takes `stream`: it runs on that stream
-(default: the current one), and what it returns is allocated for it.
+(default: the current one), and what it returns is allocated for it.  The caller
+orders it after the work that makes its inputs; memory of inputs that are freed
+meanwhile is not used again before the call's work is done.
 """
 from __future__ import annotations
 
@@ -21,9 +23,15 @@ MAX_EXPERTS_PER_TOKEN = 64
 
 
 def _on(stream, call, *args):
-    """`call` on another stream: what it returns is allocated for that stream."""
+    """`call` on another stream: what it returns is allocated for that stream, and
+    its inputs' memory is kept until that stream has passed the call."""
     with torch.cuda.stream(stream):
-        return call(*args)
+        result = call(*args)
+    for arg in args:
+        for t in (arg.offsets, arg.src, arg.pos) if isinstance(arg, ExpertPlan) else (arg,):
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
+    return result
 
 
 def _stream(device: torch.device) -> int:

@@ -467,3 +467,28 @@ def test_the_library_refuses_on_the_host():
         assert L.emb_expert_linear(*args, None) == bad, args
     assert L.emb_expert_linear_grad_rows(p, 0x4000, 16, 0x5000, 24, 16, 2, 0x6004, None) == bad
     assert L.emb_expert_linear_grad_weight(p, 0x4000, 16, 0x5000, 20, 24, 16, 2, 0x6000, None) == bad
+
+
+@gpu
+def test_inputs_freed_while_another_stream_still_reads_them():
+    g = gen(77)
+    E, side = 4, torch.cuda.Stream()
+    ids, x = make_ids(g, 700, 2, E), normal(g, 700, 264, dtype=BF)
+    update = normal(g, 200, 136)
+    ref, orthogonal = emb.expert_dispatch(emb.expert_sort(ids, E), x), emb.orthogonalize(update)
+    for _ in range(2):                                # the first time, kernels are loaded
+        copies = [ids.clone(), x.clone(), update.clone()]
+        plan = emb.expert_sort(copies[0], E)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)
+        again = emb.expert_sort(copies[0], E, stream=side)
+        rows = emb.expert_dispatch(plan, copies[1], stream=side)
+        result = emb.orthogonalize(copies[2], stream=side)
+        shapes = [(t.shape, t.dtype) for t in copies + [plan.offsets, plan.src, plan.pos]]
+        del copies, plan
+        keep = [torch.full(shape, 1, dtype=dtype, device="cuda") for shape, dtype in shapes for _ in range(8)]
+        torch.cuda.synchronize()
+        assert len(keep) == 8 * len(shapes)
+        assert torch.equal(rows, ref) and torch.equal(result, orthogonal)
+        assert torch.equal(emb.expert_dispatch(again, x), ref)
