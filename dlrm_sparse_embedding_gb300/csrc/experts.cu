@@ -40,7 +40,8 @@ __global__ void take_status(int* status) { status[1] = atomicExch(&status[0], 0)
 constexpr int kPlaceThreads = 1024;
 constexpr int kPlaceWarps = kPlaceThreads / 32;
 constexpr int kOneChunk = 4 * kPlaceThreads;   // up to so many assignments one block does everything, without expert_count
-constexpr int kMaxChunks = 2 * 152;            // at most two blocks an SM
+constexpr int kSms = 152;
+constexpr int kMaxChunks = 2 * kSms;           // at most two blocks an SM
 
 template <class ID>
 __device__ __forceinline__ int bucket_of(const ID* ids, int64_t a, int E, int* status)
@@ -275,14 +276,18 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_rows(emb_expert_plan pla
 // dispatch's gradient).  Bound by memory: ROWS rows' pieces of kSumUnroll vectors
 // are on their way at once (one row after another, four vectors each: 105 us where
 // this takes 67, and 181 where it takes 90; eight vectors a lane for 2 rows: 77).
-constexpr int kSumUnroll = 2;
+// Single elements are more at once, as far as there are registers (16384 x 2, 1025
+// wide: 70 us with two and 41 with eight; 32768 x 4, weighted: 145 with two or eight
+// and 106 with four).
+template <int V, int ROWS, bool WEIGHTED>
+constexpr int kSumUnroll = V == 8 ? 2 : ROWS == 4 && WEIGHTED ? 4 : 8;
 
 template <int V, class R, class O, bool WEIGHTED, int ROWS>
 __global__ void __launch_bounds__(kRowThreads) gather_sum(emb_expert_plan plan, const R* __restrict__ rows,
                                                           int64_t rows_stride, const float* __restrict__ weights,
                                                           int64_t width, int64_t pieces, O* __restrict__ out)
 {
-    constexpr int U = kSumUnroll;
+    constexpr int U = kSumUnroll<V, ROWS, WEIGHTED>;
     const int lane = threadIdx.x & 31, P = (int)(plan.tokens * plan.k);
     let_next_begin();
     wait_for_earlier();
@@ -325,6 +330,8 @@ __global__ void __launch_bounds__(kRowThreads) gather_sum(emb_expert_plan plan, 
 // take a token: its gradient is loaded once for kPart of its experts at a time, and
 // each row's dot product is added up over the block in a fixed order.
 constexpr int kPart = 4;
+template <int V>
+constexpr int kGradUnroll = V == 1 ? 8 : 1;   // of a lane's vectors on their way at once (16384 x 2, 1025 wide: 1 92 us, 8 49)
 
 template <int V, class O, class R>
 __global__ void __launch_bounds__(kRowThreads) combine_grad(emb_expert_plan plan, const O* __restrict__ grad_out,
@@ -336,7 +343,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad(emb_expert_plan plan
     __shared__ float part[kRowThreads / 32][kPart];
     const int P = (int)(plan.tokens * plan.k), lane = threadIdx.x & 31;
     const int warps_of = blockDim.x / 32, wx = threadIdx.x >> 5, wy = threadIdx.y * warps_of;
-    const int64_t step = (int64_t)gridDim.x * blockDim.y;
+    const int64_t step = (int64_t)gridDim.x * blockDim.y, next = (int64_t)blockDim.x * V;
     let_next_begin();
     wait_for_earlier();
     // a block's tokens move on together: every thread meets every barrier
@@ -352,26 +359,38 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad(emb_expert_plan plan
                 if ((unsigned)p[q] >= (unsigned)P) p[q] = -1;
                 if (p[q] >= 0) w[q] = __ldg(&weights[token * plan.k + j0 + q]);
             }
-            if (has) {
-                for (int64_t c = (int64_t)threadIdx.x * V; c < width; c += (int64_t)blockDim.x * V) {
-                    Raw<V, O> g;
-                    Raw<V, R> y[kPart];
-                    g.load(grad_out + token * grad_stride + c);
+            const auto step_of = [&](auto many, int64_t c0) {
+                constexpr int U = decltype(many)::value;
+                Raw<V, O> g[U];
+                Raw<V, R> y[U][kPart];
 #pragma unroll
-                    for (int q = 0; q < kPart; ++q)
-                        if (p[q] >= 0) y[q].load(rows + p[q] * rows_stride + c);
+                for (int u = 0; u < U; ++u) g[u].load(grad_out + token * grad_stride + c0 + u * next);
 #pragma unroll
-                    for (int q = 0; q < kPart; ++q)
-                        if (p[q] >= 0) {
+                for (int q = 0; q < kPart; ++q)
+                    if (p[q] >= 0) {
+#pragma unroll
+                        for (int u = 0; u < U; ++u) y[u][q].load(rows + p[q] * rows_stride + c0 + u * next);
+                    }
+#pragma unroll
+                for (int q = 0; q < kPart; ++q)
+                    if (p[q] >= 0) {
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
                             float d[V];
 #pragma unroll
                             for (int i = 0; i < V; ++i) {
-                                dot[q] = __fmaf_rn(g[i], y[q][i], dot[q]);
-                                d[i] = w[q] * g[i];
+                                dot[q] = __fmaf_rn(g[u][i], y[u][q][i], dot[q]);
+                                d[i] = w[q] * g[u][i];
                             }
-                            store_vec<V, R>(grad_rows + (int64_t)p[q] * width + c, d);
+                            store_vec<V, R>(grad_rows + (int64_t)p[q] * width + c0 + u * next, d);
                         }
-                }
+                    }
+            };
+            if (has) {
+                int64_t c = (int64_t)threadIdx.x * V;
+                if constexpr (kGradUnroll<V> > 1)
+                    for (; c + (kGradUnroll<V> - 1) * next < width; c += kGradUnroll<V> * next) step_of(std::integral_constant<int, kGradUnroll<V>>(), c);
+                for (; c < width; c += next) step_of(std::integral_constant<int, 1>(), c);
             }
 #pragma unroll
             for (int q = 0; q < kPart; ++q) {
@@ -429,19 +448,17 @@ int launch_gather_sum(const emb_expert_plan& plan, const void* rows, int rows_dt
         return with_type(out_dtype, [&](auto o) {
             using R = decltype(r);
             using O = decltype(o);
-            const int at_once = plan.k <= 1 ? 1 : plan.k <= 2 ? 2 : 4;
-            const int64_t pieces = pieces_of(width, w8 ? 8 : 1, kSumUnroll);
-            const unsigned blocks = row_blocks(plan.tokens * pieces);
-            const auto go = [&](auto kernel) {
-                return launch_next(kernel, blocks, kRowThreads, 0, st, 1, plan, (const R*)rows, stride, weights, width, pieces, (O*)out);
+            const auto go = [&](auto kernel, int64_t pieces) {
+                return launch_next(kernel, row_blocks(plan.tokens * pieces), kRowThreads, 0, st, 1, plan, (const R*)rows, stride, weights, width,
+                                   pieces, (O*)out);
             };
-            if (w8)
-                return at_once == 1   ? go(gather_sum<8, R, O, WEIGHTED, 1>)
-                       : at_once == 2 ? go(gather_sum<8, R, O, WEIGHTED, 2>)
-                                      : go(gather_sum<8, R, O, WEIGHTED, 4>);
-            return at_once == 1   ? go(gather_sum<1, R, O, WEIGHTED, 1>)
-                   : at_once == 2 ? go(gather_sum<1, R, O, WEIGHTED, 2>)
-                                  : go(gather_sum<1, R, O, WEIGHTED, 4>);
+            const auto pick = [&](auto v) {
+                constexpr int V = decltype(v)::value;
+                return plan.k <= 1   ? go(gather_sum<V, R, O, WEIGHTED, 1>, pieces_of(width, V, kSumUnroll<V, 1, WEIGHTED>))
+                       : plan.k <= 2 ? go(gather_sum<V, R, O, WEIGHTED, 2>, pieces_of(width, V, kSumUnroll<V, 2, WEIGHTED>))
+                                     : go(gather_sum<V, R, O, WEIGHTED, 4>, pieces_of(width, V, kSumUnroll<V, 4, WEIGHTED>));
+            };
+            return w8 ? pick(std::integral_constant<int, 8>()) : pick(std::integral_constant<int, 1>());
         });
     });
 }
@@ -592,9 +609,11 @@ extern "C" int emb_expert_combine_grad(const emb_expert_plan* plan, const void* 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool w8 = wide(grad_out, out_dtype, grad_stride, width) && wide(rows, rows_dtype, rows_stride, width) &&
                     wide(grad_rows, rows_dtype, width, width);
-    const int V = w8 ? 8 : 1;
-    int tx = 32;   // threads a token: enough that each has two vectors of its row
-    while (tx < kRowThreads && (int64_t)tx * 2 * V < width) tx *= 2;
+    // Threads a token: 64 elements each, because the more tokens a block has the less it
+    // waits for one, and down to 16 where tokens are too few to fill the GPU.  With 64 and
+    // 16, 3328 wide: 16384 x 2 100 and 119 us, 300 x 8 22.5 and 14.3 us.
+    int tx = 32;
+    while (tx < kRowThreads && (tx * 64 < width || (tx * 16 < width && plan->tokens * tx * 2 <= kSms * 1024))) tx *= 2;
     const dim3 block(tx, kRowThreads / tx);
     const int64_t b = (plan->tokens + block.y - 1) / block.y;
     const unsigned blocks = (unsigned)(b > (1 << 20) ? (1 << 20) : b);
