@@ -10,6 +10,7 @@
 // the sorted rows: a token's row (its gradient) is loaded into registers once
 // and stored to (combined from) its k places, so the k copies never come from
 // memory again.
+#include <algorithm>
 #include <mutex>
 #include <type_traits>
 
@@ -238,24 +239,41 @@ __device__ __forceinline__ void zero_tail(T* rows, int64_t width, int kept, int 
         for (int64_t c = (int64_t)lane * V; c < width; c += 32 * V) store_vec<V, T>(rows + p * width + c, zero);
 }
 
-// A warp takes kUnroll * 32 vectors of one token's row: loaded once, stored to
-// each of its k rows (walking the sorted rows instead would read it k times).
-template <int V, class X, class R>
+// LANES lanes take UNROLL vectors each of a token's row.  A row of the grid is the
+// row's pieces, its blocks 256 / LANES tokens: nobody divides, which costs as much as
+// the loads of a few elements (16384 x 2, 1025 wide, gather: 36.8 us with, 32.7 without).
+template <int V, int LANES, int UNROLL>
+struct Share {
+    static constexpr int kTokens = kRowThreads / LANES, kPiece = LANES * UNROLL * V;
+    static constexpr int64_t kMaxRows = 65535;
+
+    static dim3 grid(int64_t tokens, int64_t width)
+    {
+        return dim3((unsigned)((width + kPiece - 1) / kPiece), (unsigned)std::min((tokens + kTokens - 1) / kTokens, kMaxRows));
+    }
+    __device__ static int64_t first_token() { return (int64_t)blockIdx.y * kTokens + threadIdx.x / LANES; }
+    __device__ static int64_t token_step() { return (int64_t)gridDim.y * kTokens; }
+    __device__ static int64_t column() { return (int64_t)blockIdx.x * kPiece + threadIdx.x % LANES * V; }
+    __device__ static int64_t warp() { return ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (kRowThreads / 32) + threadIdx.x / 32; }
+    __device__ static int64_t warps() { return (int64_t)gridDim.x * gridDim.y * (kRowThreads / 32); }
+};
+
+// A token's row is loaded once and stored to each of its k rows (walking the sorted
+// rows instead would read it k times).
+template <int V, int LANES, class X, class R>
 __global__ void __launch_bounds__(kRowThreads) dispatch_rows(emb_expert_plan plan, const X* __restrict__ x,
-                                                             int64_t x_stride, int64_t width, int64_t pieces,
-                                                             R* __restrict__ rows)
+                                                             int64_t x_stride, int64_t width, R* __restrict__ rows)
 {
-    const int lane = threadIdx.x & 31, P = (int)(plan.tokens * plan.k);
+    using S = Share<V, LANES, kUnroll>;
+    const int P = (int)(plan.tokens * plan.k);
+    const int64_t c0 = S::column();
     let_next_begin();
     wait_for_earlier();
-    const int64_t warps = (int64_t)gridDim.x * (kRowThreads / 32);
-    const int64_t first = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-    for (int64_t u = first; u < plan.tokens * pieces; u += warps) {
-        const int64_t token = u / pieces, c0 = (u - token * pieces) * (32 * V * kUnroll) + lane * V;
+    for (int64_t token = S::first_token(); token < plan.tokens; token += S::token_step()) {
         Raw<V, X> raw[kUnroll];
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i)
-            if (c0 + i * 32 * V < width) raw[i].load(x + token * x_stride + c0 + i * 32 * V);
+            if (c0 + i * LANES * V < width) raw[i].load(x + token * x_stride + c0 + i * LANES * V);
         float v[kUnroll][V];
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i)
@@ -266,10 +284,10 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_rows(emb_expert_plan pla
             if ((unsigned)p >= (unsigned)P) continue;
 #pragma unroll
             for (int i = 0; i < kUnroll; ++i)
-                if (c0 + i * 32 * V < width) store_vec<V, R>(rows + (int64_t)p * width + c0 + i * 32 * V, v[i]);
+                if (c0 + i * LANES * V < width) store_vec<V, R>(rows + (int64_t)p * width + c0 + i * LANES * V, v[i]);
         }
     }
-    zero_tail<V, R>(rows, width, plan_offset(plan.offsets, plan.experts, P), P, first, warps, lane);
+    zero_tail<V, R>(rows, width, plan_offset(plan.offsets, plan.experts, P), P, S::warp(), S::warps(), threadIdx.x % 32);
 }
 
 // out[t] = sum_j w[t, j] rows[pos[t, j]]; without weights, the plain sum (the
@@ -282,19 +300,18 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_rows(emb_expert_plan pla
 template <int V, int ROWS, bool WEIGHTED>
 constexpr int kSumUnroll = V == 8 ? 2 : ROWS == 4 && WEIGHTED ? 4 : 8;
 
-template <int V, class R, class O, bool WEIGHTED, int ROWS>
+template <int V, int LANES, class R, class O, bool WEIGHTED, int ROWS>
 __global__ void __launch_bounds__(kRowThreads) gather_sum(emb_expert_plan plan, const R* __restrict__ rows,
                                                           int64_t rows_stride, const float* __restrict__ weights,
-                                                          int64_t width, int64_t pieces, O* __restrict__ out)
+                                                          int64_t width, O* __restrict__ out)
 {
     constexpr int U = kSumUnroll<V, ROWS, WEIGHTED>;
-    const int lane = threadIdx.x & 31, P = (int)(plan.tokens * plan.k);
+    using S = Share<V, LANES, U>;
+    const int P = (int)(plan.tokens * plan.k);
+    const int64_t c0 = S::column();
     let_next_begin();
     wait_for_earlier();
-    const int64_t warps = (int64_t)gridDim.x * (kRowThreads / 32);
-    const int64_t first = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-    for (int64_t u = first; u < plan.tokens * pieces; u += warps) {
-        const int64_t token = u / pieces, c0 = (u - token * pieces) * (32 * V * U) + lane * V;
+    for (int64_t token = S::first_token(); token < plan.tokens; token += S::token_step()) {
         float s[U][V] = {};
         for (int j0 = 0; j0 < plan.k; j0 += ROWS) {
             int p[ROWS];
@@ -309,8 +326,8 @@ __global__ void __launch_bounds__(kRowThreads) gather_sum(emb_expert_plan plan, 
             for (int j = 0; j < ROWS; ++j)
 #pragma unroll
                 for (int i = 0; i < U; ++i)
-                    if ((unsigned)p[j] < (unsigned)P && c0 + i * 32 * V < width)
-                        v[j][i].load(rows + p[j] * rows_stride + c0 + i * 32 * V);
+                    if ((unsigned)p[j] < (unsigned)P && c0 + i * LANES * V < width)
+                        v[j][i].load(rows + p[j] * rows_stride + c0 + i * LANES * V);
 #pragma unroll
             for (int j = 0; j < ROWS; ++j) {
                 if ((unsigned)p[j] >= (unsigned)P) continue;
@@ -322,13 +339,13 @@ __global__ void __launch_bounds__(kRowThreads) gather_sum(emb_expert_plan plan, 
         }
 #pragma unroll
         for (int i = 0; i < U; ++i)
-            if (c0 + i * 32 * V < width) store_vec<V, O>(out + token * width + c0 + i * 32 * V, s[i]);
+            if (c0 + i * LANES * V < width) store_vec<V, O>(out + token * width + c0 + i * LANES * V, s[i]);
     }
 }
 
 // Both gradients of the weighted sum in one pass over the rows.  blockDim.x threads
 // take a token: its gradient is loaded once for kPart of its experts at a time, and
-// each row's dot product is added up over the block in a fixed order.
+// each row's dot product is added up over them in a fixed order.
 constexpr int kPart = 4;
 template <int V>
 constexpr int kGradUnroll = V == 1 ? 8 : 1;   // of a lane's vectors on their way at once (16384 x 2, 1025 wide: 1 92 us, 8 49)
@@ -341,8 +358,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad(emb_expert_plan plan
                                                             float* __restrict__ grad_weights)
 {
     __shared__ float part[kRowThreads / 32][kPart];
-    const int P = (int)(plan.tokens * plan.k), lane = threadIdx.x & 31;
-    const int warps_of = blockDim.x / 32, wx = threadIdx.x >> 5, wy = threadIdx.y * warps_of;
+    const int P = (int)(plan.tokens * plan.k), thread = threadIdx.y * blockDim.x + threadIdx.x, lane = thread & 31, warp = thread >> 5;
     const int64_t step = (int64_t)gridDim.x * blockDim.y, next = (int64_t)blockDim.x * V;
     let_next_begin();
     wait_for_earlier();
@@ -395,21 +411,29 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad(emb_expert_plan plan
 #pragma unroll
             for (int q = 0; q < kPart; ++q) {
 #pragma unroll
-                for (int d = 16; d; d >>= 1) dot[q] += __shfl_xor_sync(0xffffffffu, dot[q], d);
-                if (lane == 0) part[wy + wx][q] = dot[q];
+                for (int d = 16; d; d >>= 1)
+                    if (d < blockDim.x) dot[q] += __shfl_xor_sync(0xffffffffu, dot[q], d);
             }
-            __syncthreads();
-            if (has && threadIdx.x < kPart && j0 + threadIdx.x < plan.k) {
-                float s = 0.f;
-                for (int v = 0; v < warps_of; ++v) s += part[wy + v][threadIdx.x];
-                grad_weights[token * plan.k + j0 + threadIdx.x] = s;
+            float s = 0.f;
+            if (blockDim.x > 32) {   // a token's warps meet
+#pragma unroll
+                for (int q = 0; q < kPart; ++q)
+                    if (lane == 0) part[warp][q] = dot[q];
+                __syncthreads();
+                if (threadIdx.x < kPart)
+                    for (int v = 0; v < blockDim.x / 32; ++v) s += part[warp + v][threadIdx.x];
+                __syncthreads();
+            } else {
+#pragma unroll
+                for (int q = 0; q < kPart; ++q)
+                    if (q == threadIdx.x) s = dot[q];
             }
-            __syncthreads();
+            if (has && threadIdx.x < kPart && j0 + threadIdx.x < plan.k) grad_weights[token * plan.k + j0 + threadIdx.x] = s;
         }
     }
     const int64_t warps = (int64_t)gridDim.x * (kRowThreads / 32);
     zero_tail<V, R>(grad_rows, width, plan_offset(plan.offsets, plan.experts, P), P,
-                    (int64_t)blockIdx.x * (kRowThreads / 32) + wy + wx, warps, lane);
+                    (int64_t)blockIdx.x * (kRowThreads / 32) + warp, warps, lane);
 }
 
 // Whether rows of `width` elements can be moved 16 bytes at a time.
@@ -423,13 +447,12 @@ bool rows_valid(const void* p, int dtype, int64_t stride, int64_t width, int64_t
     return dtype_valid(dtype) && stride >= width && aligned_to(p, dtype_bytes(dtype)) && (p || n == 0);
 }
 
-int64_t pieces_of(int64_t width, int V, int unroll) { return (width + 32 * V * unroll - 1) / (32 * V * unroll); }
+template <int N>
+using number = std::integral_constant<int, N>;
 
-unsigned row_blocks(int64_t warps)
-{
-    const int64_t per = kRowThreads / 32, b = (warps + per - 1) / per;
-    return (unsigned)(b < 1 ? 1 : b > (1 << 20) ? (1 << 20) : b);
-}
+// Aligned rows of at most so many elements are taken by 8 lanes instead of 32 (32768 x 4:
+// gather 12.3 us for 24.6 at 64 wide, 20.5 for 28.3 at 256).
+constexpr int64_t kShortRow = 256;
 
 template <class F>
 int with_type(int dtype, F f)
@@ -448,17 +471,17 @@ int launch_gather_sum(const emb_expert_plan& plan, const void* rows, int rows_dt
         return with_type(out_dtype, [&](auto o) {
             using R = decltype(r);
             using O = decltype(o);
-            const auto go = [&](auto kernel, int64_t pieces) {
-                return launch_next(kernel, row_blocks(plan.tokens * pieces), kRowThreads, 0, st, 1, plan, (const R*)rows, stride, weights, width,
-                                   pieces, (O*)out);
+            const auto go = [&](auto v, auto lanes, auto at_once) {
+                constexpr int V = decltype(v)::value, LANES = decltype(lanes)::value, ROWS = decltype(at_once)::value;
+                return launch_next(gather_sum<V, LANES, R, O, WEIGHTED, ROWS>, Share<V, LANES, kSumUnroll<V, ROWS, WEIGHTED>>::grid(plan.tokens, width),
+                                   kRowThreads, 0, st, 1, plan, (const R*)rows, stride, weights, width, (O*)out);
             };
-            const auto pick = [&](auto v) {
-                constexpr int V = decltype(v)::value;
-                return plan.k <= 1   ? go(gather_sum<V, R, O, WEIGHTED, 1>, pieces_of(width, V, kSumUnroll<V, 1, WEIGHTED>))
-                       : plan.k <= 2 ? go(gather_sum<V, R, O, WEIGHTED, 2>, pieces_of(width, V, kSumUnroll<V, 2, WEIGHTED>))
-                                     : go(gather_sum<V, R, O, WEIGHTED, 4>, pieces_of(width, V, kSumUnroll<V, 4, WEIGHTED>));
+            const auto pick = [&](auto v, auto lanes) {
+                return plan.k <= 1   ? go(v, lanes, number<1>())
+                       : plan.k <= 2 ? go(v, lanes, number<2>())
+                                     : go(v, lanes, number<4>());
             };
-            return w8 ? pick(std::integral_constant<int, 8>()) : pick(std::integral_constant<int, 1>());
+            return !w8 ? pick(number<1>(), number<32>()) : width <= kShortRow ? pick(number<8>(), number<8>()) : pick(number<8>(), number<32>());
         });
     });
 }
@@ -569,10 +592,12 @@ extern "C" int emb_expert_dispatch(const emb_expert_plan* plan, const void* x, i
         return with_type(rows_dtype, [&](auto rt) {
             using X = decltype(xt);
             using R = decltype(rt);
-            const int64_t pieces = pieces_of(width, w8 ? 8 : 1, kUnroll);
-            const unsigned blocks = row_blocks(plan->tokens * pieces);
-            return launch_next(w8 ? dispatch_rows<8, X, R> : dispatch_rows<1, X, R>, blocks, kRowThreads, 0, st, 1, *plan, (const X*)x, x_stride,
-                               width, pieces, (R*)rows);
+            const auto go = [&](auto v, auto lanes) {
+                constexpr int V = decltype(v)::value, LANES = decltype(lanes)::value;
+                return launch_next(dispatch_rows<V, LANES, X, R>, Share<V, LANES, kUnroll>::grid(plan->tokens, width), kRowThreads, 0, st, 1, *plan,
+                                   (const X*)x, x_stride, width, (R*)rows);
+            };
+            return !w8 ? go(number<1>(), number<32>()) : width <= kShortRow ? go(number<8>(), number<8>()) : go(number<8>(), number<32>());
         });
     });
 }
@@ -611,9 +636,11 @@ extern "C" int emb_expert_combine_grad(const emb_expert_plan* plan, const void* 
                     wide(grad_rows, rows_dtype, width, width);
     // Threads a token: 64 elements each, because the more tokens a block has the less it
     // waits for one, and down to 16 where tokens are too few to fill the GPU.  With 64 and
-    // 16, 3328 wide: 16384 x 2 100 and 119 us, 300 x 8 22.5 and 14.3 us.
-    int tx = 32;
-    while (tx < kRowThreads && (tx * 64 < width || (tx * 16 < width && plan->tokens * tx * 2 <= kSms * 1024))) tx *= 2;
+    // 16, 3328 wide: 16384 x 2 100 and 119 us, 300 x 8 22.5 and 14.3 us.  Less than a warp
+    // has 16 (32768 x 4, 64 wide: 28.7 us by 32 threads, 14.3 by 8).
+    int tx = w8 ? 8 : 32;
+    while (tx < 32 && tx * 16 < width) tx *= 2;
+    while (tx >= 32 && tx < kRowThreads && (tx * 64 < width || (tx * 16 < width && plan->tokens * tx * 2 <= kSms * 1024))) tx *= 2;
     const dim3 block(tx, kRowThreads / tx);
     const int64_t b = (plan->tokens + block.y - 1) / block.y;
     const unsigned blocks = (unsigned)(b > (1 << 20) ? (1 << 20) : b);

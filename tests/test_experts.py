@@ -492,3 +492,20 @@ def test_inputs_freed_while_another_stream_still_reads_them():
         assert len(keep) == 8 * len(shapes)
         assert torch.equal(rows, ref) and torch.equal(result, orthogonal)
         assert torch.equal(emb.expert_dispatch(again, x), ref)
+
+
+@gpu
+@pytest.mark.parametrize("width", [32, 56, 64, 65, 120, 128, 136, 200, 256, 264, 519, 1025, 2064])
+@pytest.mark.parametrize("k", [1, 2, 6])
+@pytest.mark.parametrize("T", [50, 1500])
+def test_rows_of_many_widths(T, k, width):
+    for extra in (0, 8, 3):
+        test_dispatch_and_its_gradient(T, k, 7, width, 0.1, F32, BF, extra)
+        test_combine_and_its_gradients(T, k, 7, width, 0.1, HF, F32, extra)
+
+
+@gpu
+@pytest.mark.parametrize("T,width", [(600011, 9), (2200003, 8), (600011, 40)])   # more than blocks take at once
+def test_very_many_short_rows(T, width):
+    test_dispatch_and_its_gradient(T, 1, 3, width, 0.01, BF, BF, 0)
+    test_combine_and_its_gradients(T, 1, 3, width, 0.01, BF, BF, 0)
