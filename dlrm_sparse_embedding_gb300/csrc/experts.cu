@@ -40,7 +40,7 @@ __global__ void take_status(int* status) { status[1] = atomicExch(&status[0], 0)
 // 31 us).
 constexpr int kPlaceThreads = 1024;
 constexpr int kPlaceWarps = kPlaceThreads / 32;
-constexpr int kOneChunk = 4 * kPlaceThreads;   // up to so many assignments one block does everything, without expert_count
+constexpr int kOneChunk = EMB_EXPERT_SORT_ALONE;   // up to so many assignments one block does everything, without expert_count
 constexpr int kSms = 152;
 constexpr int kMaxChunks = 2 * kSms;           // at most two blocks an SM
 

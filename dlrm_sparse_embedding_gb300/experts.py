@@ -20,6 +20,7 @@ from ._lib import DTYPES, EmbExpertPlan, check, lib
 _DTYPE_CODE = {torch.float32: DTYPES["f32"], torch.float16: DTYPES["f16"], torch.bfloat16: DTYPES["bf16"]}
 MAX_EXPERTS = 1024
 MAX_EXPERTS_PER_TOKEN = 64
+SORT_ALONE = 4096   # assignments up to which a sort leaves its workspace alone
 
 
 def _on(stream, call, *args):
@@ -120,6 +121,12 @@ def _sort_workspace(tokens: int, k: int, experts: int) -> int:
     return n.value
 
 
+@functools.lru_cache(maxsize=None)
+def _untouched(device: torch.device) -> torch.Tensor:
+    """The workspace of sorts that do not use theirs (an allocation takes 2 us of a small sort's 15)."""
+    return torch.empty(_sort_workspace(1, 1, 1), dtype=torch.uint8, device=device)
+
+
 def expert_sort(ids: torch.Tensor, num_experts: int, stream=None) -> ExpertPlan:
     """The plan of int32 or int64 ids [tokens, k] of experts in [0, num_experts).
 
@@ -144,7 +151,10 @@ def expert_sort(ids: torch.Tensor, num_experts: int, stream=None) -> ExpertPlan:
         torch.empty(E + 1, dtype=i32, device=device), torch.empty(T * k, dtype=i32, device=device),
         torch.empty((T, k), dtype=i32, device=device), T, k, E, device)
     size = _sort_workspace(T, k, E)
-    ws = torch.empty(size, dtype=torch.uint8, device=device)   # torch's blocks start at 512 bytes
+    if T * k <= SORT_ALONE:
+        ws = _untouched(device)
+    else:
+        ws = torch.empty(size, dtype=torch.uint8, device=device)   # torch's blocks start at 512 bytes
     check(lib.emb_expert_sort(ids.data_ptr(), ids.element_size(), plan._ref, ws.data_ptr(), size, _stream(device)),
           "emb_expert_sort")
     return plan

@@ -404,8 +404,10 @@ typedef struct {
  * (a dropped one).  Any other id outside [0, E) is treated as -1 and recorded
  * as EMB_ERR_KEY_RANGE.  The arrays of `plan` are written.  The workspace
  * (256-byte aligned, emb_expert_sort_workspace bytes) is free again once the
- * call's work on the stream is done.  No passage: library convenience (the
- * pages stop at the embeddings). */
+ * call's work on the stream is done; up to EMB_EXPERT_SORT_ALONE assignments
+ * nothing reads or writes it.  No passage: library convenience (the pages stop
+ * at the embeddings). */
+#define EMB_EXPERT_SORT_ALONE 4096
 int emb_expert_sort_workspace(int64_t tokens, int32_t k, int32_t experts, size_t* bytes);
 int emb_expert_sort(const void* ids, int32_t id_bytes, const emb_expert_plan* plan, void* workspace,
                     size_t workspace_bytes, void* stream);
