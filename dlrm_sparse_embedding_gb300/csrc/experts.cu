@@ -5,11 +5,17 @@
 // All of it is bound by memory: each row is read once and written once per
 // place it goes to.  16384 tokens, 2 experts each, 3328 wide, fp32 to bf16: sort 9 us,
 // gather 61 us (436 MB, 7.1 TB/s with what L2 keeps), its gradient 69 us (6.4 TB/s).
-// 32768 tokens, 4 experts each, 2048 wide, bf16: the weighted sum 102 us (6.4 TB/s),
-// its gradients 177 us (6.6 TB/s).  The kernels that touch rows therefore walk the tokens, not
-// the sorted rows: a token's row (its gradient) is loaded into registers once
-// and stored to (combined from) its k places, so the k copies never come from
+// 32768 tokens, 4 experts each, 2048 wide, bf16: the weighted sum 100 us (6.7 TB/s),
+// its gradients 173 us (7.0 TB/s).  The kernels that touch rows therefore walk the
+// tokens, not the sorted rows: a token's row (its gradient) is loaded into registers
+// once and stored to (combined from) its k places, so the k copies never come from
 // memory again.
+//
+// Rows that are not whole 16-byte vectors go an element a lane, bound by the number
+// of loads: 16384 x 2, 1025 wide, bf16, gather 33, its gradient 39, sum 41 and its
+// gradients 51 us, 1024 wide 22.5, 24.6, 24.6 and 37 us.  (Vectors from each written
+// row's own 16-byte boundary, shifted out of the words around them, took 35, 45, 57
+// and 200 us.)
 #include <algorithm>
 #include <mutex>
 #include <type_traits>
