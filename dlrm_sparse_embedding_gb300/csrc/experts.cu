@@ -11,11 +11,11 @@
 // once and stored to (combined from) its k places, so the k copies never come from
 // memory again.
 //
-// Rows that are not whole 16-byte vectors go an element a lane, bound by the number
-// of loads: 16384 x 2, 1025 wide, bf16, gather 33, its gradient 39, sum 41 and its
-// gradients 51 us, 1024 wide 22.5, 24.6, 24.6 and 37 us.  (Vectors from each written
-// row's own 16-byte boundary, shifted out of the words around them, took 35, 45, 57
-// and 200 us.)
+// Rows that are not whole 16-byte vectors go in pairs, or an element a lane, bound by
+// the number of loads: 16384 x 2, bf16, gather, its gradient, sum and its gradients
+// take 22.5, 24.6, 24.6 and 37 us at 1024 wide, 28.7, 28.7, 28.7 and 43 at 1026, 33,
+// 39, 41 and 51 at 1025.  (Vectors from each written row's own 16-byte boundary,
+// shifted out of the words around them, took 35, 45, 57 and 200 us.)
 #include <algorithm>
 #include <mutex>
 #include <type_traits>
@@ -189,34 +189,31 @@ size_t place_smem(int E)
 // rows
 // ---------------------------------------------------------------------------
 // V consecutive elements: 8 (moved 16 bytes at a time) where everything is
-// aligned for it, else 1.  They are kept as they are in memory until they are
-// used: a load in flight costs no more registers than its bytes.  Rows are read and
-// written once, so vectors pass as streams, which leave L2 first (gradients and
-// weighted sum of 32768 x 4 x 2048 together 299 us without, 273 with).
-template <class W>
-__device__ __forceinline__ W load_word(const W* p)
-{
-    if constexpr (sizeof(W) == 16) return __ldcs(p);
-    else return *p;
-}
-
-template <class W>
-__device__ __forceinline__ void store_word(W* p, const W& v)
-{
-    if constexpr (sizeof(W) == 16) __stcs(p, v);
-    else *p = v;
-}
+// aligned for it, else 2 where everything is for that, else 1.  They are kept as they
+// are in memory until they are used: a load in flight costs no more registers than its
+// bytes.  Rows are read and written once, so vectors pass as streams, which leave L2
+// first (gradients and weighted sum of 32768 x 4 x 2048 together 299 us without, 273
+// with).
+template <int V, class T>
+struct WordOf { using type = uint4; };
+template <class T>
+struct WordOf<2, T> { using type = typename std::conditional<sizeof(T) == 2, uint32_t, uint2>::type; };
+template <class T>
+struct WordOf<1, T> { using type = T; };
 
 template <int V, class T>
 struct Raw {
-    using Word = typename std::conditional<V == 1, T, uint4>::type;
+    using Word = typename WordOf<V, T>::type;
     static constexpr int kWords = V * sizeof(T) / sizeof(Word);
     Word w[kWords];
 
     __device__ __forceinline__ void load(const T* p)
     {
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) w[i] = load_word(reinterpret_cast<const Word*>(p) + i);
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (V > 1) w[i] = __ldcs(reinterpret_cast<const Word*>(p) + i);
+            else w[i] = p[i];
+        }
     }
     __device__ __forceinline__ float operator[](int i) const { return to_float<T>(reinterpret_cast<const T*>(w)[i]); }
 };
@@ -229,7 +226,10 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[V])
 #pragma unroll
     for (int i = 0; i < V; ++i) reinterpret_cast<T*>(r.w)[i] = from_float<T>(v[i]);
 #pragma unroll
-    for (int i = 0; i < Raw<V, T>::kWords; ++i) store_word(reinterpret_cast<Word*>(p) + i, r.w[i]);
+    for (int i = 0; i < Raw<V, T>::kWords; ++i) {
+        if constexpr (V > 1) __stcs(reinterpret_cast<Word*>(p) + i, r.w[i]);
+        else p[i] = r.w[i];
+    }
 }
 
 constexpr int kRowThreads = 256;
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_rows(emb_expert_plan pla
 // wide: 70 us with two and 41 with eight; 32768 x 4, weighted: 145 with two or eight
 // and 106 with four).
 template <int V, int ROWS, bool WEIGHTED>
-constexpr int kSumUnroll = V == 8 ? 2 : ROWS == 4 && WEIGHTED ? 4 : 8;
+constexpr int kSumUnroll = V == 8 ? 2 : ROWS == 4 && WEIGHTED ? 4 : 8 / V;
 
 template <int V, int LANES, class R, class O, bool WEIGHTED, int ROWS>
 __global__ void __launch_bounds__(kRowThreads) gather_sum(emb_expert_plan plan, const R* __restrict__ rows,
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kRowThreads) gather_sum(emb_expert_plan plan, 
 // each row's dot product is added up over them in a fixed order.
 constexpr int kPart = 4;
 template <int V>
-constexpr int kGradUnroll = V == 1 ? 8 : 1;   // of a lane's vectors on their way at once (16384 x 2, 1025 wide: 1 92 us, 8 49)
+constexpr int kGradUnroll = 8 / V;   // of a lane's vectors on their way at once (16384 x 2, 1025 wide: 1 92 us, 8 49)
 
 template <int V, class O, class R>
 __global__ void __launch_bounds__(kRowThreads) combine_grad(emb_expert_plan plan, const O* __restrict__ grad_out,
@@ -442,10 +442,12 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad(emb_expert_plan plan
                     (int64_t)blockIdx.x * (kRowThreads / 32) + warp, warps, lane);
 }
 
-// Whether rows of `width` elements can be moved 16 bytes at a time.
-bool wide(const void* p, int dtype, int64_t stride, int64_t width)
+// How many elements of such rows can be moved at a time.
+int vector_of(const void* p, int dtype, int64_t stride, int64_t width)
 {
-    return aligned_to(p, 16) && (stride * dtype_bytes(dtype)) % 16 == 0 && width % 8 == 0;
+    const int64_t bytes = dtype_bytes(dtype);
+    if (aligned_to(p, 16) && stride * bytes % 16 == 0 && width % 8 == 0) return 8;
+    return aligned_to(p, 2 * bytes) && stride % 2 == 0 && width % 2 == 0 ? 2 : 1;
 }
 
 bool rows_valid(const void* p, int dtype, int64_t stride, int64_t width, int64_t n)
@@ -456,9 +458,18 @@ bool rows_valid(const void* p, int dtype, int64_t stride, int64_t width, int64_t
 template <int N>
 using number = std::integral_constant<int, N>;
 
-// Aligned rows of at most so many elements are taken by 8 lanes instead of 32 (32768 x 4:
-// gather 12.3 us for 24.6 at 64 wide, 20.5 for 28.3 at 256).
+// f(vector, lanes a token).  Vectors of 8 of at most kShortRow elements are taken by 8
+// lanes instead of 32 (32768 x 4: gather 12.3 us for 24.6 at 64 wide, 20.5 for 28.3 at
+// 256); pairs (16384 x 2, 1026 wide: gather 28.7 us for 32.8 by elements, its gradient
+// 28.7 for 38.9, sum 28.7 for 41.0, its gradients 43.0 for 51.2).
 constexpr int64_t kShortRow = 256;
+
+template <class F>
+int with_vector(int vector, int64_t width, F f)
+{
+    if (vector == 8) return width <= kShortRow ? f(number<8>(), number<8>()) : f(number<8>(), number<32>());
+    return vector == 2 ? f(number<2>(), number<32>()) : f(number<1>(), number<32>());
+}
 
 template <class F>
 int with_type(int dtype, F f)
@@ -472,7 +483,7 @@ template <bool WEIGHTED>
 int launch_gather_sum(const emb_expert_plan& plan, const void* rows, int rows_dtype, int64_t stride, const float* weights,
                       int64_t width, void* out, int out_dtype, cudaStream_t st)
 {
-    const bool w8 = wide(rows, rows_dtype, stride, width) && wide(out, out_dtype, width, width);
+    const int vector = std::min(vector_of(rows, rows_dtype, stride, width), vector_of(out, out_dtype, width, width));
     return with_type(rows_dtype, [&](auto r) {
         return with_type(out_dtype, [&](auto o) {
             using R = decltype(r);
@@ -482,12 +493,11 @@ int launch_gather_sum(const emb_expert_plan& plan, const void* rows, int rows_dt
                 return launch_next(gather_sum<V, LANES, R, O, WEIGHTED, ROWS>, Share<V, LANES, kSumUnroll<V, ROWS, WEIGHTED>>::grid(plan.tokens, width),
                                    kRowThreads, 0, st, 1, plan, (const R*)rows, stride, weights, width, (O*)out);
             };
-            const auto pick = [&](auto v, auto lanes) {
+            return with_vector(vector, width, [&](auto v, auto lanes) {
                 return plan.k <= 1   ? go(v, lanes, number<1>())
                        : plan.k <= 2 ? go(v, lanes, number<2>())
                                      : go(v, lanes, number<4>());
-            };
-            return !w8 ? pick(number<1>(), number<32>()) : width <= kShortRow ? pick(number<8>(), number<8>()) : pick(number<8>(), number<32>());
+            });
         });
     });
 }
@@ -593,17 +603,16 @@ extern "C" int emb_expert_dispatch(const emb_expert_plan* plan, const void* x, i
         return EMB_ERR_INVALID_ARG;
     if (plan->tokens == 0) return EMB_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool w8 = wide(x, x_dtype, x_stride, width) && wide(rows, rows_dtype, width, width);
+    const int vector = std::min(vector_of(x, x_dtype, x_stride, width), vector_of(rows, rows_dtype, width, width));
     return with_type(x_dtype, [&](auto xt) {
         return with_type(rows_dtype, [&](auto rt) {
             using X = decltype(xt);
             using R = decltype(rt);
-            const auto go = [&](auto v, auto lanes) {
+            return with_vector(vector, width, [&](auto v, auto lanes) {
                 constexpr int V = decltype(v)::value, LANES = decltype(lanes)::value;
                 return launch_next(dispatch_rows<V, LANES, X, R>, Share<V, LANES, kUnroll>::grid(plan->tokens, width), kRowThreads, 0, st, 1, *plan,
                                    (const X*)x, x_stride, width, (R*)rows);
-            };
-            return !w8 ? go(number<1>(), number<32>()) : width <= kShortRow ? go(number<8>(), number<8>()) : go(number<8>(), number<32>());
+            });
         });
     });
 }
@@ -638,13 +647,13 @@ extern "C" int emb_expert_combine_grad(const emb_expert_plan* plan, const void* 
         return EMB_ERR_INVALID_ARG;
     if (plan->tokens == 0) return EMB_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool w8 = wide(grad_out, out_dtype, grad_stride, width) && wide(rows, rows_dtype, rows_stride, width) &&
-                    wide(grad_rows, rows_dtype, width, width);
+    const int vector = std::min({vector_of(grad_out, out_dtype, grad_stride, width), vector_of(rows, rows_dtype, rows_stride, width),
+                                 vector_of(grad_rows, rows_dtype, width, width)});
     // Threads a token: 64 elements each, because the more tokens a block has the less it
     // waits for one, and down to 16 where tokens are too few to fill the GPU.  With 64 and
     // 16, 3328 wide: 16384 x 2 100 and 119 us, 300 x 8 22.5 and 14.3 us.  Less than a warp
     // has 16 (32768 x 4, 64 wide: 28.7 us by 32 threads, 14.3 by 8).
-    int tx = w8 ? 8 : 32;
+    int tx = vector == 8 ? 8 : 32;
     while (tx < 32 && tx * 16 < width) tx *= 2;
     while (tx >= 32 && tx < kRowThreads && (tx * 64 < width || (tx * 16 < width && plan->tokens * tx * 2 <= kSms * 1024))) tx *= 2;
     const dim3 block(tx, kRowThreads / tx);
@@ -654,7 +663,7 @@ extern "C" int emb_expert_combine_grad(const emb_expert_plan* plan, const void* 
         return with_type(rows_dtype, [&](auto rt) {
             using O = decltype(ot);
             using R = decltype(rt);
-            return launch_next(w8 ? combine_grad<8, O, R> : combine_grad<1, O, R>, blocks, block, 0, st, 1, *plan, (const O*)grad_out, grad_stride,
+            return launch_next(vector == 8 ? combine_grad<8, O, R> : vector == 2 ? combine_grad<2, O, R> : combine_grad<1, O, R>, blocks, block, 0, st, 1, *plan, (const O*)grad_out, grad_stride,
                                (const R*)rows, rows_stride, weights, width, (R*)grad_rows, grad_weights);
         });
     });

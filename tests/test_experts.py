@@ -509,3 +509,13 @@ def test_rows_of_many_widths(T, k, width):
 def test_very_many_short_rows(T, width):
     test_dispatch_and_its_gradient(T, 1, 3, width, 0.01, BF, BF, 0)
     test_combine_and_its_gradients(T, 1, 3, width, 0.01, BF, BF, 0)
+
+
+@gpu
+@pytest.mark.parametrize("width", [2, 34, 130, 514, 1026, 2058])
+@pytest.mark.parametrize("types", [(F32, BF), (HF, HF), (BF, F32), (F32, F32)])
+@pytest.mark.parametrize("k", [1, 2, 3])
+def test_rows_of_even_widths(width, types, k):
+    for extra in (0, 2, 5):
+        test_dispatch_and_its_gradient(700, k, 7, width, 0.1, *types, extra)
+        test_combine_and_its_gradients(700, k, 7, width, 0.1, types[1], types[0], extra)
