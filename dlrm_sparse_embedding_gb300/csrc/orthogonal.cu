@@ -188,7 +188,8 @@ __device__ __forceinline__ void put_scaled(const Input& q, const T* g, double su
         if (norm > 0 && norm < INFINITY) e = max(-120, min(120, ilogbf(kRange) - ilogb(norm)));
         factor = ldexpf(1.f, e);
         if (blockIdx.x == 0) {
-            q.scale[blockIdx.y] = (float)(1.0 / ((norm + q.eps) * factor));
+            // (a zero matrix stays zero: 1 / eps, or its square in the first A, may be infinite)
+            q.scale[blockIdx.y] = norm == 0 && q.eps > 0.f ? 0.f : (float)(1.0 / ((norm + q.eps) * factor));
             q.done[blockIdx.y] = 0;
         }
     }

@@ -1,0 +1,41 @@
+"""Orthogonalised updates where they could go wrong: matrices that are zero, tiny
+or broken, step counts, coefficients and strides, on every way through the steps.
+
+Which way a batch takes depends on its sizes.  With 152 SMs: short sides up to 128
+stay in one CTA (96 x 200), 200 x 333 is shared by clusters, 24 of 300 x 500 go to
+single CTAs and 3 of 1401 x 1299 to pairs.
+
+Tolerance.  The steps' roundings (X in two fp16 numbers, A and B in one) and the
+output's to bf16 were emulated in 64 bits.  The default coefficients do not
+converge: singular values stay spread over 0.7 to 1.2 and every step passes on what
+the earlier ones have lost, so the error grows with their number.  Largest error
+(2-norm) over flat, power-law and low-rank spectra, 200 x 333 to 1401 x 1299:
+"""
+import pytest
+import torch
+
+import dlrm_sparse_embedding_gb300 as emb
+from test_orthogonal import ABC, BF, F32, HF, matrices, off, plain
+
+gpu = pytest.mark.gpu
+EMULATED = {1: 1.7e-3, 2: 2.0e-3, 3: 2.3e-3, 5: 2.1e-3, 6: 2.5e-3, 8: 3.4e-3, 12: 4.8e-3, 32: 1.8e-2}
+BOUND = {steps: 2 * e for steps, e in EMULATED.items()}     # for sizes and spectra that were not emulated
+CONVERGENT, CONVERGENT_BOUND = (1.875, -1.25, 0.375), 2 * 1.8e-3   # up to 32 steps
+
+SHORT, CLUSTERS, SINGLE, PAIRS = (2, 96, 200), (2, 200, 333), (24, 300, 500), (3, 1401, 1299)
+WAYS = [SHORT, (2, 200, 96), CLUSTERS, (1, 333, 200), SINGLE, (24, 500, 300), PAIRS]
+
+
+def worst(got, ref):
+    return max(off(got[i], ref[i]) for i in range(len(ref)))
+
+
+@gpu
+@pytest.mark.parametrize("batch,rows,cols", WAYS)
+@pytest.mark.parametrize("eps", [1e-7, 1e-20, 1e-30, 1e-38, 1.0])
+def test_a_zero_matrix_stays_zero(batch, rows, cols, eps):
+    G = matrices(1, batch, rows, cols, "flat", BF)
+    G[0] = 0
+    got = emb.orthogonalize(G, eps=eps)
+    assert not got[0].any()
+    assert batch == 1 or worst(got[1:], plain(G[1:], eps=eps)) <= BOUND[5]
