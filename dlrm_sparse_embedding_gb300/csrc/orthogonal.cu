@@ -723,12 +723,14 @@ __global__ void __launch_bounds__(kThreads, 1) newton_schulz(const __grid_consta
         }
     } else if (warp == 2) {
         // a tile's stores, once all its warps have made them, are ordered before the matrix's count by one
-        // thread: each warp waiting for its own to reach L2 would hold the epilogue up
+        // thread: each warp waiting for its own to reach L2 would hold the epilogue up.  Eight lanes have
+        // acquired a warp's count each (the vote orders no memory): they meet before that thread releases for all.
         int made = 0;
         for (Walk<S> walk(q); walk.more(); walk.next()) {
             const Tile tile = walk.tile();
             ++made;
             if (!__all_sync(0xffffffffu, wait_count(&counts->stored[lane % kEpilogueWarps], made, b.gave_up))) break;
+            __syncwarp();
             if (lane == 0) {
                 __threadfence();
                 asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(q.done + tile.matrix) : "memory");

@@ -39,3 +39,15 @@ def test_a_zero_matrix_stays_zero(batch, rows, cols, eps):
     got = emb.orthogonalize(G, eps=eps)
     assert not got[0].any()
     assert batch == 1 or worst(got[1:], plain(G[1:], eps=eps)) <= BOUND[5]
+
+
+@gpu
+@pytest.mark.parametrize("batch,rows,cols", WAYS + [(40, 130, 129), (12, 1030, 1300)])
+def test_the_same_bits_every_time(batch, rows, cols):
+    # tiles read what other SMs have stored: a store that came late would change the result
+    G = matrices(8, batch, rows, cols, "decay", F32)
+    first = emb.orthogonalize(G)
+    assert worst(first, plain(G)) <= BOUND[5]
+    for _ in range(30):
+        assert torch.equal(emb.orthogonalize(G), first)
+    assert emb.dense_status() == emb.EMB_OK
