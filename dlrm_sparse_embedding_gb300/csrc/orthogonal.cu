@@ -769,12 +769,12 @@ __global__ void __launch_bounds__(kThreads, 1) newton_schulz(const __grid_consta
                     ok = finish<S, kGram>(q, tile, part, reinterpret_cast<float*>(in + part.c0 / kChunk * kStaging), b.rank, parts,
                                           tc::smem_addr(&counts->received), turn, b.gave_up);
                     if (ok) stored();
-                    if (ok && lane < S::SPLIT) tc::bar_arrive(tc::in_cta(tc::smem_addr(&counts->sent), lane));
+                    if (ok && lane < S::SPLIT) tc::bar_arrive_cluster(tc::in_cta(tc::smem_addr(&counts->sent), lane));
                 } else if (ok) {
                     stored();
                 }
                 // every CTA has used what came from here: the room for it is free again
-                ok = ok && tc::bar_wait_warp(tc::smem_addr(&counts->sent), turn, b.gave_up);
+                ok = ok && tc::bar_wait_cluster(tc::smem_addr(&counts->sent), turn, b.gave_up);
             } else {
                 ok = __all_sync(0xffffffffu, wait_count(&counts->ahead, made + 1, b.gave_up));
                 if (ok)

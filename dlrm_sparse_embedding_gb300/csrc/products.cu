@@ -265,9 +265,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_products(const __grid_cons
                     tc::fence_async_shared();
                     __syncwarp();
                     if (b.rank) {
-                        if (lane == 0) tc::bar_arrive(tc::in_cta(tc::smem_addr(&b.ring->peer_part[s]), 0));
+                        if (lane == 0) tc::bar_arrive_cluster(tc::in_cta(tc::smem_addr(&b.ring->peer_part[s]), 0));
                     } else {
-                        if (S::CTAS == 2) ok = tc::bar_wait_warp(tc::smem_addr(&b.ring->peer_part[s]), time & 1, b.gave_up);
+                        if (S::CTAS == 2) ok = tc::bar_wait_cluster(tc::smem_addr(&b.ring->peer_part[s]), time & 1, b.gave_up);
                         if (ok && lane == 0) tc::bar_arrive(tc::smem_addr(&b.ring->full[s]));
                     }
                 }

@@ -53,10 +53,18 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
-// `bar` may be another CTA's (in_cta).
+// `bar` may be another CTA's (in_cta).  What it orders by itself is the CTA's memory
+// (the tensor memory's order comes from the fences around it).
 __device__ __forceinline__ void bar_arrive(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The same where the CTA that waits for it (bar_wait_cluster) goes on with shared
+// memory that this thread has read or written before.
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
@@ -94,7 +102,8 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     return true;
 }
 
-// bar_wait_warp for what other CTAs of the cluster stored here.
+// bar_wait_warp for what threads of the cluster's other CTAs did before they arrived
+// (bar_arrive_cluster), or copied here.
 __device__ __forceinline__ bool bar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* gave_up)
 {
     const auto reached = [&] {

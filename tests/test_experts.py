@@ -519,3 +519,18 @@ def test_rows_of_even_widths(width, types, k):
     for extra in (0, 2, 5):
         test_dispatch_and_its_gradient(700, k, 7, width, 0.1, *types, extra)
         test_combine_and_its_gradients(700, k, 7, width, 0.1, types[1], types[0], extra)
+
+
+@gpu
+@pytest.mark.parametrize("T,k,E,K,N", [(1777, 2, 12, 1032, 776), (9000, 2, 7, 1032, 776), (2000, 1, 5, 512, 384)])
+def test_weight_gradients_of_ragged_groups_repeat_bit_for_bit(T, k, E, K, N):
+    # pairs of CTAs zero the rows past a group, each its own half, before one of them multiplies both
+    plan, off, x, gy, w = linear_case(T, k, E, K, N, 0.05, BF, skew=True)
+    first = emb.expert_linear_grad(plan, gy, x, w, need_rows=False)[1]
+    for _ in range(30):
+        assert torch.equal(emb.expert_linear_grad(plan, gy, x, w, need_rows=False)[1], first)
+    for e in range(E):
+        a, b = off[e], off[e + 1]
+        p, q = gy[a:b].double().t(), x[a:b].double()
+        check_close(first[e], p @ q, out_bound(p @ q, BF, p.abs() @ q.abs(), b - a, 2.0 ** -23))
+    assert emb.dense_status() == emb.EMB_OK
