@@ -17,6 +17,7 @@
 // 39, 41 and 51 at 1025.  (Vectors from each written row's own 16-byte boundary,
 // shifted out of the words around them, took 35, 45, 57 and 200 us.)
 #include <algorithm>
+#include <condition_variable>
 #include <mutex>
 #include <type_traits>
 
@@ -27,12 +28,41 @@ namespace emb {
 namespace {
 
 constexpr int kMaxDevices = 64;
-__device__ int g_status[2];   // [0] sticky bits, [1] the bits taken by emb_dense_status
+// The sticky bits, then a place for the bits that a call of emb_dense_status has taken:
+// calls of several threads may be under way at once, and each reads its own.
+constexpr int kTakers = 64;
+__device__ int g_status[1 + kTakers];
 
 std::mutex g_status_mutex;
+std::condition_variable g_taker_left;
 int* g_status_addr[kMaxDevices] = {};
+uint64_t g_takers[kMaxDevices] = {};   // of each device, the places in use
 
-__global__ void take_status(int* status) { status[1] = atomicExch(&status[0], 0); }
+__global__ void take_status(int* status, int place) { status[1 + place] = atomicExch(&status[0], 0); }
+
+// A place of the current device's, waited for while all are in use.
+struct Taker {
+    int dev = 0, place = -1;
+    Taker()
+    {
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return;
+        std::unique_lock<std::mutex> lock(g_status_mutex);
+        g_taker_left.wait(lock, [&] { return g_takers[dev] != ~uint64_t(0); });
+        for (place = 0; g_takers[dev] >> place & 1;) ++place;
+        g_takers[dev] |= uint64_t(1) << place;
+    }
+    ~Taker()
+    {
+        if (place < 0) return;
+        {
+            std::lock_guard<std::mutex> lock(g_status_mutex);
+            g_takers[dev] &= ~(uint64_t(1) << place);
+        }
+        g_taker_left.notify_all();   // of any device
+    }
+    Taker(const Taker&) = delete;
+    Taker& operator=(const Taker&) = delete;
+};
 
 // ---------------------------------------------------------------------------
 // sort
@@ -537,10 +567,13 @@ extern "C" int emb_dense_status(void* stream)
 {
     int* const word = dense_status_word();
     if (!word) return EMB_ERR_CUDA;
+    const Taker taker;
+    if (taker.place < 0) return EMB_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int bits = 0;
-    take_status<<<1, 1, 0, st>>>(word);
-    if (cudaGetLastError() != cudaSuccess || cudaMemcpyAsync(&bits, word + 1, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+    take_status<<<1, 1, 0, st>>>(word, taker.place);
+    if (cudaGetLastError() != cudaSuccess ||
+        cudaMemcpyAsync(&bits, word + 1 + taker.place, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
         cudaStreamSynchronize(st) != cudaSuccess)
         return EMB_ERR_CUDA;
     return bits & ERRBIT_TIMEOUT ? EMB_ERR_TIMEOUT : bits & ERRBIT_KEY_RANGE ? EMB_ERR_KEY_RANGE : EMB_OK;

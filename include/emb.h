@@ -474,8 +474,9 @@ int emb_orthogonalize(const void* update, int32_t dtype, int64_t batch_stride, i
                       void* workspace, size_t workspace_bytes, void* stream);
 
 /* Wait for the stream; return and clear the device's sticky status of the
- * calls of this section (EMB_OK, EMB_ERR_KEY_RANGE or EMB_ERR_TIMEOUT).  No
- * passage: library convenience. */
+ * calls of this section (EMB_OK, EMB_ERR_KEY_RANGE or EMB_ERR_TIMEOUT).  Of
+ * several threads that ask at once, one gets what there is.  No passage:
+ * library convenience. */
 int emb_dense_status(void* stream);
 
 /* Static description of an emb_status value.  No passage: library convenience. */
