@@ -2,10 +2,10 @@
 each expert's weights and added back, with the gradients.
 
 Argument checks and marshalling only; the work is in libemb.so.  Tensors are on
-the current CUDA device.  Every call takes `stream`: it runs on that stream
-(default: the current one), and what it returns is allocated for it.  The caller
-orders it after the work that makes its inputs; memory of inputs that are freed
-meanwhile is not used again before the call's work is done.
+the current CUDA device (ValueError if not).  Every call takes `stream`: it runs
+on that stream (default: the current one), and what it returns is allocated for
+it.  The caller orders it after the work that makes its inputs; memory of inputs
+that are freed meanwhile is not used again before the call's work is done.
 """
 from __future__ import annotations
 
@@ -36,8 +36,12 @@ def _on(stream, call, *args):
 
 
 def _stream(device: torch.device) -> int:
-    """The device's current stream, as an address."""
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    """The current stream, as an address; `device`, the tensors', has to be the current one
+    (the library's calls run there, whatever their arguments' addresses)."""
+    current = torch._C._cuda_getDevice()
+    if device.index != current:
+        raise ValueError("the tensors are on %s, the current device is cuda:%d" % (device, current))
+    return torch._C._cuda_getCurrentRawStream(current)
 
 
 def _matrix(t, name: str, rows: int, device, width: Optional[int] = None):
@@ -299,5 +303,11 @@ def expert_linear_grad(plan: ExpertPlan, grad_y: torch.Tensor, rows: Optional[to
 
 def dense_status(stream=None) -> int:
     """Waits for the stream; returns and clears the device's sticky status of the
-    expert calls and of orthogonalize (EMB_OK, EMB_ERR_KEY_RANGE, EMB_ERR_TIMEOUT)."""
-    return int(lib.emb_dense_status((torch.cuda.current_stream() if stream is None else stream).cuda_stream))
+    expert calls and of orthogonalize (EMB_OK, EMB_ERR_KEY_RANGE, EMB_ERR_TIMEOUT).
+    The stream, if given, is one of the current device's."""
+    if stream is None:
+        return int(lib.emb_dense_status(torch.cuda.current_stream().cuda_stream))
+    current = torch._C._cuda_getDevice()
+    if stream.device.index != current:
+        raise ValueError("the stream is on %s, the current device is cuda:%d" % (stream.device, current))
+    return int(lib.emb_dense_status(stream.cuda_stream))

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import dlrm_sparse_embedding_gb300 as emb
+from dlrm_sparse_embedding_gb300 import experts
 
 gpu = pytest.mark.gpu
 
@@ -30,3 +31,31 @@ def test_of_many_callers_one_gets_the_status(callers):
         for t in threads:
             t.join()
         assert sorted(got) == sorted([emb.EMB_ERR_KEY_RANGE] + [emb.EMB_OK] * (callers - 1))
+
+
+def test_a_device_that_is_not_the_current_one_is_refused(monkeypatch):
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    with pytest.raises(ValueError, match="current device"):
+        experts._stream(torch.device("cuda", 1))
+
+
+@gpu
+def test_every_call_refuses_tensors_of_another_device(monkeypatch):
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(*s, dtype=dtype, device="cuda")  # noqa: E731
+    ids, w, weights, stream = z(6, 2, dtype=torch.int32), z(4, 16, 24), z(6, 2, dtype=torch.float32), torch.cuda.Stream()
+    plan = emb.expert_sort(ids, 4)
+    calls = [
+        lambda: emb.expert_sort(ids, 4), lambda: emb.expert_dispatch(plan, z(6, 8)), lambda: emb.expert_dispatch_grad(plan, z(12, 8)),
+        lambda: emb.expert_combine(plan, z(12, 8), weights), lambda: emb.expert_combine_grad(plan, z(6, 8), z(12, 8), weights),
+        lambda: emb.expert_linear(plan, z(12, 24), w), lambda: emb.expert_linear_grad(plan, z(12, 16), z(12, 24), w),
+        lambda: emb.expert_linear_grad(plan, z(12, 16), z(12, 24), w, need_rows=False), lambda: emb.orthogonalize(z(4, 4)),
+        lambda: emb.dense_status(stream),
+    ]
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)      # nothing is launched: the tensors are on 0
+    for i, call in enumerate(calls):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+            pytest.fail("call %d was taken" % i)
+    monkeypatch.undo()
+    for call in calls:
+        call()
