@@ -24,7 +24,8 @@
 // Matrices whose short side is at most 128 go another way (orthogonal_short.cu).
 //
 // G is scaled by a power of two before it is rounded, exact for bf16, and the
-// rest of the norm goes into the first step's factors.
+// rest of the norm goes into the first step's factors.  X after a step is scaled
+// by one too where it is small (Lift in orthogonal.cuh).
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -43,11 +44,12 @@ constexpr int kNormBlocks = 4 * 152;  // of all: four an SM (16 of 1024 x 3328: 
 constexpr int kOneBlockThreads = 1024;
 constexpr int64_t kOneBlock = 8 * 8 * kOneBlockThreads;   // elements that one block reads twice sooner than two launches pass
 constexpr float kRange = 256.f;       // the scaled norm is in [kRange, 2 kRange)
+constexpr int kMaxLift = 250;         // beyond it X0 is below the output's range
 
 struct Layout {
     int64_t ld, ldm, m, x_elems, a_elems;   // pitches (multiples of 8), the short side, elements a matrix
     int norm_blocks;
-    size_t x[2], x_low[2], a, b, scale, done, partial, total;   // byte offsets
+    size_t x[2], x_low[2], a, b, scale, lift, done, partial, total;   // byte offsets
 };
 
 Layout layout_of(int64_t batch, int64_t rows, int64_t cols)
@@ -71,6 +73,7 @@ Layout layout_of(int64_t batch, int64_t rows, int64_t cols)
     l.a = take(2 * (size_t)batch * l.a_elems);
     l.b = take(2 * (size_t)batch * l.a_elems);
     l.scale = take(sizeof(float) * (size_t)batch);
+    l.lift = take(sizeof(int) * (size_t)batch);
     l.done = take(sizeof(unsigned) * (size_t)batch);
     l.partial = take(sizeof(double) * (size_t)batch * l.norm_blocks);
     l.total = at;
@@ -170,13 +173,14 @@ struct Input {
     int64_t ld;              // of X
     __half *x, *x_low;
     float* scale;
+    int* lift;
     unsigned* done;
     double* partial;         // norm_blocks of each matrix
     int norm_blocks;
 };
 
 // X = G 2^e as a sum of two fp16 (for 16-bit G one: its 8 or 11 bits fit, but for
-// entries below 2^-24 of the norm), and the factor that makes it G / (|G| + eps).
+// entries below 2^-24 of the norm), and the factor that makes it 2^lift G / (|G| + eps).
 // Thread 0 has the sum of squares.
 template <bool WIDE, class T>
 __device__ __forceinline__ void put_scaled(const Input& q, const T* g, double sum_of_squares)
@@ -188,8 +192,11 @@ __device__ __forceinline__ void put_scaled(const Input& q, const T* g, double su
         if (norm > 0 && norm < INFINITY) e = max(-120, min(120, ilogbf(kRange) - ilogb(norm)));
         factor = ldexpf(1.f, e);
         if (blockIdx.x == 0) {
+            const double share = norm / (norm + q.eps);   // |X0|
+            const int lift = share > 0 && share < 0.5 ? min(kMaxLift, -ilogb(share) - 1) : 0;
             // (a zero matrix stays zero: 1 / eps, or its square in the first A, may be infinite)
-            q.scale[blockIdx.y] = norm == 0 && q.eps > 0.f ? 0.f : (float)(1.0 / ((norm + q.eps) * factor));
+            q.scale[blockIdx.y] = norm == 0 && q.eps > 0.f ? 0.f : (float)(ldexp(1.0, lift) / ((norm + q.eps) * factor));
+            q.lift[blockIdx.y] = lift;
             q.done[blockIdx.y] = 0;
         }
     }
@@ -308,6 +315,7 @@ struct Steps {
     __half *x[2], *x_low[2], *a, *b;
     __nv_bfloat16* out;
     const float* scale;
+    Lift lift;
     unsigned* done;          // of each matrix: CTAs that have finished a tile
     int64_t rows, cols, ld, ldm, m;
     int64_t long_stride, short_stride;   // between matrices: of X, of A and B
@@ -456,9 +464,10 @@ __device__ __forceinline__ void set_count(int* count, int v)
 // in rows r0 + 8 i, which meet C there and leave again.  C for the next columns
 // is on its way meanwhile; it was written in this launch by other SMs, so it
 // comes from L2.
-//   kGram       D = s^2 sum, s in the first step
+//   kGram       D = s sum
 //   kQuadratic  D = cc sum + cb C + diagonal I
 //   kUpdate     D = s (sum + beta (C + C's low part))
+// with s for X's lift, and the input's scale in the first step.
 template <class S, Product F, bool SHARED = (S::SPLIT > 1 && F == kGram)>
 __device__ __forceinline__ bool finish(const Steps& q, const Tile& tile, const Part& part, float* mine, uint32_t rank, unsigned parts,
                                        uint32_t received, uint32_t turn_of, volatile int* gave_up)
@@ -485,7 +494,11 @@ __device__ __forceinline__ bool finish(const Steps& q, const Tile& tile, const P
         d = q.x[(tile.step + 1) & 1] + at, d_low = q.x_low[(tile.step + 1) & 1] + at;
     }
     const float beta = F == kUpdate ? q.ca - diagonal : q.cb;
-    const float s = F != kQuadratic && tile.step == 0 ? (F == kGram ? q.scale[tile.matrix] * q.scale[tile.matrix] : q.scale[tile.matrix]) : 1.f;
+    float s = 1.f;
+    if (F != kQuadratic) {
+        s = F == kGram ? q.lift.of_square(tile.matrix, tile.step) : q.lift.between(tile.matrix, tile.step, tile.step + 1);
+        if (tile.step == 0) s *= F == kGram ? q.scale[tile.matrix] * q.scale[tile.matrix] : q.scale[tile.matrix];
+    }
     const bool out_wide = (q.cols & 7) == 0 && (reinterpret_cast<uintptr_t>(q.out) & 15) == 0;
     __nv_bfloat16* const out = q.out + tile.matrix * q.rows * q.cols + (m_first + r0) * q.cols + tile.n0 + p * 8;
 
@@ -923,6 +936,7 @@ extern "C" int emb_orthogonalize(const void* update, int32_t dtype, int64_t batc
     in.x = reinterpret_cast<__half*>(ws + l.x[0]);
     in.x_low = reinterpret_cast<__half*>(ws + l.x_low[0]);
     in.scale = reinterpret_cast<float*>(ws + l.scale);
+    in.lift = reinterpret_cast<int*>(ws + l.lift);
     in.done = reinterpret_cast<unsigned*>(ws + l.done);
     in.partial = reinterpret_cast<double*>(ws + l.partial);
     in.norm_blocks = l.norm_blocks;
@@ -940,6 +954,7 @@ extern "C" int emb_orthogonalize(const void* update, int32_t dtype, int64_t batc
     }
     p.low_in = dtype == EMB_F32;
     p.scale = reinterpret_cast<const float*>(ws + l.scale);
+    p.lift = reinterpret_cast<const int*>(ws + l.lift);
     p.batch = batch, p.rows = rows, p.cols = cols, p.ld = l.ld;
     p.steps = steps;
     p.a = a, p.b = b, p.c = c;
@@ -956,6 +971,7 @@ extern "C" int emb_orthogonalize(const void* update, int32_t dtype, int64_t batc
     q.a = p.w, q.b = p.w_low;
     q.out = p.out;
     q.scale = p.scale;
+    q.lift = lift_of(p.lift, a, steps);
     q.done = reinterpret_cast<unsigned*>(ws + l.done);
     q.short_stride = l.a_elems, q.long_stride = l.x_elems;
     return run_steps(q, st);

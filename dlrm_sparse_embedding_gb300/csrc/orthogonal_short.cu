@@ -41,6 +41,8 @@ struct Short {
     CUtensorMap x, x_low;          // of A0 = X X^T
     CUtensorMap x_apply, x_low_apply, w_map, w_low_map;
     const float* scale;            // or null for 1
+    Lift lift;
+    int before;                    // steps of earlier passes
     __half *w, *w_low;
     __half *x_out, *x_low_out;     // of the pass; null in the last one
     __nv_bfloat16* out;
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(kStepsThreads, 1) short_steps(const __grid_con
             *reinterpret_cast<uint4*>(q.w_low + at) = l;
         };
         {
-            const float s = q.scale ? q.scale[z] * q.scale[z] : 1.f;
+            const float s = q.lift.of_square(z, q.before) * (q.scale ? q.scale[z] * q.scale[z] : 1.f);
             const int chains = (q.k_steps + kChain - 1) / kChain;
             float sum[32] = {};
             for (int chain = 0; chain < chains; ++chain) {
@@ -391,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) short_apply(const __grid_constant
         // rows of the accumulator are the short side, or the long one where the matrix is tall
         const int w = warp & 3, c0 = (warp - 4) / 4 * 64, r0 = lane >> 2, p = lane & 3;
         float* const mine = reinterpret_cast<float*>(base + 4 * kMatrix + (warp - 4) * kApplyStaging);
-        const float s = q.scale ? q.scale[z] : 1.f;
+        const float s = q.lift.between(z, q.before, q.before + q.steps) * (q.scale ? q.scale[z] : 1.f);
         const int64_t m_first = (q.tall ? n0 : 0) + w * 32;
         const bool wide = (q.cols & 7) == 0 && (reinterpret_cast<uintptr_t>(q.out) & 15) == 0;
         for (int c = c0; c < c0 + 64; c += kChunk) {
@@ -479,6 +481,7 @@ int run_short(const StepsArgs& p, cudaStream_t st)
     q.rows = p.rows, q.cols = p.cols, q.ld = p.ld;
     q.w = p.w, q.w_low = p.w_low, q.out = p.out, q.status = status;
     q.a = p.a, q.b = p.b, q.c = p.c;
+    q.lift = lift_of(p.lift, p.a, p.steps);
     const int64_t n = q.tall ? p.rows : p.cols, x_elems = p.rows * p.ld;
     q.k_steps = (int)((n + kStep - 1) / kStep);
     q.tiles = (int)((n + kRows - 1) / kRows);
@@ -493,6 +496,7 @@ int run_short(const StepsArgs& p, cudaStream_t st)
         q.low_in = i > 0 || p.low_in;
         q.scale = i > 0 ? nullptr : p.scale;
         q.steps = (p.steps - done + passes - i - 1) / (passes - i);
+        q.before = done;
         done += q.steps;
         const bool last = i + 1 == passes;
         q.x_out = last ? nullptr : p.x[from ^ 1];

@@ -462,8 +462,9 @@ int emb_expert_linear_grad_weight(const emb_expert_plan* plan, const void* grad_
  *   X = G / (|G|_F + eps);  steps times:  A = X X^T,  X <- a X + (b A + c A A) X
  * (on the transpose where rows > cols).  G is any emb_dtype, with
  * batch_stride and row_stride in elements; out is bf16 [batch, rows, cols],
- * contiguous.  Between the steps X is held as the sum of two fp16 numbers and
- * A as one, sums are fp32: about a tenth of the error of bf16 arithmetic.  A
+ * contiguous.  Between the steps X is held as the sum of two fp16 numbers
+ * (times a power of two of its own, so |G| may be far below eps) and A as one,
+ * sums are fp32: about a tenth of the error of bf16 arithmetic.  A
  * zero matrix stays zero, or with eps 0 gives NaNs (0 / 0); one that holds an
  * infinity or a NaN gives NaNs and leaves the others alone.  rows and cols in [1, 65536].  The workspace is
  * 256-byte aligned, emb_orthogonalize_workspace bytes.  No passage: library

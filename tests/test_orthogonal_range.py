@@ -51,3 +51,23 @@ def test_the_same_bits_every_time(batch, rows, cols):
     for _ in range(30):
         assert torch.equal(emb.orthogonalize(G), first)
     assert emb.dense_status() == emb.EMB_OK
+
+
+@gpu
+@pytest.mark.parametrize("batch,rows,cols", WAYS)
+@pytest.mark.parametrize("norm", [1e-10, 1e-14, 1e-16, 1e-20, 1e-30])
+@pytest.mark.parametrize("dtype,eps,steps", [(F32, 1e-7, 5), (BF, 1e-7, 3), (F32, 1e-2, 8), (BF, 1e-7, 12)])
+def test_matrices_far_smaller_than_eps(batch, rows, cols, norm, dtype, eps, steps):
+    G = matrices(2, batch, rows, cols, "decay", F32)
+    G = (G * (norm / G.double().norm(dim=(1, 2), keepdim=True))).to(dtype)
+    assert worst(emb.orthogonalize(G, steps=steps, eps=eps), plain(G, steps, eps=eps)) <= BOUND[steps]
+
+
+@gpu
+@pytest.mark.parametrize("batch,rows,cols", WAYS)
+def test_small_and_large_matrices_side_by_side(batch, rows, cols):
+    # each has its own size, coefficients other than the default ones
+    G = matrices(3, batch, rows, cols, "flat", F32)
+    G *= 10.0 ** -torch.arange(batch, device="cuda").float().mul(7).remainder(31)[:, None, None]
+    for abc in ((0.5, 0.2, 0.1), (1.0, -0.5, 0.1), (6.0, -20.0, 15.0)):
+        assert worst(emb.orthogonalize(G, 3, abc), plain(G, 3, abc)) <= BOUND[3]
