@@ -185,29 +185,30 @@ struct Input {
 template <bool WIDE, class T>
 __device__ __forceinline__ void put_scaled(const Input& q, const T* g, double sum_of_squares)
 {
-    __shared__ float factor;
+    __shared__ float factor[2];   // their product is 2^e: for numbers below fp32's normal ones it is above its range
     if (threadIdx.x == 0) {
         const double norm = sqrt(sum_of_squares);
         int e = 0;
-        if (norm > 0 && norm < INFINITY) e = max(-120, min(120, ilogbf(kRange) - ilogb(norm)));
-        factor = ldexpf(1.f, e);
+        if (norm > 0 && norm < INFINITY) e = max(-120, ilogbf(kRange) - ilogb(norm));
+        factor[0] = ldexpf(1.f, min(e, 100));
+        factor[1] = ldexpf(1.f, max(0, e - 100));
         if (blockIdx.x == 0) {
             const double share = norm / (norm + q.eps);   // |X0|
             const int lift = share > 0 && share < 0.5 ? min(kMaxLift, -ilogb(share) - 1) : 0;
             // (a zero matrix stays zero: 1 / eps, or its square in the first A, may be infinite)
-            q.scale[blockIdx.y] = norm == 0 && q.eps > 0.f ? 0.f : (float)(ldexp(1.0, lift) / ((norm + q.eps) * factor));
+            q.scale[blockIdx.y] = norm == 0 && q.eps > 0.f ? 0.f : (float)(ldexp(1.0, lift) / ldexp(norm + q.eps, e));
             q.lift[blockIdx.y] = lift;
             q.done[blockIdx.y] = 0;
         }
     }
     __syncthreads();
-    const float up = factor;
+    const float up = factor[0], up_more = factor[1];
     const int64_t at = (int64_t)blockIdx.y * q.rows * q.ld;
     each_piece<WIDE, T>(g, q.row_stride, q.rows, q.cols, [&](int64_t row, int64_t c, const float (&v)[8]) {
         float h[8], l[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            h[i] = up * v[i];
+            h[i] = up * v[i] * up_more;
             l[i] = kLowScale * (h[i] - __half2float(__float2half_rn(h[i])));
         }
         // rows of X start at 16 bytes and have room for whole vectors

@@ -71,3 +71,14 @@ def test_small_and_large_matrices_side_by_side(batch, rows, cols):
     G *= 10.0 ** -torch.arange(batch, device="cuda").float().mul(7).remainder(31)[:, None, None]
     for abc in ((0.5, 0.2, 0.1), (1.0, -0.5, 0.1), (6.0, -20.0, 15.0)):
         assert worst(emb.orthogonalize(G, 3, abc), plain(G, 3, abc)) <= BOUND[3]
+
+
+@gpu
+@pytest.mark.parametrize("batch,rows,cols", WAYS)
+def test_the_smallest_numbers(batch, rows, cols):
+    # whole multiples of fp32's smallest one, 1.4e-45
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    G = torch.randint(-8, 9, (batch, rows, cols), generator=g, device="cuda").int()
+    G = (G.abs() | (G < 0).int() << 31).view(F32)
+    assert worst(emb.orthogonalize(G, eps=0.0), plain(G, eps=0.0)) <= BOUND[5]
