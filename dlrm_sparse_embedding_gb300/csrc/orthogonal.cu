@@ -141,19 +141,28 @@ __device__ __forceinline__ void each_piece(const T* g, int64_t row_stride, int64
     }
 }
 
-// This warp's sum of squares, in every lane: fp32, a thread has some dozens of
-// elements; in double again where the squares could leave fp32's range.
+// This warp's sum of squares, in every lane: fp32, eight at a time, and what rounding
+// takes from the running sum is added up beside it (a thread has 44 pieces of eight
+// of 16 matrices of 1024 x 3328 and 8192 of one of 65536 x 65536: by itself that sum
+// could be off by as many times 2^-24); in double again where the squares could leave
+// fp32's range.
 template <bool WIDE, class T>
 __device__ __forceinline__ double squares(const T* g, int64_t row_stride, int64_t rows, int64_t cols)
 {
-    float s = 0.f, top = 0.f;
+    float s = 0.f, rest = 0.f, top = 0.f;
     each_piece<WIDE, T>(g, row_stride, rows, cols, [&](int64_t, int64_t, const float (&v)[8]) {
+        float t = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            s = __fmaf_rn(v[i], v[i], s);
+            t = __fmaf_rn(v[i], v[i], t);
             top = fmaxf(top, fabsf(v[i]));
         }
+        const bool over = t > s;   // (a NaN in either stays)
+        const float more = over ? t : s, less = over ? s : t, sum = __fadd_rn(more, less);
+        rest = __fadd_rn(rest, __fsub_rn(less, __fsub_rn(sum, more)));
+        s = sum;
     });
+    s += rest;
     if (__any_sync(0xffffffffu, top > 1e15f || (top < 1e-15f && top > 0.f))) {
         double d = 0;
         each_piece<WIDE, T>(g, row_stride, rows, cols, [&](int64_t, int64_t, const float (&v)[8]) {

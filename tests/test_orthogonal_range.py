@@ -82,3 +82,13 @@ def test_the_smallest_numbers(batch, rows, cols):
     G = torch.randint(-8, 9, (batch, rows, cols), generator=g, device="cuda").int()
     G = (G.abs() | (G < 0).int() << 31).view(F32)
     assert worst(emb.orthogonalize(G, eps=0.0), plain(G, eps=0.0)) <= BOUND[5]
+
+
+@gpu
+def test_the_norm_of_very_many_elements():
+    # One step without products gives G / |G|, and of equal numbers 1 / sqrt(rows cols): here 6e-6 of it below the
+    # middle between two bf16 numbers.  Their squares added up one after another in fp32 come out 5e-5 too small.
+    rows, cols = 4096, 60248
+    G = torch.full((rows, cols), 1.1228819, device="cuda")
+    got = emb.orthogonalize(G, steps=1, coefficients=(1.0, 0.0, 0.0))
+    assert (got == torch.tensor((rows * cols) ** -0.5, dtype=torch.float64).to(BF).item()).all()
