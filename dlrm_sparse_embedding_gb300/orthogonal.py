@@ -27,6 +27,11 @@ def orthogonalize(update: torch.Tensor, steps: int = 5, coefficients: Tuple[floa
     bfloat16) with its singular values driven towards 1, by `steps` steps
     X <- a X + (b A + c A A) X, A = X X^T, from X = update / (|update|_F + eps).
 
+    The steps' products take fp16 numbers, so the result is not fp32's: with the
+    output's rounding to bf16 (1.7e-3 of the 2-norm) it is 2.1e-3 off after five
+    steps, 3.4e-3 after eight and up to 2e-2 after 32 with the default coefficients,
+    1.8e-3 with ones that converge.
+
     update: [rows, cols] or [batch, rows, cols] with contiguous rows, rows and
     cols up to 65536; steps 1 to 32.  out, if given, is contiguous bfloat16 of
     update's shape and may not overlap it."""

@@ -464,11 +464,15 @@ int emb_expert_linear_grad_weight(const emb_expert_plan* plan, const void* grad_
  * batch_stride and row_stride in elements; out is bf16 [batch, rows, cols],
  * contiguous.  Between the steps X is held as the sum of two fp16 numbers
  * (times a power of two of its own, so |G| may be far below eps) and A as one,
- * sums are fp32: about a tenth of the error of bf16 arithmetic.  A
- * zero matrix stays zero, or with eps 0 gives NaNs (0 / 0); one that holds an
- * infinity or a NaN gives NaNs and leaves the others alone.  rows and cols in [1, 65536].  The workspace is
- * 256-byte aligned, emb_orthogonalize_workspace bytes.  No passage: library
- * convenience. */
+ * of the products only the first one's; sums are fp32.  That is about a tenth of
+ * the error of bf16 arithmetic, not fp32's.  Of the result's 2-norm (the output's
+ * rounding to bf16 alone is 1.7e-3): with coefficients that converge 1.8e-3, up to
+ * 32 steps; with Muon's, which do not, it grows with the steps, to 2.1e-3 at 5,
+ * 2.5e-3 at 6, 3.4e-3 at 8, 4.8e-3 at 12 and 2e-2 at 32.  A zero matrix stays
+ * zero, or with eps 0 gives NaNs (0 / 0); one that holds an infinity or a NaN
+ * gives NaNs and leaves the others alone.  rows and cols in [1, 65536].  The
+ * workspace is 256-byte aligned, emb_orthogonalize_workspace bytes.  No passage:
+ * library convenience. */
 int emb_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols, size_t* bytes);
 int emb_orthogonalize(const void* update, int32_t dtype, int64_t batch_stride, int64_t row_stride, int64_t batch,
                       int64_t rows, int64_t cols, int32_t steps, float a, float b, float c, float eps, void* out,

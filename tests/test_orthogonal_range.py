@@ -92,3 +92,43 @@ def test_the_norm_of_very_many_elements():
     G = torch.full((rows, cols), 1.1228819, device="cuda")
     got = emb.orthogonalize(G, steps=1, coefficients=(1.0, 0.0, 0.0))
     assert (got == torch.tensor((rows * cols) ** -0.5, dtype=torch.float64).to(BF).item()).all()
+
+
+@gpu
+@pytest.mark.parametrize("batch,rows,cols", WAYS)
+@pytest.mark.parametrize("steps,dtype", [(1, BF), (2, F32), (3, BF), (6, F32), (8, BF), (12, F32), (32, BF)])
+def test_steps_coefficients_and_eps(batch, rows, cols, steps, dtype):
+    G = matrices(5, batch, rows, cols, "flat", dtype)
+    assert worst(emb.orthogonalize(G, steps), plain(G, steps)) <= BOUND[steps]
+    assert worst(emb.orthogonalize(G, steps, eps=0.5), plain(G, steps, eps=0.5)) <= BOUND[steps]
+    assert worst(emb.orthogonalize(G, steps, CONVERGENT), plain(G, steps, CONVERGENT)) <= CONVERGENT_BOUND
+    assert emb.dense_status() == emb.EMB_OK
+
+
+@gpu
+@pytest.mark.parametrize("batch,rows,cols", [SINGLE, (24, 500, 300), PAIRS, (5, 200, 333)])
+@pytest.mark.parametrize("steps", [1, 2, 5])
+def test_broken_matrices_stay_by_themselves(batch, rows, cols, steps):
+    G = matrices(6, batch, rows, cols, "flat", F32)
+    clean = emb.orthogonalize(G, steps)
+    bad = G.clone()
+    bad[0, 3, 5] = float("inf")
+    bad[batch - 1, rows - 1, cols - 1] = float("nan")
+    got = emb.orthogonalize(bad, steps)
+    assert torch.isnan(got[0]).all() and torch.isnan(got[-1]).all()
+    assert torch.equal(got[1:-1], clean[1:-1])
+
+
+@gpu
+@pytest.mark.parametrize("rows,cols", [(200, 333), (333, 200)])
+@pytest.mark.parametrize("dtype", [F32, HF])
+def test_strides_of_larger_matrices(rows, cols, dtype):
+    big = matrices(7, 5, rows + 9, cols + 11, "flat", dtype)
+    view = big[::2, 3:3 + rows, 5:5 + cols]
+    ref = emb.orthogonalize(view.contiguous())
+    assert torch.equal(emb.orthogonalize(view), ref)
+    same = view[:1].expand(4, rows, cols)                       # the batch's stride is 0
+    out = torch.empty(4, rows, cols, dtype=BF, device="cuda")
+    assert emb.orthogonalize(same, out=out) is out
+    assert worst(out, plain(same)) <= BOUND[5]
+    assert torch.equal(out[0], out[3])
