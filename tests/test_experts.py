@@ -534,3 +534,15 @@ def test_weight_gradients_of_ragged_groups_repeat_bit_for_bit(T, k, E, K, N):
         p, q = gy[a:b].double().t(), x[a:b].double()
         check_close(first[e], p @ q, out_bound(p @ q, BF, p.abs() @ q.abs(), b - a, 2.0 ** -23))
     assert emb.dense_status() == emb.EMB_OK
+
+
+@gpu
+@pytest.mark.parametrize("P", [4096, 65536, 262144])
+def test_long_sums_of_one_sign(P):
+    # a cut after every 16 products, below fp32's last bit of the running sum (2^-23 of it), then one rounding
+    g = gen(P)
+    plan = emb.expert_sort(torch.zeros(P, 1, dtype=torch.int32, device="cuda"), 1)
+    x, gy = ((torch.rand(P, n, generator=g, device="cuda") * (4 / P) ** 0.5).to(HF) for n in (136, 264))
+    got = emb.expert_linear_grad(plan, gy, x, torch.zeros(1, 264, 136, dtype=HF, device="cuda"), need_rows=False)[1][0]
+    ref = gy.double().t() @ x.double()
+    check_close(got, ref, out_bound(ref, HF, ref, P / 16, 2.0 ** -23))
