@@ -6,6 +6,11 @@ the current CUDA device (ValueError if not).  Every call takes `stream`: it runs
 on that stream (default: the current one), and what it returns is allocated for
 it.  The caller orders it after the work that makes its inputs; memory of inputs
 that are freed meanwhile is not used again before the call's work is done.
+
+As everywhere in this package, the backward pass is explicit: no call is part of
+autograd's graph, and what one returns requires no gradient even where its
+inputs do.  The *_grad calls give the gradients; code under autograd calls them
+from a torch.autograd.Function.
 """
 from __future__ import annotations
 

@@ -1,4 +1,5 @@
-"""Orthogonalised updates (Muon): argument checks and marshalling only."""
+"""Orthogonalised updates (Muon): argument checks and marshalling only.  Not part
+of autograd's graph: the result requires no gradient even where the update does."""
 from __future__ import annotations
 
 import ctypes

@@ -59,3 +59,47 @@ def test_every_call_refuses_tensors_of_another_device(monkeypatch):
     monkeypatch.undo()
     for call in calls:
         call()
+
+
+@gpu
+def test_results_require_no_gradient():
+    # the backward pass is explicit: inputs that require gradients are read, and nothing joins autograd's graph
+    r = lambda *s, dtype=torch.bfloat16: torch.randn(*s, device="cuda").to(dtype).requires_grad_()  # noqa: E731
+    plan = emb.expert_sort(torch.randint(0, 4, (6, 2), device="cuda"), 4)
+    x, rows, y, w, weights, g = r(6, 24), r(12, 24), r(12, 16), r(4, 16, 24), r(6, 2, dtype=torch.float32), r(6, 16)
+    got = [emb.expert_dispatch(plan, x), emb.expert_dispatch_grad(plan, rows), emb.expert_linear(plan, rows, w),
+           emb.expert_combine(plan, y, weights), emb.orthogonalize(w), *emb.expert_linear_grad(plan, y, rows, w),
+           *emb.expert_combine_grad(plan, g, y, weights)]
+    assert not any(t.requires_grad for t in got)
+    assert torch.equal(got[2], emb.expert_linear(plan, rows.detach(), w.detach()))
+
+
+@gpu
+def test_a_function_of_autograd_takes_the_calls():
+    class Expert(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, plan, x, w, weights):
+            rows = emb.expert_dispatch(plan, x, torch.float16)
+            y = emb.expert_linear(plan, rows, w)
+            ctx.plan = plan
+            ctx.save_for_backward(rows, w, y, weights)
+            return emb.expert_combine(plan, y, weights, torch.float32)
+
+        @staticmethod
+        def backward(ctx, grad):
+            rows, w, y, weights = ctx.saved_tensors
+            grad_y, grad_weights = emb.expert_combine_grad(ctx.plan, grad.contiguous(), y, weights)
+            grad_rows, grad_w = emb.expert_linear_grad(ctx.plan, grad_y, rows, w)
+            return None, emb.expert_dispatch_grad(ctx.plan, grad_rows, torch.float32), grad_w, grad_weights
+
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    ids = torch.randint(0, 3, (20, 2), generator=g, device="cuda")
+    # small whole numbers: exact in every type
+    ints = lambda *s, dtype=torch.float32: torch.randint(-2, 3, s, generator=g, device="cuda").to(dtype).requires_grad_()  # noqa: E731
+    x, w, weights = ints(20, 16), ints(3, 8, 16, dtype=torch.float16), ints(20, 2)
+    Expert.apply(emb.expert_sort(ids, 3), x, w, weights).sum().backward()
+    xr, wr, sr = (t.detach().double().requires_grad_() for t in (x, w, weights))
+    (torch.einsum("tjoi,ti->tjo", wr[ids], xr) * sr[:, :, None]).sum().backward()
+    for t, ref in ((x, xr), (w, wr), (weights, sr)):
+        assert torch.equal(t.grad.double(), ref.grad)
