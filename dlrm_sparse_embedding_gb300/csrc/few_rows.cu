@@ -4,12 +4,14 @@
 // reading them: at 128 x 128 a tile, a row of 1024 outputs would keep 8 of the
 // 152 SMs busy.  Here a warp has one output of one row, in fp32, and reads the
 // weights 16 bytes a lane, whole sectors at a time.  Rows that share an expert
-// read its weights again, from L2.  3328 x 1024: 3.4 us for one row and 6.8 for
-// four (in tiles 11.9 and 14.3), 1024 x 4096: 3.8 and 8.9 (6.9 and 10.3); from
-// eight rows on that share experts, tiles are faster (16.1 and 10.5), so
-// kFewRows ends it there.  (A gradient's rows have the weights' long side as
-// their sum's other one and fill the GPU with tiles: 8.7 us against 9.3 for
-// two rows at 3328 x 1024 when it was written this way.)
+// read its weights again, from L2.  Weights from memory, rows of different experts
+// (of one): 3328 x 1024 takes 4.4 us for one row and 8.7 (6.4) for four, in tiles
+// 12.9 and 19.2 (12.9); 1024 x 4096 3.4 and 10.8 (8.5), in tiles 7.8 and 12.2 (7.7).
+// From five rows on, those that share experts are faster in tiles (1024 x 4096:
+// 8.0 us for 10.3; of different experts 15.3 for 12.8), so kFewRows ends it there.
+// (A gradient's rows have the weights' long side as their sum's other one and fill the
+// GPU with tiles: 8.7 us against 9.3 for two rows at 3328 x 1024 when it was written
+// this way.)
 #include "products.cuh"
 
 namespace emb {

@@ -277,11 +277,11 @@ int start(const Input& q, const T* g, int64_t batch, cudaStream_t st)
 // ---------------------------------------------------------------------------
 // the steps
 // ---------------------------------------------------------------------------
-// 16 matrices of 1024 x 3328 take 966 us for five steps, 955 TFLOP/s of what symmetry
+// 16 matrices of 1024 x 3328 take 970 us for five steps, 950 TFLOP/s of what symmetry
 // leaves: reading G twice and writing X takes 51 us of them, and of the rest the
 // tensor cores are busy 52%, DRAM 63% (3.7 GB): A's products (33 thousand cycles a
 // tile, 27 of them products) run beside nothing that uses memory, the update (16 and
-// 8) beside 512 KB of X a tile.  One of 1777 x 519 takes 121 us,
+// 8) beside 512 KB of X a tile.  One of 1777 x 519 takes 123 us,
 // bound by the chain of 15 products: 7 us each, of which the products are 1 to 2.
 //
 // All products of all steps are one list of tiles for one persistent grid (see

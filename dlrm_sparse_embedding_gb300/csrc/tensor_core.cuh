@@ -102,6 +102,12 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     return true;
 }
 
+// The same by a whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity, volatile int* gave_up)
+{
+    return __all_sync(0xffffffffu, bar_wait(bar, parity, gave_up));
+}
+
 // bar_wait_warp for what threads of the cluster's other CTAs did before they arrived
 // (bar_arrive_cluster), or copied here.
 __device__ __forceinline__ bool bar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* gave_up)
@@ -127,12 +133,6 @@ __device__ __forceinline__ void copy_cluster(uint32_t to, uint32_t from, uint32_
 {
     asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                  ::"r"(to), "r"(from), "r"(bytes), "r"(bar) : "memory");
-}
-
-// The same by a whole warp, with one answer for all its lanes.
-__device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity, volatile int* gave_up)
-{
-    return __all_sync(0xffffffffu, bar_wait(bar, parity, gave_up));
 }
 
 // ---------------------------------------------------------------------------

@@ -375,8 +375,9 @@ int emb_phase_times(emb_layer* layer, float* ms_host, int32_t n, int64_t* steps_
  * caller's.  Types named "dtype" are an emb_dtype.  A "stride" is the distance
  * in elements between the starts of two consecutive rows, at least the row's
  * width; the elements of a row are contiguous.  Arrays without a stride are
- * contiguous.  A 16-byte aligned array with rows of a multiple of 16 bytes is
- * moved 16 bytes at a time, any other one element at a time.
+ * contiguous.  Rows of a multiple of 8 elements, all at 16-byte boundaries, are
+ * moved 16 bytes at a time, rows of even widths, strides and addresses two elements
+ * at a time, any other one element at a time.
  * What the GPU alone can see (an id outside [-1, E), a bounded wait that ran
  * out) is recorded in a sticky word of the device, see emb_dense_status.
  * ------------------------------------------------------------------------- */
