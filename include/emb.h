@@ -483,6 +483,42 @@ int emb_orthogonalize(const void* update, int32_t dtype, int64_t batch_stride, i
                       int64_t rows, int64_t cols, int32_t steps, float a, float b, float c, float eps, void* out,
                       void* workspace, size_t workspace_bytes, void* stream);
 
+/* Layer norm of the rows of x [rows, width], and its gradients, g = grad_y:
+ *   h = (x - mean) rstd,  rstd = 1 / sqrt(variance + eps),  y = h weight + bias
+ *   grad_x      = rstd (g weight - mean(g weight) - h mean(g weight h))   in x's dtype
+ *   grad_weight = sum over the rows of g h,  grad_bias = sum over the rows of g
+ * weight, bias, grad_weight and grad_bias are [width] of param_dtype; a null weight
+ * stands for ones, a null bias for zeros.  Any dtypes; y and grad_x are contiguous, x and
+ * grad_y have a row stride.  Statistics and sums are fp32 in a fixed order, with one
+ * rounding at the end; the mean's own rounding is taken off again, and rows of any
+ * finite size keep their variance.  A row that holds an infinity or a NaN is NaN, and so
+ * are its columns' sums; other rows are not touched.  A null grad_x, grad_weight or
+ * grad_bias is not computed; without rows the sums are zero.  width in [1, 2^24], eps
+ * in [1e-24, fp32's largest].  The workspace is 256-byte aligned,
+ * emb_layer_norm_grad_workspace bytes.  No passage: library convenience. */
+int emb_layer_norm(const void* x, int32_t x_dtype, int64_t x_stride, int64_t rows, int64_t width, const void* weight,
+                   const void* bias, int32_t param_dtype, float eps, void* y, int32_t y_dtype, void* stream);
+int emb_layer_norm_grad_workspace(int64_t rows, int64_t width, size_t* bytes);
+int emb_layer_norm_grad(const void* grad_y, int32_t y_dtype, int64_t grad_stride, const void* x, int32_t x_dtype,
+                        int64_t x_stride, int64_t rows, int64_t width, const void* weight, int32_t param_dtype,
+                        float eps, void* grad_x, void* grad_weight, void* grad_bias, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Dropout: y = residual + x / (1 - rate) where the element is kept, residual where it
+ * is dropped, whatever x holds there (a null residual stands for zeros); x and y
+ * [rows, width] of any dtypes, residual of y's, y contiguous.  The gradient of x is the
+ * same call on grad_y without a residual.  Element i = row * width + column is kept
+ * when u >= rate * 2^16 (rounded to a whole number, and 1 - rate with it), u being 16
+ * bits of Philox4x32 with 7 rounds (J. Salmon et al., "Parallel random numbers: as easy as
+ * 1, 2, 3", 2011): counter words (i / 8, its high word, offset, its high word), key
+ * the low and high word of the seed, half i % 2 (0: low) of the result's word
+ * i % 8 / 2.  So the mask depends on seed, offset and i alone and is never stored.
+ * seed_at (nullable, 8-byte aligned) is the seed in device memory, read when the call
+ * runs, in place of `seed`.  rate in [0, 1].  No passage: library convenience. */
+int emb_dropout(const void* x, int32_t x_dtype, int64_t x_stride, int64_t rows, int64_t width, double rate,
+                uint64_t seed, const uint64_t* seed_at, uint64_t offset, const void* residual,
+                int64_t residual_stride, void* y, int32_t y_dtype, void* stream);
+
 /* Wait for the stream; return and clear the device's sticky status of the
  * calls of this section (EMB_OK, EMB_ERR_KEY_RANGE or EMB_ERR_TIMEOUT).  Of
  * several threads that ask at once, one gets what there is.  No passage:
