@@ -13,37 +13,39 @@ constexpr int kSms = 152;
 constexpr int64_t kMaxWidth = 1 << 24;
 
 // Threads a row and elements a thread.  Up to a warp the threads are a power of two and
-// a block takes several rows; beyond, whole warps and one row a block.  The grid is what
-// the GPU holds at once: a block goes through its rows with the next one's loads on
-// their way.
+// a warp takes several rows; beyond, whole warps and one row a block.  The grid is what
+// the GPU holds at once: a block goes through its rows with the next ones on their way.
 Shape shape_of(int64_t rows, int64_t width, bool grad)
 {
     Shape s = {};
     s.chunks = 1;
     if (width > kRegisterWidth) {
+        s.kind = kWideRows;
         s.tx = kWideThreads, s.ty = 1;
         s.blocks = (int)std::min<int64_t>(rows, 2 * kSms);
         const int64_t columns = (width + 31) / 32;   // of blocks of the column sums, at most
         s.chunks = (int)std::max<int64_t>(1, std::min((rows + kColumnRows - 1) / kColumnRows, 8 * kSms / columns));
         return s;
     }
-    s.per_thread = width <= 8 * kMaxThreads ? 8 : 16;
-    s.tx = 1;
+    s.kind = width <= kWarpWidth ? kWarpRows : kBlockRows;
+    s.per_thread = width <= 256 || (width > kWarpWidth && width <= 2048) ? 8 : 16;
     const int threads = (int)((width + s.per_thread - 1) / s.per_thread);
-    if (threads <= 32)
-        while (s.tx < threads) s.tx *= 2;
-    else
-        s.tx = (threads + 31) / 32 * 32;
-    s.ty = s.tx <= 32 ? kThreads / s.tx : 1;
-    const int at_once = std::max(1, 65536 / (registers(s.per_thread, grad) * s.tx * s.ty));
-    s.blocks = (int)std::min<int64_t>((rows + s.ty - 1) / s.ty, (int64_t)kSms * at_once);
+    if (s.kind == kWarpRows) {
+        for (s.tx = 1; s.tx < threads;) s.tx *= 2;
+        s.ty = kThreads / s.tx;
+    } else {
+        s.tx = (threads + 31) / 32 * 32, s.ty = 1;
+    }
+    s.per_sm = std::max(1, std::min(8, 65536 / (registers(s.per_thread, grad) * s.tx * s.ty)));
+    if (s.kind == kBlockRows) s.per_sm = std::max(1, std::min(s.per_sm, kSharedBytes / (int)(3 * width * (grad ? 8 : 4) + kOwnBytes)));
+    s.blocks = (int)std::min<int64_t>((rows + s.ty - 1) / s.ty, (int64_t)kSms * s.per_sm);
     return s;
 }
 
 // Parts that the parameters' gradients come in.
-int64_t parts_of(const Shape& s) { return s.per_thread ? s.blocks : s.chunks; }
+int64_t parts_of(const Shape& s) { return s.kind == kWideRows ? s.chunks : s.blocks; }
 
-size_t stats_bytes(const Shape& s, int64_t rows) { return s.per_thread ? 0 : (size_t)rows * sizeof(float4); }
+size_t stats_bytes(const Shape& s, int64_t rows) { return s.kind == kWideRows ? (size_t)rows * sizeof(float4) : 0; }
 
 bool sizes_valid(int64_t rows, int64_t width) { return rows >= 0 && width >= 1 && width <= kMaxWidth && rows <= (int64_t(1) << 40); }
 
@@ -76,11 +78,12 @@ __global__ void __launch_bounds__(32 * kGroups) sum_parts(const float* __restric
     }
 }
 
-int launch(const Args& a, int x_dtype, int y_dtype, int vector, const Shape& s, cudaStream_t st)
+int launch(Args& a, int x_dtype, int y_dtype, bool vectors, const Shape& s, cudaStream_t st)
 {
-    if (x_dtype == EMB_F32) return launch_rows<float>(a, y_dtype, vector, s, st);
-    if (x_dtype == EMB_F16) return launch_rows<__half>(a, y_dtype, vector, s, st);
-    return launch_rows<__nv_bfloat16>(a, y_dtype, vector, s, st);
+    if (!(a.status = dense_status_word())) return EMB_ERR_CUDA;
+    if (x_dtype == EMB_F32) return launch_rows<float>(a, y_dtype, vectors, s, st);
+    if (x_dtype == EMB_F16) return launch_rows<__half>(a, y_dtype, vectors, s, st);
+    return launch_rows<__nv_bfloat16>(a, y_dtype, vectors, s, st);
 }
 
 bool params_valid(const void* weight, const void* bias, int dtype)
@@ -107,7 +110,7 @@ extern "C" int emb_layer_norm(const void* x, int32_t x_dtype, int64_t x_stride, 
     a.x = x, a.x_stride = x_stride, a.rows = rows, a.width = (int)width;
     a.weight = weight, a.bias = bias, a.param_dtype = param_dtype, a.eps = eps, a.out = y;
     const int vector = std::min(vector_of(x, x_dtype, x_stride, width), vector_of(y, y_dtype, width, width));
-    return norm::launch(a, x_dtype, y_dtype, vector, norm::shape_of(rows, width, false), static_cast<cudaStream_t>(stream));
+    return norm::launch(a, x_dtype, y_dtype, vector == 8, norm::shape_of(rows, width, false), static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int emb_layer_norm_grad_workspace(int64_t rows, int64_t width, size_t* bytes)
@@ -143,13 +146,13 @@ extern "C" int emb_layer_norm_grad(const void* grad_y, int32_t y_dtype, int64_t 
     a.g = grad_y, a.g_stride = grad_stride;
     a.weight = weight, a.param_dtype = param_dtype, a.eps = eps;
     a.out = grad_x, a.dw = grad_weight, a.db = grad_bias;
-    if (!s.per_thread) a.stats = static_cast<float4*>(workspace);
+    if (s.kind == norm::kWideRows) a.stats = static_cast<float4*>(workspace);
     a.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + norm::stats_bytes(s, rows));
     int vector = std::min(vector_of(x, x_dtype, x_stride, width), vector_of(grad_y, y_dtype, grad_stride, width));
     if (grad_x) vector = std::min(vector, vector_of(grad_x, x_dtype, width, width));
-    if (int rc = norm::launch(a, x_dtype, y_dtype, vector, s, st)) return rc;
+    if (int rc = norm::launch(a, x_dtype, y_dtype, vector == 8, s, st)) return rc;
     const int64_t parts = norm::parts_of(s);
-    if (!params || (s.per_thread && parts == 1)) return EMB_OK;   // one block wrote the sums itself
+    if (!params || (s.kind != norm::kWideRows && parts == 1)) return EMB_OK;   // one block wrote the sums itself
     return launch_next(norm::sum_parts, dim3((unsigned)((2 * width + 31) / 32)), dim3(32, norm::kGroups), 0, st, 1, (const float*)a.partial,
                        (int)parts, (int)width, param_dtype, grad_weight, grad_bias);
 }

@@ -19,7 +19,11 @@
 // fixed order, so results repeat bit for bit.
 #pragma once
 
+#include <algorithm>
+
+#include "emb_internal.cuh"
 #include "rows.cuh"
+#include "tensor_core.cuh"
 
 namespace emb {
 namespace norm {
@@ -38,24 +42,37 @@ struct Args {
     void* db = nullptr;            // nullable
     float* partial = nullptr;      // [blocks][2][width]
     float4* stats = nullptr;       // of each row, wide rows only: m, d, rstd, scale
+    int* status = nullptr;
+    // the ring of stages that rows are copied to
+    int stages = 0, chunk = 1;     // rows of a stage
+    bool x_whole = false, g_whole = false;   // a stage's rows are one piece of memory
+    int x_pitch = 0, g_pitch = 0;  // bytes between a stage's rows in shared memory, where they are not
+    int x_slot = 0, g_slot = 0;    // bytes of a stage
 };
 
-// How the rows are laid on the grid.
+// How rows are laid on the grid.
+enum Kind { kWarpRows, kBlockRows, kWideRows };
 struct Shape {
-    int per_thread;        // elements of a row a thread holds: 8 or 16, or 0 for wide rows
-    int tx, ty;            // threads a row (up to a warp, or several and then ty is 1); rows a block
-    int blocks;
+    Kind kind;
+    int per_thread;        // elements of a row a thread holds: 8 or 16 (not of wide rows)
+    int tx, ty;            // threads a row; rows a block
+    int blocks, per_sm;
     int chunks;            // wide rows' gradients: parts the rows are added up in
 };
 
 constexpr int kThreads = 256, kMaxThreads = 512, kWideThreads = 1024;
-constexpr int kRegisterWidth = 16 * kMaxThreads;   // the widest row kept in registers
-// Registers a thread: what its elements take (16 of a gradient spill a few words).
-constexpr int registers(int per_thread, bool grad) { return per_thread == 16 ? 128 : grad ? 80 : 64; }
-constexpr int kColumnRows = 8;              // rows at a time of a block of wide_columns
+constexpr int kWarpWidth = 16 * 32;              // the widest row of a warp's lanes
+constexpr int kRegisterWidth = 16 * kMaxThreads; // the widest row kept in registers
+constexpr int kMaxStages = 8;
+constexpr int kSharedBytes = 226 * 1024;         // of an SM, for its blocks
+constexpr int kOwnBytes = 2560;                  // of a block beside its stages
+constexpr int kColumnRows = 8;                   // rows at a time of a block of wide_columns
+// Registers a thread: what its elements take.
+constexpr int registers(int per_thread, bool grad) { return per_thread == 16 ? (grad ? 128 : 80) : grad ? 80 : 64; }
 
-// int launch(const Args&, x type, out type, g type ...): one translation unit for each type of x
-template <class X> int launch_rows(const Args& a, int y_dtype, int vector, const Shape& s, cudaStream_t st);
+// One translation unit for each type of x.  `vectors`: rows of both types are whole
+// vectors, all at 16-byte boundaries.
+template <class X> int launch_rows(Args a, int y_dtype, bool vectors, const Shape& s, cudaStream_t st);
 
 #ifdef EMB_NORM_KERNELS
 
@@ -75,27 +92,32 @@ __device__ __forceinline__ void store_param(void* p, int dtype, int64_t i, float
     else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
-// s, summed over the blockDim.x threads of a row, in all of them.  Two calls in turn
-// on two buffers need no barrier more: the other call's lies between.
+// s, summed over the lanes of a row (a power of two of them), in all of them.
 template <int N>
-__device__ __forceinline__ void row_sums(float (&s)[N], float (*part)[4])
+__device__ __forceinline__ void lane_sums(float (&s)[N], int lanes)
 {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+    for (int d = 16; d; d >>= 1)
+        if (d < lanes)
 #pragma unroll
-        for (int d = 16; d; d >>= 1)
-            if (d < blockDim.x) s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
-    if (blockDim.x <= 32) return;
+            for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
+}
+
+// The same over a block.  Two calls in turn on two buffers need no barrier more: the other
+// call's lies between.
+template <int N>
+__device__ __forceinline__ void block_sums(float (&s)[N], float (*part)[4])
+{
+    lane_sums(s, 32);
     const int warps = blockDim.x >> 5;
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
         for (int i = 0; i < N; ++i) part[threadIdx.x >> 5][i] = s[i];
     __syncthreads();
+    const int from = threadIdx.x & 15;     // of at most 16 warps, twice
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = 0.f;
-    for (int v = 0; v < warps; ++v)
-#pragma unroll
-        for (int i = 0; i < N; ++i) s[i] += part[v][i];
+    for (int i = 0; i < N; ++i) s[i] = from < warps ? part[from][i] : 0.f;
+    lane_sums(s, 16);
 }
 
 // Squares up to here are summed as they are; a row beyond is scaled.
@@ -103,7 +125,7 @@ constexpr float kLargeSquares = 0x1p100f, kDown = 0x1p-80f;
 
 struct Moments {
     float m, d, rstd, scale;
-    __device__ __forceinline__ float h(float x) const { return ((x * scale - m) - d) * rstd; }
+    __device__ __forceinline__ float h(float x) const { return __fmaf_rn(x * scale - m, rstd, -d * rstd); }
 };
 
 __device__ __forceinline__ Moments moments(float m, float shifted, float squares, float inv_n, float eps, float scale)
@@ -118,151 +140,338 @@ __device__ __forceinline__ Moments moments(float m, float shifted, float squares
     return r;
 }
 
-// Rows of up to kRegisterWidth elements: U vectors of V a thread.
+// What a thread holds of a row, U vectors of V, and adds up over rows.
 template <int V, int U, bool GRAD, class X, class Y>
-__global__ void __maxnreg__(registers(U * V, GRAD)) norm_rows(const Args a)
-{
-    __shared__ float part[2][32][4];
-    extern __shared__ float dynamic[];
-    let_next_begin();
-    wait_for_earlier();
-    const int tx = threadIdx.x, width = a.width;
-    const float inv_n = 1.f / (float)width;
-    const X* const x = static_cast<const X*>(a.x);
-    const Y* const g = static_cast<const Y*>(a.g);
-    const auto column = [&](int u) { return (tx + u * (int)blockDim.x) * V; };
+struct Piece {
+    float v[U][V], g[U][V], w[U][V], b[U][V], acc_w[U][V], acc_b[U][V];
+    int first, step, width;    // its columns: V from first + u * step on
 
-    float w[U][V], b[U][V], acc_w[U][V], acc_b[U][V];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int q = 0; q < V; ++q) {
-            const bool in = column(u) < width;
-            w[u][q] = in ? param(a.weight, a.param_dtype, column(u) + q, 1.f) : 0.f;
-            if (!GRAD) b[u][q] = in ? param(a.bias, a.param_dtype, column(u) + q, 0.f) : 0.f;
-            acc_w[u][q] = acc_b[u][q] = 0.f;
-        }
+    __device__ __forceinline__ bool in(int u) const { return first + u * step < width; }
 
-    const int64_t step = (int64_t)gridDim.x * blockDim.y;
-    Raw<V, X> next_x[U];
-    Raw<V, Y> next_g[U];
-    const auto fetch = [&](int64_t row) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (row < a.rows && column(u) < width) {
-                next_x[u].load(x + row * a.x_stride + column(u));
-                if (GRAD) next_g[u].load(g + row * a.g_stride + column(u));
-            }
-    };
-    int64_t first = (int64_t)blockIdx.x * blockDim.y;
-    fetch(first + threadIdx.y);
-    // a block's rows move on together: every thread meets every barrier
-    for (; first < a.rows; first += step) {
-        const int64_t row = first + threadIdx.y;
-        const bool has = row < a.rows;
-        float v[U][V], gr[U][V];
+    __device__ __forceinline__ void open(const Args& a, int tx, int threads)
+    {
+        first = tx * V, step = threads * V, width = a.width;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int q = 0; q < V; ++q) {
-                const bool in = has && column(u) < width;
-                v[u][q] = in ? next_x[u][q] : 0.f;
-                if (GRAD) gr[u][q] = in ? next_g[u][q] : 0.f;
+                w[u][q] = in(u) ? param(a.weight, a.param_dtype, first + u * step + q, 1.f) : 0.f;
+                if (!GRAD) b[u][q] = in(u) ? param(a.bias, a.param_dtype, first + u * step + q, 0.f) : 0.f;
+                acc_w[u][q] = acc_b[u][q] = 0.f;
             }
-        fetch(row + step);
+    }
 
+    // Takes the row from shared memory.
+    __device__ __forceinline__ void take(const X* x, const Y* gy, bool has)
+    {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            Raw<V, X> rx;
+            Raw<V, Y> rg;
+            if (has && in(u)) {
+                rx.load_shared(x + first + u * step);
+                if (GRAD) rg.load_shared(gy + first + u * step);
+            }
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                v[u][q] = has && in(u) ? rx[q] : 0.f;
+                if (GRAD) g[u][q] = has && in(u) ? rg[q] : 0.f;
+            }
+        }
+    }
+
+    // The row's results.  first_sums and second_sums add up over its threads;
+    // any(flag) tells whether a row's of all that add up together is set.
+    template <class S1, class S2, class ANY>
+    __device__ __forceinline__ void finish(const Args& a, int64_t row, bool has, float inv_n, S1 first_sums, S2 second_sums, ANY any)
+    {
+        constexpr int N = GRAD ? 4 : 2;
         Moments mo;
-        float along = 0.f, mean_gw = 0.f;
-        float scale = 1.f;
-        for (bool again = false;; again = true) {
+        float scale = 1.f, s[N];
+        for (;;) {
             float s1[1] = {};
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int q = 0; q < V; ++q) s1[0] += v[u][q] * scale;
-            row_sums<1>(s1, part[0]);
-            const float m = s1[0] * inv_n;
-            float s[GRAD ? 4 : 2] = {};
+                for (int q = 0; q < V; ++q) s1[0] += v[u][q];
+            first_sums(s1);
+            mo.m = s1[0] * inv_n;
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[i] = 0.f;
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (column(u) < width) {
+                if (in(u)) {
 #pragma unroll
                     for (int q = 0; q < V; ++q) {
-                        const float c = v[u][q] * scale - m;
+                        const float c = v[u][q] - mo.m;
                         s[0] += c;
                         s[1] = __fmaf_rn(c, c, s[1]);
                         if constexpr (GRAD) {
-                            const float gw = gr[u][q] * w[u][q];
+                            const float gw = g[u][q] * w[u][q];
                             s[2] += gw;
                             s[3] = __fmaf_rn(gw, c, s[3]);
                         }
                     }
                 }
-            row_sums<GRAD ? 4 : 2>(s, part[1]);
-            const bool large = !(s[1] <= kLargeSquares);
-            if (!again && __any_sync(0xffffffffu, large)) {   // the same in all threads of a row, and in all that meet a barrier
-                scale = large ? kDown : 1.f;
-                continue;
+            second_sums(s);
+            const bool large = scale == 1.f && !(s[1] <= kLargeSquares);
+            if (!any(large)) break;
+            if (large) {     // once more, smaller
+                scale = kDown;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int q = 0; q < V; ++q) v[u][q] *= kDown;
             }
-            mo = moments(m, s[0], s[1], inv_n, a.eps, scale);
-            if constexpr (GRAD) {
-                mean_gw = s[2] * inv_n;
-                along = (s[3] - mo.d * s[2]) * mo.rstd * inv_n;
-            }
-            break;
         }
-        const float outer = mo.rstd * mo.scale;
+        mo = moments(mo.m, s[0], s[1], inv_n, a.eps, scale);
+        const float shift = -mo.d * mo.rstd;
+        float k1 = 0.f, k2 = 0.f, k3 = 0.f;     // dx = k1 g w + k2 h + k3
+        if constexpr (GRAD) {
+            k1 = mo.rstd * scale;
+            k2 = -k1 * ((s[3] - mo.d * s[2]) * mo.rstd * inv_n);
+            k3 = -k1 * (s[2] * inv_n);
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float o[V];
 #pragma unroll
             for (int q = 0; q < V; ++q) {
-                const float h = mo.h(v[u][q]);
+                const float h = __fmaf_rn(v[u][q] - mo.m, mo.rstd, shift);
                 if constexpr (GRAD) {
-                    acc_w[u][q] = __fmaf_rn(gr[u][q], h, acc_w[u][q]);
-                    acc_b[u][q] += gr[u][q];
-                    o[q] = outer * ((gr[u][q] * w[u][q] - mean_gw) - h * along);
+                    acc_w[u][q] = __fmaf_rn(g[u][q], h, acc_w[u][q]);
+                    acc_b[u][q] += g[u][q];
+                    o[q] = __fmaf_rn(g[u][q] * w[u][q], k1, __fmaf_rn(h, k2, k3));
                 } else {
                     o[q] = __fmaf_rn(h, w[u][q], b[u][q]);
                 }
             }
-            if (has && column(u) < width && a.out) {
-                if constexpr (GRAD) store_vec<V, X>(static_cast<X*>(a.out) + row * width + column(u), o);
-                else store_vec<V, Y>(static_cast<Y*>(a.out) + row * width + column(u), o);
+            if (has && in(u) && a.out) {
+                if constexpr (GRAD) store_vec<V, X>(static_cast<X*>(a.out) + row * width + first + u * step, o);
+                else store_vec<V, Y>(static_cast<Y*>(a.out) + row * width + first + u * step, o);
             }
         }
+    }
+};
+
+// Where `bytes` at p lie between 16-byte boundaries.
+struct Span {
+    const unsigned char* from;
+    uint32_t bytes, skip;
+    __device__ __forceinline__ Span(const void* p, int64_t n)
+    {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p), begin = at & ~uintptr_t(15);
+        from = reinterpret_cast<const unsigned char*>(begin);
+        skip = (uint32_t)(at - begin);
+        bytes = (uint32_t)((at + n + 15 - begin) & ~uintptr_t(15));
+    }
+};
+
+// If a wait gave up, what was copied last lands before the block ends.
+__device__ __forceinline__ void gave_up_end(int* gave_up, int* status)
+{
+    const uint64_t t0 = tc::now_ns();
+    while (tc::now_ns() - t0 < 2000000) {}
+    if (status) atomicOr(status, ERRBIT_TIMEOUT);
+}
+
+// The sums of a block's threads, which take up to blockDim.y rows at a time: to its part
+// of the workspace, or, of a block alone, to their place.
+template <class PIECE, int V, int U>
+__device__ __forceinline__ void put_sums(const Args& a, const PIECE& p, float* shared, int ty)
+{
+    const auto put = [&](int which, int c, float sum) {
+        if (gridDim.x == 1) store_param(which ? a.db : a.dw, a.param_dtype, c, sum);
+        else a.partial[((int64_t)blockIdx.x * 2 + which) * a.width + c] = sum;
+    };
+    const int threads = blockDim.x * blockDim.y, thread = threadIdx.y * blockDim.x + threadIdx.x, cols = p.step * U;
+    for (int which = 0; which < 2; ++which) {
+        if (ty > 1) {   // the rows meet: shared[row][column]
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int q = 0; q < V; ++q) shared[threadIdx.y * cols + p.first + u * p.step + q] = which ? p.acc_b[u][q] : p.acc_w[u][q];
+            __syncthreads();
+            for (int c = thread; c < a.width; c += threads) {
+                float sum = 0.f;
+                for (int r = 0; r < ty; ++r) sum += shared[r * cols + c];
+                put(which, c, sum);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (p.in(u)) {
+#pragma unroll
+                    for (int q = 0; q < V; ++q) put(which, p.first + u * p.step + q, which ? p.acc_b[u][q] : p.acc_w[u][q]);
+                }
+        }
+    }
+}
+
+// Rows of kWarpWidth < width <= kRegisterWidth: a block takes one at a time.  Its rows are
+// copied to a ring of stages; a stage is free for the next row when the first sums'
+// barrier has been met.
+template <int V, int U, bool GRAD, class X, class Y>
+__global__ void __maxnreg__(registers(U * V, GRAD)) block_rows(const Args a)
+{
+    __shared__ float part[2][32][4];
+    __shared__ uint64_t full[kMaxStages];
+    __shared__ int gave_up;
+    extern __shared__ __align__(128) unsigned char dynamic[];
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < a.stages; ++i) tc::bar_init(tc::smem_addr(&full[i]), 1);
+        gave_up = 0;
+        tc::bar_init_fence();
+    }
+    __syncthreads();
+    let_next_begin();
+    wait_for_earlier();
+    const float inv_n = 1.f / (float)a.width;
+    const X* const x = static_cast<const X*>(a.x);
+    const Y* const g = static_cast<const Y*>(a.g);
+    const auto copy = [&](int64_t row, int stage) {
+        unsigned char* const to = dynamic + stage * (a.x_slot + a.g_slot);
+        const uint32_t bar = tc::smem_addr(&full[stage]);
+        const Span sx(x + row * a.x_stride, a.width * (int64_t)sizeof(X));
+        if constexpr (GRAD) {
+            const Span sg(g + row * a.g_stride, a.width * (int64_t)sizeof(Y));
+            tc::bar_expect(bar, sx.bytes + sg.bytes);
+            tc::copy_bytes(tc::smem_addr(to + a.x_slot), sg.from, sg.bytes, bar);
+        } else {
+            tc::bar_expect(bar, sx.bytes);
+        }
+        tc::copy_bytes(tc::smem_addr(to), sx.from, sx.bytes, bar);
+    };
+    if (threadIdx.x == 0)
+        for (int i = 0; i < a.stages; ++i)
+            if (blockIdx.x + (int64_t)i * gridDim.x < a.rows) copy(blockIdx.x + (int64_t)i * gridDim.x, i);
+    Piece<V, U, GRAD, X, Y> p;
+    p.open(a, threadIdx.x, blockDim.x);
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        if (!(ok = tc::bar_wait(tc::smem_addr(&full[stage]), phase, &gave_up))) break;
+        const unsigned char* const at = dynamic + stage * (a.x_slot + a.g_slot);
+        const uint32_t skip_x = V > 1 ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(x + row * a.x_stride) & 15);
+        const uint32_t skip_g = V > 1 || !GRAD ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(g + row * a.g_stride) & 15);
+        p.take(reinterpret_cast<const X*>(at + skip_x), reinterpret_cast<const Y*>(at + a.x_slot + skip_g), true);
+        bool taken = false;
+        p.finish(
+            a, row, true, inv_n,
+            [&](auto& s) {
+                block_sums(s, part[0]);
+                const int64_t next = row + (int64_t)a.stages * gridDim.x;
+                if (threadIdx.x == 0 && !taken && next < a.rows) copy(next, stage);
+                taken = true;
+            },
+            [&](auto& s) { block_sums(s, part[1]); }, [](bool large) { return large; });
+        if (++stage == a.stages) stage = 0, phase ^= 1;
+    }
+    if (!ok) {
+        gave_up_end(&gave_up, threadIdx.x == 0 ? a.status : nullptr);
+        return;
     }
     if constexpr (GRAD) {
-        if (!a.dw && !a.db) return;
-        const auto put = [&](int which, int c, float sum) {
-            if (gridDim.x == 1) store_param(which ? a.db : a.dw, a.param_dtype, c, sum);
-            else a.partial[((int64_t)blockIdx.x * 2 + which) * width + c] = sum;
-        };
-        for (int which = 0; which < 2; ++which) {
-            if (blockDim.y > 1) {   // the block's rows meet: dynamic[ty][column]
-                const int cols = (int)blockDim.x * U * V;
-                __syncthreads();
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int q = 0; q < V; ++q) dynamic[threadIdx.y * cols + column(u) + q] = which ? acc_b[u][q] : acc_w[u][q];
-                __syncthreads();
-                for (int c = threadIdx.y * blockDim.x + tx; c < width; c += blockDim.x * blockDim.y) {
-                    float sum = 0.f;
-                    for (int r = 0; r < blockDim.y; ++r) sum += dynamic[r * cols + c];
-                    put(which, c, sum);
-                }
-            } else {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (column(u) < width) {
-#pragma unroll
-                        for (int q = 0; q < V; ++q)
-                            put(which, column(u) + q, which ? acc_b[u][q] : acc_w[u][q]);
-                    }
-            }
-        }
+        if (a.dw || a.db) put_sums<Piece<V, U, GRAD, X, Y>, V, U>(a, p, nullptr, 1);
     }
+}
+
+// Rows of up to kWarpWidth: some lanes take one, a warp several, and each warp has its
+// own ring of stages, of a.chunk rows each.  No warp waits for another.
+template <int V, int U, bool GRAD, class X, class Y>
+__global__ void __maxnreg__(registers(U * V, GRAD)) warp_rows(const Args a)
+{
+    constexpr int kWarps = kThreads / 32;
+    __shared__ uint64_t full[kWarps][kMaxStages];
+    __shared__ int gave_up;
+    extern __shared__ __align__(128) unsigned char dynamic[];
+    const int thread = threadIdx.y * blockDim.x + threadIdx.x, warp = thread >> 5, lane = thread & 31;
+    const int lanes = blockDim.x, at_once = 32 / lanes, sub = lane / lanes;
+    if (lane == 0) {
+        for (int i = 0; i < a.stages; ++i) tc::bar_init(tc::smem_addr(&full[warp][i]), 1);
+        if (warp == 0) gave_up = 0;
+        tc::bar_init_fence();
+    }
+    __syncthreads();
+    let_next_begin();
+    wait_for_earlier();
+    const float inv_n = 1.f / (float)a.width;
+    const X* const x = static_cast<const X*>(a.x);
+    const Y* const g = static_cast<const Y*>(a.g);
+    const int64_t chunks = (a.rows + a.chunk - 1) / a.chunk, step = (int64_t)gridDim.x * kWarps;
+    unsigned char* const ring = dynamic + (size_t)warp * a.stages * (a.x_slot + a.g_slot);
+
+    const auto copy = [&](int64_t chunk, int stage) {   // the whole warp
+        unsigned char* const to = ring + stage * (a.x_slot + a.g_slot);
+        const uint32_t bar = tc::smem_addr(&full[warp][stage]);
+        const int64_t row = chunk * a.chunk;
+        const int have = (int)min((int64_t)a.chunk, a.rows - row);
+        const auto one = [&](const auto* base, int64_t stride, bool whole, int pitch, unsigned char* dst, bool send) {
+            const int i = whole ? 0 : lane;
+            const Span s(base + (row + i) * stride, (whole ? have : 1) * (int64_t)a.width * sizeof(*base));
+            const bool mine = whole ? lane == 0 : lane < have;
+            if (send && mine) tc::copy_bytes(tc::smem_addr(dst + i * pitch), s.from, s.bytes, bar);
+            return mine ? s.bytes : 0u;
+        };
+        uint32_t bytes = one(x, a.x_stride, a.x_whole, a.x_pitch, to, false);
+        if (GRAD) bytes += one(g, a.g_stride, a.g_whole, a.g_pitch, to + a.x_slot, false);
+        bytes = __reduce_add_sync(0xffffffffu, bytes);
+        if (lane == 0) tc::bar_expect(bar, bytes);
+        __syncwarp();
+        one(x, a.x_stride, a.x_whole, a.x_pitch, to, true);
+        if (GRAD) one(g, a.g_stride, a.g_whole, a.g_pitch, to + a.x_slot, true);
+    };
+    // row i of a stage
+    const auto place = [&](const auto* base, int64_t stride, bool whole, int pitch, const unsigned char* from, int64_t first, int i) {
+        using T = typename std::remove_cv<typename std::remove_pointer<decltype(base)>::type>::type;
+        const uint32_t skip = V > 1 ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(base + (whole ? first : first + i) * stride) & 15);
+        return reinterpret_cast<const T*>(from + skip + (whole ? i * a.width * (int)sizeof(T) : i * pitch));
+    };
+
+    const int64_t mine = (int64_t)blockIdx.x * kWarps + warp;
+    for (int i = 0; i < a.stages; ++i)
+        if (mine + i * step < chunks) copy(mine + i * step, i);
+    Piece<V, U, GRAD, X, Y> p;
+    p.open(a, lane % lanes, lanes);
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int64_t chunk = mine; chunk < chunks; chunk += step) {
+        if (!(ok = tc::bar_wait_warp(tc::smem_addr(&full[warp][stage]), phase, &gave_up))) break;
+        const unsigned char* const at = ring + stage * (a.x_slot + a.g_slot);
+        const int64_t first = chunk * a.chunk;
+        for (int i = sub; i < a.chunk; i += at_once) {
+            const int64_t row = first + i;
+            const bool has = row < a.rows;
+            p.take(place(x, a.x_stride, a.x_whole, a.x_pitch, at, first, i), place(g, a.g_stride, a.g_whole, a.g_pitch, at + a.x_slot, first, i), has);
+            p.finish(
+                a, row, has, inv_n, [&](auto& s) { lane_sums(s, lanes); }, [&](auto& s) { lane_sums(s, lanes); },
+                [](bool large) { return __any_sync(0xffffffffu, large) != 0; });
+        }
+        __syncwarp();
+        if (chunk + a.stages * step < chunks) copy(chunk + a.stages * step, stage);
+        if (++stage == a.stages) stage = 0, phase ^= 1;
+    }
+    if (!ok) gave_up_end(&gave_up, lane == 0 ? a.status : nullptr);
+    if constexpr (GRAD) {
+        if (a.dw || a.db) put_sums<Piece<V, U, GRAD, X, Y>, V, U>(a, p, reinterpret_cast<float*>(dynamic), blockDim.y);
+    }
+}
+
+// block_sums of up to 32 warps.
+template <int N>
+__device__ __forceinline__ void wide_sums(float (&s)[N], float (*part)[4])
+{
+    lane_sums(s, 32);
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) part[threadIdx.x >> 5][i] = s[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = part[threadIdx.x & 31][i];
+    lane_sums(s, 32);
 }
 
 // Wider rows: a block takes one, three times over, the later ones from the caches.
@@ -287,7 +496,7 @@ __global__ void __launch_bounds__(kWideThreads) wide_rows(const Args a)
 #pragma unroll
                 for (int q = 0; q < V; ++q) s1[0] += v[q] * scale;
             }
-            row_sums<1>(s1, part[0]);
+            wide_sums(s1, part[0]);
             const float m = s1[0] * inv_n;
             float s[GRAD ? 4 : 2] = {};
             for (int c = threadIdx.x * V; c < width; c += step) {
@@ -307,7 +516,7 @@ __global__ void __launch_bounds__(kWideThreads) wide_rows(const Args a)
                     }
                 }
             }
-            row_sums<GRAD ? 4 : 2>(s, part[1]);
+            wide_sums(s, part[1]);
             if (!again && !(s[1] <= kLargeSquares)) {
                 scale = kDown;
                 continue;
@@ -381,28 +590,50 @@ __global__ void __launch_bounds__(32 * kColumnRows) wide_columns(const Args a)
 }
 
 template <class X>
-int launch_rows(const Args& a, int y_dtype, int vector, const Shape& s, cudaStream_t st)
+int launch_rows(Args a, int y_dtype, bool vectors, const Shape& s, cudaStream_t st)
 {
     return with_type(y_dtype, [&](auto yt) {
         using Y = decltype(yt);
-        const auto go = [&](auto v, auto grad) {
+        const auto go = [&](auto v, auto grad) -> int {
             constexpr int V = decltype(v)::value;
             constexpr bool GRAD = decltype(grad)::value;
-            const dim3 block(s.tx, s.ty);
-            if (!s.per_thread) {
+            if (s.kind == kWideRows) {
                 if (int rc = launch_next(wide_rows<V, GRAD, X, Y>, s.blocks, kWideThreads, 0, st, 1, a)) return rc;
                 if constexpr (GRAD) {
                     if (a.dw || a.db)
                         return launch_next(wide_columns<V, X, Y>, dim3((a.width + 32 * V - 1) / (32 * V), s.chunks), dim3(32, kColumnRows), 0, st, 1, a);
                 }
-                return (int)EMB_OK;
+                return EMB_OK;
             }
-            const size_t smem = GRAD && s.ty > 1 ? (size_t)s.tx * s.ty * s.per_thread * sizeof(float) : 0;
-            return launch_next(s.per_thread == 8 ? norm_rows<V, 8 / V, GRAD, X, Y> : norm_rows<V, 16 / V, GRAD, X, Y>,
-                               s.blocks, block, smem, st, 1, a);
+            // a stage's rows: whole, or each from its own 16-byte boundary on
+            const auto slot = [&](int bytes, int64_t stride, bool& whole, int& pitch) {
+                whole = stride == a.width || a.chunk == 1;
+                pitch = (a.width * bytes + 15) / 16 * 16 + (V > 1 ? 0 : 16);
+                return whole ? ((a.chunk * a.width * bytes + 15) / 16 * 16 + (V > 1 ? 0 : 16)) : a.chunk * pitch;
+            };
+            const bool warps = s.kind == kWarpRows;
+            if (warps) {
+                // about 2 KB of a stage's rows, so that copies are long; a lane sends a row
+                const int at_once = 32 / s.tx, row_bytes = a.width * (int)(sizeof(X) + (GRAD ? sizeof(Y) : 0));
+                a.chunk = std::max(at_once, std::min(32, 2048 / row_bytes / at_once * at_once));
+            }
+            a.x_slot = slot(sizeof(X), a.x_stride, a.x_whole, a.x_pitch);
+            if (GRAD) a.g_slot = slot(sizeof(Y), a.g_stride, a.g_whole, a.g_pitch);
+            const int stage = (a.x_slot + a.g_slot) * (warps ? kThreads / 32 : 1);
+            a.stages = std::max(2, std::min(kMaxStages, (kSharedBytes / s.per_sm - kOwnBytes) / stage));
+            size_t smem = (size_t)a.stages * stage;
+            if (warps && GRAD) smem = std::max(smem, (size_t)kThreads * s.per_thread * sizeof(float));
+            const auto kernel = warps ? (s.per_thread == 8 ? warp_rows<V, 8 / V, GRAD, X, Y> : warp_rows<V, 16 / V, GRAD, X, Y>)
+                                      : (s.per_thread == 8 ? block_rows<V, 8 / V, GRAD, X, Y> : block_rows<V, 16 / V, GRAD, X, Y>);
+            if (smem + kOwnBytes > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+                cudaGetLastError();
+                return EMB_ERR_CUDA;
+            }
+            return launch_next(kernel, s.blocks, dim3(s.tx, s.ty), smem, st, 1, a);
         };
+        constexpr int kVector = sizeof(X) == 2 && sizeof(Y) == 2 ? 8 : 4;   // of fp32 16 bytes, so that lanes' loads meet no bank twice
         const auto with_v = [&](auto grad) {
-            return vector == 8 ? go(std::integral_constant<int, 8>(), grad) : go(std::integral_constant<int, 1>(), grad);
+            return vectors ? go(std::integral_constant<int, kVector>(), grad) : go(std::integral_constant<int, 1>(), grad);
         };
         return a.g ? with_v(std::true_type()) : with_v(std::false_type());
     });

@@ -5,7 +5,7 @@
 namespace emb {
 namespace norm {
 
-template int launch_rows<__half>(const Args&, int, int, const Shape&, cudaStream_t);
+template int launch_rows<__half>(Args, int, bool, const Shape&, cudaStream_t);
 
 }  // namespace norm
 }  // namespace emb

@@ -5,7 +5,7 @@
 namespace emb {
 namespace norm {
 
-template int launch_rows<float>(const Args&, int, int, const Shape&, cudaStream_t);
+template int launch_rows<float>(Args, int, bool, const Shape&, cudaStream_t);
 
 }  // namespace norm
 }  // namespace emb

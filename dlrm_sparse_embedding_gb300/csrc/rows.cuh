@@ -16,6 +16,8 @@ namespace emb {
 template <int V, class T>
 struct WordOf { using type = uint4; };
 template <class T>
+struct WordOf<4, T> { using type = typename std::conditional<sizeof(T) == 2, uint2, uint4>::type; };
+template <class T>
 struct WordOf<2, T> { using type = typename std::conditional<sizeof(T) == 2, uint32_t, uint2>::type; };
 template <class T>
 struct WordOf<1, T> { using type = T; };
@@ -33,6 +35,12 @@ struct Raw {
             if constexpr (V > 1) w[i] = __ldcs(reinterpret_cast<const Word*>(p) + i);
             else w[i] = p[i];
         }
+    }
+    // from shared memory
+    __device__ __forceinline__ void load_shared(const T* p)
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const Word*>(p)[i];
     }
     __device__ __forceinline__ float operator[](int i) const { return to_float<T>(reinterpret_cast<const T*>(w)[i]); }
 };
