@@ -28,15 +28,14 @@ Shape shape_of(int64_t rows, int64_t width, bool grad)
         return s;
     }
     s.kind = width <= kWarpWidth ? kWarpRows : kBlockRows;
-    s.per_thread = width <= 256 || (width > kWarpWidth && width <= 2048) ? 8 : 16;
-    const int threads = (int)((width + s.per_thread - 1) / s.per_thread);
+    const int threads = (int)((width + kPerThread - 1) / kPerThread);
     if (s.kind == kWarpRows) {
         for (s.tx = 1; s.tx < threads;) s.tx *= 2;
         s.ty = kThreads / s.tx;
     } else {
         s.tx = (threads + 31) / 32 * 32, s.ty = 1;
     }
-    s.per_sm = std::max(1, std::min(8, 65536 / (registers(s.per_thread, grad) * s.tx * s.ty)));
+    s.per_sm = std::max(1, std::min(8, 65536 / (registers(grad) * s.tx * s.ty)));
     if (s.kind == kBlockRows) s.per_sm = std::max(1, std::min(s.per_sm, kSharedBytes / (int)(3 * width * (grad ? 8 : 4) + kOwnBytes)));
     s.blocks = (int)std::min<int64_t>((rows + s.ty - 1) / s.ty, (int64_t)kSms * s.per_sm);
     return s;

@@ -54,21 +54,21 @@ struct Args {
 enum Kind { kWarpRows, kBlockRows, kWideRows };
 struct Shape {
     Kind kind;
-    int per_thread;        // elements of a row a thread holds: 8 or 16 (not of wide rows)
     int tx, ty;            // threads a row; rows a block
     int blocks, per_sm;
     int chunks;            // wide rows' gradients: parts the rows are added up in
 };
 
 constexpr int kThreads = 256, kMaxThreads = 512, kWideThreads = 1024;
-constexpr int kWarpWidth = 16 * 32;              // the widest row of a warp's lanes
-constexpr int kRegisterWidth = 16 * kMaxThreads; // the widest row kept in registers
+constexpr int kPerThread = 16;                   // elements of a row a thread holds
+constexpr int kWarpWidth = kPerThread * 32;      // the widest row of a warp's lanes
+constexpr int kRegisterWidth = kPerThread * kMaxThreads; // the widest row kept in registers
 constexpr int kMaxStages = 8;
 constexpr int kSharedBytes = 226 * 1024;         // of an SM, for its blocks
 constexpr int kOwnBytes = 2560;                  // of a block beside its stages
 constexpr int kColumnRows = 8;                   // rows at a time of a block of wide_columns
 // Registers a thread: what its elements take.
-constexpr int registers(int per_thread, bool grad) { return per_thread == 16 ? (grad ? 128 : 80) : grad ? 80 : 64; }
+constexpr int registers(bool grad) { return grad ? 128 : 80; }
 
 // One translation unit for each type of x.  `vectors`: rows of both types are whole
 // vectors, all at 16-byte boundaries.
@@ -92,33 +92,95 @@ __device__ __forceinline__ void store_param(void* p, int dtype, int64_t i, float
     else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
-// s, summed over the lanes of a row (a power of two of them), in all of them.
+// s, summed over `lanes` lanes (a power of two), in all of them.  The lanes first share the
+// values out, each half of them going on with half of the values, so that N values
+// take N - 1 + log2(lanes / N) exchanges and N to hand them back instead of N log2(lanes).
 template <int N>
 __device__ __forceinline__ void lane_sums(float (&s)[N], int lanes)
 {
+    constexpr uint32_t kAll = 0xffffffffu;
+    const int lane = threadIdx.x + threadIdx.y * blockDim.x;
+    if (N == 1 || lanes < 2 * N) {
 #pragma unroll
-    for (int d = 16; d; d >>= 1)
-        if (d < lanes)
+        for (int d = 16; d; d >>= 1)
+            if (d < lanes)
 #pragma unroll
-            for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
+                for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(kAll, s[i], d);
+        return;
+    }
+    float v = 0.f;
+    if constexpr (N == 4) {
+        const bool up = lane & 2, odd = lane & 1;
+        float p = up ? s[2] : s[0], q = up ? s[3] : s[1];
+        p += __shfl_xor_sync(kAll, up ? s[0] : s[2], 2);
+        q += __shfl_xor_sync(kAll, up ? s[1] : s[3], 2);
+        v = (odd ? q : p) + __shfl_xor_sync(kAll, odd ? p : q, 1);
+    } else if constexpr (N == 2) {
+        const bool odd = lane & 1;
+        v = (odd ? s[1] : s[0]) + __shfl_xor_sync(kAll, odd ? s[0] : s[1], 1);
+    }
+#pragma unroll
+    for (int d = 16; d >= N; d >>= 1)
+        if (d < lanes) v += __shfl_xor_sync(kAll, v, d);
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = __shfl_sync(kAll, v, (lane & 31 & ~(N - 1)) | i);   // value i is lane i's of every N
 }
 
-// The same over a block.  Two calls in turn on two buffers need no barrier more: the other
-// call's lies between.
+// The same over a block of at most 16 warps.  Two calls in turn on two buffers need no
+// barrier more: the other call's lies between.
 template <int N>
 __device__ __forceinline__ void block_sums(float (&s)[N], float (*part)[4])
 {
     lane_sums(s, 32);
-    const int warps = blockDim.x >> 5;
-    if ((threadIdx.x & 31) == 0)
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (lane == 0)
 #pragma unroll
         for (int i = 0; i < N; ++i) part[threadIdx.x >> 5][i] = s[i];
     __syncthreads();
-    const int from = threadIdx.x & 15;     // of at most 16 warps, twice
+    // lane (w, i) adds up warps w, w + 32 / N, ...
+    const int i = lane & (N - 1);
+    float v = 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = from < warps ? part[from][i] : 0.f;
-    lane_sums(s, 16);
+    for (int w = 0; w < 16; w += 32 / N)
+        if (w + lane / N < warps) v += part[w + lane / N][i];
+#pragma unroll
+    for (int d = 16; d >= N; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+#pragma unroll
+    for (int j = 0; j < N; ++j) s[j] = __shfl_sync(0xffffffffu, v, (lane & ~(N - 1)) | j);
 }
+
+// Two fp32 numbers that one instruction takes.
+struct Two {
+    uint64_t bits;
+    __device__ __forceinline__ Two() = default;
+    __device__ __forceinline__ Two(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(bits) : "f"(x), "f"(y)); }
+    __device__ __forceinline__ explicit Two(float x) : Two(x, x) {}
+    __device__ __forceinline__ float2 both() const
+    {
+        float2 r;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(bits));
+        return r;
+    }
+};
+__device__ __forceinline__ Two operator+(Two a, Two b)
+{
+    Two r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.bits) : "l"(a.bits), "l"(b.bits));
+    return r;
+}
+__device__ __forceinline__ Two operator*(Two a, Two b)
+{
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.bits) : "l"(a.bits), "l"(b.bits));
+    return r;
+}
+__device__ __forceinline__ Two fma(Two a, Two b, Two c)
+{
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.bits) : "l"(a.bits), "l"(b.bits), "l"(c.bits));
+    return r;
+}
+__device__ __forceinline__ float sum(Two a) { const float2 v = a.both(); return v.x + v.y; }
 
 // Squares up to here are summed as they are; a row beyond is scaled.
 constexpr float kLargeSquares = 0x1p100f, kDown = 0x1p-80f;
@@ -128,6 +190,13 @@ struct Moments {
     __device__ __forceinline__ float h(float x) const { return __fmaf_rn(x * scale - m, rstd, -d * rstd); }
 };
 
+// 1 / sqrt(v): the approximation and one step of Newton's method, within 2^-23.
+__device__ __forceinline__ float root(float v)
+{
+    const float r = rsqrtf(v);
+    return __fmaf_rn(0.5f * r, __fmaf_rn(-v * r, r, 1.f), r);
+}
+
 __device__ __forceinline__ Moments moments(float m, float shifted, float squares, float inv_n, float eps, float scale)
 {
     Moments r;
@@ -135,7 +204,7 @@ __device__ __forceinline__ Moments moments(float m, float shifted, float squares
     r.d = shifted * inv_n;
     const float var = fmaxf(squares * inv_n - r.d * r.d, 0.f) + eps * scale * scale;
     // fmaxf drops a NaN: rows that hold one, or an infinity, are NaN all over
-    r.rstd = squares == squares ? (var > 0.f ? 1.f / sqrtf(var) : 0.f) : squares;
+    r.rstd = squares == squares ? (var > 0.f ? root(var) : 0.f) : squares;
     r.scale = scale;
     return r;
 }
@@ -143,7 +212,8 @@ __device__ __forceinline__ Moments moments(float m, float shifted, float squares
 // What a thread holds of a row, U vectors of V, and adds up over rows.
 template <int V, int U, bool GRAD, class X, class Y>
 struct Piece {
-    float v[U][V], g[U][V], w[U][V], b[U][V], acc_w[U][V], acc_b[U][V];
+    static constexpr int E = U * V;
+    Two v[E / 2], g[E / 2], w[E / 2], b[E / 2], acc_w[E / 2], acc_b[E / 2];
     int first, step, width;    // its columns: V from first + u * step on
 
     __device__ __forceinline__ bool in(int u) const { return first + u * step < width; }
@@ -151,106 +221,121 @@ struct Piece {
     __device__ __forceinline__ void open(const Args& a, int tx, int threads)
     {
         first = tx * V, step = threads * V, width = a.width;
+        const auto get = [&](const void* p, int e, float none) { return in(e / V) ? param(p, a.param_dtype, first + e / V * step + e % V, none) : 0.f; };
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int q = 0; q < V; ++q) {
-                w[u][q] = in(u) ? param(a.weight, a.param_dtype, first + u * step + q, 1.f) : 0.f;
-                if (!GRAD) b[u][q] = in(u) ? param(a.bias, a.param_dtype, first + u * step + q, 0.f) : 0.f;
-                acc_w[u][q] = acc_b[u][q] = 0.f;
-            }
-    }
-
-    // Takes the row from shared memory.
-    __device__ __forceinline__ void take(const X* x, const Y* gy, bool has)
-    {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            Raw<V, X> rx;
-            Raw<V, Y> rg;
-            if (has && in(u)) {
-                rx.load_shared(x + first + u * step);
-                if (GRAD) rg.load_shared(gy + first + u * step);
-            }
-#pragma unroll
-            for (int q = 0; q < V; ++q) {
-                v[u][q] = has && in(u) ? rx[q] : 0.f;
-                if (GRAD) g[u][q] = has && in(u) ? rg[q] : 0.f;
-            }
+        for (int e = 0; e < E; e += 2) {
+            w[e / 2] = Two(get(a.weight, e, 1.f), get(a.weight, e + 1, 1.f));
+            if (!GRAD) b[e / 2] = Two(get(a.bias, e, 0.f), get(a.bias, e + 1, 0.f));
+            acc_w[e / 2] = acc_b[e / 2] = Two(0.f);
         }
     }
 
-    // The row's results.  first_sums and second_sums add up over its threads;
-    // any(flag) tells whether a row's of all that add up together is set.
+    template <class T>
+    __device__ __forceinline__ void take(const T* p, bool has, Two (&to)[E / 2])
+    {
+        Raw<V, T> r[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            r[u].clear();
+            if (has && in(u)) r[u].load_shared(p + first + u * step);
+        }
+#pragma unroll
+        for (int e = 0; e < E; e += 2) to[e / 2] = Two(r[e / V][e % V], r[(e + 1) / V][(e + 1) % V]);
+    }
+
+    // A row in shared memory and its results.  first_sums and second_sums add up over the
+    // row's threads; any(flag) tells whether a row's of all that add up together is set.
     template <class S1, class S2, class ANY>
-    __device__ __forceinline__ void finish(const Args& a, int64_t row, bool has, float inv_n, S1 first_sums, S2 second_sums, ANY any)
+    __device__ __forceinline__ void row(const Args& a, const X* x, const Y* gy, int64_t row, bool has, float inv_n, S1 first_sums, S2 second_sums, ANY any)
     {
         constexpr int N = GRAD ? 4 : 2;
+        take(x, has, v);
+        if constexpr (GRAD) take(gy, has, g);
         Moments mo;
         float scale = 1.f, s[N];
         for (;;) {
-            float s1[1] = {};
+            Two t = v[0];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int q = 0; q < V; ++q) s1[0] += v[u][q];
+            for (int i = 1; i < E / 2; ++i) t = t + v[i];
+            float s1[1] = {sum(t)};
             first_sums(s1);
             mo.m = s1[0] * inv_n;
+            const Two minus(-mo.m);
+            Two s0(0.f), sq(0.f), sg(0.f), sgc(0.f);
+            const auto add = [&](int i) {
+                s0 = s0 + v[i];
+                sq = fma(v[i], v[i], sq);
+                if constexpr (GRAD) {
+                    const Two gw = g[i] * w[i];
+                    sg = sg + gw;
+                    sgc = fma(gw, v[i], sgc);
+                }
+            };
+            if constexpr (V > 1) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) s[i] = 0.f;
+                for (int u = 0; u < U; ++u)
+                    if (in(u)) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (in(u)) {
-#pragma unroll
-                    for (int q = 0; q < V; ++q) {
-                        const float c = v[u][q] - mo.m;
-                        s[0] += c;
-                        s[1] = __fmaf_rn(c, c, s[1]);
-                        if constexpr (GRAD) {
-                            const float gw = g[u][q] * w[u][q];
-                            s[2] += gw;
-                            s[3] = __fmaf_rn(gw, c, s[3]);
+                        for (int i = u * V / 2; i < (u + 1) * V / 2; ++i) {
+                            v[i] = v[i] + minus;
+                            add(i);
                         }
                     }
+            } else {
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) {
+                    const float2 c = (v[i] + minus).both();
+                    v[i] = Two(in(2 * i) ? c.x : 0.f, in(2 * i + 1) ? c.y : 0.f);
+                    add(i);
                 }
+            }
+            s[0] = sum(s0), s[1] = sum(sq);
+            if constexpr (GRAD) s[2] = sum(sg), s[3] = sum(sgc);
             second_sums(s);
             const bool large = scale == 1.f && !(s[1] <= kLargeSquares);
             if (!any(large)) break;
-            if (large) {     // once more, smaller
-                scale = kDown;
+            // once more, those rows smaller
+            if (large) scale = kDown;
+            take(x, has, v);
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int q = 0; q < V; ++q) v[u][q] *= kDown;
-            }
+            for (int i = 0; i < E / 2; ++i) v[i] = v[i] * Two(scale);
         }
         mo = moments(mo.m, s[0], s[1], inv_n, a.eps, scale);
-        const float shift = -mo.d * mo.rstd;
-        float k1 = 0.f, k2 = 0.f, k3 = 0.f;     // dx = k1 g w + k2 h + k3
+        const Two rstd(mo.rstd), shift(-mo.d * mo.rstd);
+        Two k1, k2, k3;     // dx = k1 g w + k2 h + k3
         if constexpr (GRAD) {
-            k1 = mo.rstd * scale;
-            k2 = -k1 * ((s[3] - mo.d * s[2]) * mo.rstd * inv_n);
-            k3 = -k1 * (s[2] * inv_n);
+            const float k = mo.rstd * scale;
+            k1 = Two(k);
+            k2 = Two(-k * ((s[3] - mo.d * s[2]) * mo.rstd * inv_n));
+            k3 = Two(-k * (s[2] * inv_n));
         }
+        float o[E];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float o[V];
-#pragma unroll
-            for (int q = 0; q < V; ++q) {
-                const float h = __fmaf_rn(v[u][q] - mo.m, mo.rstd, shift);
-                if constexpr (GRAD) {
-                    acc_w[u][q] = __fmaf_rn(g[u][q], h, acc_w[u][q]);
-                    acc_b[u][q] += g[u][q];
-                    o[q] = __fmaf_rn(g[u][q] * w[u][q], k1, __fmaf_rn(h, k2, k3));
-                } else {
-                    o[q] = __fmaf_rn(h, w[u][q], b[u][q]);
-                }
+        for (int i = 0; i < E / 2; ++i) {
+            const Two h = fma(v[i], rstd, shift);
+            Two r;
+            if constexpr (GRAD) {
+                acc_w[i] = fma(g[i], h, acc_w[i]);
+                acc_b[i] = acc_b[i] + g[i];
+                r = fma(g[i] * w[i], k1, fma(h, k2, k3));
+            } else {
+                r = fma(h, w[i], b[i]);
             }
-            if (has && in(u) && a.out) {
-                if constexpr (GRAD) store_vec<V, X>(static_cast<X*>(a.out) + row * width + first + u * step, o);
-                else store_vec<V, Y>(static_cast<Y*>(a.out) + row * width + first + u * step, o);
-            }
+            const float2 both = r.both();
+            o[2 * i] = both.x, o[2 * i + 1] = both.y;
         }
+        if (!has || !a.out) return;
+        using O = typename std::conditional<GRAD, X, Y>::type;
+        O* const out = static_cast<O*>(a.out) + row * width + first;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (in(u)) store_vec<V, O>(out + u * step, reinterpret_cast<const float(&)[V]>(o[u * V]));
+    }
+
+    __device__ __forceinline__ float sum_of(int which, int e) const
+    {
+        const float2 both = (which ? acc_b[e / 2] : acc_w[e / 2]).both();
+        return e & 1 ? both.y : both.x;
     }
 };
 
@@ -291,7 +376,7 @@ __device__ __forceinline__ void put_sums(const Args& a, const PIECE& p, float* s
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int q = 0; q < V; ++q) shared[threadIdx.y * cols + p.first + u * p.step + q] = which ? p.acc_b[u][q] : p.acc_w[u][q];
+                for (int q = 0; q < V; ++q) shared[threadIdx.y * cols + p.first + u * p.step + q] = p.sum_of(which, u * V + q);
             __syncthreads();
             for (int c = thread; c < a.width; c += threads) {
                 float sum = 0.f;
@@ -303,17 +388,17 @@ __device__ __forceinline__ void put_sums(const Args& a, const PIECE& p, float* s
             for (int u = 0; u < U; ++u)
                 if (p.in(u)) {
 #pragma unroll
-                    for (int q = 0; q < V; ++q) put(which, p.first + u * p.step + q, which ? p.acc_b[u][q] : p.acc_w[u][q]);
+                    for (int q = 0; q < V; ++q) put(which, p.first + u * p.step + q, p.sum_of(which, u * V + q));
                 }
         }
     }
 }
 
 // Rows of kWarpWidth < width <= kRegisterWidth: a block takes one at a time.  Its rows are
-// copied to a ring of stages; a stage is free for the next row when the first sums'
+// copied to a ring of stages; a stage is free for the next row when the second sums'
 // barrier has been met.
 template <int V, int U, bool GRAD, class X, class Y>
-__global__ void __maxnreg__(registers(U * V, GRAD)) block_rows(const Args a)
+__global__ void __maxnreg__(registers(GRAD)) block_rows(const Args a)
 {
     __shared__ float part[2][32][4];
     __shared__ uint64_t full[kMaxStages];
@@ -356,17 +441,12 @@ __global__ void __maxnreg__(registers(U * V, GRAD)) block_rows(const Args a)
         const unsigned char* const at = dynamic + stage * (a.x_slot + a.g_slot);
         const uint32_t skip_x = V > 1 ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(x + row * a.x_stride) & 15);
         const uint32_t skip_g = V > 1 || !GRAD ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(g + row * a.g_stride) & 15);
-        p.take(reinterpret_cast<const X*>(at + skip_x), reinterpret_cast<const Y*>(at + a.x_slot + skip_g), true);
-        bool taken = false;
-        p.finish(
-            a, row, true, inv_n,
-            [&](auto& s) {
-                block_sums(s, part[0]);
-                const int64_t next = row + (int64_t)a.stages * gridDim.x;
-                if (threadIdx.x == 0 && !taken && next < a.rows) copy(next, stage);
-                taken = true;
-            },
-            [&](auto& s) { block_sums(s, part[1]); }, [](bool large) { return large; });
+        p.row(
+            a, reinterpret_cast<const X*>(at + skip_x), reinterpret_cast<const Y*>(at + a.x_slot + skip_g), row, true, inv_n,
+            [&](auto& s) { block_sums(s, part[0]); }, [&](auto& s) { block_sums(s, part[1]); }, [](bool large) { return large; });
+        // every thread has taken the row for good: the second sums' barrier has been met
+        const int64_t next = row + (int64_t)a.stages * gridDim.x;
+        if (threadIdx.x == 0 && next < a.rows) copy(next, stage);
         if (++stage == a.stages) stage = 0, phase ^= 1;
     }
     if (!ok) {
@@ -381,7 +461,7 @@ __global__ void __maxnreg__(registers(U * V, GRAD)) block_rows(const Args a)
 // Rows of up to kWarpWidth: some lanes take one, a warp several, and each warp has its
 // own ring of stages, of a.chunk rows each.  No warp waits for another.
 template <int V, int U, bool GRAD, class X, class Y>
-__global__ void __maxnreg__(registers(U * V, GRAD)) warp_rows(const Args a)
+__global__ void __maxnreg__(registers(GRAD)) warp_rows(const Args a)
 {
     constexpr int kWarps = kThreads / 32;
     __shared__ uint64_t full[kWarps][kMaxStages];
@@ -445,9 +525,9 @@ __global__ void __maxnreg__(registers(U * V, GRAD)) warp_rows(const Args a)
         for (int i = sub; i < a.chunk; i += at_once) {
             const int64_t row = first + i;
             const bool has = row < a.rows;
-            p.take(place(x, a.x_stride, a.x_whole, a.x_pitch, at, first, i), place(g, a.g_stride, a.g_whole, a.g_pitch, at + a.x_slot, first, i), has);
-            p.finish(
-                a, row, has, inv_n, [&](auto& s) { lane_sums(s, lanes); }, [&](auto& s) { lane_sums(s, lanes); },
+            p.row(
+                a, place(x, a.x_stride, a.x_whole, a.x_pitch, at, first, i), place(g, a.g_stride, a.g_whole, a.g_pitch, at + a.x_slot, first, i), row, has,
+                inv_n, [&](auto& s) { lane_sums(s, lanes); }, [&](auto& s) { lane_sums(s, lanes); },
                 [](bool large) { return __any_sync(0xffffffffu, large) != 0; });
         }
         __syncwarp();
@@ -622,9 +702,8 @@ int launch_rows(Args a, int y_dtype, bool vectors, const Shape& s, cudaStream_t 
             const int stage = (a.x_slot + a.g_slot) * (warps ? kThreads / 32 : 1);
             a.stages = std::max(2, std::min(kMaxStages, (kSharedBytes / s.per_sm - kOwnBytes) / stage));
             size_t smem = (size_t)a.stages * stage;
-            if (warps && GRAD) smem = std::max(smem, (size_t)kThreads * s.per_thread * sizeof(float));
-            const auto kernel = warps ? (s.per_thread == 8 ? warp_rows<V, 8 / V, GRAD, X, Y> : warp_rows<V, 16 / V, GRAD, X, Y>)
-                                      : (s.per_thread == 8 ? block_rows<V, 8 / V, GRAD, X, Y> : block_rows<V, 16 / V, GRAD, X, Y>);
+            if (warps && GRAD) smem = std::max(smem, (size_t)kThreads * kPerThread * sizeof(float));
+            const auto kernel = warps ? warp_rows<V, kPerThread / V, GRAD, X, Y> : block_rows<V, kPerThread / V, GRAD, X, Y>;
             if (smem + kOwnBytes > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
                 cudaGetLastError();
                 return EMB_ERR_CUDA;

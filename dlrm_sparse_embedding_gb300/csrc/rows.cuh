@@ -36,6 +36,11 @@ struct Raw {
             else w[i] = p[i];
         }
     }
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = Word{};
+    }
     // from shared memory
     __device__ __forceinline__ void load_shared(const T* p)
     {
