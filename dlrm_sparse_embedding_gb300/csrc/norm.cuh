@@ -55,20 +55,21 @@ enum Kind { kWarpRows, kBlockRows, kWideRows };
 struct Shape {
     Kind kind;
     int tx, ty;            // threads a row; rows a block
+    int per_thread;        // elements of a row a thread holds
     int blocks, per_sm;
     int chunks;            // wide rows' gradients: parts the rows are added up in
 };
 
 constexpr int kThreads = 256, kMaxThreads = 512, kWideThreads = 1024;
-constexpr int kPerThread = 16;                   // elements of a row a thread holds
-constexpr int kWarpWidth = kPerThread * 32;      // the widest row of a warp's lanes
-constexpr int kRegisterWidth = kPerThread * kMaxThreads; // the widest row kept in registers
+// Elements of a row a thread holds: 16, and 32 of longer rows where only the forward's two
+// parameters are held beside them and elements come in vectors.
+constexpr int kFew = 16, kMany = 32;
 constexpr int kMaxStages = 8;
 constexpr int kSharedBytes = 226 * 1024;         // of an SM, for its blocks
 constexpr int kOwnBytes = 2560;                  // of a block beside its stages
 constexpr int kColumnRows = 8;                   // rows at a time of a block of wide_columns
 // Registers a thread: what its elements take.
-constexpr int registers(bool grad) { return grad ? 128 : 80; }
+constexpr int registers(int per_thread, bool grad, bool vectors) { return grad || per_thread == kMany ? 128 : vectors ? 80 : 96; }
 
 // One translation unit for each type of x.  `vectors`: rows of both types are whole
 // vectors, all at 16-byte boundaries.
@@ -210,7 +211,7 @@ __device__ __forceinline__ Moments moments(float m, float shifted, float squares
 }
 
 // What a thread holds of a row, U vectors of V, and adds up over rows.
-template <int V, int U, bool GRAD, class X, class Y>
+template <int V, int U, bool GRAD, bool BLOCK, class X, class Y>
 struct Piece {
     static constexpr int E = U * V;
     Two v[E / 2], g[E / 2], w[E / 2], b[E / 2], acc_w[E / 2], acc_b[E / 2];
@@ -260,7 +261,6 @@ struct Piece {
             float s1[1] = {sum(t)};
             first_sums(s1);
             mo.m = s1[0] * inv_n;
-            const Two minus(-mo.m);
             Two s0(0.f), sq(0.f), sg(0.f), sgc(0.f);
             const auto add = [&](int i) {
                 s0 = s0 + v[i];
@@ -273,18 +273,21 @@ struct Piece {
             };
             if constexpr (V > 1) {
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (in(u)) {
+                for (int u = 0; u < U; ++u) {
+                    // where there is nothing, zero stays zero; a block's gradient is faster without the
+                    // branch (16384 x 3328, fp32 to bf16: 97 and 88 us), a warp's with it (425984 x 128: 93 and 105)
+                    const Two less(in(u) ? -mo.m : 0.f);
+                    if (!BLOCK && !in(u)) continue;
 #pragma unroll
-                        for (int i = u * V / 2; i < (u + 1) * V / 2; ++i) {
-                            v[i] = v[i] + minus;
-                            add(i);
-                        }
+                    for (int i = u * V / 2; i < (u + 1) * V / 2; ++i) {
+                        v[i] = v[i] + less;
+                        add(i);
                     }
+                }
             } else {
 #pragma unroll
                 for (int i = 0; i < E / 2; ++i) {
-                    const float2 c = (v[i] + minus).both();
+                    const float2 c = (v[i] + Two(-mo.m)).both();
                     v[i] = Two(in(2 * i) ? c.x : 0.f, in(2 * i + 1) ? c.y : 0.f);
                     add(i);
                 }
@@ -394,11 +397,11 @@ __device__ __forceinline__ void put_sums(const Args& a, const PIECE& p, float* s
     }
 }
 
-// Rows of kWarpWidth < width <= kRegisterWidth: a block takes one at a time.  Its rows are
+// Longer rows: a block takes one at a time.  Its rows are
 // copied to a ring of stages; a stage is free for the next row when the second sums'
 // barrier has been met.
 template <int V, int U, bool GRAD, class X, class Y>
-__global__ void __maxnreg__(registers(GRAD)) block_rows(const Args a)
+__global__ void __maxnreg__(registers(U * V, GRAD, V > 1)) block_rows(const Args a)
 {
     __shared__ float part[2][32][4];
     __shared__ uint64_t full[kMaxStages];
@@ -431,7 +434,7 @@ __global__ void __maxnreg__(registers(GRAD)) block_rows(const Args a)
     if (threadIdx.x == 0)
         for (int i = 0; i < a.stages; ++i)
             if (blockIdx.x + (int64_t)i * gridDim.x < a.rows) copy(blockIdx.x + (int64_t)i * gridDim.x, i);
-    Piece<V, U, GRAD, X, Y> p;
+    Piece<V, U, GRAD, true, X, Y> p;
     p.open(a, threadIdx.x, blockDim.x);
     int stage = 0;
     uint32_t phase = 0;
@@ -454,14 +457,14 @@ __global__ void __maxnreg__(registers(GRAD)) block_rows(const Args a)
         return;
     }
     if constexpr (GRAD) {
-        if (a.dw || a.db) put_sums<Piece<V, U, GRAD, X, Y>, V, U>(a, p, nullptr, 1);
+        if (a.dw || a.db) put_sums<Piece<V, U, GRAD, true, X, Y>, V, U>(a, p, nullptr, 1);
     }
 }
 
-// Rows of up to kWarpWidth: some lanes take one, a warp several, and each warp has its
+// Rows that some lanes, or all of a warp's, can hold: some lanes take one, a warp several, and each warp has its
 // own ring of stages, of a.chunk rows each.  No warp waits for another.
 template <int V, int U, bool GRAD, class X, class Y>
-__global__ void __maxnreg__(registers(GRAD)) warp_rows(const Args a)
+__global__ void __maxnreg__(registers(U * V, GRAD, V > 1)) warp_rows(const Args a)
 {
     constexpr int kWarps = kThreads / 32;
     __shared__ uint64_t full[kWarps][kMaxStages];
@@ -513,7 +516,7 @@ __global__ void __maxnreg__(registers(GRAD)) warp_rows(const Args a)
     const int64_t mine = (int64_t)blockIdx.x * kWarps + warp;
     for (int i = 0; i < a.stages; ++i)
         if (mine + i * step < chunks) copy(mine + i * step, i);
-    Piece<V, U, GRAD, X, Y> p;
+    Piece<V, U, GRAD, false, X, Y> p;
     p.open(a, lane % lanes, lanes);
     int stage = 0;
     uint32_t phase = 0;
@@ -536,7 +539,7 @@ __global__ void __maxnreg__(registers(GRAD)) warp_rows(const Args a)
     }
     if (!ok) gave_up_end(&gave_up, lane == 0 ? a.status : nullptr);
     if constexpr (GRAD) {
-        if (a.dw || a.db) put_sums<Piece<V, U, GRAD, X, Y>, V, U>(a, p, reinterpret_cast<float*>(dynamic), blockDim.y);
+        if (a.dw || a.db) put_sums<Piece<V, U, GRAD, false, X, Y>, V, U>(a, p, reinterpret_cast<float*>(dynamic), blockDim.y);
     }
 }
 
@@ -702,8 +705,11 @@ int launch_rows(Args a, int y_dtype, bool vectors, const Shape& s, cudaStream_t 
             const int stage = (a.x_slot + a.g_slot) * (warps ? kThreads / 32 : 1);
             a.stages = std::max(2, std::min(kMaxStages, (kSharedBytes / s.per_sm - kOwnBytes) / stage));
             size_t smem = (size_t)a.stages * stage;
-            if (warps && GRAD) smem = std::max(smem, (size_t)kThreads * kPerThread * sizeof(float));
-            const auto kernel = warps ? warp_rows<V, kPerThread / V, GRAD, X, Y> : block_rows<V, kPerThread / V, GRAD, X, Y>;
+            if (warps && GRAD) smem = std::max(smem, (size_t)kThreads * kFew * sizeof(float));
+            constexpr int kLong = GRAD || V == 1 ? kFew : kMany;
+            const bool few = s.per_thread == kFew;
+            const auto kernel = warps ? (few ? warp_rows<V, kFew / V, GRAD, X, Y> : warp_rows<V, kLong / V, GRAD, X, Y>)
+                                      : (few ? block_rows<V, kFew / V, GRAD, X, Y> : block_rows<V, kLong / V, GRAD, X, Y>);
             if (smem + kOwnBytes > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
                 cudaGetLastError();
                 return EMB_ERR_CUDA;
