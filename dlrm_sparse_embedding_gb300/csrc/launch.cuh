@@ -11,7 +11,8 @@ namespace emb {
 
 // Every thread of every kernel launched with launch_next calls this before its
 // first access to global memory: returns once all earlier work of the stream is
-// done and visible.
+// done and visible.  (Where the kernel before lets the next one begin only after its own
+// wait, what stood before that kernel may be read before this one's.)
 __device__ __forceinline__ void wait_for_earlier() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // The stream's next kernel may begin to set itself up.

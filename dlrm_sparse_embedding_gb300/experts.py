@@ -20,11 +20,12 @@ from typing import Optional
 
 import torch
 
-from ._lib import DTYPES, EmbExpertPlan, check, lib
+from ._lib import ACTIVATIONS, DTYPES, EmbExpertPlan, check, lib
 
 _DTYPE_CODE = {torch.float32: DTYPES["f32"], torch.float16: DTYPES["f16"], torch.bfloat16: DTYPES["bf16"]}
 MAX_EXPERTS = 1024
 MAX_EXPERTS_PER_TOKEN = 64
+MAX_LAYER_ASSIGNMENTS = 512   # of expert_layer
 SORT_ALONE = 4096   # assignments up to which a sort leaves its workspace alone
 
 
@@ -304,6 +305,83 @@ def expert_linear_grad(plan: ExpertPlan, grad_y: torch.Tensor, rows: Optional[to
                                                 grad_weight.data_ptr(), _stream(device)),
               "emb_expert_linear_grad_weight")
     return grad_rows, grad_weight
+
+
+@functools.lru_cache(maxsize=256)
+def _layer_workspace(tokens: int, k: int, hidden: int, out: int) -> int:
+    n = ctypes.c_size_t()
+    check(lib.emb_expert_layer_workspace(tokens, k, hidden, out, ctypes.byref(n)), "emb_expert_layer_workspace")
+    return n.value
+
+
+def expert_layer(ids: torch.Tensor, x: torch.Tensor, up: torch.Tensor, down: torch.Tensor, weights: torch.Tensor,
+                 activation: str = "relu", dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+    """[tokens, out] in `dtype` (default up's): the whole expert layer for a few tokens,
+    sum_j weights[t, j] down[e] act(up[e] x[t]) with e = ids[t, j], in two kernels.
+
+    What expert_sort, expert_dispatch, expert_linear, the activation, expert_linear and
+    expert_combine give, but that the second product's rows stay fp32 up to the sum; up to
+    512 assignments (tokens * k), bound by the chosen experts' weights.
+
+    ids: int32 or int64 [tokens, k], -1 for none (others out of range are reported by
+    dense_status()).  x: float32 or up's dtype [tokens, in], any row stride of whole 16
+    bytes.  up: float16 or bfloat16 [E, hidden, in], for "swiglu" [E, 2 * hidden, in] with the
+    gates' rows first; down: [E, out, hidden]; weights: float32 [tokens, k].
+    activation: "relu", "silu", "gelu" or "swiglu"."""
+    if stream is not None:
+        return _on(stream, expert_layer, ids, x, up, down, weights, activation, dtype)
+    if not isinstance(ids, torch.Tensor) or ids.dtype not in (torch.int32, torch.int64) or ids.dim() != 2 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int32 or int64 tensor [tokens, k]")
+    if not ids.is_cuda:
+        raise ValueError("ids must be a CUDA tensor")
+    device = ids.device
+    T, k = ids.shape
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError("activation must be one of %s, got %r" % (", ".join(ACTIVATIONS), activation))
+    if not 1 <= k <= MAX_EXPERTS_PER_TOKEN or T * k > MAX_LAYER_ASSIGNMENTS:
+        raise ValueError("1 to %d experts a token and up to %d assignments are supported, got %d and %d: more tokens go through "
+                         "expert_sort" % (MAX_EXPERTS_PER_TOKEN, MAX_LAYER_ASSIGNMENTS, k, T * k))
+    for name, w in (("up", up), ("down", down)):
+        if not isinstance(w, torch.Tensor) or w.dtype not in (torch.float16, torch.bfloat16) or w.dim() != 3 or not w.is_contiguous():
+            raise ValueError("%s must be a contiguous float16 or bfloat16 tensor of 3 dimensions" % name)
+        if w.device != device:
+            raise ValueError("%s is on %s, ids on %s" % (name, w.device, device))
+        if w.data_ptr() % 16:
+            raise ValueError("%s must be 16-byte aligned" % name)
+    E, rows, D = up.shape
+    N, H = down.shape[1:]
+    if down.dtype != up.dtype or down.shape[0] != E or rows != (2 * H if activation == "swiglu" else H):
+        raise ValueError("up %s of %s and down %s of %s do not belong together for %s"
+                         % (tuple(up.shape), up.dtype, tuple(down.shape), down.dtype, activation))
+    if not 1 <= E <= MAX_EXPERTS or min(D, H, N) < 8 or D % 8 or H % 8 or N % 8:
+        raise ValueError("1 to %d experts and widths that are multiples of 8 are supported, got up %s and down %s"
+                         % (MAX_EXPERTS, tuple(up.shape), tuple(down.shape)))
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape != (T, D) or x.dtype not in (torch.float32, up.dtype):
+        raise ValueError("x must be float32 or %s [%d, %d]" % (up.dtype, T, D))
+    if x.device != device:
+        raise ValueError("x is on %s, ids on %s" % (x.device, device))
+    stride, c = x.stride()
+    if T <= 1:
+        stride = D
+    if stride < D or c != 1:
+        raise ValueError("x must have contiguous rows that do not overlap")
+    if stride * x.element_size() % 16 or x.data_ptr() % 16:
+        raise ValueError("x's rows must stand at multiples of 16 bytes")
+    if (not isinstance(weights, torch.Tensor) or weights.dtype != torch.float32 or weights.shape != ids.shape
+            or not weights.is_contiguous()):
+        raise ValueError("weights must be contiguous float32 [%d, %d]" % (T, k))
+    if weights.device != device:
+        raise ValueError("weights is on %s, ids on %s" % (weights.device, device))
+    dtype = dtype or up.dtype
+    out_code = _dtype(dtype)
+    out = torch.empty((T, N), dtype=dtype, device=device)
+    size = _layer_workspace(T, k, H, N)
+    ws = torch.empty(size, dtype=torch.uint8, device=device)   # torch's blocks start at 512 bytes
+    check(lib.emb_expert_layer(ids.data_ptr(), ids.element_size(), T, k, E, x.data_ptr(), _DTYPE_CODE[x.dtype], stride, D, up.data_ptr(),
+                               down.data_ptr(), _DTYPE_CODE[up.dtype], H, N, act, weights.data_ptr(), out.data_ptr(), out_code,
+                               ws.data_ptr(), size, _stream(device)), "emb_expert_layer")
+    return out
 
 
 def dense_status(stream=None) -> int:

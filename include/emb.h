@@ -461,6 +461,32 @@ int emb_expert_linear_grad_weight(const emb_expert_plan* plan, const void* grad_
                                   const void* rows, int64_t rows_stride, int64_t in_width, int64_t out_width,
                                   int32_t dtype, void* grad_weight, void* stream);
 
+/* The whole expert layer for a few tokens, from their ids to their sums, in two kernels
+ * that read each chosen expert's weights once:
+ *   out[t] = sum_j weights[t, j] down[e] act(up[e] x[t]),  e = ids[t, j]
+ * ids [tokens, k] as for emb_expert_sort (-1: none; any other id outside [0, E) is
+ * treated as -1 and recorded as EMB_ERR_KEY_RANGE); tokens * k is at most
+ * EMB_EXPERT_LAYER_ASSIGNMENTS (more go through a plan).  x [tokens, in_width] is fp32
+ * (rounded to dtype first, as by emb_expert_dispatch) or of dtype, EMB_F16 or EMB_BF16;
+ * up is [E, hidden, in_width] ([E, 2 hidden, in_width] for EMB_ACT_SWIGLU: the gates' rows,
+ * then the rows they let through), down [E, out_width, hidden], both of dtype; weights
+ * fp32 [tokens, k]; out [tokens, out_width] of any emb_dtype.  Widths are multiples of 8,
+ * x, up, down and out 16-byte aligned, x's rows at multiples of 16 bytes.  Sums are
+ * fp32 as in the experts' products; what the activation gives is rounded to dtype, the
+ * type the second product takes, y stays fp32 up to the sum over j, in order.  A token
+ * without experts gets zeros; the weight of an assignment without one is not used.
+ * Activations: relu, v / (1 + exp(-v)), v (1 + erf(v / sqrt 2)) / 2, and
+ * gate / (1 + exp(-gate)) times the other half.  The workspace is 256-byte aligned,
+ * emb_expert_layer_workspace bytes, and free again once the call's work is done.  No
+ * passage: library convenience. */
+#define EMB_EXPERT_LAYER_ASSIGNMENTS 512
+enum { EMB_ACT_RELU = 0, EMB_ACT_SILU = 1, EMB_ACT_GELU = 2, EMB_ACT_SWIGLU = 3 };
+int emb_expert_layer_workspace(int64_t tokens, int32_t k, int64_t hidden, int64_t out_width, size_t* bytes);
+int emb_expert_layer(const void* ids, int32_t id_bytes, int64_t tokens, int32_t k, int32_t experts, const void* x,
+                     int32_t x_dtype, int64_t x_stride, int64_t in_width, const void* up, const void* down,
+                     int32_t dtype, int64_t hidden, int64_t out_width, int32_t activation, const float* weights,
+                     void* out, int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Orthogonalise `batch` matrices G [rows, cols] by `steps` (1..32) quintic
  * Newton-Schulz steps, as the Muon optimiser does with a momentum
  * (K. Jordan et al., 2024):
