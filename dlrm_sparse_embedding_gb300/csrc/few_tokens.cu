@@ -16,103 +16,23 @@
 // and add up in shared memory, in order.
 //
 // Every block makes the groups for itself in shared memory.  The first kernel leaves
-// hidden in memory, the second y in fp32; whichever warp finishes the last expert's tile of
-// 16 outputs adds up these columns of every token, in the order of j: results repeat bit
-// for bit.
-#include <algorithm>
-#include <type_traits>
-
-#include "emb_internal.cuh"
-#include "rows.cuh"
+// hidden in memory, the second y in fp32; whoever finishes a tile of outputs of a
+// token's last assignment adds up these columns of the token, in the order of j: results
+// repeat bit for bit.
+#include "few_tokens.cuh"
 
 namespace emb {
 namespace {
 
-constexpr int kMost = EMB_EXPERT_LAYER_ASSIGNMENTS;
+using namespace few;
+
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kSms = 152, kPerSm = 2;
-constexpr int kTile = 16;       // rows of a weight a warp takes
+constexpr int kPerSm = 2;
+constexpr int kSumInDown = 32;  // assignments up to which layer_down adds up the tokens itself: a third launch costs 2 us, the warps that finish last more
 constexpr int kStep = 32;       // k of a lane group's 16 bytes
 constexpr int kChunk = 64;      // of a group's assignments at once, at most
-
-struct Args {
-    const void* ids;
-    int id_bytes, tokens, k, experts;
-    const void* x;
-    int64_t x_stride;
-    const void* up;
-    const void* down;
-    int in_width, hidden, out_width;
-    const float* weights;
-    void* out;
-    int out_dtype;
-    void* hidden_at;         // [assignments][hidden]
-    float* y;                // [assignments][out_width]
-    int* done;               // of each tile of outputs, the experts
-    int* status;
-    int share;               // warps of a tile
-};
-
-struct Groups {
-    int count[kMaxExperts];
-    short expert_of[kMost];      // of each assignment, -1: none
-    short expert[kMost];         // the experts with assignments, in order
-    short first[kMost + 1];      // their first member
-    short member[kMost];         // assignments by expert
-    int warp_sums[kWarps];
-    int active;
-};
-
-// The assignments by expert.  Within a group the order is whatever the atomics make it:
-// an assignment's results do not depend on its neighbours.
-__device__ void make_groups(const Args& a, Groups& g, bool report)
-{
-    const int t = threadIdx.x, P = a.tokens * a.k;
-    for (int e = t; e < a.experts; e += kThreads) g.count[e] = 0;
-    __syncthreads();
-    for (int i = t; i < P; i += kThreads) {
-        const long long id = a.id_bytes == 8 ? __ldg(static_cast<const long long*>(a.ids) + i) : (long long)__ldg(static_cast<const int32_t*>(a.ids) + i);
-        const bool has = id >= 0 && id < a.experts;
-        if (!has && id != -1 && report) atomicOr(a.status, ERRBIT_KEY_RANGE);
-        g.expert_of[i] = has ? (short)id : (short)-1;
-        if (has) atomicAdd(&g.count[id], 1);
-    }
-    __syncthreads();
-    // each thread's experts: how many have members, and how many members, in one number
-    constexpr int kEach = kMaxExperts / kThreads;
-    int mine = 0;
-    for (int i = 0; i < kEach; ++i) {
-        const int e = t * kEach + i;
-        if (e < a.experts && g.count[e]) mine += (1 << 16) + g.count[e];
-    }
-    int upto = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, upto, d);
-        if ((t & 31) >= d) upto += u;
-    }
-    if ((t & 31) == 31) g.warp_sums[t >> 5] = upto;
-    __syncthreads();
-    int before = upto - mine;
-    for (int w = 0; w < t >> 5; ++w) before += g.warp_sums[w];
-    if (t == kThreads - 1) {
-        g.active = (before + mine) >> 16;
-        g.first[(before + mine) >> 16] = (short)((before + mine) & 0xffff);
-    }
-    for (int i = 0; i < kEach; ++i) {
-        const int e = t * kEach + i;
-        if (e >= a.experts || !g.count[e]) continue;
-        g.expert[before >> 16] = (short)e;
-        g.first[before >> 16] = (short)(before & 0xffff);
-        const int members = g.count[e];
-        g.count[e] = before & 0xffff;      // from here on, the next member's place
-        before += (1 << 16) + members;
-    }
-    __syncthreads();
-    for (int i = t; i < P; i += kThreads)
-        if (g.expert_of[i] >= 0) g.member[atomicAdd(&g.count[g.expert_of[i]], 1)] = (short)i;
-    __syncthreads();
-}
+constexpr int kShared = kWarps * (kChunk / 8) * 4 * 32;    // floats that warps add up through
+static_assert(kShared * (int)sizeof(float) >= kCountBytes, "the groups are made there");
 
 __device__ __forceinline__ uint4 load_weight(const void* p)
 {
@@ -148,11 +68,13 @@ __device__ __forceinline__ void multiply(float (&c)[4], uint32_t a0, uint32_t a1
 
 // 16 rows of a weight (rows g and g + 8 of a lane's at w0 and w1, null: none) times NT x 8 rows
 // (row(n): the n-th, null: none), over steps [s0, s1) of k.  The weights of the
-// next AHEAD steps are on their way while the products of these are made.
-template <class T, class X, int NT, class ROW>
-__device__ __forceinline__ void products(float (&acc)[NT][4], const T* w0, const T* w1, ROW row, int k, int s0, int s1)
+// next AHEAD steps are on their way while the products of these are made; ready() comes
+// between the first of them and the first row.
+template <class T, class X, int NT, class ROW, class READY>
+__device__ __forceinline__ void products(float (&acc)[NT][4], const T* w0, const T* w1, ROW row, int k, int s0, int s1, READY ready)
 {
     constexpr int AHEAD = NT >= 4 ? 2 : 4;
+    constexpr int AT_ONCE = NT >= 4 ? 1 : AHEAD;     // steps whose rows are in registers
     const int lane = threadIdx.x & 31, g = lane >> 2, c = (lane & 3) * 8;
     const X* x[NT];
 #pragma unroll
@@ -169,7 +91,6 @@ __device__ __forceinline__ void products(float (&acc)[NT][4], const T* w0, const
         }
     };
     const auto use = [&](const uint4 (&p)[AHEAD], const uint4 (&q)[AHEAD], int s) {
-        constexpr int AT_ONCE = NT >= 4 ? 1 : AHEAD;     // steps whose rows are in registers
 #pragma unroll
         for (int i0 = 0; i0 < AHEAD; i0 += AT_ONCE) {
             uint4 b[AT_ONCE][NT];
@@ -189,6 +110,7 @@ __device__ __forceinline__ void products(float (&acc)[NT][4], const T* w0, const
         }
     };
     fetch(a0[0], a1[0], s0);
+    ready();
     for (int s = s0; s < s1; s += 2 * AHEAD) {
         fetch(a0[1], a1[1], s + AHEAD);
         use(a0[0], a1[0], s);
@@ -207,11 +129,12 @@ __device__ __forceinline__ void with_eights(int n, F f)
     else f(std::integral_constant<int, 8>());
 }
 
-// Walks a weight's tiles.  place(expert, tile, g, &w0, &w1) gives a lane's two rows, row(a) an
-// assignment's operand, take(expert's place, tile, n0, rows, acc) has a tile's sums for
-// members n0 on of a group, last(tile) comes after a tile's last group.
-template <class T, class X, class PLACE, class ROW, class TAKE, class LAST>
-__device__ __forceinline__ void walk(const Args& a, const Groups& g, float* shared, int tiles, int k, PLACE place, ROW row, TAKE take, LAST last)
+// Walks a weight's tiles.  place(expert, tile, i) gives a lane's row, i 0 or 1, row(a) an
+// assignment's operand, take(tile, a, low, high) has an assignment's sums for the two, last(tile,
+// first, rows) comes after a group's tile.
+template <class T, class X, class READY, class PLACE, class ROW, class TAKE, class LAST>
+__device__ __forceinline__ void walk(const Args& a, const Groups& g, float* shared, int tiles, int k, READY ready, PLACE place, ROW row, TAKE take,
+                                     LAST last)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slots = kWarps / a.share, slot = warp / a.share, part = warp % a.share;
@@ -224,16 +147,16 @@ __device__ __forceinline__ void walk(const Args& a, const Groups& g, float* shar
         const bool has = item < total;
         const int which = has ? item / tiles : 0, tile = has ? item - which * tiles : 0;
         const int first = g.first[which], rows = has ? g.first[which + 1] - first : 0;
-        const T *w0 = nullptr, *w1 = nullptr;
-        if (has) place(g.expert[which], tile, lane >> 2, w0, w1);
+        const T* const w0 = has ? place(g.expert[which], tile, 0) : nullptr;
+        const T* const w1 = has ? place(g.expert[which], tile, 1) : nullptr;
         // (with shared tiles, the slots of a block go through as many chunks as the longest)
         int longest = rows;
         if (a.share > 1) {
             longest = 0;
             for (int s = 0; s < slots; ++s)
                 if (item0 + s < total) {
-                    const int w = (item0 + s) / tiles;
-                    longest = max(longest, g.first[w + 1] - g.first[w]);
+                    const int o = (item0 + s) / tiles;
+                    longest = max(longest, g.first[o + 1] - g.first[o]);
                 }
         }
         for (int n0 = 0; n0 < longest; n0 += kChunk) {
@@ -242,7 +165,7 @@ __device__ __forceinline__ void walk(const Args& a, const Groups& g, float* shar
                 constexpr int NT = decltype(eights)::value;
                 float acc[NT][4] = {};
                 const auto member_row = [&](int n) -> const X* { return n < have ? row(g.member[first + n0 + n]) : nullptr; };
-                if (have > 0) products<T, X, NT>(acc, w0, w1, member_row, k, s0, s1);
+                if (have > 0) products<T, X, NT>(acc, w0, w1, member_row, k, s0, s1, ready);
                 if (a.share > 1) {
                     float* const mine = shared + warp * (NT * 4 * 32) + lane;
 #pragma unroll
@@ -259,60 +182,63 @@ __device__ __forceinline__ void walk(const Args& a, const Groups& g, float* shar
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            const int m = n * 8 + (lane & 3) * 2 + q;
-                            if (m < have) take(tile, (int)g.member[first + n0 + m], lane >> 2, acc[n][q], acc[n][2 + q]);
+                            const int r = n * 8 + (lane & 3) * 2 + q;
+                            if (r < have) take(tile, (int)g.member[first + n0 + r], acc[n][q], acc[n][2 + q]);
                         }
                 }
             });
         }
-        if (part == 0 && has) last(tile);
+        if (part == 0 && has) last(tile, first, rows);
     }
 }
 
-template <int ACT>
-__device__ __forceinline__ float activate(float v)
-{
-    if (ACT == EMB_ACT_RELU) return v < 0.f ? 0.f : v;      // a NaN stays one
-    if (ACT == EMB_ACT_GELU) return 0.5f * v * (1.f + erff(v * 0.70710678f));
-    return v / (1.f + expf(-v));
-}
-
-constexpr int kShared = kWarps * (kChunk / 8) * 4 * 32;    // floats
-
 // hidden = act(up x), rounded to T, the type the second product takes
-template <class T, class X, int ACT>
+template <class T, class X, bool GATED>
 __global__ void __launch_bounds__(kThreads, kPerSm) layer_up(const Args a)
 {
-    constexpr bool GATED = ACT == EMB_ACT_SWIGLU;
     __shared__ Groups g;
-    __shared__ float shared[kShared];
+    __shared__ __align__(16) float shared[kShared];
     wait_for_earlier();
     let_next_begin();      // after the wait: what stood before this kernel is there for the next one's first reads
-    make_groups(a, g, blockIdx.x == 0);
-    if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < (a.out_width + kTile - 1) / kTile; i += kThreads) a.done[i] = 0;
-    const int units = GATED ? kTile / 2 : kTile;       // of hidden a tile has: rows g are gates, g + 8 what they let through
+    make_groups(a, g, reinterpret_cast<unsigned char*>(shared), blockIdx.x == 0);
+    if (a.done) {
+        clear_done(a);
+        store_nothing(a, g);
+    }
+    constexpr int kUnits = GATED ? kTile / 2 : kTile;       // of hidden a tile has: 8 gates and what they let through, or 16 rows
+    const int r = (threadIdx.x & 31) >> 2;
     T* const hidden = static_cast<T*>(a.hidden_at);
     walk<T, X>(
-        a, g, shared, (a.hidden + units - 1) / units, a.in_width,
-        [&](int expert, int tile, int r, const T*& w0, const T*& w1) {
-            const T* const w = static_cast<const T*>(a.up) + (int64_t)expert * (GATED ? 2 : 1) * a.hidden * a.in_width;
-            const int m = tile * units + r, m1 = GATED ? a.hidden + m : m + 8;
-            if (m < a.hidden) w0 = w + (int64_t)m * a.in_width;
-            if (GATED ? m < a.hidden : m1 < a.hidden) w1 = w + (int64_t)m1 * a.in_width;
+        a, g, shared, (a.hidden + kUnits - 1) / kUnits, a.in_width, [] {},
+        [&](int expert, int tile, int i) -> const T* {
+            const int m = tile * kUnits + r + (GATED ? 0 : i * 8);
+            if (m >= a.hidden) return nullptr;
+            return static_cast<const T*>(a.up) + ((int64_t)expert * (GATED ? 2 : 1) * a.hidden + (GATED ? i * a.hidden : 0) + m) * a.in_width;
         },
         [&](int assignment) { return static_cast<const X*>(a.x) + (assignment / a.k) * a.x_stride; },
-        [&](int tile, int assignment, int r, float low, float high) {
-            T* const to = hidden + (int64_t)assignment * a.hidden + tile * units + r;
-            const int left = a.hidden - tile * units - r;
+        [&](int tile, int assignment, float low, float high) {
+            const int unit = tile * kUnits + r, left = a.hidden - unit;
+            T* const to = hidden + (int64_t)assignment * a.hidden + unit;
             if constexpr (GATED) {
-                if (left > 0) to[0] = from_float<T>(activate<ACT>(low) * high);
+                if (left > 0) to[0] = from_float<T>(activate(a.act, low) * high);
             } else {
-                if (left > 0) to[0] = from_float<T>(activate<ACT>(low));
-                if (left > 8) to[8] = from_float<T>(activate<ACT>(high));
+                if (left > 0) to[0] = from_float<T>(activate(a.act, low));
+                if (left > 8) to[8] = from_float<T>(activate(a.act, high));
             }
         },
-        [](int) {});
+        [](int, int, int) {});
+}
+
+// Where the n-th bit of a mask is (somewhere, if it has no more than n).
+__device__ __forceinline__ int nth_bit(unsigned mask, int n)
+{
+    int at = 0;
+#pragma unroll
+    for (int w = 16; w; w >>= 1) {
+        const int c = __popc(mask >> at & ((1u << w) - 1));
+        if (n >= c) n -= c, at += w;
+    }
+    return at & 31;
 }
 
 // y = down hidden, and the tokens' sums
@@ -320,71 +246,63 @@ template <class T>
 __global__ void __launch_bounds__(kThreads, kPerSm) layer_down(const Args a)
 {
     __shared__ Groups g;
-    __shared__ float shared[kShared];
+    __shared__ __align__(16) float shared[kShared];
     let_next_begin();
-    make_groups(a, g, false);      // the ids were there before layer_up's blocks let this kernel begin
-    wait_for_earlier();
-    const int N = a.out_width;
-    const auto store = [&](int token, int col, const float4& v) {
-        const int64_t at = (int64_t)token * N + col;
-        const float f[4] = {v.x, v.y, v.z, v.w};
-        if (a.out_dtype == EMB_F32) store_vec<4, float>(static_cast<float*>(a.out) + at, f);
-        else if (a.out_dtype == EMB_F16) store_vec<4, __half>(static_cast<__half*>(a.out) + at, f);
-        else store_vec<4, __nv_bfloat16>(static_cast<__nv_bfloat16*>(a.out) + at, f);
-    };
-    if (!g.active) {
-        for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < (int64_t)a.tokens * (N / 4); i += (int64_t)gridDim.x * kThreads)
-            store((int)(i / (N / 4)), (int)(i % (N / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
-        return;
-    }
+    make_groups(a, g, reinterpret_cast<unsigned char*>(shared), false);      // the ids, and the first weights, were there before layer_up's blocks let this kernel begin
+    const int N = a.out_width, lane = threadIdx.x & 31, r = lane >> 2;
     const T* const hidden = static_cast<const T*>(a.hidden_at);
     walk<T, T>(
-        a, g, shared, (N + kTile - 1) / kTile, a.hidden,
-        [&](int expert, int tile, int r, const T*& w0, const T*& w1) {
-            const T* const w = static_cast<const T*>(a.down) + (int64_t)expert * N * a.hidden;
-            const int m = tile * kTile + r;
-            if (m < N) w0 = w + (int64_t)m * a.hidden;
-            if (m + 8 < N) w1 = w + (int64_t)(m + 8) * a.hidden;
+        a, g, shared, (N + kTile - 1) / kTile, a.hidden, [] { wait_for_earlier(); },
+        [&](int expert, int tile, int i) -> const T* {
+            const int m = tile * kTile + i * 8 + r;
+            return m < N ? static_cast<const T*>(a.down) + ((int64_t)expert * N + m) * a.hidden : nullptr;
         },
         [&](int assignment) { return hidden + (int64_t)assignment * a.hidden; },
-        [&](int tile, int assignment, int r, float low, float high) {
-            float* const to = a.y + (int64_t)assignment * N + tile * kTile + r;
+        [&](int tile, int assignment, float low, float high) {
+            const int col = tile * kTile + r;
+            float* const to = a.y + (int64_t)assignment * N + col;
             to[0] = low;
-            if (tile * kTile + r + 8 < N) to[8] = high;
+            if (col + 8 < N) to[8] = high;
         },
-        [&](int tile) {
-            const int lane = threadIdx.x & 31;
+        [&](int tile, int first, int rows) {
+            if (!a.done) return;
+            // whose last assignment this was is added up, eight tokens at a time by four lanes each
             __threadfence();
             __syncwarp();
-            int before = 0;
-            if (lane == 0) before = atomicAdd(&a.done[tile], 1);
-            before = __shfl_sync(0xffffffffu, before, 0);
-            if (before != g.active - 1) return;
+            int token = 0;
+            bool whole = false;
+            if (lane < rows) {
+                token = g.member[first + lane] / a.k;
+                whole = atomicAdd(&a.done[tile * a.tokens + token], 1) == g.experts[token] - 1;
+            }
+            const unsigned all = __ballot_sync(0xffffffffu, whole);
+            if (!all) return;
             __threadfence();
             const int col = tile * kTile + (lane & 3) * 4;
-            if (col >= N) return;
-            for (int t = lane >> 2; t < a.tokens; t += 8) {
-                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                for (int j = 0; j < a.k; ++j) {
-                    const int p = t * a.k + j;
-                    if (g.expert_of[p] < 0) continue;
-                    const float w = __ldg(&a.weights[p]);
-                    const float4 v = __ldcg(reinterpret_cast<const float4*>(a.y + (int64_t)p * N + col));
-                    s.x = __fmaf_rn(w, v.x, s.x), s.y = __fmaf_rn(w, v.y, s.y), s.z = __fmaf_rn(w, v.z, s.z), s.w = __fmaf_rn(w, v.w, s.w);
-                }
-                store(t, col, s);
+            for (int i = 0; i < __popc(all); i += 8) {
+                const int t = __shfl_sync(0xffffffffu, token, nth_bit(all, i + (lane >> 2)));
+                if (i + (lane >> 2) < __popc(all) && col < N) sum_token(a, [&](int p) { return g.expert_of[p] >= 0; }, t, col);
             }
         });
+    wait_for_earlier();      // a block without a tile, too: what follows takes this kernel's end for both
+}
+
+// The tokens' sums: a thread has four columns of one.
+__global__ void __launch_bounds__(kThreads) layer_sum(const Args a)
+{
+    let_next_begin();
+    wait_for_earlier();
+    const int col = (blockIdx.x * kThreads + threadIdx.x) * 4;
+    if (col < a.out_width) sum_token(a, [&](int p) { return id_of(a, p, false) >= 0; }, blockIdx.y, col);
 }
 
 size_t rounded(size_t n) { return (n + 255) & ~size_t(255); }
 
 struct Room {
     size_t hidden, y, done;
-    Room(int64_t assignments, int64_t hidden_width, int64_t out_width)
+    Room(int64_t tokens, int64_t assignments, int64_t hidden_width, int64_t out_width)
         : hidden(rounded((size_t)assignments * hidden_width * 2)), y(rounded((size_t)assignments * out_width * sizeof(float))),
-          done(rounded((size_t)(out_width + kTile - 1) / kTile * sizeof(int)))
+          done(assignments > kSumInDown ? 0 : rounded((size_t)(out_width + kTile - 1) / kTile * tokens * sizeof(int)))
     {
     }
 };
@@ -413,8 +331,8 @@ using namespace emb;
 extern "C" int emb_expert_layer_workspace(int64_t tokens, int32_t k, int64_t hidden, int64_t out_width, size_t* bytes)
 {
     if (!bytes || !sizes_valid(tokens, k, hidden, out_width)) return EMB_ERR_INVALID_ARG;
-    const Room r(tokens * k, hidden, out_width);
-    *bytes = r.hidden + r.y + r.done;
+    const Room r(tokens, tokens * k, hidden, out_width);
+    *bytes = std::max<size_t>(r.hidden + r.y + r.done, 256);
     return EMB_OK;
 }
 
@@ -437,30 +355,37 @@ extern "C" int emb_expert_layer(const void* ids, int32_t id_bytes, int64_t token
     a.ids = ids, a.id_bytes = id_bytes, a.tokens = (int)tokens, a.k = k, a.experts = experts;
     a.x = x, a.x_stride = x_stride, a.up = up, a.down = down;
     a.in_width = (int)in_width, a.hidden = (int)hidden, a.out_width = (int)out_width;
-    a.weights = weights, a.out = out, a.out_dtype = out_dtype;
-    const Room room(tokens * k, hidden, out_width);
+    a.weights = weights, a.out = out, a.out_dtype = out_dtype, a.act = activation;
+    const Room room(tokens, tokens * k, hidden, out_width);
     unsigned char* const at = static_cast<unsigned char*>(workspace);
-    a.hidden_at = at, a.y = reinterpret_cast<float*>(at + room.hidden), a.done = reinterpret_cast<int*>(at + room.hidden + room.y);
+    a.hidden_at = at, a.y = reinterpret_cast<float*>(at + room.hidden), a.done = room.done ? reinterpret_cast<int*>(at + room.hidden + room.y) : nullptr;
     if (!(a.status = dense_status_word())) return EMB_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int64_t groups = std::min<int64_t>(tokens * k, experts);     // at most
-    const auto blocks = [](int64_t tiles, int share) { return (unsigned)std::min<int64_t>((tiles * share + kWarps - 1) / kWarps, kSms * kPerSm); };
+    static const int force = getenv("EMB_FORCE") ? atoi(getenv("EMB_FORCE")) : -1;
+    const auto sums = [&]() -> int {
+        if (a.done) return EMB_OK;
+        return launch_next(layer_sum, dim3((unsigned)((out_width / 4 + kThreads - 1) / kThreads), (unsigned)tokens), kThreads, 0, st, 1, a);
+    };
+    if (force == 1 && !a.done) {
+        if (int rc = launch_tiles(a, x_dtype, dtype, st)) return rc;
+        return sums();
+    }
     const auto go = [&](auto t) -> int {
         using T = decltype(t);
-        const int units = activation == EMB_ACT_SWIGLU ? kTile / 2 : kTile;
-        const int64_t up_tiles = groups * ((hidden + units - 1) / units), down_tiles = groups * ((out_width + kTile - 1) / kTile);
+        const auto launch = [&](auto kernel, int64_t width, int units, int64_t sum) {
+            const int64_t tiles = groups * ((width + units - 1) / units);
+            a.share = sharing(tiles, sum);
+            const unsigned blocks = (unsigned)std::min<int64_t>((tiles * a.share + kWarps - 1) / kWarps, kSms * kPerSm);
+            return launch_next(kernel, blocks, kThreads, 0, st, 1, a);
+        };
         const auto first = [&](auto xt) -> int {
             using X = decltype(xt);
-            a.share = sharing(up_tiles, in_width);
-            const auto kernel = activation == EMB_ACT_RELU   ? layer_up<T, X, EMB_ACT_RELU>
-                                : activation == EMB_ACT_SILU ? layer_up<T, X, EMB_ACT_SILU>
-                                : activation == EMB_ACT_GELU ? layer_up<T, X, EMB_ACT_GELU>
-                                                             : layer_up<T, X, EMB_ACT_SWIGLU>;
-            return launch_next(kernel, blocks(up_tiles, a.share), kThreads, 0, st, 1, a);
+            return activation == EMB_ACT_SWIGLU ? launch(layer_up<T, X, true>, hidden, kTile / 2, in_width) : launch(layer_up<T, X, false>, hidden, kTile, in_width);
         };
         if (int rc = x_dtype == EMB_F32 ? first(float()) : first(T())) return rc;
-        a.share = sharing(down_tiles, hidden);
-        return launch_next(layer_down<T>, blocks(down_tiles, a.share), kThreads, 0, st, 1, a);
+        if (int rc = launch(layer_down<T>, out_width, kTile, hidden)) return rc;
+        return sums();
     };
     return dtype == EMB_F16 ? go(__half()) : go(__nv_bfloat16());
 }
