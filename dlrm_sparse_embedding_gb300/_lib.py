@@ -115,7 +115,7 @@ def _load() -> ctypes.CDLL:
     L.emb_layer_norm_grad_workspace.argtypes = [i64, i64, size]
     L.emb_layer_norm_grad.argtypes = [vp, i32, i64, vp, i32, i64, i64, i64, vp, i32, f32, vp, vp, vp, vp, ctypes.c_size_t, vp]
     L.emb_dropout.argtypes = [vp, i32, i64, i64, i64, ctypes.c_double, ctypes.c_uint64, vp, ctypes.c_uint64, vp, i64, vp, i32, vp]
-    L.emb_expert_layer_workspace.argtypes = [i64, i32, i64, i64, size]
+    L.emb_expert_layer_workspace.argtypes = [i64, i32, i64, i64, i64, size]
     L.emb_expert_layer.argtypes = [vp, i32, i64, i32, i32, vp, i32, i64, i64, vp, vp, i32, i64, i64, i32, vp, vp, i32, vp,
                                    ctypes.c_size_t, vp]
     L.emb_dense_status.argtypes = [vp]

@@ -299,19 +299,21 @@ __global__ void __launch_bounds__(kThreads) layer_sum(const Args a)
 size_t rounded(size_t n) { return (n + 255) & ~size_t(255); }
 
 struct Room {
-    size_t hidden, y, done;
-    Room(int64_t tokens, int64_t assignments, int64_t hidden_width, int64_t out_width)
-        : hidden(rounded((size_t)assignments * hidden_width * 2)), y(rounded((size_t)assignments * out_width * sizeof(float))),
+    size_t rows, hidden, y, done;
+    Room(int64_t tokens, int64_t assignments, int64_t in_width, int64_t hidden_width, int64_t out_width)
+        : rows(assignments > kSumInDown ? rounded((size_t)assignments * in_width * 2) : 0), hidden(rounded((size_t)assignments * hidden_width * 2)),
+          y(rounded((size_t)assignments * out_width * sizeof(float))),
           done(assignments > kSumInDown ? 0 : rounded((size_t)(out_width + kTile - 1) / kTile * tokens * sizeof(int)))
     {
     }
+    size_t all() const { return rows + hidden + y + done; }
 };
 
 bool widths_valid(int64_t w) { return w >= 8 && w % 8 == 0 && w <= (1 << 24); }
 
-bool sizes_valid(int64_t tokens, int32_t k, int64_t hidden, int64_t out_width)
+bool sizes_valid(int64_t tokens, int32_t k, int64_t in_width, int64_t hidden, int64_t out_width)
 {
-    return tokens >= 0 && k >= 1 && k <= kMaxExpertsPerToken && tokens <= kMost / k && widths_valid(hidden) && widths_valid(out_width);
+    return widths_valid(in_width) && tokens >= 0 && k >= 1 && k <= kMaxExpertsPerToken && tokens <= kMost / k && widths_valid(hidden) && widths_valid(out_width);
 }
 
 // Warps that share a tile's k: as many as keep eight warps of every SM busy, but four
@@ -328,11 +330,10 @@ int sharing(int64_t tiles, int64_t k)
 
 using namespace emb;
 
-extern "C" int emb_expert_layer_workspace(int64_t tokens, int32_t k, int64_t hidden, int64_t out_width, size_t* bytes)
+extern "C" int emb_expert_layer_workspace(int64_t tokens, int32_t k, int64_t in_width, int64_t hidden, int64_t out_width, size_t* bytes)
 {
-    if (!bytes || !sizes_valid(tokens, k, hidden, out_width)) return EMB_ERR_INVALID_ARG;
-    const Room r(tokens, tokens * k, hidden, out_width);
-    *bytes = std::max<size_t>(r.hidden + r.y + r.done, 256);
+    if (!bytes || !sizes_valid(tokens, k, in_width, hidden, out_width)) return EMB_ERR_INVALID_ARG;
+    *bytes = std::max<size_t>(Room(tokens, tokens * k, in_width, hidden, out_width).all(), 256);
     return EMB_OK;
 }
 
@@ -342,7 +343,7 @@ extern "C" int emb_expert_layer(const void* ids, int32_t id_bytes, int64_t token
                                 size_t workspace_bytes, void* stream)
 {
     size_t need = 0;
-    if (emb_expert_layer_workspace(tokens, k, hidden, out_width, &need) != EMB_OK || !widths_valid(in_width) || experts < 1 ||
+    if (emb_expert_layer_workspace(tokens, k, in_width, hidden, out_width, &need) != EMB_OK || experts < 1 ||
         experts > kMaxExperts || (id_bytes != 4 && id_bytes != 8) || (dtype != EMB_F16 && dtype != EMB_BF16) ||
         (x_dtype != dtype && x_dtype != EMB_F32) || !dtype_valid(out_dtype) || activation < EMB_ACT_RELU || activation > EMB_ACT_SWIGLU ||
         !workspace || !aligned_to(workspace, 256) || workspace_bytes < need)
@@ -356,9 +357,10 @@ extern "C" int emb_expert_layer(const void* ids, int32_t id_bytes, int64_t token
     a.x = x, a.x_stride = x_stride, a.up = up, a.down = down;
     a.in_width = (int)in_width, a.hidden = (int)hidden, a.out_width = (int)out_width;
     a.weights = weights, a.out = out, a.out_dtype = out_dtype, a.act = activation;
-    const Room room(tokens, tokens * k, hidden, out_width);
+    const Room room(tokens, tokens * k, in_width, hidden, out_width);
     unsigned char* const at = static_cast<unsigned char*>(workspace);
-    a.hidden_at = at, a.y = reinterpret_cast<float*>(at + room.hidden), a.done = room.done ? reinterpret_cast<int*>(at + room.hidden + room.y) : nullptr;
+    a.rows = at, a.hidden_at = at + room.rows, a.y = reinterpret_cast<float*>(at + room.rows + room.hidden);
+    a.done = room.done ? reinterpret_cast<int*>(at + room.rows + room.hidden + room.y) : nullptr;
     if (!(a.status = dense_status_word())) return EMB_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int64_t groups = std::min<int64_t>(tokens * k, experts);     // at most

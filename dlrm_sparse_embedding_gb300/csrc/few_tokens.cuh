@@ -25,6 +25,7 @@ struct Args {
     const float* weights;
     void* out;
     int out_dtype;
+    void* rows;              // [assignments, by group][in_width], of the tiles
     void* hidden_at;         // [assignments, by group][hidden]
     float* y;                // [assignments][out_width]
     int* done;               // [tiles of outputs][tokens]: a token's assignments that are done (null: layer_sum adds up)

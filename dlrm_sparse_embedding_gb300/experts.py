@@ -308,9 +308,9 @@ def expert_linear_grad(plan: ExpertPlan, grad_y: torch.Tensor, rows: Optional[to
 
 
 @functools.lru_cache(maxsize=256)
-def _layer_workspace(tokens: int, k: int, hidden: int, out: int) -> int:
+def _layer_workspace(tokens: int, k: int, width: int, hidden: int, out: int) -> int:
     n = ctypes.c_size_t()
-    check(lib.emb_expert_layer_workspace(tokens, k, hidden, out, ctypes.byref(n)), "emb_expert_layer_workspace")
+    check(lib.emb_expert_layer_workspace(tokens, k, width, hidden, out, ctypes.byref(n)), "emb_expert_layer_workspace")
     return n.value
 
 
@@ -376,7 +376,7 @@ def expert_layer(ids: torch.Tensor, x: torch.Tensor, up: torch.Tensor, down: tor
     dtype = dtype or up.dtype
     out_code = _dtype(dtype)
     out = torch.empty((T, N), dtype=dtype, device=device)
-    size = _layer_workspace(T, k, H, N)
+    size = _layer_workspace(T, k, D, H, N)
     ws = torch.empty(size, dtype=torch.uint8, device=device)   # torch's blocks start at 512 bytes
     check(lib.emb_expert_layer(ids.data_ptr(), ids.element_size(), T, k, E, x.data_ptr(), _DTYPE_CODE[x.dtype], stride, D, up.data_ptr(),
                                down.data_ptr(), _DTYPE_CODE[up.dtype], H, N, act, weights.data_ptr(), out.data_ptr(), out_code,

@@ -481,7 +481,8 @@ int emb_expert_linear_grad_weight(const emb_expert_plan* plan, const void* grad_
  * passage: library convenience. */
 #define EMB_EXPERT_LAYER_ASSIGNMENTS 512
 enum { EMB_ACT_RELU = 0, EMB_ACT_SILU = 1, EMB_ACT_GELU = 2, EMB_ACT_SWIGLU = 3 };
-int emb_expert_layer_workspace(int64_t tokens, int32_t k, int64_t hidden, int64_t out_width, size_t* bytes);
+int emb_expert_layer_workspace(int64_t tokens, int32_t k, int64_t in_width, int64_t hidden, int64_t out_width,
+                               size_t* bytes);
 int emb_expert_layer(const void* ids, int32_t id_bytes, int64_t tokens, int32_t k, int32_t experts, const void* x,
                      int32_t x_dtype, int64_t x_stride, int64_t in_width, const void* up, const void* down,
                      int32_t dtype, int64_t hidden, int64_t out_width, int32_t activation, const float* weights,

@@ -259,8 +259,10 @@ def test_refusals_without_a_gpu():
         emb.expert_layer(torch.zeros(3, 2), x, up, up, w)
     n, bad = ctypes.c_size_t(), emb.EMB_ERR_INVALID_ARG
     size = lambda *a: emb.lib.emb_expert_layer_workspace(*a, ctypes.byref(n))  # noqa: E731
-    assert size(64, 8, 16, 16) == emb.EMB_OK and n.value % 256 == 0 and n.value >= 512 * 16 * 6
-    for a in ((65, 8, 16, 16), (-1, 1, 16, 16), (1, 0, 16, 16), (1, 65, 16, 16), (1, 1, 12, 16), (1, 1, 16, 0), (2 ** 40, 2, 16, 16)):
+    assert size(64, 8, 16, 16, 16) == emb.EMB_OK and n.value % 256 == 0 and n.value >= 512 * 16 * 6
+    assert size(0, 8, 16, 16, 16) == emb.EMB_OK and n.value > 0
+    for a in ((65, 8, 8, 16, 16), (-1, 1, 8, 16, 16), (1, 0, 8, 16, 16), (1, 65, 8, 16, 16), (1, 1, 8, 12, 16), (1, 1, 8, 16, 0),
+              (2 ** 40, 2, 8, 16, 16), (1, 1, 4, 16, 16)):
         assert size(*a) == bad, a
     at = 0x10000
     ok = [at, 4, 3, 2, 4, at, 2, 16, 16, at, at, 2, 8, 16, 0, at, at, 2, at, 1 << 20, None]
