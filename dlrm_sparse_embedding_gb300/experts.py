@@ -307,11 +307,45 @@ def expert_linear_grad(plan: ExpertPlan, grad_y: torch.Tensor, rows: Optional[to
     return grad_rows, grad_weight
 
 
-@functools.lru_cache(maxsize=256)
-def _layer_workspace(tokens: int, k: int, width: int, hidden: int, out: int) -> int:
+@functools.lru_cache(maxsize=1024)
+def _layer_sizes(ids, ids_type, x, x_stride, x_type, up, up_type, down, down_type, weights, weights_type, activation, dtype):
+    """What expert_layer's checks of shapes and types, which a serving loop repeats call for call,
+    give: the sizes and codes of its call.  ValueError if they do not fit."""
+    if ids_type not in (torch.int32, torch.int64) or len(ids) != 2:
+        raise ValueError("ids must be a contiguous int32 or int64 tensor [tokens, k]")
+    T, k = ids
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError("activation must be one of %s, got %r" % (", ".join(ACTIVATIONS), activation))
+    if not 1 <= k <= MAX_EXPERTS_PER_TOKEN or T * k > MAX_LAYER_ASSIGNMENTS:
+        raise ValueError("1 to %d experts a token and up to %d assignments are supported, got %d and %d: more tokens go through "
+                         "expert_sort" % (MAX_EXPERTS_PER_TOKEN, MAX_LAYER_ASSIGNMENTS, k, T * k))
+    for name, shape, kind in (("up", up, up_type), ("down", down, down_type)):
+        if kind not in (torch.float16, torch.bfloat16) or len(shape) != 3:
+            raise ValueError("%s must be a contiguous float16 or bfloat16 tensor of 3 dimensions" % name)
+    E, rows, D = up
+    N, H = down[1:]
+    if down_type != up_type or down[0] != E or rows != (2 * H if activation == "swiglu" else H):
+        raise ValueError("up %s of %s and down %s of %s do not belong together for %s"
+                         % (tuple(up), up_type, tuple(down), down_type, activation))
+    if not 1 <= E <= MAX_EXPERTS or min(D, H, N) < 8 or D % 8 or H % 8 or N % 8:
+        raise ValueError("1 to %d experts and widths that are multiples of 8 are supported, got up %s and down %s"
+                         % (MAX_EXPERTS, tuple(up), tuple(down)))
+    if len(x) != 2 or tuple(x) != (T, D) or x_type not in (torch.float32, up_type):
+        raise ValueError("x must be float32 or %s [%d, %d]" % (up_type, T, D))
+    stride, c = x_stride
+    if T <= 1:
+        stride = D
+    if stride < D or c != 1:
+        raise ValueError("x must have contiguous rows that do not overlap")
+    if stride * x_type.itemsize % 16:
+        raise ValueError("x's rows must stand at multiples of 16 bytes")
+    if weights_type != torch.float32 or weights != ids:
+        raise ValueError("weights must be contiguous float32 [%d, %d]" % (T, k))
+    dtype = dtype or up_type
     n = ctypes.c_size_t()
-    check(lib.emb_expert_layer_workspace(tokens, k, width, hidden, out, ctypes.byref(n)), "emb_expert_layer_workspace")
-    return n.value
+    check(lib.emb_expert_layer_workspace(T, k, D, H, N, ctypes.byref(n)), "emb_expert_layer_workspace")
+    return (T, k, E, D, H, N, ids_type.itemsize, _DTYPE_CODE[x_type], stride, _DTYPE_CODE[up_type], act, dtype, _dtype(dtype), n.value)
 
 
 def expert_layer(ids: torch.Tensor, x: torch.Tensor, up: torch.Tensor, down: torch.Tensor, weights: torch.Tensor,
@@ -330,57 +364,28 @@ def expert_layer(ids: torch.Tensor, x: torch.Tensor, up: torch.Tensor, down: tor
     activation: "relu", "silu", "gelu" or "swiglu"."""
     if stream is not None:
         return _on(stream, expert_layer, ids, x, up, down, weights, activation, dtype)
-    if not isinstance(ids, torch.Tensor) or ids.dtype not in (torch.int32, torch.int64) or ids.dim() != 2 or not ids.is_contiguous():
-        raise ValueError("ids must be a contiguous int32 or int64 tensor [tokens, k]")
+    tensor = torch.Tensor
+    if not (isinstance(ids, tensor) and isinstance(x, tensor) and isinstance(up, tensor) and isinstance(down, tensor)
+            and isinstance(weights, tensor)):
+        raise ValueError("ids, x, up, down and weights must be torch tensors")
+    device = ids.device
     if not ids.is_cuda:
         raise ValueError("ids must be a CUDA tensor")
-    device = ids.device
-    T, k = ids.shape
-    act = ACTIVATIONS.get(activation)
-    if act is None:
-        raise ValueError("activation must be one of %s, got %r" % (", ".join(ACTIVATIONS), activation))
-    if not 1 <= k <= MAX_EXPERTS_PER_TOKEN or T * k > MAX_LAYER_ASSIGNMENTS:
-        raise ValueError("1 to %d experts a token and up to %d assignments are supported, got %d and %d: more tokens go through "
-                         "expert_sort" % (MAX_EXPERTS_PER_TOKEN, MAX_LAYER_ASSIGNMENTS, k, T * k))
-    for name, w in (("up", up), ("down", down)):
-        if not isinstance(w, torch.Tensor) or w.dtype not in (torch.float16, torch.bfloat16) or w.dim() != 3 or not w.is_contiguous():
-            raise ValueError("%s must be a contiguous float16 or bfloat16 tensor of 3 dimensions" % name)
-        if w.device != device:
-            raise ValueError("%s is on %s, ids on %s" % (name, w.device, device))
-        if w.data_ptr() % 16:
-            raise ValueError("%s must be 16-byte aligned" % name)
-    E, rows, D = up.shape
-    N, H = down.shape[1:]
-    if down.dtype != up.dtype or down.shape[0] != E or rows != (2 * H if activation == "swiglu" else H):
-        raise ValueError("up %s of %s and down %s of %s do not belong together for %s"
-                         % (tuple(up.shape), up.dtype, tuple(down.shape), down.dtype, activation))
-    if not 1 <= E <= MAX_EXPERTS or min(D, H, N) < 8 or D % 8 or H % 8 or N % 8:
-        raise ValueError("1 to %d experts and widths that are multiples of 8 are supported, got up %s and down %s"
-                         % (MAX_EXPERTS, tuple(up.shape), tuple(down.shape)))
-    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape != (T, D) or x.dtype not in (torch.float32, up.dtype):
-        raise ValueError("x must be float32 or %s [%d, %d]" % (up.dtype, T, D))
-    if x.device != device:
-        raise ValueError("x is on %s, ids on %s" % (x.device, device))
-    stride, c = x.stride()
-    if T <= 1:
-        stride = D
-    if stride < D or c != 1:
-        raise ValueError("x must have contiguous rows that do not overlap")
-    if stride * x.element_size() % 16 or x.data_ptr() % 16:
-        raise ValueError("x's rows must stand at multiples of 16 bytes")
-    if (not isinstance(weights, torch.Tensor) or weights.dtype != torch.float32 or weights.shape != ids.shape
-            or not weights.is_contiguous()):
-        raise ValueError("weights must be contiguous float32 [%d, %d]" % (T, k))
-    if weights.device != device:
-        raise ValueError("weights is on %s, ids on %s" % (weights.device, device))
-    dtype = dtype or up.dtype
-    out_code = _dtype(dtype)
+    T, k, E, D, H, N, id_bytes, x_code, stride, code, act, dtype, out_code, size = _layer_sizes(
+        ids.shape, ids.dtype, x.shape, x.stride(), x.dtype, up.shape, up.dtype, down.shape, down.dtype, weights.shape, weights.dtype,
+        activation, dtype)
+    if x.device != device or up.device != device or down.device != device or weights.device != device:
+        raise ValueError("x is on %s, up on %s, down on %s, weights is on %s, ids on %s"
+                         % (x.device, up.device, down.device, weights.device, device))
+    if not (ids.is_contiguous() and up.is_contiguous() and down.is_contiguous() and weights.is_contiguous()):
+        raise ValueError("ids, up, down and weights must be contiguous")
+    x_ptr, up_ptr, down_ptr = x.data_ptr(), up.data_ptr(), down.data_ptr()
+    if (x_ptr | up_ptr | down_ptr) % 16:
+        raise ValueError("x, up and down must be 16-byte aligned")
     out = torch.empty((T, N), dtype=dtype, device=device)
-    size = _layer_workspace(T, k, D, H, N)
     ws = torch.empty(size, dtype=torch.uint8, device=device)   # torch's blocks start at 512 bytes
-    check(lib.emb_expert_layer(ids.data_ptr(), ids.element_size(), T, k, E, x.data_ptr(), _DTYPE_CODE[x.dtype], stride, D, up.data_ptr(),
-                               down.data_ptr(), _DTYPE_CODE[up.dtype], H, N, act, weights.data_ptr(), out.data_ptr(), out_code,
-                               ws.data_ptr(), size, _stream(device)), "emb_expert_layer")
+    check(lib.emb_expert_layer(ids.data_ptr(), id_bytes, T, k, E, x_ptr, x_code, stride, D, up_ptr, down_ptr, code, H, N, act,
+                               weights.data_ptr(), out.data_ptr(), out_code, ws.data_ptr(), size, _stream(device)), "emb_expert_layer")
     return out
 
 

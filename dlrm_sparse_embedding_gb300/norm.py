@@ -11,40 +11,68 @@ from typing import Optional, Union
 
 import torch
 
-from ._lib import DTYPES, check, lib
+from ._lib import check, lib
 from .experts import _DTYPE_CODE, _dtype, _on, _stream
 
-_F32 = DTYPES["f32"]
 _LOW64 = 2 ** 64 - 1
 
 
-def _rows(t, name: str, device=None, shape=None):
-    """Checks a [rows, width] matrix with contiguous rows on the GPU (on `device`, of `shape`);
-    returns its address, type code and row stride."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
-        raise ValueError("%s must be a 2-d torch tensor" % name)
-    code = _DTYPE_CODE.get(t.dtype)
+# Checks of shapes and types, which a program repeats call for call, are kept by those.
+@functools.lru_cache(maxsize=1024)
+def _rows(shape, stride, dtype, name: str, like=None):
+    """Checks a [rows, width] matrix with contiguous rows (of shape `like`); returns its type code and row stride."""
+    code = _DTYPE_CODE.get(dtype)
     if code is None:
-        raise ValueError("%s must be float32, float16 or bfloat16, got %s" % (name, t.dtype))
-    n, w = t.shape
-    if w < 1 or (shape is not None and t.shape != shape):
-        raise ValueError("%s must have shape %s, got %s" % (name, "(rows, width)" if shape is None else tuple(shape), tuple(t.shape)))
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError("%s must be a CUDA tensor%s, is on %s" % (name, "" if device is None else " on %s" % device, t.device))
-    s, c = t.stride()
+        raise ValueError("%s must be float32, float16 or bfloat16, got %s" % (name, dtype))
+    if len(shape) != 2:
+        raise ValueError("%s must be a 2-d torch tensor" % name)
+    n, w = shape
+    if w < 1 or (like is not None and shape != like):
+        raise ValueError("%s must have shape %s, got %s" % (name, "(rows, width)" if like is None else tuple(like), tuple(shape)))
+    s, c = stride
     if n <= 1:
         s = w
     if s < w or (c != 1 and w > 1):
         raise ValueError("%s must have contiguous rows that do not overlap" % name)
-    return t.data_ptr(), code, s
+    return code, s
 
 
-def _param(t, name: str, x: torch.Tensor) -> int:
-    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPE_CODE or t.shape != x.shape[1:] or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous float32, float16 or bfloat16 tensor of %d elements" % (name, x.shape[1]))
-    if t.device != x.device:
-        raise ValueError("%s must be on %s, is on %s" % (name, x.device, t.device))
+@functools.lru_cache(maxsize=1024)
+def _params(width: int, weight, bias) -> int:
+    """Checks a norm's rows' width and its parameters' types and shapes; returns their type code."""
+    if width > 1 << 24:
+        raise ValueError("rows of up to 2^24 elements are supported, got %d" % width)
+    dtype = (weight or bias or (torch.float32,))[0]
+    for name, given in (("weight", weight), ("bias", bias)):
+        if given and (given[0] not in _DTYPE_CODE or tuple(given[1]) != (width,)):
+            raise ValueError("%s must be a contiguous float32, float16 or bfloat16 tensor of %d elements" % (name, width))
+        if given and given[0] != dtype:
+            raise ValueError("weight and bias must have one type, got %s and %s" % (dtype, given[0]))
+    return _DTYPE_CODE[dtype]
+
+
+def _tensor(t, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError("%s must be a 2-d torch tensor" % name)
+
+
+def _cuda(x, name: str) -> torch.device:
+    device = x.device
+    if device.type != "cuda":
+        raise ValueError("%s must be a CUDA tensor, is on %s" % (name, device))
+    return device
+
+
+def _there(t, name: str, device) -> int:
+    if t.device != device:
+        raise ValueError("%s must be on %s, is on %s" % (name, device, t.device))
     return t.data_ptr()
+
+
+def _param(t, name: str, device) -> int:
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return _there(t, name, device)
 
 
 def _eps(eps) -> float:
@@ -54,13 +82,6 @@ def _eps(eps) -> float:
     return eps
 
 
-def _width(x) -> int:
-    width = x.shape[1]
-    if width > 1 << 24:
-        raise ValueError("rows of up to 2^24 elements are supported, got %d" % width)
-    return width
-
-
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, eps: float = 1e-5,
                dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
     """[rows, width] in `dtype` (default x's): each row of x [rows, width] less its mean,
@@ -68,22 +89,25 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     one type; None: ones, zeros).  Sums and statistics are fp32; x of any row stride."""
     if stream is not None:
         return _on(stream, layer_norm, x, weight, bias, eps, dtype)
-    ptr, code, stride = _rows(x, "x")
-    width, device = _width(x), x.device
-    weight_ptr = bias_ptr = None
-    param = _F32
+    _tensor(x, "x")
+    shape = x.shape
+    code, stride = _rows(shape, x.stride(), x.dtype, "x")
+    device = _cuda(x, "x")
+    weight_ptr = bias_ptr = weight_is = bias_is = None
     if weight is not None:
-        weight_ptr, param = _param(weight, "weight", x), _DTYPE_CODE[weight.dtype]
+        _tensor(weight, "weight")
+        weight_is = weight.dtype, weight.shape
+        weight_ptr = _param(weight, "weight", device)
     if bias is not None:
-        bias_ptr = _param(bias, "bias", x)
-        if weight is not None and bias.dtype != weight.dtype:
-            raise ValueError("weight and bias must have one type, got %s and %s" % (weight.dtype, bias.dtype))
-        param = _DTYPE_CODE[bias.dtype]
+        _tensor(bias, "bias")
+        bias_is = bias.dtype, bias.shape
+        bias_ptr = _param(bias, "bias", device)
+    param = _params(shape[1], weight_is, bias_is)
     eps = _eps(eps)
     dtype = dtype or x.dtype
     out_code = _dtype(dtype)
-    y = torch.empty(x.shape, dtype=dtype, device=device)
-    check(lib.emb_layer_norm(ptr, code, stride, x.shape[0], width, weight_ptr, bias_ptr, param, eps, y.data_ptr(), out_code,
+    y = torch.empty(shape, dtype=dtype, device=device)
+    check(lib.emb_layer_norm(x.data_ptr(), code, stride, shape[0], shape[1], weight_ptr, bias_ptr, param, eps, y.data_ptr(), out_code,
                              _stream(device)), "emb_layer_norm")
     return y
 
@@ -102,26 +126,34 @@ def layer_norm_grad(grad_y: torch.Tensor, x: torch.Tensor, weight: Optional[torc
     The statistics are taken from x again."""
     if stream is not None:
         return _on(stream, layer_norm_grad, grad_y, x, weight, eps, need_x, need_weight)
-    ptr, code, stride = _rows(x, "x")
-    width, device = _width(x), x.device
-    grad_ptr, grad_code, grad_stride = _rows(grad_y, "grad_y", device, x.shape)
-    weight_ptr, param_dtype = None, torch.float32
+    _tensor(x, "x")
+    _tensor(grad_y, "grad_y")
+    shape = x.shape
+    code, stride = _rows(shape, x.stride(), x.dtype, "x")
+    grad_code, grad_stride = _rows(grad_y.shape, grad_y.stride(), grad_y.dtype, "grad_y", shape)
+    device = _cuda(x, "x")
+    grad_ptr = _there(grad_y, "grad_y", device)
+    rows, width = shape
+    weight_ptr, weight_is, param_dtype = None, None, torch.float32
     if weight is not None:
-        weight_ptr, param_dtype = _param(weight, "weight", x), weight.dtype
+        _tensor(weight, "weight")
+        param_dtype = weight.dtype
+        weight_is = param_dtype, weight.shape
+        weight_ptr = _param(weight, "weight", device)
+    param = _params(width, weight_is, None)
     eps = _eps(eps)
     grad_x = grad_weight = grad_bias = x_out = weight_out = bias_out = None
     if need_x:
-        grad_x = torch.empty(x.shape, dtype=x.dtype, device=device)
+        grad_x = torch.empty(shape, dtype=x.dtype, device=device)
         x_out = grad_x.data_ptr()
     if need_weight:
         grad_weight = torch.empty(width, dtype=param_dtype, device=device)
         grad_bias = torch.empty(width, dtype=param_dtype, device=device)
         weight_out, bias_out = grad_weight.data_ptr(), grad_bias.data_ptr()
-    size = _grad_workspace(x.shape[0], width)
+    size = _grad_workspace(rows, width)
     ws = torch.empty(size, dtype=torch.uint8, device=device)   # torch's blocks start at 512 bytes
-    check(lib.emb_layer_norm_grad(grad_ptr, grad_code, grad_stride, ptr, code, stride, x.shape[0], width, weight_ptr,
-                                  _DTYPE_CODE[param_dtype], eps, x_out, weight_out, bias_out, ws.data_ptr(), size, _stream(device)),
-          "emb_layer_norm_grad")
+    check(lib.emb_layer_norm_grad(grad_ptr, grad_code, grad_stride, x.data_ptr(), code, stride, rows, width, weight_ptr, param, eps,
+                                  x_out, weight_out, bias_out, ws.data_ptr(), size, _stream(device)), "emb_layer_norm_grad")
     return grad_x, grad_weight, grad_bias
 
 
@@ -138,8 +170,10 @@ def dropout(x: torch.Tensor, rate: float, seed: Union[int, torch.Tensor], offset
     64 bits are used."""
     if stream is not None:
         return _on(stream, dropout, x, rate, seed, offset, residual, dtype)
-    ptr, code, stride = _rows(x, "x")
-    device = x.device
+    _tensor(x, "x")
+    shape = x.shape
+    code, stride = _rows(shape, x.stride(), x.dtype, "x")
+    device = _cuda(x, "x")
     rate = float(rate)
     if not 0.0 <= rate <= 1.0:
         raise ValueError("rate must be in 0 .. 1, got %r" % (rate,))
@@ -147,17 +181,19 @@ def dropout(x: torch.Tensor, rate: float, seed: Union[int, torch.Tensor], offset
     out_code = _dtype(dtype)
     residual_ptr, residual_stride = None, 0
     if residual is not None:
-        residual_ptr, residual_code, residual_stride = _rows(residual, "residual", device, x.shape)
+        _tensor(residual, "residual")
+        residual_code, residual_stride = _rows(residual.shape, residual.stride(), residual.dtype, "residual", shape)
         if residual_code != out_code:
             raise ValueError("residual must have the result's dtype %s, got %s" % (dtype, residual.dtype))
+        residual_ptr = _there(residual, "residual", device)
     seed_ptr = None
     if isinstance(seed, torch.Tensor):
         if seed.dtype != torch.int64 or seed.numel() != 1 or seed.device != device:
             raise ValueError("seed must be an int or an int64 tensor of one element on %s" % device)
         seed_ptr, seed = seed.data_ptr(), 0
-    y = torch.empty(x.shape, dtype=dtype, device=device)
-    check(lib.emb_dropout(ptr, code, stride, x.shape[0], x.shape[1], rate, int(seed) & _LOW64, seed_ptr, int(offset) & _LOW64, residual_ptr,
-                          residual_stride, y.data_ptr(), out_code, _stream(device)), "emb_dropout")
+    y = torch.empty(shape, dtype=dtype, device=device)
+    check(lib.emb_dropout(x.data_ptr(), code, stride, shape[0], shape[1], rate, int(seed) & _LOW64, seed_ptr, int(offset) & _LOW64,
+                          residual_ptr, residual_stride, y.data_ptr(), out_code, _stream(device)), "emb_dropout")
     return y
 
 

@@ -255,8 +255,6 @@ def test_refusals_without_a_gpu():
     x, w, up = torch.zeros(3, 16), torch.zeros(3, 2), torch.zeros(4, 8, 16, dtype=BF)
     with pytest.raises(ValueError, match="CUDA"):
         emb.expert_layer(torch.zeros(3, 2, dtype=torch.int32), x, up, up, w)
-    with pytest.raises(ValueError, match="int32 or int64"):
-        emb.expert_layer(torch.zeros(3, 2), x, up, up, w)
     n, bad = ctypes.c_size_t(), emb.EMB_ERR_INVALID_ARG
     size = lambda *a: emb.lib.emb_expert_layer_workspace(*a, ctypes.byref(n))  # noqa: E731
     assert size(64, 8, 16, 16, 16) == emb.EMB_OK and n.value % 256 == 0 and n.value >= 512 * 16 * 6
@@ -275,6 +273,8 @@ def test_refusals_without_a_gpu():
 
 
 REFUSALS = [
+    ("int32 or int64", lambda a: dict(ids=a["ids"].float())),
+    ("tensors", lambda a: dict(x=a["x"].cpu().numpy())),
     ("activation", lambda a: dict(activation="tanh")),
     ("dtype", lambda a: dict(dtype=torch.float64)),
     ("assignments", lambda a: dict(ids=torch.zeros(257, 2, dtype=torch.int32, device="cuda"))),
@@ -289,7 +289,7 @@ REFUSALS = [
     ("x is on", lambda a: dict(x=a["x"].cpu())),
     ("contiguous rows", lambda a: dict(x=torch.zeros(16, 3, device="cuda").t())),
     ("16 bytes", lambda a: dict(x=torch.zeros(3, 17, device="cuda")[:, :16])),
-    ("16 bytes", lambda a: dict(x=torch.zeros(3, 20, device="cuda")[:, 1:17])),
+    ("16-byte", lambda a: dict(x=torch.zeros(3, 20, device="cuda")[:, 1:17])),
     ("weights must", lambda a: dict(weights=a["weights"].half())),
     ("weights is on", lambda a: dict(weights=a["weights"].cpu())),
     ("16-byte", lambda a: dict(up=torch.zeros(4 * 8 * 16 + 1, dtype=BF, device="cuda")[1:].reshape(4, 8, 16))),
