@@ -80,26 +80,45 @@ __device__ __forceinline__ bool epilogue_agrees(bool ok)
     return all != 0;
 }
 
-// The tokens' rows in the products' type, by group.
+// The tokens' rows in the products' type, by group: a block has an assignment, whose place is
+// the number of those of smaller experts and of its own's earlier ones.  The row is on its
+// way meanwhile.
+constexpr int kPieces = 2;      // of 8 elements a thread has on their way
+
 template <class T, class X>
 __global__ void __launch_bounds__(kThreads) gather_rows(const Args a)
 {
-    __shared__ Groups g;
-    __shared__ __align__(16) unsigned char counts[kCountBytes];
     wait_for_earlier();
     let_next_begin();      // after the wait: what stood before this kernel is there for the next ones' first reads
-    make_groups(a, g, counts, blockIdx.x == 0);
-    const int pieces = a.in_width / 8, kept = g.first[g.active];
-    for (int p = blockIdx.x; p < kept; p += gridDim.x) {
-        const X* const from = static_cast<const X*>(a.x) + (g.member[p] / a.k) * a.x_stride;
-        uint4* const to = reinterpret_cast<uint4*>(static_cast<T*>(a.rows) + (int64_t)p * a.in_width);
-        for (int i = threadIdx.x; i < pieces; i += kThreads) {
-            if constexpr (std::is_same<T, X>::value) to[i] = reinterpret_cast<const uint4*>(from)[i];
-            else {
-                const float4 u = reinterpret_cast<const float4*>(from)[2 * i], v = reinterpret_cast<const float4*>(from)[2 * i + 1];
-                to[i] = make_uint4(core::pack2<T>(u.x, u.y), core::pack2<T>(u.z, u.w), core::pack2<T>(v.x, v.y), core::pack2<T>(v.z, v.w));
-            }
+    const int p = blockIdx.x, P = a.tokens * a.k, pieces = a.in_width / 8;
+    const X* const from = static_cast<const X*>(a.x) + (p / a.k) * a.x_stride;
+    uint4 v[kPieces];
+    const auto load = [&](int i) {
+        if constexpr (std::is_same<T, X>::value) return reinterpret_cast<const uint4*>(from)[i];
+        else {
+            const float4 u = reinterpret_cast<const float4*>(from)[2 * i], w = reinterpret_cast<const float4*>(from)[2 * i + 1];
+            return make_uint4(core::pack2<T>(u.x, u.y), core::pack2<T>(u.z, u.w), core::pack2<T>(w.x, w.y), core::pack2<T>(w.z, w.w));
         }
+    };
+    const auto fetch = [&](int i0) {
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j)
+            if (i0 + j * kThreads < pieces) v[j] = load(i0 + j * kThreads);
+    };
+    fetch(threadIdx.x);
+    const int mine = id_of(a, p, threadIdx.x == 0);
+    int place = 0;
+    for (int i0 = 0; i0 < P; i0 += kThreads) {
+        const int i = i0 + threadIdx.x, other = i < P ? id_of(a, i, false) : -1;
+        place += __syncthreads_count(other >= 0 && (other < mine || (other == mine && i < p)));
+    }
+    if (mine < 0) return;
+    uint4* const to = reinterpret_cast<uint4*>(static_cast<T*>(a.rows) + (int64_t)place * a.in_width);
+    for (int i = threadIdx.x; i < pieces; i += kPieces * kThreads) {
+        if (i != threadIdx.x) fetch(i);
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j)
+            if (i + j * kThreads < pieces) to[i + j * kThreads] = v[j];
     }
 }
 
@@ -296,7 +315,7 @@ int launch_tiles(const Args& a, int x_dtype, int dtype, cudaStream_t st)
     const auto go = [&](auto t, auto shape) -> int {
         using T = decltype(t);
         using S = decltype(shape);
-        const int blocks = std::min(a.tokens * a.k, dev.sms);
+        const int blocks = a.tokens * a.k;
         if (int rc = x_dtype == EMB_F32 ? launch_next(gather_rows<T, float>, blocks, kThreads, 0, st, 1, a) : launch_next(gather_rows<T, T>, blocks, kThreads, 0, st, 1, a)) return rc;
         if (int rc = a.act == EMB_ACT_SWIGLU ? launch_kernel<T, true, true, S>(q, dev, st) : launch_kernel<T, true, false, S>(q, dev, st)) return rc;
         return launch_kernel<T, false, false, S>(q, dev, st);

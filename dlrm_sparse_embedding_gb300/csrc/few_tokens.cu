@@ -301,9 +301,9 @@ size_t rounded(size_t n) { return (n + 255) & ~size_t(255); }
 struct Room {
     size_t rows, hidden, y, done;
     Room(int64_t tokens, int64_t assignments, int64_t in_width, int64_t hidden_width, int64_t out_width)
-        : rows(assignments > kSumInDown ? rounded((size_t)assignments * in_width * 2) : 0), hidden(rounded((size_t)assignments * hidden_width * 2)),
+        : rows(rounded((size_t)assignments * in_width * 2)), hidden(rounded((size_t)assignments * hidden_width * 2)),
           y(rounded((size_t)assignments * out_width * sizeof(float))),
-          done(assignments > kSumInDown ? 0 : rounded((size_t)(out_width + kTile - 1) / kTile * tokens * sizeof(int)))
+          done(rounded((size_t)(out_width + kTile - 1) / kTile * std::min<int64_t>(tokens, kSumInDown) * sizeof(int)))
     {
     }
     size_t all() const { return rows + hidden + y + done; }
@@ -321,7 +321,8 @@ bool sizes_valid(int64_t tokens, int32_t k, int64_t in_width, int64_t hidden, in
 int sharing(int64_t tiles, int64_t k)
 {
     int share = 1;
-    while (share < kWarps && tiles * share < kSms * 8 && (k / kStep) / (share * 2) >= 4) share *= 2;
+    static const int tgt = getenv("EMB_TGT") ? atoi(getenv("EMB_TGT")) : 8;
+    while (share < kWarps && tiles * share < kSms * tgt && (k / kStep) / (share * 2) >= 4) share *= 2;
     return share;
 }
 
@@ -360,16 +361,18 @@ extern "C" int emb_expert_layer(const void* ids, int32_t id_bytes, int64_t token
     const Room room(tokens, tokens * k, in_width, hidden, out_width);
     unsigned char* const at = static_cast<unsigned char*>(workspace);
     a.rows = at, a.hidden_at = at + room.rows, a.y = reinterpret_cast<float*>(at + room.rows + room.hidden);
-    a.done = room.done ? reinterpret_cast<int*>(at + room.rows + room.hidden + room.y) : nullptr;
     if (!(a.status = dense_status_word())) return EMB_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int64_t groups = std::min<int64_t>(tokens * k, experts);     // at most
-    static const int force = getenv("EMB_FORCE") ? atoi(getenv("EMB_FORCE")) : -1;
+    static const double thr = getenv("EMB_THR") ? atof(getenv("EMB_THR")) : 6;
+    const double megabytes = groups * (double)hidden * ((activation == EMB_ACT_SWIGLU ? 2 : 1) * in_width + out_width) * 2e-6;
+    const bool tiles = megabytes * (0.028 + 0.006 * tokens * k / groups) > thr;
+    if (!tiles && tokens * k <= kSumInDown) a.done = reinterpret_cast<int*>(at + room.rows + room.hidden + room.y);
     const auto sums = [&]() -> int {
         if (a.done) return EMB_OK;
         return launch_next(layer_sum, dim3((unsigned)((out_width / 4 + kThreads - 1) / kThreads), (unsigned)tokens), kThreads, 0, st, 1, a);
     };
-    if (force == 1 && !a.done) {
+    if (tiles) {
         if (int rc = launch_tiles(a, x_dtype, dtype, st)) return rc;
         return sums();
     }

@@ -68,14 +68,13 @@ __device__ __forceinline__ void make_groups(const Args& a, Groups& g, unsigned c
             const unsigned all = __ballot_sync(0xffffffffu, id >= 0), same = __match_any_sync(0xffffffffu, id) & all;
             const bool leads = id >= 0 && !(same & below);
             const unsigned leaders = __ballot_sync(0xffffffffu, leads);
-            int before = 0;      // members of groups that are led by a lower lane
+            int before = 0, place = 0;      // members of smaller experts' groups, and these groups
             for (unsigned l = leaders; l; l &= l - 1) {
-                const int from = __ffs(l) - 1, members = __popc(__shfl_sync(0xffffffffu, same, from));
-                if (from < __ffs(same) - 1) before += members;
+                const int from = __ffs(l) - 1, members = __popc(__shfl_sync(0xffffffffu, same, from)), other = __shfl_sync(0xffffffffu, id, from);
+                if (other < id) before += members, ++place;
             }
             if (t < P) g.expert_of[t] = (short)id;
             if (leads) {
-                const int place = __popc(leaders & below);
                 g.expert[place] = (short)id;
                 g.first[place] = (short)before;
             }
