@@ -1,4 +1,4 @@
-// The whole expert layer for a few tokens, in two kernels.
+// The whole expert layer for a few tokens.
 //
 //   hidden[a] = act(up[e] x[t]),  y[a] = down[e] hidden[a],  out[t] = sum_j weights[t, j] y[t k + j]
 //
@@ -8,17 +8,20 @@
 // the warp's matrix instruction, 16 bytes a lane; the group's tokens, 8 at a time, are the
 // right one.  The order of k within an instruction is free as long as both operands
 // agree, so a lane's 8 consecutive elements serve two instructions and nothing passes
-// through shared memory.  (The tensor cores' own tiles of 128 rows would leave most SMs
-// without one for a single token, and idle otherwise: at 64 tokens an expert the
-// products take a tenth of the time the weights do.)
+// through shared memory.  (Tiles of 128 rows on the tensor cores leave most SMs without one
+// for a single token; many_weights says from where on they are faster, few_tiles.cu has them.)
 //
 // Where there are fewer tiles of 16 rows than warps, the warps of a block share a tile's k
 // and add up in shared memory, in order.
 //
-// Every block makes the groups for itself in shared memory.  The first kernel leaves
-// hidden in memory, the second y in fp32; whoever finishes a tile of outputs of a
-// token's last assignment adds up these columns of the token, in the order of j: results
-// repeat bit for bit.
+// Two kernels, and up to kSumInDown assignments no more: whoever finishes a tile of outputs of a
+// token's last assignment adds up these columns of the token.  A third one does beyond.
+// Either adds in the order of j, so results repeat bit for bit.  Every block makes the groups
+// for itself in shared memory.
+//
+// One token, 2 of 16 experts, 3328 -> 1024 -> 1024, bf16: 14 us (18 MB; 6 us of it are two kernels of
+// next to nothing); 8 tokens 26 us (94 MB, 3.6 TB/s).  Measured and not kept: twice the weights on their way,
+// in one block an SM (14.0 us for 14.3, 26.0 for 25.9); rows ahead with the weights (13.7 and 27.1).
 #include "few_tokens.cuh"
 
 namespace emb {
@@ -28,7 +31,9 @@ using namespace few;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kPerSm = 2;
-constexpr int kSumInDown = 32;  // assignments up to which layer_down adds up the tokens itself: a third launch costs 2 us, the warps that finish last more
+// Assignments up to which layer_down adds up the tokens itself: a third launch costs 2 us, the last warps' sums more
+// (64 x 8 of 8 in 64 columns: 29 us, and 16 with a third kernel).
+constexpr int kSumInDown = 32;
 constexpr int kStep = 32;       // k of a lane group's 16 bytes
 constexpr int kChunk = 64;      // of a group's assignments at once, at most
 constexpr int kShared = kWarps * (kChunk / 8) * 4 * 32;    // floats that warps add up through
@@ -316,13 +321,24 @@ bool sizes_valid(int64_t tokens, int32_t k, int64_t in_width, int64_t hidden, in
     return widths_valid(in_width) && tokens >= 0 && k >= 1 && k <= kMaxExpertsPerToken && tokens <= kMost / k && widths_valid(hidden) && widths_valid(out_width);
 }
 
+// Whether tiles on the tensor cores are faster.  They cost two more launches, some 6 us, and
+// save 28 ns a megabyte of weights and 6 ns more for each assignment of a group,
+// whose rows the warps here load again for every 16 rows of a weight.  Measured, here and
+// in tiles: 48 x 4 of 64, 1024 -> 2048 -> 1024 (512 MB, 3 a group) 88 and 79 us; 64 x 4 of 16, 3328 -> 2048 -> 1024
+// (287 MB, 16) 87 and 59; 64 x 8 of 8, 2048 -> 2048 -> 2048 (134 MB, 64) 67 and 46; 64 x 2 of 64, 512 -> 512 -> 512
+// (67 MB, 2) 19 and 21; 16 x 2 of 16, 3328 -> 1024 -> 1024 (143 MB, 2) 29 and 35; 1 x 2 of 16, 18 MB, 14 and 26.
+bool many_weights(int64_t assignments, int64_t groups, int64_t hidden, int64_t widths)
+{
+    const double megabytes = (double)groups * hidden * widths * 2e-6;
+    return megabytes * (0.028 + 0.006 * assignments / groups) > 6.0;
+}
+
 // Warps that share a tile's k: as many as keep eight warps of every SM busy, but four
-// steps of k for each.
+// steps of k for each.  (8 x 2 of 16, 3328 -> 1024 -> 1024: 26 us; for four warps 34, for sixteen 30.)
 int sharing(int64_t tiles, int64_t k)
 {
     int share = 1;
-    static const int tgt = getenv("EMB_TGT") ? atoi(getenv("EMB_TGT")) : 8;
-    while (share < kWarps && tiles * share < kSms * tgt && (k / kStep) / (share * 2) >= 4) share *= 2;
+    while (share < kWarps && tiles * share < kSms * 8 && (k / kStep) / (share * 2) >= 4) share *= 2;
     return share;
 }
 
@@ -364,9 +380,7 @@ extern "C" int emb_expert_layer(const void* ids, int32_t id_bytes, int64_t token
     if (!(a.status = dense_status_word())) return EMB_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int64_t groups = std::min<int64_t>(tokens * k, experts);     // at most
-    static const double thr = getenv("EMB_THR") ? atof(getenv("EMB_THR")) : 6;
-    const double megabytes = groups * (double)hidden * ((activation == EMB_ACT_SWIGLU ? 2 : 1) * in_width + out_width) * 2e-6;
-    const bool tiles = megabytes * (0.028 + 0.006 * tokens * k / groups) > thr;
+    const bool tiles = many_weights(tokens * k, groups, hidden, (activation == EMB_ACT_SWIGLU ? 2 : 1) * in_width + out_width);
     if (!tiles && tokens * k <= kSumInDown) a.done = reinterpret_cast<int*>(at + room.rows + room.hidden + room.y);
     const auto sums = [&]() -> int {
         if (a.done) return EMB_OK;

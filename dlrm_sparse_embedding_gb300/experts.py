@@ -351,7 +351,7 @@ def _layer_sizes(ids, ids_type, x, x_stride, x_type, up, up_type, down, down_typ
 def expert_layer(ids: torch.Tensor, x: torch.Tensor, up: torch.Tensor, down: torch.Tensor, weights: torch.Tensor,
                  activation: str = "relu", dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
     """[tokens, out] in `dtype` (default up's): the whole expert layer for a few tokens,
-    sum_j weights[t, j] down[e] act(up[e] x[t]) with e = ids[t, j], in two kernels.
+    sum_j weights[t, j] down[e] act(up[e] x[t]) with e = ids[t, j], in two to four kernels.
 
     What expert_sort, expert_dispatch, expert_linear, the activation, expert_linear and
     expert_combine give, but that the second product's rows stay fp32 up to the sum; up to

@@ -461,8 +461,8 @@ int emb_expert_linear_grad_weight(const emb_expert_plan* plan, const void* grad_
                                   const void* rows, int64_t rows_stride, int64_t in_width, int64_t out_width,
                                   int32_t dtype, void* grad_weight, void* stream);
 
-/* The whole expert layer for a few tokens, from their ids to their sums, in two kernels
- * that read each chosen expert's weights once:
+/* The whole expert layer for a few tokens, from their ids to their sums, in two to four
+ * kernels that read each chosen expert's weights once:
  *   out[t] = sum_j weights[t, j] down[e] act(up[e] x[t]),  e = ids[t, j]
  * ids [tokens, k] as for emb_expert_sort (-1: none; any other id outside [0, E) is
  * treated as -1 and recorded as EMB_ERR_KEY_RANGE); tokens * k is at most

@@ -86,13 +86,27 @@ def check(args, act, dtype=None, out=None):
     return got
 
 
-SIZES = [(1, 1, 1, 8, 8, 8), (1, 2, 16, 3328, 1024, 1024), (2, 1, 3, 16, 24, 40), (3, 4, 5, 40, 72, 8), (7, 3, 12, 1032, 776, 520),
+# the second list's weights are read in tiles on the tensor cores: few or no tokens an expert, up to 64, 128, 512 of one expert
+SMALL = [(1, 1, 1, 8, 8, 8), (1, 2, 16, 3328, 1024, 1024), (2, 1, 3, 16, 24, 40), (3, 4, 5, 40, 72, 8), (7, 3, 12, 1032, 776, 520),
          (8, 8, 1000, 128, 64, 128), (16, 2, 32, 512, 264, 256), (64, 4, 16, 256, 512, 136), (64, 8, 8, 96, 200, 64), (512, 1, 3, 72, 48, 56),
          (100, 5, 1, 64, 32, 24), (8, 64, 7, 64, 56, 72), (33, 2, 1024, 64, 40, 16), (1, 64, 200, 2048, 128, 32), (5, 2, 4, 16, 8, 4104)]
+LARGE = [(64, 8, 8, 520, 1032, 536), (128, 4, 4, 512, 1032, 520), (512, 1, 1, 520, 1160, 512), (8, 4, 32, 1024, 1544, 1032),
+         (60, 4, 40, 1032, 776, 1048), (65, 5, 3, 1000, 1000, 1000)]
+
+
+def in_tiles(T, k, E, D, H, N, act):
+    """The library's rule of when tiles are faster, by megabytes of weights and assignments a group."""
+    groups = min(T * k, E)
+    return groups * H * (D * (2 if act == "swiglu" else 1) + N) * 2e-6 * (0.028 + 0.006 * T * k / groups) > 6
+
+
+def test_the_lists_are_of_both_kinds():
+    for act in ("relu", "swiglu"):
+        assert all(in_tiles(*c, act) for c in LARGE) and not any(in_tiles(*c, act) for c in SMALL)
 
 
 @gpu
-@pytest.mark.parametrize("T,k,E,D,H,N", SIZES)
+@pytest.mark.parametrize("T,k,E,D,H,N", SMALL + LARGE)
 @pytest.mark.parametrize("act", ["relu", "silu", "gelu", "swiglu"])
 @pytest.mark.parametrize("dtype,xt", [(BF, F32), (BF, BF), (HF, HF), (HF, F32)])
 def test_the_layer(T, k, E, D, H, N, act, dtype, xt):
@@ -111,17 +125,31 @@ def test_groups_of_every_size():
 
 
 @gpu
+def test_groups_of_every_size_in_tiles():
+    for n in [1, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 200, 255]:
+        ids, x, up, down, weights = case(n, n, 2, 64, 1024, 1544, 1032, BF, BF)
+        ids[:, 0], ids[:, 1] = 2, -1
+        if n > 20:
+            ids[3, 1], ids[9, 1] = 63, 0
+            weights[3, 1] = weights[9, 1] = 0.5
+        assert in_tiles(n, 2, 64, 1024, 1544, 1032, "relu") == (n >= 15)
+        check((ids, x, up, down, weights), "relu")
+
+
+@gpu
 @pytest.mark.parametrize("extra", [8, 24])
-def test_rows_of_any_stride(extra):
-    ids, x, up, down, weights = case(1, 6, 2, 4, 128, 64, 64, BF, F32)
-    big = torch.full((6, 128 + extra), float("nan"), device="cuda")
-    big[:, :128] = x
-    assert torch.equal(check((ids, big[:, :128], up, down, weights), "gelu"), emb.expert_layer(ids, x, up, down, weights, "gelu"))
+@pytest.mark.parametrize("T,k,E,D,H,N", [(6, 2, 4, 128, 64, 64), LARGE[0]])
+@pytest.mark.parametrize("xt", [F32, BF])
+def test_rows_of_any_stride(extra, T, k, E, D, H, N, xt):
+    ids, x, up, down, weights = case(1, T, k, E, D, H, N, BF, xt)
+    big = torch.full((T, D + extra), float("nan"), device="cuda", dtype=xt)
+    big[:, :D] = x
+    assert torch.equal(check((ids, big[:, :D], up, down, weights), "gelu"), emb.expert_layer(ids, x, up, down, weights, "gelu"))
 
 
 @gpu
 def test_tokens_without_experts_and_nothing_at_all():
-    for T, k, E, D, H, N in ((5, 3, 4, 64, 32, 24), (64, 8, 8, 512, 1024, 2056)):
+    for T, k, E, D, H, N in ((5, 3, 4, 64, 32, 24), (40, 3, 4, 64, 32, 24), (64, 8, 8, 512, 1024, 2056)):
         ids, x, up, down, weights = case(2, T, k, E, D, H, N, HF, HF)
         ids[T // 2] = -1
         x[T // 2] = float("nan")       # not read
@@ -135,8 +163,10 @@ def test_tokens_without_experts_and_nothing_at_all():
 
 @gpu
 @pytest.mark.parametrize("bad", [7, -2, 2 ** 31 - 1, -2 ** 31])
-def test_ids_out_of_range_are_dropped_and_reported(bad):
-    ids, x, up, down, weights = case(3, 5, 2, 7, 64, 32, 24, BF, BF)
+@pytest.mark.parametrize("T,D,H,N", [(5, 64, 32, 24), (50, 64, 32, 24), (256, 512, 1032, 520)])
+def test_ids_out_of_range_are_dropped_and_reported(bad, T, D, H, N):
+    ids, x, up, down, weights = case(3, T, 2, 7, D, H, N, BF, BF)
+    assert in_tiles(T, 2, 7, D, H, N, "relu") == (T == 256)
     ids[2, 1] = bad
     weights[2, 1] = float("nan")
     got = check((ids, x, up, down, weights), "relu")
@@ -149,8 +179,10 @@ def test_ids_out_of_range_are_dropped_and_reported(bad):
 
 @gpu
 @pytest.mark.parametrize("act", ["relu", "silu", "gelu", "swiglu"])
-def test_a_tokens_infinities_and_nans_stay_its_own(act):
-    ids, x, up, down, weights = case(4, 20, 2, 3, 128, 64, 40, BF, BF, act)
+@pytest.mark.parametrize("D,H,N", [(128, 64, 40), (4096, 4096, 4096)])
+def test_a_tokens_infinities_and_nans_stay_its_own(act, D, H, N):
+    ids, x, up, down, weights = case(4, 20, 2, 3, D, H, N, BF, BF, act)
+    assert in_tiles(20, 2, 3, D, H, N, act) == (D == 4096)
     clean = emb.expert_layer(ids, x, up, down, weights, act)
     x[11, 5] = float("nan")
     got = emb.expert_layer(ids, x, up, down, weights, act)
@@ -163,7 +195,7 @@ def test_a_tokens_infinities_and_nans_stay_its_own(act):
 
 
 @gpu
-@pytest.mark.parametrize("T,k,E,D,H,N", [(1, 2, 16, 3328, 1024, 1024), (48, 4, 64, 256, 512, 256), (64, 8, 8, 96, 200, 64)])
+@pytest.mark.parametrize("T,k,E,D,H,N", [(1, 2, 16, 3328, 1024, 1024), (48, 4, 64, 256, 512, 256), (64, 8, 8, 96, 200, 64)] + LARGE[:3])
 def test_results_repeat(T, k, E, D, H, N):
     args = case(5, T, k, E, D, H, N, BF, F32, "swiglu")
     first = emb.expert_layer(*args, "swiglu")
@@ -185,8 +217,10 @@ def test_weights_past_32_bits():
 
 
 @gpu
-def test_streams_and_graphs():
-    args = case(7, 16, 2, 8, 256, 128, 64, HF, HF, "gelu")
+@pytest.mark.parametrize("T,D,H,N", [(16, 256, 128, 64), (40, 256, 128, 64), (256, 512, 1032, 520)])
+def test_streams_and_graphs(T, D, H, N):
+    args = case(7, T, 2, 8, D, H, N, HF, HF, "gelu")
+    assert in_tiles(T, 2, 8, D, H, N, "gelu") == (T == 256)
     ref = emb.expert_layer(*args, "gelu")
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
@@ -195,7 +229,7 @@ def test_streams_and_graphs():
     assert torch.equal(got, ref)
     graphs = []
     for seed in (8, 9):
-        a = case(seed, 16, 2, 8, 256, 128, 64, HF, HF, "gelu")
+        a = case(seed, T, 2, 8, D, H, N, HF, HF, "gelu")
         emb.expert_layer(*a, "gelu")
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
@@ -204,17 +238,18 @@ def test_streams_and_graphs():
         graphs.append((graph, a, out, again))
     for turn in range(4):
         for graph, a, out, again in graphs:
-            a[0].copy_(torch.randint(-1, 8, (16, 2), generator=gen(turn), device="cuda"))
+            a[0].copy_(torch.randint(-1, 8, (T, 2), generator=gen(turn), device="cuda"))
             a[4].uniform_()
             graph.replay()
             assert torch.equal(out, emb.expert_layer(*a, "gelu")) and torch.equal(again, emb.expert_layer(*a, "silu"))
 
 
 @gpu
-def test_calls_on_two_streams_at_once():
+@pytest.mark.parametrize("T,k,E,D,H,N", [(8, 4, 16, 1024, 1024, 512), (32, 4, 16, 512, 512, 512), LARGE[0], LARGE[1]])
+def test_calls_on_two_streams_at_once(T, k, E, D, H, N):
     jobs = []
     for seed in range(2):
-        args = case(20 + seed, 32, 4, 16, 1024, 1024, 512, BF, F32)
+        args = case(20 + seed, T, k, E, D, H, N, BF, F32)
         jobs.append((torch.cuda.Stream(), args, emb.expert_layer(*args)))
     torch.cuda.synchronize()
     got = [[emb.expert_layer(*args, stream=s) for s, args, _ in jobs] for _ in range(20)]
@@ -225,7 +260,7 @@ def test_calls_on_two_streams_at_once():
 
 
 @gpu
-@pytest.mark.parametrize("T,k,E,D,H,N", [(1, 2, 16, 3328, 1024, 1024), (64, 4, 16, 512, 1024, 256)])
+@pytest.mark.parametrize("T,k,E,D,H,N", [(1, 2, 16, 3328, 1024, 1024), (64, 4, 16, 512, 1024, 256), LARGE[1]])
 def test_it_is_the_plans_calls_at_once(T, k, E, D, H, N):
     ids, x, up, down, weights = args = case(10, T, k, E, D, H, N, BF, F32, dropped=0.1)
     plan = emb.expert_sort(ids, E)
@@ -249,6 +284,17 @@ def test_a_block_of_the_dense_side():
     ref = torch.where(kept, y.double() / 0.75, 0.0) + x.double()
     assert ((z.double() - ref).abs() <= 3 * E24 * (y.double().abs() * 2 + ref.abs())).all()
     assert emb.dense_status() == emb.EMB_OK
+
+
+@gpu
+def test_inputs_that_require_gradients_and_tensors_of_another_device(monkeypatch):
+    ids, x, up, down, weights = case(12, 3, 2, 4, 64, 32, 24, BF, F32)
+    weights = torch.rand(3, 2, device="cuda").requires_grad_()
+    out = emb.expert_layer(ids, x.requires_grad_(), up.requires_grad_(), down.requires_grad_(), weights)
+    assert not out.requires_grad
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)      # nothing is launched: the tensors are on 0
+    with pytest.raises(ValueError, match="current device"):
+        emb.expert_layer(ids, x, up, down, weights)
 
 
 def test_refusals_without_a_gpu():

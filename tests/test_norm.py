@@ -398,6 +398,50 @@ def test_two_graphs_replayed_in_turn():
             assert all(torch.equal(a, b) for a, b in zip(out, emb.layer_norm_grad(gy, x, w)))
 
 
+@gpu
+def test_inputs_that_require_gradients_and_tensors_of_another_device(monkeypatch):
+    x, w = torch.randn(5, 40, device="cuda").requires_grad_(), torch.randn(40, device="cuda").requires_grad_()
+    calls = [lambda: emb.layer_norm(x, w, w), lambda: emb.layer_norm_grad(x, x, w), lambda: emb.dropout(x, 0.1, 1, residual=x),
+             lambda: emb.dropout_grad(x, 0.1, 1)]
+    for call in calls:
+        got = call()
+        assert not any(t.requires_grad for t in (got if isinstance(got, tuple) else (got,)))
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)      # nothing is launched: the tensors are on 0
+    for call in calls:
+        with pytest.raises(ValueError, match="current device"):
+            call()
+
+
+@gpu
+def test_under_autograd():
+    # the explicit gradients in a torch.autograd.Function
+    class Block(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w, b):
+            ctx.save_for_backward(x, w)
+            return emb.dropout(emb.layer_norm(x, w, b), 0.25, 5, residual=x)
+
+        @staticmethod
+        def backward(ctx, grad):
+            x, w = ctx.saved_tensors
+            grad = grad.contiguous()
+            dx, dw, db = emb.layer_norm_grad(emb.dropout_grad(grad, 0.25, 5), x, w)
+            return dx + grad, dw, db
+
+    g = gen(9)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, w, b, gy = r(300, 264).requires_grad_(), r(264).requires_grad_(), r(264).requires_grad_(), r(300, 264)
+    keep = (emb.dropout(torch.ones(300, 264, device="cuda"), 0.25, 5) != 0).double() / 0.75
+    leaves = [t.detach().double().requires_grad_() for t in (x, w, b)]
+    xd, wd, bd = leaves
+    h = (xd - xd.mean(1, keepdim=True)) / (xd.var(1, correction=0, keepdim=True) + 1e-5).sqrt()
+    ref = torch.autograd.grad(((h * wd + bd) * keep + xd).mul(gy.double()).sum(), leaves)
+    got = torch.autograd.grad(Block.apply(x, w, b).mul(gy).sum(), (x, w, b))
+    for a, e in zip(got, ref):
+        # sums of 300 terms of size 1, a chain of at most 64 + 8 roundings
+        assert (a.double() - e).abs().max() <= 300 * 72 * E
+
+
 REFUSALS = [
     ("2-d", lambda n, x, w: n.layer_norm(x[0])),
     ("CUDA", lambda n, x, w: n.layer_norm(x.cpu())),
