@@ -1,16 +1,18 @@
 """A recommender's training step with experts: pooled embeddings, k of E expert
 networks a sample, one logit, and every weight stepped.
 
-    python examples/train_experts.py [--steps 60]
+    python examples/train_experts.py [--steps 60] [--norm] [--dropout 0.1]
 
 The embedding layer's output (fp32) is each sample's token.  A router gives k
 experts and their weights; expert_sort plans the batch, expert_dispatch brings
 the rows into expert order in bf16, two expert_linear calls with a ReLU between
 them are the experts' networks, expert_combine adds their answers up.  The
 gradients take the same calls' gradients back to grad_out of the layer's
-backward_update.  The experts' weights, [E, out, in], are stepped with
-orthogonalised momentum (the Muon optimiser), the router and the last layer with
-plain SGD.
+backward_update.  With --norm the tokens go through layer_norm first, with --dropout
+the experts' answer through dropout, and their gradients likewise.  The experts'
+weights, [E, out, in], are stepped with orthogonalised momentum (the Muon
+optimiser), the router, the norm and the last layer with plain SGD.  predict() is
+the trained tower for a few samples: the whole expert layer in one call, expert_layer.
 """
 from __future__ import annotations
 
@@ -29,7 +31,8 @@ import dlrm_sparse_embedding_gb300 as emb  # noqa: E402
 class ExpertTower:
     """logit[b] = <head, sum_j w[b, j] W2[e] relu(W1[e] x[b])> over sample b's k experts e."""
 
-    def __init__(self, width: int, hidden: int, out: int, experts: int, k: int, seed: int = 0):
+    def __init__(self, width: int, hidden: int, out: int, experts: int, k: int, seed: int = 0, norm: bool = False,
+                 dropout: float = 0.0):
         g = torch.Generator(device="cuda")
         g.manual_seed(seed)
 
@@ -42,22 +45,43 @@ class ExpertTower:
         self.w = [normal(experts, hidden, width), normal(experts, out, hidden)]
         self.w16 = [w.bfloat16() for w in self.w]
         self.momentum = [torch.zeros_like(w) for w in self.w]
+        # the norm's weight and bias, and of the last backward their gradients
+        self.norm = [torch.ones(width, device="cuda"), torch.zeros(width, device="cuda")] if norm else None
+        self.norm_grad = None
+        self.dropout, self.seed, self.steps = dropout, seed, 0
+
+    def route(self, x: torch.Tensor):
+        """The tokens as the experts take them, their experts and weights."""
+        if self.norm:
+            x = emb.layer_norm(x, *self.norm)
+        scores, ids = torch.topk(x @ self.router.t(), self.k, dim=1)
+        return x, ids, torch.softmax(scores, dim=1)
+
+    def predict(self, x: torch.Tensor) -> torch.Tensor:
+        """Logits of a few samples, up to 512 / k: nothing is dropped, nothing kept."""
+        x, ids, weights = self.route(x)
+        return emb.expert_layer(ids, x, *self.w16, weights, dtype=torch.float32) @ self.head
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        scores, ids = torch.topk(x @ self.router.t(), self.k, dim=1)
-        weights = torch.softmax(scores, dim=1)
+        raw = x
+        x, ids, weights = self.route(raw)
         plan = emb.expert_sort(ids, self.experts)
         rows = emb.expert_dispatch(plan, x, dtype=torch.bfloat16)
         hidden = torch.relu_(emb.expert_linear(plan, rows, self.w16[0]))
         y = emb.expert_linear(plan, hidden, self.w16[1])
         out = emb.expert_combine(plan, y, weights, dtype=torch.float32)
+        if self.dropout:
+            out = emb.dropout(out, self.dropout, self.seed, self.steps)    # another mask every step
         self.kept = (x, ids, weights, plan, rows, hidden, y, out)
+        self.raw = raw
         return out @ self.head
 
     def backward(self, grad_logit: torch.Tensor):
         """Gradients of x, the router, the head and the experts' weights."""
         x, ids, weights, plan, rows, hidden, y, out = self.kept
         grad_out = grad_logit[:, None] * self.head
+        if self.dropout:
+            grad_out = emb.dropout_grad(grad_out, self.dropout, self.seed, self.steps)
         grad_y, grad_weights = emb.expert_combine_grad(plan, grad_out, y, weights)
         grad_hidden, grad_w2 = emb.expert_linear_grad(plan, grad_y, hidden, self.w16[1])
         grad_hidden.mul_(hidden > 0)
@@ -66,9 +90,16 @@ class ExpertTower:
         # the softmax over the chosen scores
         grad_scores = weights * (grad_weights - (weights * grad_weights).sum(1, keepdim=True))
         grad_router_out = torch.zeros(x.shape[0], self.experts, device=x.device).scatter_(1, ids, grad_scores)
-        return (grad_x + grad_router_out @ self.router, grad_router_out.t() @ x, grad_logit @ out, [grad_w1, grad_w2])
+        grad_x = grad_x + grad_router_out @ self.router
+        if self.norm:
+            grad_x, *self.norm_grad = emb.layer_norm_grad(grad_x, self.raw, self.norm[0])
+        return (grad_x, grad_router_out.t() @ x, grad_logit @ out, [grad_w1, grad_w2])
 
     def step(self, grad_router, grad_head, grad_w, lr: float, momentum: float = 0.9) -> None:
+        self.steps += 1
+        if self.norm:
+            for p, g in zip(self.norm, self.norm_grad):
+                p -= lr * g
         self.router -= lr * grad_router
         self.head -= lr * grad_head
         for w, w16, m, g in zip(self.w, self.w16, self.momentum, grad_w):
@@ -79,7 +110,8 @@ class ExpertTower:
             w16.copy_(w)
 
 
-def train(steps: int, batch: int = 1024, experts: int = 8, k: int = 2, lr: float = 0.1, report=print):
+def train(steps: int, batch: int = 1024, experts: int = 8, k: int = 2, lr: float = 0.1, report=print, norm: bool = False,
+          dropout: float = 0.0):
     """Learns whether the first table's key is in the upper half; returns the losses."""
     tables = [ci.TableSpec(2000, 32, "f32", "sum", "adagrad", lr=0.05) for _ in range(8)]
     w = ci.Workload("experts", tuple(tables), batch, "fixed", 1, 1, "uniform")
@@ -87,7 +119,7 @@ def train(steps: int, batch: int = 1024, experts: int = 8, k: int = 2, lr: float
     losses = []
     try:
         layer.init_uniform(0, -0.5, 0.5)
-        tower = ExpertTower(layer.total_dim, 512, 64, experts, k)
+        tower = ExpertTower(layer.total_dim, 512, 64, experts, k, norm=norm, dropout=dropout)
         for step in range(steps):
             b = ci.make_batch(w, seed=step)
             label = torch.from_numpy((b.keys[:batch] >= 1000).astype("float32")).cuda()
@@ -101,6 +133,11 @@ def train(steps: int, batch: int = 1024, experts: int = 8, k: int = 2, lr: float
             losses.append(loss.item())
             if step % 10 == 0 or step == steps - 1:
                 report("step %3d  loss %.4f" % (step, losses[-1]))
+        if losses:
+            few = layer.forward_infer(torch.from_numpy(b.keys).cuda(), torch.from_numpy(b.offsets).cuda(),
+                                      torch.from_numpy(b.table_ids).cuda(), batch)[:8]
+            chances = torch.sigmoid(tower.predict(few)).tolist()
+            report("served, with the label: " + " ".join("%.2f (%d)" % (p, l) for p, l in zip(chances, label.tolist())))
         if layer.sync_status() != emb.EMB_OK or emb.dense_status() != emb.EMB_OK:
             raise RuntimeError("a call reported an error")
     finally:
@@ -111,4 +148,7 @@ def train(steps: int, batch: int = 1024, experts: int = 8, k: int = 2, lr: float
 if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--steps", type=int, default=60)
-    train(ap.parse_args().steps)
+    ap.add_argument("--norm", action="store_true", help="layer norm before the experts")
+    ap.add_argument("--dropout", type=float, default=0.0, help="share of the experts' answer that is dropped")
+    args = ap.parse_args()
+    train(args.steps, norm=args.norm, dropout=args.dropout)
