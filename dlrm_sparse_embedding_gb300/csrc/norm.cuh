@@ -67,6 +67,7 @@ constexpr int kFew = 16, kMany = 32;
 constexpr int kMaxStages = 8;
 constexpr int kSharedBytes = 226 * 1024;         // of an SM, for its blocks
 constexpr int kOwnBytes = 2560;                  // of a block beside its stages
+constexpr int kChunkBytes = 4096;                // of a warp's stage
 constexpr int kColumnRows = 8;                   // rows at a time of a block of wide_columns
 // Registers a thread: what its elements take.
 constexpr int registers(int per_thread, bool grad, bool vectors) { return grad || per_thread == kMany ? 128 : vectors ? 80 : 96; }
@@ -244,10 +245,12 @@ struct Piece {
         for (int e = 0; e < E; e += 2) to[e / 2] = Two(r[e / V][e % V], r[(e + 1) / V][(e + 1) % V]);
     }
 
-    // A row in shared memory and its results.  first_sums and second_sums add up over the
-    // row's threads; any(flag) tells whether a row's of all that add up together is set.
-    template <class S1, class S2, class ANY>
-    __device__ __forceinline__ void row(const Args& a, const X* x, const Y* gy, int64_t row, bool has, float inv_n, S1 first_sums, S2 second_sums, ANY any)
+    // A row in shared memory, and its results to where() (null: nowhere).  first_sums and
+    // second_sums add up over the row's threads; any(flag) tells whether a row's of all
+    // that add up together is set.
+    using O = typename std::conditional<GRAD, X, Y>::type;
+    template <class WHERE, class S1, class S2, class ANY>
+    __device__ __forceinline__ void row(const Args& a, const X* x, const Y* gy, WHERE where, bool has, float inv_n, S1 first_sums, S2 second_sums, ANY any)
     {
         constexpr int N = GRAD ? 4 : 2;
         take(x, has, v);
@@ -327,12 +330,11 @@ struct Piece {
             const float2 both = r.both();
             o[2 * i] = both.x, o[2 * i + 1] = both.y;
         }
-        if (!has || !a.out) return;
-        using O = typename std::conditional<GRAD, X, Y>::type;
-        O* const out = static_cast<O*>(a.out) + row * width + first;
+        O* const out = where();
+        if (!has || !out) return;
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (in(u)) store_vec<V, O>(out + u * step, reinterpret_cast<const float(&)[V]>(o[u * V]));
+            if (in(u)) store_vec<V, O>(out + first + u * step, reinterpret_cast<const float(&)[V]>(o[u * V]));
     }
 
     __device__ __forceinline__ float sum_of(int which, int e) const
@@ -445,7 +447,8 @@ __global__ void __maxnreg__(registers(U * V, GRAD, V > 1)) block_rows(const Args
         const uint32_t skip_x = V > 1 ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(x + row * a.x_stride) & 15);
         const uint32_t skip_g = V > 1 || !GRAD ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(g + row * a.g_stride) & 15);
         p.row(
-            a, reinterpret_cast<const X*>(at + skip_x), reinterpret_cast<const Y*>(at + a.x_slot + skip_g), row, true, inv_n,
+            a, reinterpret_cast<const X*>(at + skip_x), reinterpret_cast<const Y*>(at + a.x_slot + skip_g),
+            [&] { return a.out ? static_cast<typename Piece<V, U, GRAD, true, X, Y>::O*>(a.out) + row * a.width : nullptr; }, true, inv_n,
             [&](auto& s) { block_sums(s, part[0]); }, [&](auto& s) { block_sums(s, part[1]); }, [](bool large) { return large; });
         // every thread has taken the row for good: the second sums' barrier has been met
         const int64_t next = row + (int64_t)a.stages * gridDim.x;
@@ -486,11 +489,21 @@ __global__ void __maxnreg__(registers(U * V, GRAD, V > 1)) warp_rows(const Args 
     const int64_t chunks = (a.rows + a.chunk - 1) / a.chunk, step = (int64_t)gridDim.x * kWarps;
     unsigned char* const ring = dynamic + (size_t)warp * a.stages * (a.x_slot + a.g_slot);
 
+    const bool whole = a.x_whole && (!GRAD || a.g_whole);
     const auto copy = [&](int64_t chunk, int stage) {   // the whole warp
         unsigned char* const to = ring + stage * (a.x_slot + a.g_slot);
         const uint32_t bar = tc::smem_addr(&full[warp][stage]);
         const int64_t row = chunk * a.chunk;
         const int have = (int)min((int64_t)a.chunk, a.rows - row);
+        if (whole) {
+            if (lane == 0) {
+                const Span sx(x + row * a.x_stride, (int64_t)have * a.width * sizeof(X)), sg(GRAD ? g + row * a.g_stride : nullptr, GRAD ? (int64_t)have * a.width * sizeof(Y) : 0);
+                tc::bar_expect(bar, sx.bytes + sg.bytes);
+                tc::copy_bytes(tc::smem_addr(to), sx.from, sx.bytes, bar);
+                if (GRAD) tc::copy_bytes(tc::smem_addr(to + a.x_slot), sg.from, sg.bytes, bar);
+            }
+            return;
+        }
         const auto one = [&](const auto* base, int64_t stride, bool whole, int pitch, unsigned char* dst, bool send) {
             const int i = whole ? 0 : lane;
             const Span s(base + (row + i) * stride, (whole ? have : 1) * (int64_t)a.width * sizeof(*base));
@@ -506,12 +519,12 @@ __global__ void __maxnreg__(registers(U * V, GRAD, V > 1)) warp_rows(const Args 
         one(x, a.x_stride, a.x_whole, a.x_pitch, to, true);
         if (GRAD) one(g, a.g_stride, a.g_whole, a.g_pitch, to + a.x_slot, true);
     };
-    // row i of a stage
-    const auto place = [&](const auto* base, int64_t stride, bool whole, int pitch, const unsigned char* from, int64_t first, int i) {
-        using T = typename std::remove_cv<typename std::remove_pointer<decltype(base)>::type>::type;
-        const uint32_t skip = V > 1 ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(base + (whole ? first : first + i) * stride) & 15);
-        return reinterpret_cast<const T*>(from + skip + (whole ? i * a.width * (int)sizeof(T) : i * pitch));
+    // where a stage's first row, or row i by itself, begins beyond a 16-byte boundary
+    const auto skip = [](const auto* base, int64_t stride, int64_t row) {
+        return V > 1 ? 0 : (int)(reinterpret_cast<uintptr_t>(base + row * stride) & 15);
     };
+    const int x_row = a.x_whole ? a.width * (int)sizeof(X) : a.x_pitch, g_row = a.g_whole ? a.width * (int)sizeof(Y) : a.g_pitch;
+    using O = typename Piece<V, U, GRAD, false, X, Y>::O;
 
     const int64_t mine = (int64_t)blockIdx.x * kWarps + warp;
     for (int i = 0; i < a.stages; ++i)
@@ -525,13 +538,20 @@ __global__ void __maxnreg__(registers(U * V, GRAD, V > 1)) warp_rows(const Args 
         if (!(ok = tc::bar_wait_warp(tc::smem_addr(&full[warp][stage]), phase, &gave_up))) break;
         const unsigned char* const at = ring + stage * (a.x_slot + a.g_slot);
         const int64_t first = chunk * a.chunk;
+        const int left = (int)min((int64_t)a.chunk, a.rows - first);
+        const unsigned char* from_x = at + sub * x_row;
+        const unsigned char* from_g = at + a.x_slot + sub * g_row;
+        if (a.x_whole) from_x += skip(x, a.x_stride, first);
+        if (GRAD && a.g_whole) from_g += skip(g, a.g_stride, first);
+        O* out = a.out ? static_cast<O*>(a.out) + (first + sub) * a.width : nullptr;
         for (int i = sub; i < a.chunk; i += at_once) {
-            const int64_t row = first + i;
-            const bool has = row < a.rows;
+            const int sx = a.x_whole ? 0 : skip(x, a.x_stride, first + i), sg = !GRAD || a.g_whole ? 0 : skip(g, a.g_stride, first + i);
             p.row(
-                a, place(x, a.x_stride, a.x_whole, a.x_pitch, at, first, i), place(g, a.g_stride, a.g_whole, a.g_pitch, at + a.x_slot, first, i), row, has,
-                inv_n, [&](auto& s) { lane_sums(s, lanes); }, [&](auto& s) { lane_sums(s, lanes); },
-                [](bool large) { return __any_sync(0xffffffffu, large) != 0; });
+                a, reinterpret_cast<const X*>(from_x + sx), reinterpret_cast<const Y*>(from_g + sg), [&] { return out; }, i < left, inv_n,
+                [&](auto& s) { lane_sums(s, lanes); }, [&](auto& s) { lane_sums(s, lanes); }, [](bool large) { return __any_sync(0xffffffffu, large) != 0; });
+            from_x += at_once * x_row;
+            from_g += at_once * g_row;
+            if (out) out += at_once * a.width;
         }
         __syncwarp();
         if (chunk + a.stages * step < chunks) copy(chunk + a.stages * step, stage);
@@ -696,9 +716,9 @@ int launch_rows(Args a, int y_dtype, bool vectors, const Shape& s, cudaStream_t 
             };
             const bool warps = s.kind == kWarpRows;
             if (warps) {
-                // about 2 KB of a stage's rows, so that copies are long; a lane sends a row
+                // about kChunkBytes of a stage's rows, so that copies are long; a lane sends a row
                 const int at_once = 32 / s.tx, row_bytes = a.width * (int)(sizeof(X) + (GRAD ? sizeof(Y) : 0));
-                a.chunk = std::max(at_once, std::min(32, 2048 / row_bytes / at_once * at_once));
+                a.chunk = std::max(at_once, std::min(32, kChunkBytes / row_bytes / at_once * at_once));
             }
             a.x_slot = slot(sizeof(X), a.x_stride, a.x_whole, a.x_pitch);
             if (GRAD) a.g_slot = slot(sizeof(Y), a.g_stride, a.g_whole, a.g_pitch);
