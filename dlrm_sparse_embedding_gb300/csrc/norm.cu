@@ -25,8 +25,8 @@ Shape shape_of(int64_t rows, int64_t width, bool grad, bool vectors)
         s.kind = kWideRows;
         s.tx = kWideThreads, s.ty = 1;
         s.blocks = (int)std::min<int64_t>(rows, 2 * kSms);
-        const int64_t columns = (width + 31) / 32;   // of blocks of the column sums, at most
-        s.chunks = (int)std::max<int64_t>(1, std::min((rows + kColumnRows - 1) / kColumnRows, 8 * kSms / columns));
+        const int64_t columns = (width + 127) / 128;   // blocks of the column sums across a row, of vectors of 4
+        s.chunks = (int)std::max<int64_t>(1, std::min((rows + 4 * kColumnRows - 1) / (4 * kColumnRows), 8 * kSms / columns));
         return s;
     }
     s.kind = width <= 32 * most ? kWarpRows : kBlockRows;

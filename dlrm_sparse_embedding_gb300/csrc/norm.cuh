@@ -86,6 +86,27 @@ __device__ __forceinline__ float param(const void* p, int dtype, int64_t i, floa
     return __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(p) + i));
 }
 
+// V of them from i on, a vector where they are at its boundary.
+template <int V>
+__device__ __forceinline__ void params(const void* p, int dtype, int64_t i, float none, float (&to)[V])
+{
+    if (V > 1 && p && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+        const auto get = [&](auto t) {
+            using T = decltype(t);
+            Raw<V, T> r;
+            r.load_again(static_cast<const T*>(p) + i);
+#pragma unroll
+            for (int q = 0; q < V; ++q) to[q] = r[q];
+        };
+        if (dtype == EMB_F32) get(float());
+        else if (dtype == EMB_F16) get(__half());
+        else get(__nv_bfloat16());
+    } else {
+#pragma unroll
+        for (int q = 0; q < V; ++q) to[q] = param(p, dtype, i + q, none);
+    }
+}
+
 __device__ __forceinline__ void store_param(void* p, int dtype, int64_t i, float v)
 {
     if (!p) return;
@@ -595,7 +616,7 @@ __global__ void __launch_bounds__(kWideThreads) wide_rows(const Args a)
             float s1[1] = {};
             for (int c = threadIdx.x * V; c < width; c += step) {
                 Raw<V, X> v;
-                v.load(x + c);
+                v.load_again(x + c);
 #pragma unroll
                 for (int q = 0; q < V; ++q) s1[0] += v[q] * scale;
             }
@@ -605,15 +626,19 @@ __global__ void __launch_bounds__(kWideThreads) wide_rows(const Args a)
             for (int c = threadIdx.x * V; c < width; c += step) {
                 Raw<V, X> v;
                 Raw<V, Y> gr;
-                v.load(x + c);
-                if (GRAD) gr.load(g + c);
+                v.load_again(x + c);
+                float w[V];
+                if (GRAD) {
+                    gr.load_again(g + c);
+                    params<V>(a.weight, a.param_dtype, c, 1.f, w);
+                }
 #pragma unroll
                 for (int q = 0; q < V; ++q) {
                     const float e = v[q] * scale - m;
                     s[0] += e;
                     s[1] = __fmaf_rn(e, e, s[1]);
                     if constexpr (GRAD) {
-                        const float gw = gr[q] * param(a.weight, a.param_dtype, c + q, 1.f);
+                        const float gw = gr[q] * w[q];
                         s[2] += gw;
                         s[3] = __fmaf_rn(gw, e, s[3]);
                     }
@@ -637,7 +662,7 @@ __global__ void __launch_bounds__(kWideThreads) wide_rows(const Args a)
         for (int c = threadIdx.x * V; c < width; c += step) {
             Raw<V, X> v;
             Raw<V, Y> gr;
-            float o[V];
+            float o[V], w[V], b[V];
             v.load(x + c);
             if (GRAD) gr.load(g + c);
 #pragma unroll
@@ -662,18 +687,30 @@ __global__ void __launch_bounds__(32 * kColumnRows) wide_columns(const Args a)
     wait_for_earlier();
     const int width = a.width, lane = threadIdx.x, c = (blockIdx.x * 32 + lane) * V;
     float acc_w[V] = {}, acc_b[V] = {};
+    constexpr int kAhead = 4;      // rows on their way
+    const int64_t step = (int64_t)gridDim.y * kColumnRows;
     if (c < width)
-        for (int64_t row = (int64_t)blockIdx.y * kColumnRows + threadIdx.y; row < a.rows; row += (int64_t)gridDim.y * kColumnRows) {
-            const float4 st = a.stats[row];
-            const Moments mo{st.x, st.y, st.z, st.w};
-            Raw<V, X> v;
-            Raw<V, Y> g;
-            v.load(static_cast<const X*>(a.x) + row * a.x_stride + c);
-            g.load(static_cast<const Y*>(a.g) + row * a.g_stride + c);
+        for (int64_t row0 = (int64_t)blockIdx.y * kColumnRows + threadIdx.y; row0 < a.rows; row0 += kAhead * step) {
+            float4 st[kAhead];
+            Raw<V, X> v[kAhead];
+            Raw<V, Y> g[kAhead];
 #pragma unroll
-            for (int q = 0; q < V; ++q) {
-                acc_w[q] = __fmaf_rn(g[q], mo.h(v[q]), acc_w[q]);
-                acc_b[q] += g[q];
+            for (int i = 0; i < kAhead; ++i) {
+                const int64_t row = row0 + i * step;
+                if (row >= a.rows) continue;
+                st[i] = a.stats[row];
+                v[i].load(static_cast<const X*>(a.x) + row * a.x_stride + c);
+                g[i].load(static_cast<const Y*>(a.g) + row * a.g_stride + c);
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (row0 + i * step >= a.rows) continue;
+                const Moments mo{st[i].x, st[i].y, st[i].z, st[i].w};
+#pragma unroll
+                for (int q = 0; q < V; ++q) {
+                    acc_w[q] = __fmaf_rn(g[i][q], mo.h(v[i][q]), acc_w[q]);
+                    acc_b[q] += g[i][q];
+                }
             }
         }
     for (int which = 0; which < 2; ++which) {

@@ -36,6 +36,12 @@ struct Raw {
             else w[i] = p[i];
         }
     }
+    // what is read again soon
+    __device__ __forceinline__ void load_again(const T* p)
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const Word*>(p) + i);
+    }
     __device__ __forceinline__ void clear()
     {
 #pragma unroll
