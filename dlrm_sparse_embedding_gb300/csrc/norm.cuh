@@ -20,6 +20,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 
 #include "emb_internal.cuh"
 #include "rows.cuh"
@@ -729,6 +730,24 @@ __global__ void __launch_bounds__(32 * kColumnRows) wide_columns(const Args a)
     }
 }
 
+// Shared memory of its blocks is asked for once a device, as much as there may be.
+template <void (*KERNEL)(Args)>
+int launch_ring(const Args& a, int blocks, dim3 block, size_t smem, cudaStream_t st)
+{
+    constexpr int kMaxDevices = 64;
+    static std::atomic<bool> sized[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return EMB_ERR_CUDA;
+    if (!sized[dev].load(std::memory_order_relaxed)) {
+        if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes - kOwnBytes) != cudaSuccess) {
+            cudaGetLastError();
+            return EMB_ERR_CUDA;
+        }
+        sized[dev].store(true, std::memory_order_relaxed);
+    }
+    return launch_next(KERNEL, blocks, block, smem, st, 1, a);
+}
+
 template <class X>
 int launch_rows(Args a, int y_dtype, bool vectors, const Shape& s, cudaStream_t st)
 {
@@ -765,13 +784,9 @@ int launch_rows(Args a, int y_dtype, bool vectors, const Shape& s, cudaStream_t 
             if (warps && GRAD) smem = std::max(smem, (size_t)kThreads * kFew * sizeof(float));
             constexpr int kLong = GRAD || V == 1 ? kFew : kMany;
             const bool few = s.per_thread == kFew;
-            const auto kernel = warps ? (few ? warp_rows<V, kFew / V, GRAD, X, Y> : warp_rows<V, kLong / V, GRAD, X, Y>)
-                                      : (few ? block_rows<V, kFew / V, GRAD, X, Y> : block_rows<V, kLong / V, GRAD, X, Y>);
-            if (smem + kOwnBytes > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-                cudaGetLastError();
-                return EMB_ERR_CUDA;
-            }
-            return launch_next(kernel, s.blocks, dim3(s.tx, s.ty), smem, st, 1, a);
+            const dim3 block(s.tx, s.ty);
+            if (warps) return few ? launch_ring<warp_rows<V, kFew / V, GRAD, X, Y>>(a, s.blocks, block, smem, st) : launch_ring<warp_rows<V, kLong / V, GRAD, X, Y>>(a, s.blocks, block, smem, st);
+            return few ? launch_ring<block_rows<V, kFew / V, GRAD, X, Y>>(a, s.blocks, block, smem, st) : launch_ring<block_rows<V, kLong / V, GRAD, X, Y>>(a, s.blocks, block, smem, st);
         };
         constexpr int kVector = sizeof(X) == 2 && sizeof(Y) == 2 ? 8 : 4;   // of fp32 16 bytes, so that lanes' loads meet no bank twice
         const auto with_v = [&](auto grad) {
