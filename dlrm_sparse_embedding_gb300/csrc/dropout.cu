@@ -62,45 +62,51 @@ __device__ __forceinline__ float result(bool keep, float x, float residual, floa
     return keep ? x * scale : 0.f;
 }
 
-// Groups as vectors of 8: every row is whole groups, or everything is one row, which
-// may end inside a group.  Bound by memory: kAhead groups a thread are on their way
-// before the first is used.
-constexpr int kAhead = 2;
-
+// Groups as vectors of 8: everything is one row, which may end inside a group (FLAT), or
+// every row is whole groups.  Bound by memory: a thread has kAhead groups, of as many rows
+// where there are rows, on their way before the first is used.
 template <class X, class Y, bool RESIDUAL>
+constexpr int kAhead = sizeof(X) == 2 && sizeof(Y) == 2 && !RESIDUAL ? 4 : 2;
+
+template <class X, class Y, bool RESIDUAL, bool FLAT>
 __global__ void __launch_bounds__(kThreads) drop_groups(const Args a)
 {
+    constexpr int N = kAhead<X, Y, RESIDUAL>;
     let_next_begin();
     wait_for_earlier();
     const uint64_t seed = a.seed_at ? *a.seed_at : a.seed;
-    const int64_t per_row = a.width / kGroup, c0 = (int64_t)blockIdx.x * (kThreads * kAhead) + threadIdx.x;
-    for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
-        const X* const x = static_cast<const X*>(a.x) + row * a.x_stride;
-        const Y* const res = static_cast<const Y*>(a.residual) + (RESIDUAL ? row * a.residual_stride : 0);
-        Y* const y = static_cast<Y*>(a.y) + row * a.width;
-        Raw<8, X> v[kAhead];
-        Raw<8, Y> r[kAhead];
+    const int64_t per_row = a.width / kGroup;
+    const X* const x = static_cast<const X*>(a.x);
+    const Y* const residual = static_cast<const Y*>(a.residual);
+    Y* const y = static_cast<Y*>(a.y);
+    const int64_t rows_at_once = (int64_t)N * blockDim.y;
+    for (int64_t row0 = FLAT ? 0 : blockIdx.y * rows_at_once; row0 < a.rows; row0 += FLAT ? a.rows : gridDim.y * rows_at_once) {
+        const auto row_of = [&](int i) { return FLAT ? 0 : row0 + i * (int64_t)blockDim.y + threadIdx.y; };
+        const auto group_of = [&](int i) { return FLAT ? (int64_t)blockIdx.x * (kThreads * N) + i * kThreads + threadIdx.x : (int64_t)blockIdx.x * blockDim.x + threadIdx.x; };
+        Raw<kGroup, X> v[N];
+        Raw<kGroup, Y> r[N];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (c0 + i * kThreads < per_row) {
-                v[i].load(x + (c0 + i * kThreads) * kGroup);
-                if (RESIDUAL) r[i].load(res + (c0 + i * kThreads) * kGroup);
+        for (int i = 0; i < N; ++i)
+            if (group_of(i) < per_row && (FLAT || row_of(i) < a.rows)) {
+                v[i].load(x + row_of(i) * a.x_stride + group_of(i) * kGroup);
+                if (RESIDUAL) r[i].load(residual + row_of(i) * a.residual_stride + group_of(i) * kGroup);
             }
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int64_t c = c0 + i * kThreads;
+        for (int i = 0; i < N; ++i) {
+            const int64_t row = row_of(i), c = group_of(i);
+            if (!FLAT && row >= a.rows) continue;
             const uint4 bits = philox((uint64_t)(row * per_row + c), a.offset, seed);
             if (c < per_row) {
                 float o[kGroup];
 #pragma unroll
                 for (int j = 0; j < kGroup; ++j) o[j] = result<RESIDUAL>(kept(bits, j, a.threshold), v[i][j], RESIDUAL ? r[i][j] : 0.f, a.scale);
-                store_vec<kGroup, Y>(y + c * kGroup, o);
-            } else if (c == per_row) {   // what is left of the one row
+                store_vec<kGroup, Y>(y + row * a.width + c * kGroup, o);
+            } else if (FLAT && c == per_row) {   // what is left of the one row
 #pragma unroll
-                for (int j = 0; j < kGroup; ++j)
-                    if (c * kGroup + j < a.width)
-                        y[c * kGroup + j] = from_float<Y>(result<RESIDUAL>(kept(bits, j, a.threshold), to_float<X>(x[c * kGroup + j]),
-                                                                           RESIDUAL ? to_float<Y>(res[c * kGroup + j]) : 0.f, a.scale));
+                for (int j = 0; j < kGroup; ++j) {
+                    const int64_t at = c * kGroup + j;
+                    if (at < a.width) y[at] = from_float<Y>(result<RESIDUAL>(kept(bits, j, a.threshold), to_float<X>(x[at]), RESIDUAL ? to_float<Y>(residual[at]) : 0.f, a.scale));
+                }
             }
         }
     }
@@ -165,24 +171,35 @@ extern "C" int emb_dropout(const void* x, int32_t x_dtype, int64_t x_stride, int
     a.scale = a.threshold < 65536 ? (float)(1.0 / (1.0 - a.threshold / 65536.0)) : 0.f;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // one row of everything, or rows of whole groups, in vectors; else by elements
-    bool vectors = false;
-    if (rows == 1 || (x_stride == width && (!residual || residual_stride == width))) {
-        vectors = aligned_to(x, 16) && aligned_to(y, 16) && aligned_to(residual, 16);
-        if (vectors) a.width = a.x_stride = a.residual_stride = rows * width, a.rows = 1;
-    } else {
-        vectors = vector_of(x, x_dtype, x_stride, width) == 8 && vector_of(y, y_dtype, width, width) == 8 &&
-                  (!residual || vector_of(residual, y_dtype, residual_stride, width) == 8);
-    }
-    const int64_t groups = (a.width + kGroup - 1) / kGroup, share = kThreads * kAhead;
-    const int64_t blocks = vectors ? (groups + share - 1) / share : std::min<int64_t>((rows * width + kThreads * kGroup - 1) / (kThreads * kGroup), INT32_MAX);
-    if (blocks > INT32_MAX) return EMB_ERR_INVALID_ARG;
-    const dim3 grid((unsigned)blocks, vectors ? (unsigned)std::min<int64_t>(a.rows, 65535) : 1);
+    const bool flat = (rows == 1 || (x_stride == width && (!residual || residual_stride == width))) && aligned_to(x, 16) && aligned_to(y, 16) &&
+                      aligned_to(residual, 16);
+    if (flat) a.width = a.x_stride = a.residual_stride = rows * width, a.rows = 1;
+    const bool vectors = flat || (vector_of(x, x_dtype, x_stride, width) == 8 && vector_of(y, y_dtype, width, width) == 8 &&
+                                  (!residual || vector_of(residual, y_dtype, residual_stride, width) == 8));
+    const int64_t groups = (a.width + kGroup - 1) / kGroup;
     return with_type(x_dtype, [&](auto xt) {
         return with_type(y_dtype, [&](auto yt) {
             using X = decltype(xt);
             using Y = decltype(yt);
-            if (vectors) return launch_next(residual ? drop_groups<X, Y, true> : drop_groups<X, Y, false>, grid, kThreads, 0, st, 1, a);
-            return launch_next(residual ? drop_elements<X, Y, true> : drop_elements<X, Y, false>, grid, kThreads, 0, st, 1, a);
+            const auto go = [&](auto has) -> int {
+                constexpr bool RESIDUAL = decltype(has)::value;
+                constexpr int N = kAhead<X, Y, RESIDUAL>;
+                const auto blocks = [](int64_t n, int64_t each) { return std::min<int64_t>((n + each - 1) / each, INT32_MAX); };
+                if (flat) {
+                    if (groups > (int64_t)INT32_MAX * kThreads * N) return EMB_ERR_INVALID_ARG;
+                    return launch_next(drop_groups<X, Y, RESIDUAL, true>, (unsigned)blocks(groups, kThreads * N), kThreads, 0, st, 1, a);
+                }
+                if (vectors) {
+                    int tx = 1;
+                    while (tx < kThreads && tx < groups) tx *= 2;
+                    if (groups > (int64_t)INT32_MAX * tx) return EMB_ERR_INVALID_ARG;
+                    const dim3 block(tx, kThreads / tx);
+                    const dim3 grid((unsigned)blocks(groups, tx), (unsigned)std::min<int64_t>(blocks(a.rows, N * (int64_t)block.y), 65535));
+                    return launch_next(drop_groups<X, Y, RESIDUAL, false>, grid, block, 0, st, 1, a);
+                }
+                return launch_next(drop_elements<X, Y, RESIDUAL>, (unsigned)blocks(rows * width, kThreads * kGroup), kThreads, 0, st, 1, a);
+            };
+            return residual ? go(std::true_type()) : go(std::false_type());
         });
     });
 }
