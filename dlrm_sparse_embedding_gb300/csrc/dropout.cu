@@ -3,9 +3,12 @@
 // Element i of the matrix (row by row, whatever its strides) is kept when its 16 bits
 // of Philox4x32 (J. Salmon et al., "Parallel random numbers: as easy as 1, 2, 3", 2011)
 // are at least 65536 times the rate.  Counter (i / 8, offset), key the seed: a counter's
-// four words are eight elements' bits.  Seven rounds are the fewest of the paper's
-// generators that pass its batteries of tests; of 10 the rate would be bound by
-// integer products, not by memory.
+// four words are eight elements' bits.  Seven rounds are the fewest with which the
+// paper's generator passes its batteries of tests; with 16 bits an element they take
+// about five of an element's instructions, and memory stays the bound.
+//
+// 32768 x 2048 bf16: 40.3 us (6.7 TB/s), with a residual 57.7 (7.0), fp32 with one 113 (7.1); rows 8
+// elements apart 63 (6.4).  By elements (rows that are no vectors) 174 us.
 #include <algorithm>
 #include <cmath>
 

@@ -1,5 +1,6 @@
 """Expert layer: tokens sorted by expert, their rows gathered, multiplied by
-each expert's weights and added back, with the gradients.
+each expert's weights and added back, with the gradients; and all of it in one
+call for a few tokens.
 
 Argument checks and marshalling only; the work is in libemb.so.  Tensors are on
 the current CUDA device (ValueError if not).  Every call takes `stream`: it runs
@@ -391,7 +392,7 @@ def expert_layer(ids: torch.Tensor, x: torch.Tensor, up: torch.Tensor, down: tor
 
 def dense_status(stream=None) -> int:
     """Waits for the stream; returns and clears the device's sticky status of the
-    expert calls and of orthogonalize (EMB_OK, EMB_ERR_KEY_RANGE, EMB_ERR_TIMEOUT).
+    expert calls, orthogonalize and layer_norm (EMB_OK, EMB_ERR_KEY_RANGE, EMB_ERR_TIMEOUT).
     The stream, if given, is one of the current device's."""
     if stream is None:
         return int(lib.emb_dense_status(torch.cuda.current_stream().cuda_stream))

@@ -7,7 +7,8 @@
  *                        and the SGD / Adagrad update, in place
  *   emb_unique           the stand-alone dedup primitive
  * and, further down, the dense side's operators: an expert layer (sort,
- * dispatch, products, combine, and their gradients) and orthogonalised updates
+ * dispatch, products, combine, and their gradients; the whole of it in one call
+ * for a few tokens), layer norm and dropout around it, and orthogonalised updates
  * for its weights.
  *
  * The operations are the ones the GTC 2022 "Merlin HugeCTR" slides name
@@ -521,8 +522,9 @@ int emb_orthogonalize(const void* update, int32_t dtype, int64_t batch_stride, i
  * finite size keep their variance.  A row that holds an infinity or a NaN is NaN, and so
  * are its columns' sums; other rows are not touched.  A null grad_x, grad_weight or
  * grad_bias is not computed; without rows the sums are zero.  width in [1, 2^24], eps
- * in [1e-24, fp32's largest].  The workspace is 256-byte aligned,
- * emb_layer_norm_grad_workspace bytes.  No passage: library convenience. */
+ * in [1e-24, fp32's largest].  Rows are copied from and to 16-byte boundaries: up to 15
+ * bytes beside x and grad_y may be read, never used.  The workspace is 256-byte
+ * aligned, emb_layer_norm_grad_workspace bytes.  No passage: library convenience. */
 int emb_layer_norm(const void* x, int32_t x_dtype, int64_t x_stride, int64_t rows, int64_t width, const void* weight,
                    const void* bias, int32_t param_dtype, float eps, void* y, int32_t y_dtype, void* stream);
 int emb_layer_norm_grad_workspace(int64_t rows, int64_t width, size_t* bytes);
