@@ -89,7 +89,8 @@ def check(args, act, dtype=None, out=None):
 # the second list's weights are read in tiles on the tensor cores: few or no tokens an expert, up to 64, 128, 512 of one expert
 SMALL = [(1, 1, 1, 8, 8, 8), (1, 2, 16, 3328, 1024, 1024), (2, 1, 3, 16, 24, 40), (3, 4, 5, 40, 72, 8), (7, 3, 12, 1032, 776, 520),
          (8, 8, 1000, 128, 64, 128), (16, 2, 32, 512, 264, 256), (64, 4, 16, 256, 512, 136), (64, 8, 8, 96, 200, 64), (512, 1, 3, 72, 48, 56),
-         (100, 5, 1, 64, 32, 24), (8, 64, 7, 64, 56, 72), (33, 2, 1024, 64, 40, 16), (1, 64, 200, 2048, 128, 32), (5, 2, 4, 16, 8, 4104)]
+         (100, 5, 1, 64, 32, 24), (8, 64, 7, 64, 56, 72), (33, 2, 1024, 64, 40, 16), (1, 64, 200, 2048, 128, 32), (5, 2, 4, 16, 8, 4104),
+         (64, 8, 1000, 16, 24, 40), (512, 1, 1024, 8, 16, 8), (2, 16, 4, 40, 24, 16), (3, 11, 9, 64, 32, 24)]
 LARGE = [(64, 8, 8, 520, 1032, 536), (128, 4, 4, 512, 1032, 520), (512, 1, 1, 520, 1160, 512), (8, 4, 32, 1024, 1544, 1032),
          (60, 4, 40, 1032, 776, 1048), (65, 5, 3, 1000, 1000, 1000)]
 
@@ -295,6 +296,48 @@ def test_inputs_that_require_gradients_and_tensors_of_another_device(monkeypatch
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)      # nothing is launched: the tensors are on 0
     with pytest.raises(ValueError, match="current device"):
         emb.expert_layer(ids, x, up, down, weights)
+
+
+@gpu
+def test_calls_of_several_threads():
+    import threading
+    jobs = []
+    for i, c in enumerate([SMALL[1], (40, 3, 8, 256, 128, 64), LARGE[0], LARGE[1]]):
+        args = case(30 + i, *c, BF, F32)
+        jobs.append((torch.cuda.Stream(), args, emb.expert_layer(*args)))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(stream, args, ref):
+        for _ in range(30):
+            out = emb.expert_layer(*args, stream=stream)
+            stream.synchronize()
+            wrong.extend([] if torch.equal(out, ref) else [1])
+
+    threads = [threading.Thread(target=work, args=job) for job in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+@gpu
+def test_inputs_freed_while_another_stream_reads_them():
+    args = case(13, 40, 2, 8, 1024, 1024, 512, BF, F32)
+    ref = emb.expert_layer(*args)
+    stream = torch.cuda.Stream()
+    for _ in range(20):
+        x, ids = args[1].clone(), args[0].clone()
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            torch.cuda._sleep(200000)
+        out = emb.expert_layer(ids, x, *args[2:], stream=stream)
+        del x, ids
+        torch.full((40, 1024), float("nan"), device="cuda")      # takes their memory, if it is to be had
+        torch.full((40, 2), 5, dtype=torch.int32, device="cuda")
+        torch.cuda.current_stream().wait_stream(stream)
+        assert torch.equal(out, ref)
 
 
 def test_refusals_without_a_gpu():

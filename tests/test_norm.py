@@ -131,6 +131,53 @@ def test_norm_and_its_gradients(rows, width, xt, yt, extra):
 
 
 @gpu
+@pytest.mark.parametrize("width", [5, 40, 129, 520, 1000, 3328, 9000])
+@pytest.mark.parametrize("first", [1, 3, 8])
+@pytest.mark.parametrize("xt,yt", [(F32, BF), (BF, BF), (HF, F32)])
+def test_rows_that_begin_anywhere(width, first, xt, yt):
+    # columns of a wider matrix: neighbours are read at most, never used
+    g = gen(width + first)
+    rows = 37
+    big = torch.randn(rows, width + 16, generator=g, device="cuda").to(xt)
+    wide = torch.randn(rows, width + 24, generator=g, device="cuda").to(yt)
+    for t in (big, wide):
+        t[:, :first], t[:, first + width:] = float("nan"), float("inf")
+    x, gy = big[:, first:first + width], wide[:, first:first + width]
+    w = torch.randn(width + 1, generator=g, device="cuda")[1:]      # a parameter off a vector's boundary
+    check_norm(x, w, w, 1e-5, yt)
+    check_grad(gy, x, w, 1e-5)
+    check_grad(gy.contiguous(), x, w, 1e-5)
+    check_grad(gy, x.contiguous(), w, 1e-5)
+    assert torch.equal(emb.dropout(gy, 0.5, 3, residual=gy), emb.dropout(gy.contiguous(), 0.5, 3, residual=gy.contiguous()))
+
+
+@gpu
+def test_calls_of_several_threads():
+    import threading
+    jobs = []
+    for i in range(4):
+        g = gen(i)
+        x, w = torch.randn(500 + i, 700 + 100 * i, generator=g, device="cuda"), torch.randn(700 + 100 * i, generator=g, device="cuda")
+        jobs.append((torch.cuda.Stream(), x, w, (emb.layer_norm(x, w), *emb.layer_norm_grad(x, x, w), emb.dropout(x, 0.3, i))))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(seed, stream, x, w, ref):
+        for _ in range(30):
+            with torch.cuda.stream(stream):
+                got = emb.layer_norm(x, w), *emb.layer_norm_grad(x, x, w), emb.dropout(x, 0.3, seed)
+            stream.synchronize()
+            wrong.extend(1 for a, b in zip(got, ref) if not torch.equal(a, b))
+
+    threads = [threading.Thread(target=work, args=(i, *job)) for i, job in enumerate(jobs)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+@gpu
 def test_weight_and_bias_may_be_left_out():
     g = gen(1)
     r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
