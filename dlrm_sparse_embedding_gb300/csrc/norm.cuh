@@ -27,7 +27,8 @@
 // Measured and not kept: rows by loads into registers a row ahead (333 us for the first line's 143);
 // eight elements a thread (forward 65, gradients 102); statistics around the mean of 32 samples, a barrier
 // less, whose second try for rows they do not fit costs registers (bf16 gradients 85 us, but
-// fp32's 101).
+// fp32's 101); short rows' parameters in shared memory, for more warps (42 and 84 us where 39 and 70); rows
+// past 8192 shared by a cluster's blocks (307 us).
 #pragma once
 
 #include <algorithm>
