@@ -13,7 +13,7 @@
 // few for the sums' latency and instructions: bf16 alone 48 (4.5 TB/s) and 92 (3.6); 425984 x 128
 // bf16 39 (5.6) and 70 (4.7).  Rows without a 16-byte rhythm go element by element: 32768 x 1025 fp16 84
 // and 99 us (1.6 and 2.0).  Past 8192 elements (of a forward in vectors, 16384) a row is read three times
-// and its columns' sums by a second kernel: 4000 x 16384 gradients 291 us (2.3).
+// and its columns' sums by a second kernel: 4000 x 16384 gradients 307 us, bf16 192 (2.1 both).
 //
 // The mean is a rounded sum; what the rounding left, d = mean(x - m), is measured in the
 // second pass and taken off again, so rows far from zero lose no more than their own
@@ -73,7 +73,7 @@ struct Shape {
     int chunks;            // wide rows' gradients: parts the rows are added up in
 };
 
-constexpr int kThreads = 256, kMaxThreads = 512, kWideThreads = 1024;
+constexpr int kThreads = 256, kMaxThreads = 512, kWideThreads = 512;
 // Elements of a row a thread holds: 16, and 32 of longer rows where only the forward's two
 // parameters are held beside them and elements come in vectors.
 constexpr int kFew = 16, kMany = 32;
@@ -597,7 +597,7 @@ __global__ void __maxnreg__(registers(U * V, GRAD, V > 1)) warp_rows(const Args 
     }
 }
 
-// block_sums of up to 32 warps.
+// block_sums of kWideThreads.
 template <int N>
 __device__ __forceinline__ void wide_sums(float (&s)[N], float (*part)[4])
 {
@@ -607,11 +607,14 @@ __device__ __forceinline__ void wide_sums(float (&s)[N], float (*part)[4])
         for (int i = 0; i < N; ++i) part[threadIdx.x >> 5][i] = s[i];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = part[threadIdx.x & 31][i];
-    lane_sums(s, 32);
+    for (int i = 0; i < N; ++i) s[i] = part[threadIdx.x & (kWideThreads / 32 - 1)][i];
+    lane_sums(s, kWideThreads / 32);
 }
 
-// Wider rows: a block takes one, three times over, the later ones from the caches.
+// Wider rows: a block takes one, three times over, the later ones from the caches, kWideAhead
+// vectors a thread on their way (4000 x 16384 bf16: 231 us with one, by 1024 threads; 9000 x 8193 705, and 412).
+constexpr int kWideAhead = 4;
+
 template <int V, bool GRAD, class X, class Y>
 __global__ void __launch_bounds__(kWideThreads) wide_rows(const Args a)
 {
@@ -623,40 +626,48 @@ __global__ void __launch_bounds__(kWideThreads) wide_rows(const Args a)
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const X* const x = static_cast<const X*>(a.x) + row * a.x_stride;
         const Y* const g = static_cast<const Y*>(a.g) + row * a.g_stride;
+        // f(column, its vectors of x and, with_g, of g) for the thread's vectors
+        const auto each = [&](bool with_g, auto f) {
+            for (int c0 = threadIdx.x * V; c0 < width; c0 += kWideAhead * step) {
+                Raw<V, X> v[kWideAhead];
+                Raw<V, Y> r[kWideAhead];
+#pragma unroll
+                for (int i = 0; i < kWideAhead; ++i)
+                    if (c0 < width - i * step) {
+                        v[i].load_again(x + c0 + i * step);
+                        if (with_g) r[i].load_again(g + c0 + i * step);
+                    }
+#pragma unroll
+                for (int i = 0; i < kWideAhead; ++i)
+                    if (c0 < width - i * step) f(c0 + i * step, v[i], r[i]);
+            }
+        };
         Moments mo;
         float along = 0.f, mean_gw = 0.f, scale = 1.f;
         for (bool again = false;; again = true) {
             float s1[1] = {};
-            for (int c = threadIdx.x * V; c < width; c += step) {
-                Raw<V, X> v;
-                v.load_again(x + c);
+            each(false, [&](int, const Raw<V, X>& v, const Raw<V, Y>&) {
 #pragma unroll
                 for (int q = 0; q < V; ++q) s1[0] += v[q] * scale;
-            }
+            });
             wide_sums(s1, part[0]);
             const float m = s1[0] * inv_n;
             float s[GRAD ? 4 : 2] = {};
-            for (int c = threadIdx.x * V; c < width; c += step) {
-                Raw<V, X> v;
-                Raw<V, Y> gr;
-                v.load_again(x + c);
+            each(GRAD, [&](int c, const Raw<V, X>& v, const Raw<V, Y>& r) {
                 float w[V];
-                if (GRAD) {
-                    gr.load_again(g + c);
-                    params<V>(a.weight, a.param_dtype, c, 1.f, w);
-                }
+                if (GRAD) params<V>(a.weight, a.param_dtype, c, 1.f, w);
 #pragma unroll
                 for (int q = 0; q < V; ++q) {
                     const float e = v[q] * scale - m;
                     s[0] += e;
                     s[1] = __fmaf_rn(e, e, s[1]);
                     if constexpr (GRAD) {
-                        const float gw = gr[q] * w[q];
+                        const float gw = r[q] * w[q];
                         s[2] += gw;
                         s[3] = __fmaf_rn(gw, e, s[3]);
                     }
                 }
-            }
+            });
             wide_sums(s, part[1]);
             if (!again && !(s[1] <= kLargeSquares)) {
                 scale = kDown;
@@ -672,21 +683,19 @@ __global__ void __launch_bounds__(kWideThreads) wide_rows(const Args a)
         if (GRAD && a.stats && threadIdx.x == 0) a.stats[row] = make_float4(mo.m, mo.d, mo.rstd, mo.scale);
         if (!a.out) continue;
         const float outer = mo.rstd * mo.scale;
-        for (int c = threadIdx.x * V; c < width; c += step) {
-            Raw<V, X> v;
-            Raw<V, Y> gr;
+        each(GRAD, [&](int c, const Raw<V, X>& v, const Raw<V, Y>& r) {
             float o[V], w[V], b[V];
-            v.load(x + c);
-            if (GRAD) gr.load(g + c);
+            params<V>(a.weight, a.param_dtype, c, 1.f, w);
+            if (!GRAD) params<V>(a.bias, a.param_dtype, c, 0.f, b);
 #pragma unroll
             for (int q = 0; q < V; ++q) {
-                const float h = mo.h(v[q]), w = param(a.weight, a.param_dtype, c + q, 1.f);
-                if constexpr (GRAD) o[q] = outer * ((gr[q] * w - mean_gw) - h * along);
-                else o[q] = __fmaf_rn(h, w, param(a.bias, a.param_dtype, c + q, 0.f));
+                const float h = mo.h(v[q]);
+                if constexpr (GRAD) o[q] = outer * ((r[q] * w[q] - mean_gw) - h * along);
+                else o[q] = __fmaf_rn(h, w[q], b[q]);
             }
             if constexpr (GRAD) store_vec<V, X>(static_cast<X*>(a.out) + row * width + c, o);
             else store_vec<V, Y>(static_cast<Y*>(a.out) + row * width + c, o);
-        }
+        });
     }
 }
 
