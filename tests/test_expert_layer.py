@@ -246,6 +246,46 @@ def test_streams_and_graphs(T, D, H, N):
 
 
 @gpu
+@pytest.mark.parametrize("T,k,E,D,H,N", [SMALL[1], (4, 2, 4, 256, 256, 256), (40, 3, 8, 256, 128, 64), LARGE[0], LARGE[1]])
+def test_weights_and_ids_that_change_between_calls(T, k, E, D, H, N):
+    # the second kernel's first weights and the groups are read before the first kernel's end:
+    # what stood in the stream before the call has to be seen, be it a copy or a kernel that lets the next one begin early
+    args = [case(40 + i, T, k, E, D, H, N, BF, BF) for i in range(3)]
+    refs = [emb.expert_layer(*a) for a in args]
+    ids, x, up, down, weights = (t.clone() for t in args[0])
+
+    def put(i):
+        for to, t in zip((ids, x, up, down, weights), args[i]):
+            to.copy_(t)
+
+    for turn in range(60):
+        put(turn % 3)
+        assert torch.equal(emb.expert_layer(ids, x, up, down, weights), refs[turn % 3]), turn
+    put(0)
+    graph, at = torch.cuda.CUDAGraph(), torch.zeros(1, dtype=torch.int64, device="cuda")
+    several = [torch.stack([a[j] for a in args]) for j in range(5)]
+    with torch.cuda.graph(graph):
+        for to, t in zip((ids, x, up, down, weights), several):
+            to.copy_(torch.index_select(t, 0, at)[0])
+        out = emb.expert_layer(ids, x, up, down, weights)
+    for turn in range(30):
+        at.fill_(turn % 3)
+        graph.replay()
+        assert torch.equal(out, refs[turn % 3]), turn
+
+
+@gpu
+def test_weights_straight_from_a_call():
+    T, k, E, D, H, N = 4, 2, 4, 256, 256, 128
+    ids, x, up, down, weights = case(50, T, k, E, D, H, N, BF, BF)
+    for turn in range(20):
+        update = torch.randn(E, N, H, generator=gen(turn), device="cuda")
+        got = emb.expert_layer(ids, x, up, emb.orthogonalize(update), weights)
+        torch.cuda.synchronize()
+        assert torch.equal(got, emb.expert_layer(ids, x, up, emb.orthogonalize(update).clone(), weights)), turn
+
+
+@gpu
 @pytest.mark.parametrize("T,k,E,D,H,N", [(8, 4, 16, 1024, 1024, 512), (32, 4, 16, 512, 512, 512), LARGE[0], LARGE[1]])
 def test_calls_on_two_streams_at_once(T, k, E, D, H, N):
     jobs = []
