@@ -254,16 +254,50 @@ struct Piece {
 
     __device__ __forceinline__ bool in(int u) const { return first + u * step < width; }
 
+    // A parameter's elements, all of them on their way before the first is used.
+    __device__ __forceinline__ void fill(const void* p, int dtype, float none, Two (&to)[E / 2])
+    {
+        float t[E];
+        const auto get = [&](auto as) {
+            using T = decltype(as);
+            const T* const from = static_cast<const T*>(p) + first;
+            if (V > 1 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+                Raw<V, T> r[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    r[u].clear();
+                    if (in(u)) r[u].load_again(from + u * step);
+                }
+#pragma unroll
+                for (int e = 0; e < E; ++e) t[e] = r[e / V][e % V];
+            } else {
+                Raw<1, T> r[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    r[e].clear();
+                    if (in(e / V)) r[e].load_again(from + e / V * step + e % V);
+                }
+#pragma unroll
+                for (int e = 0; e < E; ++e) t[e] = r[e][0];
+            }
+        };
+        if (!p) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) t[e] = in(e / V) ? none : 0.f;
+        } else if (dtype == EMB_F32) get(float());
+        else if (dtype == EMB_F16) get(__half());
+        else get(__nv_bfloat16());
+#pragma unroll
+        for (int e = 0; e < E; e += 2) to[e / 2] = Two(t[e], t[e + 1]);
+    }
+
     __device__ __forceinline__ void open(const Args& a, int tx, int threads)
     {
         first = tx * V, step = threads * V, width = a.width;
-        const auto get = [&](const void* p, int e, float none) { return in(e / V) ? param(p, a.param_dtype, first + e / V * step + e % V, none) : 0.f; };
+        fill(a.weight, a.param_dtype, 1.f, w);
+        if (!GRAD) fill(a.bias, a.param_dtype, 0.f, b);
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-            w[e / 2] = Two(get(a.weight, e, 1.f), get(a.weight, e + 1, 1.f));
-            if (!GRAD) b[e / 2] = Two(get(a.bias, e, 0.f), get(a.bias, e + 1, 0.f));
-            acc_w[e / 2] = acc_b[e / 2] = Two(0.f);
-        }
+        for (int i = 0; i < E / 2; ++i) acc_w[i] = acc_b[i] = Two(0.f);
     }
 
     template <class T>
