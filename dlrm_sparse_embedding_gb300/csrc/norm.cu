@@ -36,10 +36,11 @@ Shape shape_of(int64_t rows, int64_t width, bool grad, bool vectors)
         for (s.tx = 1; s.tx < threads;) s.tx *= 2;
         s.ty = kThreads / s.tx;
     } else {
-        s.tx = (threads + 31) / 32 * 32, s.ty = 1;
+        s.tx = (threads + 31) / 32 * 32;
+        s.ty = grad ? std::max(1, std::min(kMaxSubs, kThreads / s.tx)) : 1;
     }
     s.per_sm = std::max(1, std::min(8, 65536 / (registers(s.per_thread, grad, vectors) * s.tx * s.ty)));
-    if (s.kind == kBlockRows) s.per_sm = std::max(1, std::min(s.per_sm, kSharedBytes / (int)(3 * width * (grad ? 8 : 4) + kOwnBytes)));
+    if (s.kind == kBlockRows) s.per_sm = std::max(1, std::min(s.per_sm, kSharedBytes / (int)(3 * width * s.ty * (grad ? 8 : 4) + kOwnBytes)));
     s.blocks = (int)std::min<int64_t>((rows + s.ty - 1) / s.ty, (int64_t)kSms * s.per_sm);
     return s;
 }
