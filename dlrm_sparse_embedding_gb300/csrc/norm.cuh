@@ -9,11 +9,11 @@
 // around it and the result are three passes over registers.  The gradient takes x again instead of
 // stored statistics: it has to read x for h.  fp32 elements take two an instruction.
 //
-// 16384 x 3328, fp32 to bf16: forward 54 us (6.0 TB/s), gradients 89 (6.1).  Two bytes an element are too
-// few for the sums' latency and instructions: bf16 alone 48 (4.5 TB/s) and 92 (3.6); 425984 x 128
-// bf16 39 (5.6) and 70 (4.7).  Rows without a 16-byte rhythm go element by element: 32768 x 1025 fp16 84
+// 16384 x 3328, fp32 to bf16: forward 51 us (6.4 TB/s), gradients 86 (6.3).  Two bytes an element are too
+// few for the sums' latency and instructions: bf16 alone 43 (5.0 TB/s) and 87 (3.8); 425984 x 128
+// bf16 39 (5.7) and 67 (4.9).  Rows without a 16-byte rhythm go element by element: 32768 x 1025 fp16 83
 // and 99 us (1.6 and 2.0).  Past 8192 elements (of a forward in vectors, 16384) a row is read three times
-// and its columns' sums by a second kernel: 4000 x 16384 gradients 307 us, bf16 192 (2.1 both).
+// and its columns' sums by a second kernel: 4000 x 16384 gradients 296 us (2.7), bf16 192 (2.1).
 //
 // The mean is a rounded sum; what the rounding left, d = mean(x - m), is measured in the
 // second pass and taken off again, so rows far from zero lose no more than their own
@@ -77,9 +77,9 @@ constexpr int kThreads = 256, kMaxThreads = 512, kWideThreads = 512;
 // Elements of a row a thread holds: 16, and 32 of longer rows where only the forward's two
 // parameters are held beside them and elements come in vectors.
 constexpr int kFew = 16, kMany = 32;
-constexpr int kMaxStages = 8, kMaxSubs = 4;
+constexpr int kMaxStages = 8, kMaxSubs = 5;
 constexpr int kSharedBytes = 226 * 1024;         // of an SM, for its blocks
-constexpr int kOwnBytes = 2560;                  // of a block beside its stages
+constexpr int kOwnBytes = 3072;                  // of a block beside its stages
 // Of an SM, for the stages, two at least: more on their way are slower (16384 x 3328, fp32 to bf16, forward:
 // 50.8 us, with all of the memory 57.7; gradients 86.3 and 87.1, with two stages 93.6).
 constexpr int kRingBytes = 120 * 1024;
@@ -474,7 +474,7 @@ __device__ __forceinline__ void put_sums(const Args& a, const PIECE& p, float* s
 
 // Longer rows: blockDim.x threads take one at a time, and a block has, SUBS, up to kMaxSubs rows'
 // threads, so that fewer blocks leave sums of a gradient's columns (1000 x 1024 bf16: 19.9 us with
-// one, 8.8 with four; 50000: 77 both).  Rows are
+// one, 8.5 with four; 50000: 75 both).  Rows are
 // copied to a ring of stages, each row's threads have their own; a stage is free for the
 // next row when the second sums' barrier has been met.
 template <int V, int U, bool GRAD, bool SUBS, class X, class Y>
@@ -848,7 +848,7 @@ int launch_rows(Args a, int y_dtype, bool vectors, const Shape& s, cudaStream_t 
             const int stage = (a.x_slot + a.g_slot) * (warps ? kThreads / 32 : s.ty);
             a.stages = std::max(2, std::min(kMaxStages, kRingBytes / s.per_sm / stage));
             size_t smem = (size_t)a.stages * stage;
-            if (GRAD && s.ty > 1) smem = std::max(smem, (size_t)kThreads * kFew * sizeof(float));
+            if (GRAD && s.ty > 1) smem = std::max(smem, (size_t)s.tx * s.ty * kFew * sizeof(float));
             constexpr int kLong = GRAD || V == 1 ? kFew : kMany;
             const bool few = s.per_thread == kFew;
             const dim3 block(s.tx, s.ty);

@@ -235,6 +235,22 @@ def test_a_rows_infinities_and_nans_stay_its_own(width, bad):
 
 
 @gpu
+@pytest.mark.parametrize("width", [513, 1024, 1288, 1301, 1536, 1700, 2048, 2049])
+@pytest.mark.parametrize("rows", [4, 803])
+@pytest.mark.parametrize("t", [F32, BF])
+def test_gradients_of_rows_that_share_a_block(rows, width, t):
+    g = gen(rows + width)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, gy, w = r(rows, width).to(t), r(rows, width).to(t), (1 + 0.3 * r(width)).to(t)
+    check_grad(gy, x, w, 1e-5)
+    clean = emb.layer_norm_grad(gy, x, w)
+    x[2] = (x[2].float() * 2.0 ** 80).to(t)     # a row that is taken twice, beside rows that are not
+    dx, _, db = emb.layer_norm_grad(gy, x, w)
+    others = torch.arange(rows, device="cuda") != 2
+    assert torch.equal(dx[others], clean[0][others]) and torch.equal(db, clean[2])
+
+
+@gpu
 @pytest.mark.parametrize("width", [24, 3328, 10000])
 def test_norm_gradients_are_the_differences(width):
     g = gen(3)
