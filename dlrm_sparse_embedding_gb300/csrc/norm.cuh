@@ -79,7 +79,7 @@ constexpr int kThreads = 256, kMaxThreads = 512, kWideThreads = 512;
 constexpr int kFew = 16, kMany = 32;
 constexpr int kMaxStages = 8, kMaxSubs = 5;
 constexpr int kSharedBytes = 226 * 1024;         // of an SM, for its blocks
-constexpr int kOwnBytes = 3072;                  // of a block beside its stages
+constexpr int kOwnBytes = 2944;                  // of a block beside its stages
 // Of an SM, for the stages, two at least: more on their way are slower (16384 x 3328, fp32 to bf16, forward:
 // 50.8 us, with all of the memory 57.7; gradients 86.3 and 87.1, with two stages 93.6).
 constexpr int kRingBytes = 120 * 1024;
