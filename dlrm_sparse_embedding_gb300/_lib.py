@@ -37,7 +37,7 @@ EXPORTS = (
     "emb_expert_combine", "emb_expert_combine_grad", "emb_expert_linear", "emb_expert_linear_grad_rows",
     "emb_expert_linear_grad_weight", "emb_orthogonalize_workspace", "emb_orthogonalize", "emb_dense_status",
     "emb_layer_norm", "emb_layer_norm_grad_workspace", "emb_layer_norm_grad", "emb_dropout",
-    "emb_expert_layer_workspace", "emb_expert_layer",
+    "emb_expert_layer_workspace", "emb_expert_layer", "emb_expert_layer_tiles",
 )
 ACTIVATIONS = {"relu": 0, "silu": 1, "gelu": 2, "swiglu": 3}
 UNIQUE_NOALLOC_MAX_KEYS = 262144
@@ -118,6 +118,7 @@ def _load() -> ctypes.CDLL:
     L.emb_expert_layer_workspace.argtypes = [i64, i32, i64, i64, i64, size]
     L.emb_expert_layer.argtypes = [vp, i32, i64, i32, i32, vp, i32, i64, i64, vp, vp, i32, i64, i64, i32, vp, vp, i32, vp,
                                    ctypes.c_size_t, vp]
+    L.emb_expert_layer_tiles.argtypes = [i64, i32, i32, i32, i64, i64, i64, i32, ctypes.POINTER(i32)]
     L.emb_dense_status.argtypes = [vp]
     L.emb_status_string.argtypes = [c_int]
     L.emb_status_string.restype = ctypes.c_char_p

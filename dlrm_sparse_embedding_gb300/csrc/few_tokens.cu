@@ -327,9 +327,10 @@ bool sizes_valid(int64_t tokens, int32_t k, int64_t in_width, int64_t hidden, in
 // in tiles: 48 x 4 of 64, 1024 -> 2048 -> 1024 (512 MB, 3 a group) 88 and 79 us; 64 x 4 of 16, 3328 -> 2048 -> 1024
 // (287 MB, 16) 87 and 59; 64 x 8 of 8, 2048 -> 2048 -> 2048 (134 MB, 64) 67 and 46; 64 x 2 of 64, 512 -> 512 -> 512
 // (67 MB, 2) 19 and 21; 16 x 2 of 16, 3328 -> 1024 -> 1024 (143 MB, 2) 29 and 35; 1 x 2 of 16, 18 MB, 14 and 26.
-bool many_weights(int64_t assignments, int64_t groups, int64_t hidden, int64_t widths)
+bool many_weights(int64_t tokens, int32_t k, int32_t experts, int64_t in_width, int64_t hidden, int64_t out_width, int32_t activation)
 {
-    const double megabytes = (double)groups * hidden * widths * 2e-6;
+    const int64_t assignments = tokens * k, groups = std::min<int64_t>(assignments, experts);     // at most
+    const double megabytes = (double)groups * hidden * ((activation == EMB_ACT_SWIGLU ? 2 : 1) * in_width + out_width) * 2e-6;
     return megabytes * (0.028 + 0.006 * assignments / groups) > 6.0;
 }
 
@@ -351,6 +352,16 @@ extern "C" int emb_expert_layer_workspace(int64_t tokens, int32_t k, int64_t in_
 {
     if (!bytes || !sizes_valid(tokens, k, in_width, hidden, out_width)) return EMB_ERR_INVALID_ARG;
     *bytes = std::max<size_t>(Room(tokens, tokens * k, in_width, hidden, out_width).all(), 256);
+    return EMB_OK;
+}
+
+extern "C" int emb_expert_layer_tiles(int64_t tokens, int32_t k, int32_t experts, int32_t x_dtype, int64_t in_width, int64_t hidden,
+                                      int64_t out_width, int32_t activation, int32_t* tiles)
+{
+    if (!tiles || !sizes_valid(tokens, k, in_width, hidden, out_width) || experts < 1 || experts > kMaxExperts || !dtype_valid(x_dtype) ||
+        activation < EMB_ACT_RELU || activation > EMB_ACT_SWIGLU)
+        return EMB_ERR_INVALID_ARG;
+    *tiles = tokens > 0 && many_weights(tokens, k, experts, in_width, hidden, out_width, activation);
     return EMB_OK;
 }
 
@@ -380,7 +391,7 @@ extern "C" int emb_expert_layer(const void* ids, int32_t id_bytes, int64_t token
     if (!(a.status = dense_status_word())) return EMB_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int64_t groups = std::min<int64_t>(tokens * k, experts);     // at most
-    const bool tiles = many_weights(tokens * k, groups, hidden, (activation == EMB_ACT_SWIGLU ? 2 : 1) * in_width + out_width);
+    const bool tiles = many_weights(tokens, k, experts, in_width, hidden, out_width, activation);
     if (!tiles && tokens * k <= kSumInDown) a.done = reinterpret_cast<int*>(at + room.rows + room.hidden + room.y);
     const auto sums = [&]() -> int {
         if (a.done) return EMB_OK;

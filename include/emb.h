@@ -478,8 +478,10 @@ int emb_expert_linear_grad_weight(const emb_expert_plan* plan, const void* grad_
  * without experts gets zeros; the weight of an assignment without one is not used.
  * Activations: relu, v / (1 + exp(-v)), v (1 + erf(v / sqrt 2)) / 2, and
  * gate / (1 + exp(-gate)) times the other half.  The workspace is 256-byte aligned,
- * emb_expert_layer_workspace bytes, and free again once the call's work is done.  No
- * passage: library convenience. */
+ * emb_expert_layer_workspace bytes, and free again once the call's work is done.
+ * emb_expert_layer_tiles tells which of its two ways a call takes, by its sizes: 1, tiles of the
+ * weights on the tensor cores, 0, warps that read them straight; either gives results
+ * within the same bounds.  No passage: library convenience. */
 #define EMB_EXPERT_LAYER_ASSIGNMENTS 512
 enum { EMB_ACT_RELU = 0, EMB_ACT_SILU = 1, EMB_ACT_GELU = 2, EMB_ACT_SWIGLU = 3 };
 int emb_expert_layer_workspace(int64_t tokens, int32_t k, int64_t in_width, int64_t hidden, int64_t out_width,
@@ -488,6 +490,8 @@ int emb_expert_layer(const void* ids, int32_t id_bytes, int64_t tokens, int32_t 
                      int32_t x_dtype, int64_t x_stride, int64_t in_width, const void* up, const void* down,
                      int32_t dtype, int64_t hidden, int64_t out_width, int32_t activation, const float* weights,
                      void* out, int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+int emb_expert_layer_tiles(int64_t tokens, int32_t k, int32_t experts, int32_t x_dtype, int64_t in_width,
+                           int64_t hidden, int64_t out_width, int32_t activation, int32_t* tiles);
 
 /* Orthogonalise `batch` matrices G [rows, cols] by `steps` (1..32) quintic
  * Newton-Schulz steps, as the Muon optimiser does with a momentum
