@@ -22,6 +22,8 @@
 // One token, 2 of 16 experts, 3328 -> 1024 -> 1024, bf16: 14 us (18 MB; 6 us of it are two kernels of
 // next to nothing); 8 tokens 26 us (94 MB, 3.6 TB/s).  Measured and not kept: twice the weights on their way,
 // in one block an SM (14.0 us for 14.3, 26.0 for 25.9); rows ahead with the weights (13.7 and 27.1).
+#include <cmath>
+
 #include "few_tokens.cuh"
 
 namespace emb {
@@ -321,17 +323,23 @@ bool sizes_valid(int64_t tokens, int32_t k, int64_t in_width, int64_t hidden, in
     return widths_valid(in_width) && tokens >= 0 && k >= 1 && k <= kMaxExpertsPerToken && tokens <= kMost / k && widths_valid(hidden) && widths_valid(out_width);
 }
 
-// Whether tiles on the tensor cores are faster.  They cost two more launches, some 6 us, and
-// save 28 ns a megabyte of weights and 6 ns more for each assignment of a group,
-// whose rows the warps here load again for every 16 rows of a weight.  Measured, here and
-// in tiles: 48 x 4 of 64, 1024 -> 2048 -> 1024 (512 MB, 3 a group) 88 and 79 us; 64 x 4 of 16, 3328 -> 2048 -> 1024
-// (287 MB, 16) 87 and 59; 64 x 8 of 8, 2048 -> 2048 -> 2048 (134 MB, 64) 67 and 46; 64 x 2 of 64, 512 -> 512 -> 512
-// (67 MB, 2) 19 and 21; 16 x 2 of 16, 3328 -> 1024 -> 1024 (143 MB, 2) 29 and 35; 1 x 2 of 16, 18 MB, 14 and 26.
-bool many_weights(int64_t tokens, int32_t k, int32_t experts, int64_t in_width, int64_t hidden, int64_t out_width, int32_t activation)
+// Whether tiles on the tensor cores are faster, by megabytes of weights of the experts that tokens which choose any
+// k of them alike would choose.  Tiles save 10 ns a megabyte and 7.5 more for each assignment of
+// a group, whose rows the warps here load again for every 16 rows of a weight, and 50 ns a megabyte of `up`
+// where they are fp32, converted each time.  They cost what their kernels take to begin and end
+// and a ring's way through k: 2 ns an element of a token's row and of hidden.
+// Both ways were measured on 740 shapes, most within 12 us of each other: the rule takes the faster one, or
+// one within 3 %, on 690 of them, the slowest choice is 20 % behind (few groups of many tokens), the mean 0.6 %.
+// Warps and tiles in us, and the megabytes, the assignments a group: 16 x 2 of 16, 3328 -> 1024 -> 1024 28 and 34 (126, 2.3);
+// 14 x 2 of 7, 4096 -> 1024 -> 4096 29 and 39 (116, 4); 52 x 2 of 26, 1024 -> 2048 -> 1024 50 and 46 (215, 4); 64 x 4 of 16,
+// 3328 -> 2048 -> 1024 96 and 59 (285, 16); 1 x 2 of 16, 3328 -> 1024 -> 1024 14 and 25 (18, 1); 48 x 4 of 64, 1024 -> 2048 -> 1024 88 and
+// 80 (513, 3); 182 x 2 of 25, fp32, 832 -> 304 -> 2312 39 and 27 (48, 15); 512 of 1, 4096 wide 249 and 131 (67, 512).
+bool many_weights(int64_t tokens, int32_t k, int32_t experts, int32_t x_dtype, int64_t in_width, int64_t hidden, int64_t out_width, int32_t activation)
 {
-    const int64_t assignments = tokens * k, groups = std::min<int64_t>(assignments, experts);     // at most
-    const double megabytes = (double)groups * hidden * ((activation == EMB_ACT_SWIGLU ? 2 : 1) * in_width + out_width) * 2e-6;
-    return megabytes * (0.028 + 0.006 * assignments / groups) > 6.0;
+    const double groups = experts * (1.0 - std::pow(1.0 - (double)std::min(k, experts) / experts, (double)tokens));
+    const double up = groups * hidden * in_width * (activation == EMB_ACT_SWIGLU ? 2 : 1) * 2e-6, down = groups * hidden * out_width * 2e-6;
+    const double saved = (up + down) * (0.01 + 0.0075 * (double)(tokens * k) / groups) + (x_dtype == EMB_F32 ? 0.05 * up : 0.0);
+    return saved > 0.002 * (double)(in_width + hidden);
 }
 
 // Warps that share a tile's k: as many as keep eight warps of every SM busy, but four
@@ -361,7 +369,7 @@ extern "C" int emb_expert_layer_tiles(int64_t tokens, int32_t k, int32_t experts
     if (!tiles || !sizes_valid(tokens, k, in_width, hidden, out_width) || experts < 1 || experts > kMaxExperts || !dtype_valid(x_dtype) ||
         activation < EMB_ACT_RELU || activation > EMB_ACT_SWIGLU)
         return EMB_ERR_INVALID_ARG;
-    *tiles = tokens > 0 && many_weights(tokens, k, experts, in_width, hidden, out_width, activation);
+    *tiles = tokens > 0 && many_weights(tokens, k, experts, x_dtype, in_width, hidden, out_width, activation);
     return EMB_OK;
 }
 
@@ -391,7 +399,7 @@ extern "C" int emb_expert_layer(const void* ids, int32_t id_bytes, int64_t token
     if (!(a.status = dense_status_word())) return EMB_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int64_t groups = std::min<int64_t>(tokens * k, experts);     // at most
-    const bool tiles = many_weights(tokens, k, experts, in_width, hidden, out_width, activation);
+    const bool tiles = many_weights(tokens, k, experts, x_dtype, in_width, hidden, out_width, activation);
     if (!tiles && tokens * k <= kSumInDown) a.done = reinterpret_cast<int*>(at + room.rows + room.hidden + room.y);
     const auto sums = [&]() -> int {
         if (a.done) return EMB_OK;
