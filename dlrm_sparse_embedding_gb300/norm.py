@@ -15,6 +15,7 @@ from ._lib import check, lib
 from .experts import _DTYPE_CODE, _dtype, _on, _stream
 
 _LOW64 = 2 ** 64 - 1
+_LARGEST = torch.finfo(torch.float32).max
 
 
 # Checks of shapes and types, which a program repeats call for call, are kept by those.
@@ -77,8 +78,8 @@ def _param(t, name: str, device) -> int:
 
 def _eps(eps) -> float:
     eps = float(eps)
-    if not 1e-24 <= eps <= 1e30:
-        raise ValueError("eps must be in 1e-24 .. 1e30, got %r" % (eps,))
+    if not 1e-24 <= eps <= _LARGEST:
+        raise ValueError("eps must be in 1e-24 .. %g, got %r" % (_LARGEST, eps))
     return eps
 
 
@@ -86,7 +87,8 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
                dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
     """[rows, width] in `dtype` (default x's): each row of x [rows, width] less its mean,
     over the root of its variance plus eps, times weight plus bias (each [width], of
-    one type; None: ones, zeros).  Sums and statistics are fp32; x of any row stride."""
+    one type; None: ones, zeros).  Sums and statistics are fp32; x of any row stride;
+    eps from 1e-24 to fp32's largest number."""
     if stream is not None:
         return _on(stream, layer_norm, x, weight, bias, eps, dtype)
     _tensor(x, "x")
