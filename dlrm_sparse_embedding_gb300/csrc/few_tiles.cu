@@ -9,10 +9,12 @@
 // rows that follow the group's are read with it and their columns left alone.
 // A kernel's first weights are copied before the kernel before it is done.
 //
-// 48 tokens, 4 of 64 experts, 1024 -> 2048 -> 1024, fp16: 78 us (513 MB, 6.6 TB/s); 64, 4 of 16, 3328 -> 2048 -> 1024, bf16: 58
-// (286 MB, 4.9 TB/s); 64, 8 of 8, 2048 wide: 46 (134 MB).  13 to 18 us are what four kernels of next to nothing take.  Measured
-// and not kept: one CTA an SM with six stages, its B brought by four warps (83, 81 and 70 us); the last
-// expert's CTA adding a tile's tokens up (85, 85 and 87).
+// 48 tokens, 4 of 64 experts, 1024 -> 2048 -> 1024, fp16: 78 us (about 460 MB of chosen experts, 5.9 TB/s); 64, 4 of 16, 3328 ->
+// 2048 -> 1024, bf16: 58 (286 MB, 4.9 TB/s); 64, 8 of 8, 2048 wide: 46 (134 MB), fewer tiles than places for CTAs.  The four kernels
+// take 11 us with 64 wide weights, and a tile's way through k 3 ns an element of it (1 of 1, 3328 -> 3328 -> 64: 33 us).  A
+// group of more than TOKENS reads its weights again for each TOKENS, from L2 where they fit: 256 tokens, 2 of 4, 2048 wide 48 us
+// (67 MB), 512 of 1, 4096 wide 131 (67 MB).  Measured and not kept: one CTA an SM with six stages, its B brought by four
+// warps (83, 81 and 70 us); the last expert's CTA adding a tile's tokens up (85, 85 and 87).
 #include "few_tokens.cuh"
 #include "product_core.cuh"
 

@@ -2,8 +2,8 @@
 //
 //   hidden[a] = act(up[e] x[t]),  y[a] = down[e] hidden[a],  out[t] = sum_j weights[t, j] y[t k + j]
 //
-// of assignment a = t k + j to expert e.  Bound by reading the chosen experts' weights,
-// once: one request's tokens use each number of them a few times.  So a warp takes
+// of assignment a = t k + j to expert e.  Bound by reading the chosen experts' weights, once for
+// each kChunk of an expert's assignments: one request's tokens use each number of them a few times.  So a warp takes
 // 16 rows of a weight and reads them straight into registers as the left operand of
 // the warp's matrix instruction, 16 bytes a lane; the group's tokens, 8 at a time, are the
 // right one.  The order of k within an instruction is free as long as both operands
@@ -19,8 +19,11 @@
 // Either adds in the order of j, so results repeat bit for bit.  Every block makes the groups
 // for itself in shared memory.
 //
-// One token, 2 of 16 experts, 3328 -> 1024 -> 1024, bf16: 14 us (18 MB; 6 us of it are two kernels of
-// next to nothing); 8 tokens 26 us (94 MB, 3.6 TB/s).  Measured and not kept: twice the weights on their way,
+// One token, 2 of 16 experts, 3328 -> 1024 -> 1024, fp32 tokens, bf16: 14 us (18 MB; 7 us are what the two kernels
+// take with 64 wide weights); 8 tokens 28 us (80 MB, 2.9 TB/s): layer_down's weights come from DRAM only when
+// layer_up is done, but for the first steps.  256 x 2 of 4, 2048 wide, each weight read twice: 89 us (tiles 48).
+// One kernel holds the products of 8, 16, 32 and 64 of a group, and the two blocks an SM leave it 128 registers: 36 to 140
+// bytes a thread spill.  Measured and not kept: twice the weights on their way,
 // in one block an SM (14.0 us for 14.3, 26.0 for 25.9); rows ahead with the weights (13.7 and 27.1).
 #include <cmath>
 
@@ -199,7 +202,9 @@ __device__ __forceinline__ void walk(const Args& a, const Groups& g, float* shar
     }
 }
 
-// hidden = act(up x), rounded to T, the type the second product takes
+// hidden = act(up x), rounded to T: the second product's operands are 16-bit numbers, as in expert_linear.  Of bf16's
+// output 2.3e-3 of its size is off 64 bits, 1.7e-3 where hidden stays fp32 (fp16 2.9e-4 and 2.1e-4): the output's own
+// rounding is the larger part.  Nothing else of the call is held in fewer bits than fp32.
 template <class T, class X, bool GATED>
 __global__ void __launch_bounds__(kThreads, kPerSm) layer_up(const Args a)
 {

@@ -38,7 +38,7 @@ Shape shape_of(int64_t rows, int64_t width, bool grad, bool vectors)
     } else {
         s.tx = (threads + 31) / 32 * 32;
         // A gradient's short rows share a block by as many as leave the SM as many rows as ones alone would: 20000 x 1536
-        // bf16 50.7 us with five, 55 with two; of more than four warps a row alone (16384 x 3328 87 us, with two 91).
+        // bf16 48.5 us with five, 52 with two; of more than four warps a row alone (16384 x 3328 87 us, with two 91).
         const int held = 65536 / (registers(s.per_thread, grad, vectors) * s.tx);
         s.ty = !grad || s.tx > 128 ? 1 : held <= kMaxSubs ? held : held / 2;
     }

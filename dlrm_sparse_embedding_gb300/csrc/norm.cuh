@@ -9,11 +9,13 @@
 // around it and the result are three passes over registers.  The gradient takes x again instead of
 // stored statistics: it has to read x for h.  fp32 elements take two an instruction.
 //
-// 16384 x 3328, fp32 to bf16: forward 51 us (6.4 TB/s), gradients 86 (6.3).  Two bytes an element are too
-// few for the sums' latency and instructions: bf16 alone 43 (5.0 TB/s) and 87 (3.8); 425984 x 128
-// bf16 39 (5.7) and 67 (4.9).  Rows without a 16-byte rhythm go element by element: 32768 x 1025 fp16 83
-// and 99 us (1.6 and 2.0).  Past 8192 elements (of a forward in vectors, 16384) a row is read three times
-// and its columns' sums by a second kernel: 4000 x 16384 gradients 296 us (2.7), bf16 192 (2.1).
+// 16384 x 3328, fp32 to bf16: forward 51 us (6.5 TB/s), gradients 87 (6.3).  Two bytes an element are too
+// few for the sums' latency and instructions: bf16 alone 42 (5.2 TB/s) and 86 (3.8); 425984 x 128
+// bf16 39 (5.7) and 67 (4.9).  Rows without a 16-byte rhythm go element by element: 32768 x 1025 fp16 81
+// and 94 us (1.7 and 2.1), and their kernels spill 16 to 100 bytes a thread (a warp's rows of 32 elements a thread
+// up to 184).  Past 8192 elements (of a forward in vectors, 16384) a row is read three times
+// and its columns' sums by a second kernel: 4000 x 16384 gradients fp32 to bf16 305 us (2.1), bf16 194 (2.0);
+// 2000 x 32768 forward 191 (2.1) and 128 (2.1).
 //
 // The mean is a rounded sum; what the rounding left, d = mean(x - m), is measured in the
 // second pass and taken off again, so rows far from zero lose no more than their own
@@ -81,7 +83,7 @@ constexpr int kMaxStages = 8, kMaxSubs = 5;
 constexpr int kSharedBytes = 226 * 1024;         // of an SM, for its blocks
 constexpr int kOwnBytes = 2944;                  // of a block beside its stages
 // Of an SM, for the stages, two at least: more on their way are slower (16384 x 3328, fp32 to bf16, forward:
-// 50.8 us, with all of the memory 57.7; gradients 86.3 and 87.1, with two stages 93.6).
+// 51 us, with all of the memory 58; gradients 86 and 87, with two stages 94).
 constexpr int kRingBytes = 120 * 1024;
 constexpr int kChunkBytes = 4096;                // of a warp's stage
 constexpr int kColumnRows = 8;                   // rows at a time of a block of wide_columns
@@ -351,7 +353,7 @@ struct Piece {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     // where there is nothing, zero stays zero; a block's gradient is faster without the
-                    // branch (16384 x 3328, fp32 to bf16: 97 and 88 us), a warp's with it (425984 x 128: 93 and 105)
+                    // branch (16384 x 3328, fp32 to bf16: 98 and 87 us), a warp's with it (425984 x 128: 93 and 105)
                     const Two less(in(u) ? -mo.m : 0.f);
                     if (!BLOCK && !in(u)) continue;
 #pragma unroll
@@ -473,8 +475,8 @@ __device__ __forceinline__ void put_sums(const Args& a, const PIECE& p, float* s
 }
 
 // Longer rows: blockDim.x threads take one at a time, and a block has, SUBS, up to kMaxSubs rows'
-// threads, so that fewer blocks leave sums of a gradient's columns (1000 x 1024 bf16: 19.9 us with
-// one, 8.5 with four; 50000: 75 both).  Rows are
+// threads, so that fewer blocks leave sums of a gradient's columns (1000 x 1024 bf16: 19.0 us with
+// one, 8.6 with four; 50000: 74.0 and 71.4).  Rows are
 // copied to a ring of stages, each row's threads have their own; a stage is free for the
 // next row when the second sums' barrier has been met.
 //

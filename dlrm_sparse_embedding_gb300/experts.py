@@ -356,7 +356,8 @@ def expert_layer(ids: torch.Tensor, x: torch.Tensor, up: torch.Tensor, down: tor
 
     What expert_sort, expert_dispatch, expert_linear, the activation, expert_linear and
     expert_combine give, but that the second product's rows stay fp32 up to the sum; up to
-    512 assignments (tokens * k), bound by the chosen experts' weights.
+    512 assignments (tokens * k), bound by the chosen experts' weights, which are read once for
+    each 64 assignments of an expert (each 128 where there are more than 64 tokens and many weights).
 
     ids: int32 or int64 [tokens, k], -1 for none (others out of range are reported by
     dense_status()).  x: float32 or up's dtype [tokens, in], any row stride of whole 16

@@ -463,7 +463,7 @@ int emb_expert_linear_grad_weight(const emb_expert_plan* plan, const void* grad_
                                   int32_t dtype, void* grad_weight, void* stream);
 
 /* The whole expert layer for a few tokens, from their ids to their sums, in two to four
- * kernels that read each chosen expert's weights once:
+ * kernels:
  *   out[t] = sum_j weights[t, j] down[e] act(up[e] x[t]),  e = ids[t, j]
  * ids [tokens, k] as for emb_expert_sort (-1: none; any other id outside [0, E) is
  * treated as -1 and recorded as EMB_ERR_KEY_RANGE); tokens * k is at most
@@ -472,7 +472,9 @@ int emb_expert_linear_grad_weight(const emb_expert_plan* plan, const void* grad_
  * up is [E, hidden, in_width] ([E, 2 hidden, in_width] for EMB_ACT_SWIGLU: the gates' rows,
  * then the rows they let through), down [E, out_width, hidden], both of dtype; weights
  * fp32 [tokens, k]; out [tokens, out_width] of any emb_dtype.  Widths are multiples of 8,
- * x, up, down and out 16-byte aligned, x's rows at multiples of 16 bytes.  Sums are
+ * x, up, down and out 16-byte aligned, x's rows at multiples of 16 bytes.  A chosen expert's
+ * weights are read once for each 64 of its assignments (in tiles, of a call of more than 64
+ * tokens, for each 128).  Sums are
  * fp32 as in the experts' products; what the activation gives is rounded to dtype, the
  * type the second product takes, y stays fp32 up to the sum over j, in order.  A token
  * without experts gets zeros; the weight of an assignment without one is not used.
