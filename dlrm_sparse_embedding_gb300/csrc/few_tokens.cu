@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) layer_up(const Args a)
             const int unit = tile * kUnits + r, left = a.hidden - unit;
             T* const to = hidden + (int64_t)assignment * a.hidden + unit;
             if constexpr (GATED) {
-                if (left > 0) to[0] = from_float<T>(activate(a.act, low) * high);
+                if (left > 0) to[0] = from_float<T>(activate(EMB_ACT_SILU, low) * high);
             } else {
                 if (left > 0) to[0] = from_float<T>(activate(a.act, low));
                 if (left > 8) to[8] = from_float<T>(activate(a.act, high));

@@ -172,7 +172,8 @@ __device__ __forceinline__ void make_groups(const Args& a, Groups& g, unsigned c
 __device__ __forceinline__ float activate(int act, float v)
 {
     if (act == EMB_ACT_RELU) return v < 0.f ? 0.f : v;      // a NaN stays one
-    if (act == EMB_ACT_GELU) return 0.5f * v * (1.f + erff(v * 0.70710678f));
+    // 1 + erf(v / sqrt 2), which loses its digits where erf comes near -1
+    if (act == EMB_ACT_GELU) return 0.5f * v * erfcf(v * -0.70710678f);
     return v / (1.f + expf(-v));
 }
 

@@ -478,8 +478,8 @@ int emb_expert_linear_grad_weight(const emb_expert_plan* plan, const void* grad_
  * fp32 as in the experts' products; what the activation gives is rounded to dtype, the
  * type the second product takes, y stays fp32 up to the sum over j, in order.  A token
  * without experts gets zeros; the weight of an assignment without one is not used.
- * Activations: relu, v / (1 + exp(-v)), v (1 + erf(v / sqrt 2)) / 2, and
- * gate / (1 + exp(-gate)) times the other half.  The workspace is 256-byte aligned,
+ * Activations: relu, v / (1 + exp(-v)), v (1 + erf(v / sqrt 2)) / 2 (as v erfc(-v / sqrt 2) / 2,
+ * so that it keeps its digits where it is small), and gate / (1 + exp(-gate)) times the other half.  The workspace is 256-byte aligned,
  * emb_expert_layer_workspace bytes, and free again once the call's work is done.
  * emb_expert_layer_tiles tells which of its two ways a call takes, by its sizes: 1, tiles of the
  * weights on the tensor cores, 0, warps that read them straight; either gives results
